@@ -26,7 +26,10 @@ EXPORTS = ("moe_packed_bytes", "moe_workspace_bytes", "moe_workspace_sync_bytes"
            "moe_decode_max_tokens", "moe_step_graph_create", "moe_step_graph_launch", "moe_step_graph_destroy",
            "moe_probe_stream_read", "moe_probe_mfma",
            "moe_status_string", "moe_tier_create", "moe_tier_destroy", "moe_tier_use", "moe_tier_prefetch",
-           "moe_tier_slot", "moe_tier_stats", "moe_tier_sync")
+           "moe_tier_slot", "moe_tier_stats", "moe_tier_sync",
+           "moe_sort_rows", "moe_sort_workspace_bytes", "moe_sort", "moe_dispatch", "moe_dispatch_backward",
+           "moe_combine", "moe_combine_backward", "moe_route_backward_workspace_bytes", "moe_route_backward",
+           "moe_adapter_workspace_bytes", "moe_adapter_forward", "moe_adapter_backward")
 MOE_TIER_LRU, MOE_TIER_HOT = 0, 1
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20  # include/moe_w4a16.h
 MOE_STEP_GRAPH_MAX_LAYERS = 4096  # include/moe_w4a16.h
@@ -46,6 +49,12 @@ class MoeWeights(ctypes.Structure):
 class MoeTierStats(ctypes.Structure):
     _fields_ = [("hits", ctypes.c_int64), ("misses", ctypes.c_int64), ("promotions", ctypes.c_int64),
                 ("evictions", ctypes.c_int64), ("prefetched", ctypes.c_int64), ("bytes_promoted", ctypes.c_int64)]
+
+
+class MoeAdapters(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("n", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("R", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -110,6 +119,27 @@ def lib():
         L.moe_tier_stats.restype = ctypes.c_int
         L.moe_tier_sync.argtypes = [P, P]
         L.moe_tier_sync.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        A = ctypes.POINTER(MoeAdapters)
+        L.moe_sort_rows.argtypes = [i32, i32, i32, i32]
+        L.moe_sort_rows.restype = i64
+        L.moe_sort_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_sort_workspace_bytes.restype = sz
+        L.moe_sort.argtypes = [P, i32, i32, i32, i32, P, P, P, P, sz, P]
+        L.moe_dispatch.argtypes = [P, i32, i32, i32, P, i32, i32, i32, P, P, P, P, P, sz, P]
+        L.moe_dispatch_backward.argtypes = [P, i32, i32, i32, P, i32, i32, P, P, P]
+        L.moe_combine.argtypes = [P, i32, i32, i32, P, P, i32, i32, P, P, P]
+        L.moe_combine_backward.argtypes = [P, P, i32, i32, i32, P, P, P, i32, i32, P, P, P]
+        L.moe_route_backward_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.moe_route_backward_workspace_bytes.restype = sz
+        L.moe_route_backward.argtypes = [P, i32, i32, i32, i32, i32, P, P, P, P, P, P, i32, P, P, P, P, P, sz, P]
+        L.moe_adapter_workspace_bytes.argtypes = [A, i32]
+        L.moe_adapter_workspace_bytes.restype = sz
+        L.moe_adapter_forward.argtypes = [A, P, i64, i32, P, P, P, P, i64, P, i64, P, P, sz, P]
+        L.moe_adapter_backward.argtypes = [A, P, i64, P, i64, P, i32, P, P, P, P, i64, P, i64, P, P, P, sz, P]
+        for n in ("moe_sort", "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+                  "moe_route_backward", "moe_adapter_forward", "moe_adapter_backward"):
+            getattr(L, n).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -437,3 +467,8 @@ class Tier:
         """moe_weights_t of one layer that reads its experts through the table."""
         ptr = self.table.data_ptr() + layer * self.dims.n_experts * 8
         return MoeWeights(ptr, shared_ptr, router_w.data_ptr(), None if router_b is None else router_b.data_ptr())
+
+
+from .dispatch import (MOE_T_BF16, MOE_T_F16, MOE_T_F32, moe_combine, moe_combine_backward, moe_dispatch,  # noqa: E402
+                       moe_dispatch_backward, moe_route_backward, moe_sort, moe_sort_rows)
+from .adapter import moe_adapter_backward, moe_adapter_forward  # noqa: E402

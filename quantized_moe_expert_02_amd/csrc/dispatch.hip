@@ -1,0 +1,375 @@
+// Tokens sorted by expert, their rows laid out and combined, and the
+// gradients (include/moe_dispatch.h).
+#include <algorithm>
+
+#include "rows.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kSortMaxBlocks = 128;
+
+// Slots per workgroup (a multiple of kSortThreads) and number of workgroups.
+struct SortSplit {
+  int per_block, blocks;
+};
+SortSplit sort_split(int64_t n) {
+  const int64_t chunks = (n + kSortThreads - 1) / kSortThreads;
+  const int64_t m = std::max<int64_t>(1, (chunks + kSortMaxBlocks - 1) / kSortMaxBlocks);
+  return {(int)(m * kSortThreads), (int)((chunks + m - 1) / m)};
+}
+
+// Lanes of the wavefront that hold the same id (0 <= id < 1024; lanes with
+// ok == false match nothing).
+__device__ __forceinline__ uint64_t match_id(int id, bool ok, int bits) {
+  uint64_t m = __ballot(ok);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (id >> b) & 1;
+    const uint64_t v = __ballot(one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
+
+__device__ __forceinline__ int lanes_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// Per-workgroup expert counts, [blocks][E].
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(const int32_t* idx, int n, int E, int per_block,
+                                                             int32_t* cnt) {
+  __shared__ int h[kMaxExperts];
+  const int tid = threadIdx.x;
+  h[tid] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * per_block, hi = min(lo + per_block, (int64_t)n);
+  for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
+    const int e = idx[i];
+    if ((unsigned)e < (unsigned)E) atomicAdd(&h[e], 1);
+  }
+  __syncthreads();
+  if (tid < E) cnt[(size_t)blockIdx.x * E + tid] = h[tid];
+}
+
+// Places every slot: a stable counting sort.  Each workgroup derives the
+// group starts from all workgroups' counts (a column per thread), then walks
+// its slots 1024 at a time: a wavefront ranks its 64 slots by matching ids,
+// the wavefronts' counts are prefixed per expert in LDS.  With one workgroup
+// the counts are its own and cnt is not read.
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx, int n, int E, int bits, int align,
+                                                             int rows, int per_block, int blocks, const int32_t* cnt,
+                                                             int32_t* offsets, int32_t* pairs, int32_t* pos) {
+  __shared__ int base[kMaxExperts];
+  __shared__ uint16_t wc[kSortWaves][kMaxExperts];
+  __shared__ int wsum[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, blk = blockIdx.x;
+  const int64_t lo = (int64_t)blk * per_block, hi = min(lo + per_block, (int64_t)n);
+
+  int total = 0, before = 0;
+  if (blocks == 1) {
+    base[tid] = 0;
+    __syncthreads();
+    for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
+      const int e = idx[i];
+      if ((unsigned)e < (unsigned)E) atomicAdd(&base[e], 1);
+    }
+    __syncthreads();
+    total = tid < E ? base[tid] : 0;
+    __syncthreads();
+  } else if (tid < E) {
+    for (int b = 0; b < blocks; ++b) {
+      const int c = cnt[(size_t)b * E + tid];
+      total += c;
+      before += b < blk ? c : 0;
+    }
+  }
+  const int padded = (total + align - 1) / align * align;
+  int incl = padded;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    incl += lane >= d ? o : 0;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int start = incl - padded, all = 0;
+  for (int w = 0; w < kSortWaves; ++w) {
+    start += w < wave ? wsum[w] : 0;
+    all += wsum[w];
+  }
+  base[tid] = start + before;
+  if (tid < E && blk == tid % blocks)
+    for (int r = start + total; r < start + padded; ++r) pairs[r] = -1;
+  if (blk == 0) {
+    if (tid < E) offsets[tid] = start;
+    if (tid == 0) offsets[E] = all;
+  }
+  for (int64_t r = (int64_t)all + (int64_t)blk * kSortThreads + tid; r < rows; r += (int64_t)blocks * kSortThreads)
+    pairs[r] = -1;
+
+  for (int64_t i0 = lo; i0 < hi; i0 += kSortThreads) {
+    const int64_t i = i0 + tid;
+    const int id = i < hi ? idx[i] : -1;
+    const bool ok = (unsigned)id < (unsigned)E;
+    const uint64_t same = match_id(id, ok, bits);
+    const int rank = lanes_below(same);
+    for (int w = wave; w < kSortWaves; w += kSortWaves)
+      for (int e = lane; e < E; e += 64) wc[w][e] = 0;
+    __syncthreads();
+    if (ok && rank == 0) wc[wave][id] = (uint16_t)__popcll(same);
+    __syncthreads();
+    int pre = 0;
+    if (tid < E)
+      for (int w = 0; w < kSortWaves; ++w) {
+        const int c = wc[w][tid];
+        wc[w][tid] = (uint16_t)pre;
+        pre += c;
+      }
+    __syncthreads();
+    if (i < hi) {
+      const int r = ok ? base[id] + wc[wave][id] + rank : -1;
+      pos[i] = r;
+      if (ok) pairs[r] = (int)i;
+    }
+    __syncthreads();
+    if (tid < E) base[tid] += pre;
+  }
+}
+
+// xs[pos(t,j)] = x[t], token by token, 16-byte vectors; workgroups past the
+// tokens' zero the rows that hold no slot.
+constexpr int kRowThreads = 256;
+constexpr int kPadRows = 64;  // rows looked over by one zeroing workgroup
+
+__device__ __forceinline__ void zero_pad_rows(const int32_t* pairs, int rows, int part, u32x4* out, int nv) {
+  const int r0 = part * kPadRows, r1 = min(r0 + kPadRows, rows);
+  for (int r = r0; r < r1; ++r)
+    if (pairs[r] < 0)
+      for (int i = threadIdx.x; i < nv; i += kRowThreads) out[(size_t)r * nv + i] = u32x4{0, 0, 0, 0};
+}
+
+__global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, int T, int nv, int k, int rows,
+                                                              const int32_t* pos, const int32_t* pairs, u32x4* xs) {
+  const int t = blockIdx.x;
+  if (t >= T) return zero_pad_rows(pairs, rows, t - T, xs, nv);
+  const int32_t* p = pos + (size_t)t * k;
+  for (int i = threadIdx.x; i < nv; i += kRowThreads) {
+    const u32x4 v = x[(size_t)t * nv + i];
+    for (int j = 0; j < k; ++j) {
+      const int r = p[j];
+      if (r >= 0) xs[(size_t)r * nv + i] = v;
+    }
+  }
+}
+
+// y[t] = add[t] + sum_j w[t][j] o[pos(t,j)] (w == NULL: all ones), slots in order.
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int rows, int nv, const float* w,
+                                                            const int32_t* pos, int k, const u32x4* add, u32x4* y) {
+  constexpr int VE = kVec<DT>;
+  const int t = blockIdx.x, i = blockIdx.y * kRowThreads + threadIdx.x;
+  if (i >= nv) return;
+  float acc[VE] = {};
+  if (add) unpack_vec<DT>(add[(size_t)t * nv + i], acc);
+  for (int j = 0; j < k; ++j) {
+    const int r = pos[(size_t)t * k + j];
+    if ((unsigned)r >= (unsigned)rows) continue;
+    float f[VE];
+    unpack_vec<DT>(o[(size_t)r * nv + i], f);
+    const float wj = w ? w[(size_t)t * k + j] : 1.0f;
+#pragma unroll
+    for (int c = 0; c < VE; ++c) acc[c] = fmaf(wj, f[c], acc[c]);
+  }
+  y[(size_t)t * nv + i] = pack_vec<DT>(acc);
+}
+
+// d_o[pos(t,j)] = w dy[t]; dw[t][j] = <dy[t], o[pos(t,j)]>.  One workgroup per
+// token; the workgroups past the tokens' zero padding rows.
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, const u32x4* o, int rows, int nv,
+                                                              const float* w, const int32_t* pos,
+                                                              const int32_t* pairs, int T, int k, u32x4* d_o,
+                                                              float* dw) {
+  constexpr int VE = kVec<DT>;
+  __shared__ float part[kRowThreads / kWave];
+  const int t = blockIdx.x;
+  if (t >= T) return zero_pad_rows(pairs, rows, t - T, d_o, nv);
+  for (int j = 0; j < k; ++j) {
+    const int r = pos[(size_t)t * k + j];
+    float dot = 0.0f;
+    if ((unsigned)r < (unsigned)rows) {
+      const float wj = w[(size_t)t * k + j];
+      for (int i = threadIdx.x; i < nv; i += kRowThreads) {
+        float g[VE], f[VE];
+        unpack_vec<DT>(dy[(size_t)t * nv + i], g);
+        unpack_vec<DT>(o[(size_t)r * nv + i], f);
+#pragma unroll
+        for (int c = 0; c < VE; ++c) {
+          dot = fmaf(g[c], f[c], dot);
+          g[c] *= wj;
+        }
+        d_o[(size_t)r * nv + i] = pack_vec<DT>(g);
+      }
+    }
+    dot = wave_sum_f32(dot);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float s = 0.0f;
+      for (int q = 0; q < kRowThreads / kWave; ++q) s += part[q];
+      dw[(size_t)t * k + j] = s;
+    }
+    __syncthreads();
+  }
+}
+
+int id_bits(int E) {
+  int b = 0;
+  while ((1 << b) < E) ++b;
+  return b;
+}
+
+// Rows given as [T][H] of `dtype`: a supported width and type.
+int check_rows(int32_t dtype, int32_t T, int32_t H) {
+  if (dtype != MOE_T_F16 && dtype != MOE_T_BF16 && dtype != MOE_T_F32) return MOE_E_INVAL;
+  if (T < 0 || H <= 0) return MOE_E_INVAL;
+  return H % 8 ? MOE_E_UNSUPPORTED : MOE_OK;
+}
+
+int check_slots(int32_t T, int32_t k, int32_t rows) {
+  if (T < 0 || k < 1 || rows < 0 || (int64_t)T * k > kMaxSlots) return MOE_E_INVAL;
+  return k > kMaxTopK ? MOE_E_UNSUPPORTED : MOE_OK;
+}
+
+inline bool bad(const void* p, unsigned align) { return !p || !aligned_to(p, align); }
+
+}  // namespace
+
+int check_sort_shape(int32_t T, int32_t k, int32_t E, int32_t align) {
+  if (T < 0 || k < 1 || E < 1 || k > E || align < 1 || align > 1024 || (int64_t)T * k > kMaxSlots) return MOE_E_INVAL;
+  if (k > kMaxTopK || E > kMaxExperts) return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+hipError_t launch_sort(const int32_t* idx, int T, int k, int E, int align, int rows, int32_t* offsets,
+                       int32_t* pairs, int32_t* pos, void* ws, hipStream_t s) {
+  const int n = T * k;
+  const SortSplit sp = sort_split(n);
+  int32_t* cnt = (int32_t*)ws;
+  if (sp.blocks > 1) {
+    k_sort_count<<<sp.blocks, kSortThreads, 0, s>>>(idx, n, E, sp.per_block, cnt);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  k_sort_place<<<std::max(1, sp.blocks), kSortThreads, 0, s>>>(idx, n, E, id_bits(E), align, rows, sp.per_block,
+                                                              std::max(1, sp.blocks), cnt, offsets, pairs, pos);
+  return hipGetLastError();
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int64_t moe_sort_rows(int32_t T, int32_t k, int32_t n_experts, int32_t align) {
+  if (check_sort_shape(T, k, n_experts, align) != MOE_OK) return -1;
+  int64_t r = (int64_t)T * k;
+  if (align > 1) r = (r + std::min<int64_t>(n_experts, r) * (align - 1) + align - 1) / align * align;
+  return r < ((int64_t)1 << 31) ? r : -1;
+}
+
+size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t n_experts) {
+  if (check_sort_shape(T, k, n_experts, 1) != MOE_OK) return 0;
+  return round256((size_t)std::max(1, sort_split((int64_t)T * k).blocks) * n_experts * 4);
+}
+
+int moe_sort(const int32_t* topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t align, int32_t* offsets,
+             int32_t* pairs, int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_sort_shape(T, k, n_experts, align);
+  if (st != MOE_OK) return st;
+  const int64_t rows = moe_sort_rows(T, k, n_experts, align);
+  if (rows < 0) return MOE_E_INVAL;
+  if (bad(offsets, 4) || (T && (bad(topk_idx, 4) || bad(pairs, 4) || bad(pos, 4)))) return MOE_E_INVAL;
+  if (bad(ws, 16)) return MOE_E_INVAL;
+  if (ws_bytes < moe_sort_workspace_bytes(T, k, n_experts)) return MOE_E_WORKSPACE;
+  return launch_sort(topk_idx, T, k, n_experts, align, (int)rows, offsets, pairs, pos, ws, (hipStream_t)stream) ==
+                 hipSuccess
+             ? MOE_OK
+             : MOE_E_HIP;
+}
+
+int moe_dispatch(const void* x, int32_t dtype, int32_t T, int32_t H, const int32_t* topk_idx, int32_t k,
+                 int32_t n_experts, int32_t align, void* xs, int32_t* offsets, int32_t* pairs, int32_t* pos,
+                 void* ws, size_t ws_bytes, void* stream) {
+  int st = check_rows(dtype, T, H);
+  if (st != MOE_OK) return st;
+  st = check_sort_shape(T, k, n_experts, align);
+  if (st != MOE_OK) return st;
+  if (T && (bad(x, 16) || bad(xs, 16))) return MOE_E_INVAL;
+  st = moe_sort(topk_idx, T, k, n_experts, align, offsets, pairs, pos, ws, ws_bytes, stream);
+  if (st != MOE_OK || T == 0) return st;
+  const int rows = (int)moe_sort_rows(T, k, n_experts, align);
+  const int nv = (int)((size_t)H * elem_bytes(dtype) / 16);
+  k_scatter_rows<<<T + (rows + kPadRows - 1) / kPadRows, kRowThreads, 0, (hipStream_t)stream>>>(
+      (const u32x4*)x, T, nv, k, rows, pos, pairs, (u32x4*)xs);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+}
+
+static int gather_sum(const void* o, int32_t dtype, int32_t rows, int32_t H, const float* w, const int32_t* pos,
+                      int32_t T, int32_t k, const void* add, void* y, void* stream) {
+  if (T == 0) return MOE_OK;
+  if ((rows && bad(o, 16)) || bad(pos, 4) || bad(y, 16) || (add && !aligned_to(add, 16))) return MOE_E_INVAL;
+  const int nv = (int)((size_t)H * elem_bytes(dtype) / 16);
+  const dim3 grid(T, (nv + kRowThreads - 1) / kRowThreads);
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, kRowThreads, 0, (hipStream_t)stream>>>((const u32x4*)o, rows, nv, w, pos, k, (const u32x4*)add,
+                                                         (u32x4*)y);
+  };
+  if (dtype == MOE_T_F16) launch(k_gather_sum<MOE_T_F16>);
+  else if (dtype == MOE_T_BF16) launch(k_gather_sum<MOE_T_BF16>);
+  else launch(k_gather_sum<MOE_T_F32>);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+}
+
+int moe_dispatch_backward(const void* dxs, int32_t dtype, int32_t rows, int32_t H, const int32_t* pos, int32_t T,
+                          int32_t k, const void* add, void* dx, void* stream) {
+  int st = check_rows(dtype, T, H);
+  if (st == MOE_OK) st = check_slots(T, k, rows);
+  if (st != MOE_OK) return st;
+  return gather_sum(dxs, dtype, rows, H, nullptr, pos, T, k, add, dx, stream);
+}
+
+int moe_combine(const void* o, int32_t dtype, int32_t rows, int32_t H, const float* topk_w, const int32_t* pos,
+                int32_t T, int32_t k, const void* add, void* y, void* stream) {
+  int st = check_rows(dtype, T, H);
+  if (st == MOE_OK) st = check_slots(T, k, rows);
+  if (st != MOE_OK) return st;
+  if (T && bad(topk_w, 4)) return MOE_E_INVAL;
+  return gather_sum(o, dtype, rows, H, topk_w, pos, T, k, add, y, stream);
+}
+
+int moe_combine_backward(const void* dy, const void* o, int32_t dtype, int32_t rows, int32_t H,
+                         const float* topk_w, const int32_t* pos, const int32_t* pairs, int32_t T, int32_t k,
+                         void* d_o, float* dw, void* stream) {
+  int st = check_rows(dtype, T, H);
+  if (st == MOE_OK) st = check_slots(T, k, rows);
+  if (st != MOE_OK) return st;
+  if (T == 0 && rows == 0) return MOE_OK;
+  if (T && (bad(dy, 16) || bad(topk_w, 4) || bad(pos, 4) || bad(dw, 4))) return MOE_E_INVAL;
+  if (rows && (bad(o, 16) || bad(d_o, 16) || bad(pairs, 4))) return MOE_E_INVAL;
+  const int nv = (int)((size_t)H * elem_bytes(dtype) / 16);
+  const int grid = T + (rows + kPadRows - 1) / kPadRows;
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, kRowThreads, 0, (hipStream_t)stream>>>((const u32x4*)dy, (const u32x4*)o, rows, nv, topk_w, pos,
+                                                         pairs, T, k, (u32x4*)d_o, dw);
+  };
+  if (dtype == MOE_T_F16) launch(k_combine_grad<MOE_T_F16>);
+  else if (dtype == MOE_T_BF16) launch(k_combine_grad<MOE_T_BF16>);
+  else launch(k_combine_grad<MOE_T_F32>);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+}
+
+}  // extern "C"

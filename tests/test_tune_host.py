@@ -1,0 +1,124 @@
+"""Refusals and sizes of the dispatch, combine, router-gradient and adapter
+entry points: decided on the host before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import quantized_moe_expert_02_amd as moe
+
+OK, INVAL, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
+P = 1 << 20  # an aligned address that a refused call never touches
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    if not os.path.exists(moe.LIB_PATH):
+        from quantized_moe_expert_02_amd import build
+        build.build()
+    return moe.lib()
+
+
+def test_sort_rows(L):
+    assert L.moe_sort_rows(5, 3, 8, 1) == 15
+    assert L.moe_sort_rows(0, 3, 8, 16) == 0
+    for T, k, E, align in ((5, 3, 8, 16), (1, 1, 4, 7), (1000, 8, 256, 64), (2, 2, 1024, 1024)):
+        n = T * k
+        # every group padded at worst: one slot in each group that can be non-empty
+        worst = n + min(E, n) * (align - 1)
+        assert L.moe_sort_rows(T, k, E, align) == -(-worst // align) * align
+    for bad in ((-1, 1, 8, 1), (1, 0, 8, 1), (1, 9, 8, 1), (1, 1, 0, 1), (1, 1, 1025, 1), (1, 33, 64, 1), (1, 1, 8, 0),
+                (1, 1, 8, 1025), (1 << 29, 4, 8, 1)):
+        assert L.moe_sort_rows(*bad) == -1
+        assert L.moe_sort_workspace_bytes(*bad[:3]) == 0 or bad[3] not in (1,)
+    assert L.moe_sort_workspace_bytes(4, 2, 8) > 0
+
+
+def _expect(fn, good, changes):
+    """Each change of one argument of an acceptable call gives its status."""
+    names = list(good)
+    for name, value, status in changes:
+        args = dict(good, **{name: value})
+        assert fn(*[args[n] for n in names]) == status, (name, value)
+
+
+def test_sort_refuses(L):
+    good = dict(idx=P, T=4, k=2, E=8, align=1, offsets=P, pairs=P, pos=P, ws=P, ws_bytes=1 << 20, stream=None)
+    _expect(L.moe_sort, good, [
+        ("idx", None, INVAL), ("idx", P + 2, INVAL), ("T", -1, INVAL), ("T", 1 << 30, INVAL), ("k", 0, INVAL), ("k", 9, INVAL),
+        ("E", 0, INVAL), ("E", 1025, UNSUPPORTED), ("align", 0, INVAL), ("align", 1025, INVAL), ("offsets", None, INVAL),
+        ("pairs", None, INVAL), ("pos", None, INVAL), ("ws", None, INVAL), ("ws", P + 8, INVAL), ("ws_bytes", 16, WORKSPACE)])
+    _expect(L.moe_sort, dict(good, E=64, k=33), [("align", 1, UNSUPPORTED)])
+
+
+def test_dispatch_refuses(L):
+    good = dict(x=P, dtype=0, T=4, H=64, idx=P, k=2, E=8, align=1, xs=P, offsets=P, pairs=P, pos=P, ws=P, ws_bytes=1 << 20,
+                stream=None)
+    _expect(L.moe_dispatch, good, [
+        ("x", None, INVAL), ("x", P + 8, INVAL), ("xs", None, INVAL), ("xs", P + 4, INVAL), ("dtype", 3, INVAL),
+        ("dtype", -1, INVAL), ("H", 0, INVAL), ("H", -8, INVAL), ("H", 60, UNSUPPORTED), ("T", -1, INVAL), ("k", 9, INVAL),
+        ("idx", None, INVAL), ("ws_bytes", 0, WORKSPACE), ("E", 2000, UNSUPPORTED), ("align", -1, INVAL)])
+
+
+def test_gather_refuses(L):
+    good = dict(o=P, dtype=1, rows=8, H=64, pos=P, T=4, k=2, add=None, out=P, stream=None)
+    changes = [("o", None, INVAL), ("o", P + 8, INVAL), ("dtype", 7, INVAL), ("rows", -1, INVAL), ("H", 12, UNSUPPORTED),
+               ("H", 0, INVAL), ("pos", None, INVAL), ("T", -1, INVAL), ("k", 0, INVAL), ("k", 33, UNSUPPORTED),
+               ("T", 1 << 30, INVAL), ("add", P + 8, INVAL), ("out", None, INVAL), ("out", P + 8, INVAL)]
+    _expect(L.moe_dispatch_backward, good, changes + [("T", 0, OK)])
+    c = dict(o=P, dtype=1, rows=8, H=64, w=P, pos=P, T=4, k=2, add=None, out=P, stream=None)
+    _expect(L.moe_combine, c, changes + [("w", None, INVAL), ("w", P + 1, INVAL), ("T", 0, OK)])
+    b = dict(dy=P, o=P, dtype=1, rows=8, H=64, w=P, pos=P, pairs=P, T=4, k=2, d_o=P, dw=P, stream=None)
+    _expect(L.moe_combine_backward, b, [
+        ("dy", None, INVAL), ("o", P + 8, INVAL), ("dtype", 5, INVAL), ("rows", -1, INVAL), ("H", 20, UNSUPPORTED),
+        ("w", None, INVAL), ("pos", None, INVAL), ("pairs", None, INVAL), ("d_o", None, INVAL), ("dw", P + 2, INVAL),
+        ("k", 40, UNSUPPORTED), ("T", -2, INVAL)])
+    assert L.moe_combine_backward(*dict(b, T=0, rows=0).values()) == OK
+
+
+def test_route_backward_refuses(L):
+    good = dict(x=P, dtype=0, T=4, H=64, E=8, k=2, wr=P, br=None, idx=P, dw=P, offsets=P, pairs=P, rows=8, add=None, dx=P,
+                dwr=P, db=P, ws=P, ws_bytes=1 << 24, stream=None)
+    _expect(L.moe_route_backward, good, [
+        ("x", None, INVAL), ("x", P + 8, INVAL), ("dtype", 2, INVAL), ("T", -1, INVAL), ("H", 60, UNSUPPORTED), ("H", 0, INVAL),
+        ("E", 1025, UNSUPPORTED), ("k", 9, INVAL), ("wr", None, INVAL), ("wr", P + 4, INVAL), ("br", P + 2, INVAL),
+        ("idx", None, INVAL), ("dw", None, INVAL), ("offsets", None, INVAL), ("pairs", None, INVAL), ("rows", -1, INVAL),
+        ("add", P + 2, INVAL), ("dx", None, INVAL), ("dwr", None, INVAL), ("dwr", P + 4, INVAL), ("db", None, INVAL),
+        ("ws", None, INVAL), ("ws_bytes", 0, WORKSPACE)])
+    assert L.moe_route_backward_workspace_bytes(4, 2, 8, 60, 8) == 0
+    assert L.moe_route_backward_workspace_bytes(4, 2, 8, 64, 8) > 0
+
+
+def _adapters(**kw):
+    v = dict(a=P, b=P, scale=P, ranks=None, n=3, K=64, N=72, R=8, dtype=0)
+    v.update(kw)
+    return ctypes.byref(moe.MoeAdapters(*v.values()))
+
+
+BAD_SETS = [(dict(a=None), INVAL), (dict(a=P + 8), INVAL), (dict(b=None), INVAL), (dict(scale=None), INVAL),
+            (dict(ranks=P + 2), INVAL), (dict(n=0), INVAL), (dict(n=1025), UNSUPPORTED), (dict(K=0), INVAL),
+            (dict(K=60), UNSUPPORTED), (dict(N=-8), INVAL), (dict(N=12), UNSUPPORTED), (dict(R=0), INVAL),
+            (dict(R=12), UNSUPPORTED), (dict(R=136), UNSUPPORTED), (dict(dtype=2), INVAL), (dict(dtype=-1), INVAL)]
+
+
+def test_adapter_refuses(L):
+    f = dict(d=_adapters(), x=P, ldx=64, T=4, ids=P, offsets=None, pairs=None, add=None, ldadd=0, y=P, ldy=72, u=None, ws=P,
+             ws_bytes=1 << 24, stream=None)
+    _expect(L.moe_adapter_forward, f, [("d", _adapters(**kw), st) for kw, st in BAD_SETS])
+    _expect(L.moe_adapter_forward, f, [
+        ("d", None, INVAL), ("x", None, INVAL), ("x", P + 8, INVAL), ("ldx", 56, INVAL), ("ldx", 68, INVAL), ("T", -1, INVAL),
+        ("ids", None, INVAL), ("offsets", P, INVAL), ("pairs", P, INVAL), ("add", P, INVAL), ("y", None, INVAL),
+        ("ldy", 64, INVAL), ("ldy", 76, INVAL), ("u", P + 8, INVAL), ("ws", None, INVAL), ("ws_bytes", 0, WORKSPACE), ("T", 0, OK)])
+    b = dict(d=_adapters(), dy=P, lddy=72, x=P, ldx=64, u=P, T=4, ids=P, offsets=None, pairs=None, add=None, ldadd=0, dx=P,
+             lddx=64, da=P, db=P, ws=P, ws_bytes=1 << 24, stream=None)
+    _expect(L.moe_adapter_backward, b, [("d", _adapters(**kw), st) for kw, st in BAD_SETS])
+    _expect(L.moe_adapter_backward, b, [
+        ("d", None, INVAL), ("dy", None, INVAL), ("lddy", 64, INVAL), ("x", None, INVAL), ("ldx", 0, INVAL), ("u", None, INVAL),
+        ("T", -1, INVAL), ("ids", None, INVAL), ("offsets", P, INVAL), ("pairs", P, INVAL), ("add", P, INVAL), ("dx", P + 8, INVAL),
+        ("lddx", 60, INVAL), ("da", None, INVAL), ("db", None, INVAL), ("da", P + 4, INVAL), ("ws", P + 4, INVAL),
+        ("ws_bytes", 16, WORKSPACE)])
+    assert L.moe_adapter_backward(*dict(b, dx=None, add=P, ldadd=64).values()) == INVAL
+    for kw, st in BAD_SETS[5:]:
+        assert L.moe_adapter_workspace_bytes(_adapters(**kw), 4) == 0
+    assert L.moe_adapter_workspace_bytes(_adapters(), 4) > 0
+    assert L.moe_adapter_workspace_bytes(_adapters(), -1) == 0
