@@ -9,7 +9,7 @@
  *   backward  v[t] = s_a * B_a^T dy[t],  dx[t] = add[t] + A_a^T v[t]
  *             dA_a = sum_t v[t] x[t]^T,  dB_a = s_a * sum_t dy[t] u[t]^T
  * with the sums over the rows of the adapter.  Rows of A_a and columns of B_a
- * at or past r_a are neither used nor read, and their gradients are zero.
+ * at or past r_a are not used, and their gradients are zero.
  *
  * Conventions are those of moe_dispatch.h.  Rows and adapters are binary16 or
  * bfloat16 (one moe_dtype_t for all); products are exact, sums are held in
@@ -29,7 +29,8 @@ extern "C" {
 #endif
 
 /* A set of adapters (host struct holding device pointers).  Supported: K and N
- * multiples of 8, R a multiple of 8 up to 128, 1 <= n <= 1024. */
+ * multiples of 8 up to 65536, R a multiple of 8 up to 128, 1 <= n <= 1024, at
+ * most 2^20 rows and 2^35 elements of x or dy. */
 typedef struct {
   const void* a;        /* [n][R][K]                                     */
   const void* b;        /* [n][N][R]                                     */

@@ -36,8 +36,8 @@
  *   - Index contents are checked on the device: an entry of idx, pos, pairs or
  *     offsets outside its range is treated as dropped and nothing outside the
  *     buffers is read or written.
- *   - Shapes: 1 <= k <= min(E, 32), E <= 1024, 0 <= T, T * k <= 2^30,
- *     1 <= align <= 1024, else MOE_E_INVAL (MOE_E_UNSUPPORTED for E, k or H).
+ *   - Shapes: 1 <= k <= E, 0 <= T, 1 <= align <= 1024, else MOE_E_INVAL;
+ *     T <= 2^20, k <= 32, E <= 1024 and H <= 65536, else MOE_E_UNSUPPORTED.
  *     T == 0 launches nothing and returns MOE_OK, except where a call has an
  *     output that does not depend on T (offsets, d_o's padding rows, dWr, db),
  *     which is written.

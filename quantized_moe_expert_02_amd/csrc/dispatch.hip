@@ -235,11 +235,11 @@ int id_bits(int E) {
 int check_rows(int32_t dtype, int32_t T, int32_t H) {
   if (dtype != MOE_T_F16 && dtype != MOE_T_BF16 && dtype != MOE_T_F32) return MOE_E_INVAL;
   if (T < 0 || H <= 0) return MOE_E_INVAL;
-  return H % 8 ? MOE_E_UNSUPPORTED : MOE_OK;
+  return H % 8 || H > kMaxWidth || T > kMaxRows ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
 int check_slots(int32_t T, int32_t k, int32_t rows) {
-  if (T < 0 || k < 1 || rows < 0 || (int64_t)T * k > kMaxSlots) return MOE_E_INVAL;
+  if (T < 0 || k < 1 || rows < 0) return MOE_E_INVAL;
   return k > kMaxTopK ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
@@ -248,8 +248,8 @@ inline bool bad(const void* p, unsigned align) { return !p || !aligned_to(p, ali
 }  // namespace
 
 int check_sort_shape(int32_t T, int32_t k, int32_t E, int32_t align) {
-  if (T < 0 || k < 1 || E < 1 || k > E || align < 1 || align > 1024 || (int64_t)T * k > kMaxSlots) return MOE_E_INVAL;
-  if (k > kMaxTopK || E > kMaxExperts) return MOE_E_UNSUPPORTED;
+  if (T < 0 || k < 1 || E < 1 || k > E || align < 1 || align > 1024) return MOE_E_INVAL;
+  if (k > kMaxTopK || E > kMaxExperts || T > kMaxRows) return MOE_E_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -56,7 +56,9 @@ inline bool aligned_to(const void* p, unsigned a) { return ((uintptr_t)p & (a - 
 inline size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 inline size_t elem_bytes(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
 
-constexpr int64_t kMaxSlots = (int64_t)1 << 30;  // T * k of one call
+// Limits of one call, which keep every launch below 2^32 threads.
+constexpr int32_t kMaxRows = 1 << 20;   // T
+constexpr int32_t kMaxWidth = 1 << 16;  // H, K, N
 
 // Shape of a sort: MOE_OK, MOE_E_INVAL or MOE_E_UNSUPPORTED.
 int check_sort_shape(int32_t T, int32_t k, int32_t E, int32_t align);

@@ -45,7 +45,7 @@ def _expect(fn, good, changes):
 def test_sort_refuses(L):
     good = dict(idx=P, T=4, k=2, E=8, align=1, offsets=P, pairs=P, pos=P, ws=P, ws_bytes=1 << 20, stream=None)
     _expect(L.moe_sort, good, [
-        ("idx", None, INVAL), ("idx", P + 2, INVAL), ("T", -1, INVAL), ("T", 1 << 30, INVAL), ("k", 0, INVAL), ("k", 9, INVAL),
+        ("idx", None, INVAL), ("idx", P + 2, INVAL), ("T", -1, INVAL), ("T", 1 << 30, UNSUPPORTED), ("k", 0, INVAL), ("k", 9, INVAL),
         ("E", 0, INVAL), ("E", 1025, UNSUPPORTED), ("align", 0, INVAL), ("align", 1025, INVAL), ("offsets", None, INVAL),
         ("pairs", None, INVAL), ("pos", None, INVAL), ("ws", None, INVAL), ("ws", P + 8, INVAL), ("ws_bytes", 16, WORKSPACE)])
     _expect(L.moe_sort, dict(good, E=64, k=33), [("align", 1, UNSUPPORTED)])
@@ -64,7 +64,7 @@ def test_gather_refuses(L):
     good = dict(o=P, dtype=1, rows=8, H=64, pos=P, T=4, k=2, add=None, out=P, stream=None)
     changes = [("o", None, INVAL), ("o", P + 8, INVAL), ("dtype", 7, INVAL), ("rows", -1, INVAL), ("H", 12, UNSUPPORTED),
                ("H", 0, INVAL), ("pos", None, INVAL), ("T", -1, INVAL), ("k", 0, INVAL), ("k", 33, UNSUPPORTED),
-               ("T", 1 << 30, INVAL), ("add", P + 8, INVAL), ("out", None, INVAL), ("out", P + 8, INVAL)]
+               ("T", 1 << 30, UNSUPPORTED), ("H", 65544, UNSUPPORTED), ("add", P + 8, INVAL), ("out", None, INVAL), ("out", P + 8, INVAL)]
     _expect(L.moe_dispatch_backward, good, changes + [("T", 0, OK)])
     c = dict(o=P, dtype=1, rows=8, H=64, w=P, pos=P, T=4, k=2, add=None, out=P, stream=None)
     _expect(L.moe_combine, c, changes + [("w", None, INVAL), ("w", P + 1, INVAL), ("T", 0, OK)])
@@ -98,7 +98,7 @@ def _adapters(**kw):
 BAD_SETS = [(dict(a=None), INVAL), (dict(a=P + 8), INVAL), (dict(b=None), INVAL), (dict(scale=None), INVAL),
             (dict(ranks=P + 2), INVAL), (dict(n=0), INVAL), (dict(n=1025), UNSUPPORTED), (dict(K=0), INVAL),
             (dict(K=60), UNSUPPORTED), (dict(N=-8), INVAL), (dict(N=12), UNSUPPORTED), (dict(R=0), INVAL),
-            (dict(R=12), UNSUPPORTED), (dict(R=136), UNSUPPORTED), (dict(dtype=2), INVAL), (dict(dtype=-1), INVAL)]
+            (dict(R=12), UNSUPPORTED), (dict(R=136), UNSUPPORTED), (dict(K=65544), UNSUPPORTED), (dict(dtype=2), INVAL), (dict(dtype=-1), INVAL)]
 
 
 def test_adapter_refuses(L):
