@@ -11,6 +11,7 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortMaxBlocks = 128;
+constexpr int kSortOne = 8;  // up to this many times 1,024 slots one workgroup sorts alone, in one launch
 
 // Slots per workgroup (a multiple of kSortThreads) and number of workgroups.
 struct SortSplit {
@@ -18,11 +19,12 @@ struct SortSplit {
 };
 SortSplit sort_split(int64_t n) {
   const int64_t chunks = (n + kSortThreads - 1) / kSortThreads;
-  const int64_t m = std::max<int64_t>(1, (chunks + kSortMaxBlocks - 1) / kSortMaxBlocks);
+  if (chunks <= kSortOne) return {kSortOne * kSortThreads, 1};
+  const int64_t m = (chunks + kSortMaxBlocks - 1) / kSortMaxBlocks;
   return {(int)(m * kSortThreads), (int)((chunks + m - 1) / m)};
 }
 
-// Lanes of the wavefront that hold the same id (0 <= id < 1024; lanes with
+// Lanes of the wavefront that hold the same id (0 <= id < 2^bits; lanes with
 // ok == false match nothing).
 __device__ __forceinline__ uint64_t match_id(int id, bool ok, int bits) {
   uint64_t m = __ballot(ok);
@@ -54,32 +56,41 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const int32_t* idx,
   if (tid < E) cnt[(size_t)blockIdx.x * E + tid] = h[tid];
 }
 
-// Places every slot: a stable counting sort.  Each workgroup derives the
-// group starts from all workgroups' counts (a column per thread), then walks
-// its slots 1024 at a time: a wavefront ranks its 64 slots by matching ids,
-// the wavefronts' counts are prefixed per expert in LDS.  With one workgroup
-// the counts are its own and cnt is not read.
+// Places every slot: a stable counting sort.  Thread e of each workgroup
+// derives expert e's place from all workgroups' counts; then the slots are
+// walked 1,024 at a time: a wavefront ranks its 64 slots by matching ids, and
+// thread e turns the wavefronts' counts of expert e into places.  ONE: a single
+// workgroup, which counts by itself and holds its slots in registers.
+template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx, int n, int E, int bits, int align,
-                                                             int rows, int per_block, int blocks, const int32_t* cnt,
+                                                             int rows, int per_block, const int32_t* cnt,
                                                              int32_t* offsets, int32_t* pairs, int32_t* pos) {
-  __shared__ int base[kMaxExperts];
-  __shared__ uint16_t wc[kSortWaves][kMaxExperts];
+  __shared__ int wc[kSortWaves][kMaxExperts];
   __shared__ int wsum[kSortWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, blk = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, blk = blockIdx.x, blocks = gridDim.x;
   const int64_t lo = (int64_t)blk * per_block, hi = min(lo + per_block, (int64_t)n);
 
+  int ids[kSortOne], ranks[kSortOne], same[kSortOne];  // ONE: same is the count of the id in the wavefront
   int total = 0, before = 0;
-  if (blocks == 1) {
-    base[tid] = 0;
+  if (ONE) {
+    int* h = wc[0];
+    h[tid] = 0;
+#pragma unroll
+    for (int c = 0; c < kSortOne; ++c) ids[c] = c * kSortThreads + tid < n ? idx[c * kSortThreads + tid] : -1;
     __syncthreads();
-    for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
-      const int e = idx[i];
-      if ((unsigned)e < (unsigned)E) atomicAdd(&base[e], 1);
+#pragma unroll
+    for (int c = 0; c < kSortOne; ++c) {
+      if (c * kSortThreads >= n) break;
+      const bool ok = (unsigned)ids[c] < (unsigned)E;
+      const uint64_t m = match_id(ids[c], ok, bits);
+      ranks[c] = lanes_below(m);
+      same[c] = __popcll(m);
+      if (ok && ranks[c] == 0) atomicAdd(&h[ids[c]], same[c]);
     }
     __syncthreads();
-    total = tid < E ? base[tid] : 0;
-    __syncthreads();
+    total = tid < E ? h[tid] : 0;
   } else if (tid < E) {
+#pragma unroll 8
     for (int b = 0; b < blocks; ++b) {
       const int c = cnt[(size_t)b * E + tid];
       total += c;
@@ -95,11 +106,12 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx,
   if (lane == 63) wsum[wave] = incl;
   __syncthreads();
   int start = incl - padded, all = 0;
+#pragma unroll
   for (int w = 0; w < kSortWaves; ++w) {
     start += w < wave ? wsum[w] : 0;
     all += wsum[w];
   }
-  base[tid] = start + before;
+  int place = start + before;  // thread e: of expert e's next slot
   if (tid < E && blk == tid % blocks)
     for (int r = start + total; r < start + padded; ++r) pairs[r] = -1;
   if (blk == 0) {
@@ -109,32 +121,43 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx,
   for (int64_t r = (int64_t)all + (int64_t)blk * kSortThreads + tid; r < rows; r += (int64_t)blocks * kSortThreads)
     pairs[r] = -1;
 
-  for (int64_t i0 = lo; i0 < hi; i0 += kSortThreads) {
-    const int64_t i = i0 + tid;
-    const int id = i < hi ? idx[i] : -1;
+  const auto chunk = [&](int64_t i0, int id, int rank, int count) {
     const bool ok = (unsigned)id < (unsigned)E;
-    const uint64_t same = match_id(id, ok, bits);
-    const int rank = lanes_below(same);
-    for (int w = wave; w < kSortWaves; w += kSortWaves)
-      for (int e = lane; e < E; e += 64) wc[w][e] = 0;
+    for (int e = lane; e < E; e += 64) wc[wave][e] = 0;
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);  // one wavefront's LDS accesses stay in order
+    if (ok && rank == 0) wc[wave][id] = count;
     __syncthreads();
-    if (ok && rank == 0) wc[wave][id] = (uint16_t)__popcll(same);
-    __syncthreads();
-    int pre = 0;
-    if (tid < E)
+    if (tid < E) {
+      int c[kSortWaves];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) c[w] = wc[w][tid];
+#pragma unroll
       for (int w = 0; w < kSortWaves; ++w) {
-        const int c = wc[w][tid];
-        wc[w][tid] = (uint16_t)pre;
-        pre += c;
+        wc[w][tid] = place;
+        place += c[w];
       }
+    }
     __syncthreads();
+    const int64_t i = i0 + tid;
     if (i < hi) {
-      const int r = ok ? base[id] + wc[wave][id] + rank : -1;
+      const int r = ok ? wc[wave][id] + rank : -1;
       pos[i] = r;
       if (ok) pairs[r] = (int)i;
     }
     __syncthreads();
-    if (tid < E) base[tid] += pre;
+  };
+  if (ONE) {
+#pragma unroll
+    for (int c = 0; c < kSortOne; ++c) {
+      if (c * kSortThreads >= n) break;
+      chunk(c * kSortThreads, ids[c], ranks[c], same[c]);
+    }
+  } else {
+    for (int64_t i0 = lo; i0 < hi; i0 += kSortThreads) {
+      const int id = i0 + tid < hi ? idx[i0 + tid] : -1;
+      const uint64_t m = match_id(id, (unsigned)id < (unsigned)E, bits);
+      chunk(i0, id, lanes_below(m), __popcll(m));
+    }
   }
 }
 
@@ -258,13 +281,14 @@ hipError_t launch_sort(const int32_t* idx, int T, int k, int E, int align, int r
   const int n = T * k;
   const SortSplit sp = sort_split(n);
   int32_t* cnt = (int32_t*)ws;
-  if (sp.blocks > 1) {
+  if (sp.blocks == 1) {
+    k_sort_place<true><<<1, kSortThreads, 0, s>>>(idx, n, E, id_bits(E), align, rows, sp.per_block, cnt, offsets, pairs,
+                                                 pos);
+  } else {
     k_sort_count<<<sp.blocks, kSortThreads, 0, s>>>(idx, n, E, sp.per_block, cnt);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    k_sort_place<false><<<sp.blocks, kSortThreads, 0, s>>>(idx, n, E, id_bits(E), align, rows, sp.per_block, cnt, offsets,
+                                                          pairs, pos);
   }
-  k_sort_place<<<std::max(1, sp.blocks), kSortThreads, 0, s>>>(idx, n, E, id_bits(E), align, rows, sp.per_block,
-                                                              std::max(1, sp.blocks), cnt, offsets, pairs, pos);
   return hipGetLastError();
 }
 
@@ -283,7 +307,8 @@ int64_t moe_sort_rows(int32_t T, int32_t k, int32_t n_experts, int32_t align) {
 
 size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t n_experts) {
   if (check_sort_shape(T, k, n_experts, 1) != MOE_OK) return 0;
-  return round256((size_t)std::max(1, sort_split((int64_t)T * k).blocks) * n_experts * 4);
+  const int blocks = sort_split((int64_t)T * k).blocks;
+  return blocks > 1 ? round256((size_t)blocks * n_experts * 4) : 0;
 }
 
 int moe_sort(const int32_t* topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t align, int32_t* offsets,
@@ -293,8 +318,9 @@ int moe_sort(const int32_t* topk_idx, int32_t T, int32_t k, int32_t n_experts, i
   const int64_t rows = moe_sort_rows(T, k, n_experts, align);
   if (rows < 0) return MOE_E_INVAL;
   if (bad(offsets, 4) || (T && (bad(topk_idx, 4) || bad(pairs, 4) || bad(pos, 4)))) return MOE_E_INVAL;
-  if (bad(ws, 16)) return MOE_E_INVAL;
-  if (ws_bytes < moe_sort_workspace_bytes(T, k, n_experts)) return MOE_E_WORKSPACE;
+  const size_t need = moe_sort_workspace_bytes(T, k, n_experts);
+  if (need && bad(ws, 16)) return MOE_E_INVAL;
+  if (ws_bytes < need) return MOE_E_WORKSPACE;
   return launch_sort(topk_idx, T, k, n_experts, align, (int)rows, offsets, pairs, pos, ws, (hipStream_t)stream) ==
                  hipSuccess
              ? MOE_OK

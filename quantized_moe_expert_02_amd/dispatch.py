@@ -49,7 +49,8 @@ def _run(fn, dev, stream, made, *args):
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
             s.wait_stream(torch.cuda.current_stream(dev))  # the allocator may hand out memory still in use there
             for t in made:
-                t.record_stream(s)
+                if t is not None:
+                    t.record_stream(s)
     if dev.index == torch.cuda.current_device():
         rc = fn(*args, handle)
     else:
@@ -78,7 +79,8 @@ def _sort_buffers(topk_idx, n_experts, align):
     offsets = torch.empty(n_experts + 1, dtype=_I32, device=dev)
     pairs = torch.empty(rows, dtype=_I32, device=dev)
     pos = torch.empty((T, k), dtype=_I32, device=dev)
-    ws = torch.empty(lib().moe_sort_workspace_bytes(T, k, n_experts), dtype=torch.uint8, device=dev)
+    need = lib().moe_sort_workspace_bytes(T, k, n_experts)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     return T, k, dev, rows, offsets, pairs, pos, ws
 
 
@@ -87,7 +89,7 @@ def moe_sort(topk_idx: torch.Tensor, n_experts: int, align: int = 1, stream=None
     dropped) sorted by expert: dict(offsets [E + 1], pairs [rows], pos [T][k])."""
     T, k, dev, _, offsets, pairs, pos, ws = _sort_buffers(topk_idx, n_experts, align)
     _run(lib().moe_sort, dev, stream, (offsets, pairs, pos, ws), topk_idx.data_ptr(), T, k, n_experts, align,
-         offsets.data_ptr(), pairs.data_ptr(), pos.data_ptr(), ws.data_ptr(), ws.numel())
+         offsets.data_ptr(), pairs.data_ptr(), pos.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return dict(offsets=offsets, pairs=pairs, pos=pos)
 
 
@@ -101,7 +103,7 @@ def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, n_experts: int, align:
     xs = torch.empty((rows, H), dtype=x.dtype, device=dev)
     _run(lib().moe_dispatch, dev, stream, (xs, offsets, pairs, pos, ws), x.data_ptr(), code, T, H,
          topk_idx.data_ptr(), k, n_experts, align, xs.data_ptr(), offsets.data_ptr(), pairs.data_ptr(),
-         pos.data_ptr(), ws.data_ptr(), ws.numel())
+         pos.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return dict(xs=xs, offsets=offsets, pairs=pairs, pos=pos)
 
 
