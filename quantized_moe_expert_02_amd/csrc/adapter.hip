@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests beside a shared projection
 // (include/moe_adapter.h), on the matrix cores.
 //
-// Rows are taken in tiles of one adapter (16 rows for small batches, 32
+// Rows are taken in tiles of one adapter (16 rows for small batches, 64
 // otherwise).  Every product is a 16x16x32 matrix instruction with fp32
 // accumulators whose operand fragments hold, in lane l, 8 consecutive terms
 // (l / 16) * 8 .. + 7 of the contraction for index l % 16; its result holds
@@ -92,24 +92,40 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& d, int a) {
 // ---------------------------------------------------------------------------
 // Tiles: up to M rows of one adapter.
 // ---------------------------------------------------------------------------
+constexpr int kSmallM = 16, kM = 64;  // rows per tile: of a small batch, otherwise
+
+// A tile as a workgroup holds it in LDS, and as a pass's first launch leaves
+// it in workspace for the next.  a: adapter, or n for rows without one; cnt:
+// rows (0: no such tile); first: place of its rows in the sorted order; rank:
+// 0 without an adapter; row: -1 past cnt.
+struct SharedTile {
+  int a, cnt, first, rank;
+  int row[kM];
+};
+constexpr int kTileWords = sizeof(SharedTile) / 4;
+
 // Which rows a call has and how they are grouped.  offsets == NULL: at most
 // 64 rows, grouped by each workgroup itself from ids.
-struct SharedTile;
 struct RowSet {
   const int32_t *ids, *offsets, *pairs;
-  SharedTile* kept;  // [tiles and those that follow]
+  SharedTile* kept;  // [tiles]
   int T;
-  int tiles;  // upper bound on tiles of adapters; with offsets, tiles of M rows in order of arrival follow, of
-              // which each stands for its rows without an adapter
+  int tiles;  // upper bound on tiles of adapters, a multiple of kXcds; with offsets, tiles of kM rows in order of
+              // arrival follow, of which each stands for its rows without an adapter
 };
 
-// a: adapter, or n for rows without one; cnt: rows (0: no such tile); first:
-// place of its rows in the sorted order; this lane's row for lane < M, -1 past
-// cnt.
+// Workgroups go to the GPU's 8 dies in turn, and each die has its own L2.  The
+// places of a launch are mapped so that a die takes consecutive tiles: it then
+// reads few adapters' factors, and a tile's operands are read by the columns'
+// workgroups through one L2.  (The launch's x size is a multiple of 8.)
+constexpr int kXcds = 8;
+__device__ __forceinline__ int tile_of_place(int place, int used) {  // -1: none
+  const int per = (used + kXcds - 1) / kXcds, j = place / kXcds, t = place % kXcds * per + j;
+  return j < per && t < used ? t : -1;
+}
+
 struct Tile {
-  int a, cnt, first, row;
-  int rank;
-  float scale;  // both 0 without an adapter
+  int a, cnt, first, row, rank;  // row: this lane's
 };
 
 __device__ __forceinline__ int lanes_under(uint64_t m) {
@@ -132,9 +148,6 @@ __device__ __forceinline__ int wave_prefix(int v) {
 }
 
 __device__ __forceinline__ int at_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
-__device__ __forceinline__ float at_lane_f(float v, int lane) {
-  return __builtin_bit_cast(float, at_lane(__builtin_bit_cast(int, v), lane));
-}
 
 // One adapter's group of rows, bounds checked.
 __device__ __forceinline__ void group_of(const RowSet& rs, int a, int n, int* first, int* count) {
@@ -160,9 +173,8 @@ __device__ __forceinline__ Tile find_tile(const AdapterArgs& d, const RowSet& rs
   if (!rs.offsets) {
     int id = rs.ids[min(lane, rs.T - 1)];
     if ((unsigned)id >= (unsigned)n) id = n;
-    const int rank = id < n ? rank_of(d, id) : 0;
-    const float scale = id < n ? d.scale[id] : 0.0f;
-    if (rs.T == 1) return {at_lane(id, 0), tile == 0, 0, lane == 0 ? 0 : -1, at_lane(rank, 0), at_lane_f(scale, 0)};
+    const int rank = id < n ? rank_of(d, min(id, n - 1)) : 0;
+    if (rs.T == 1) return {at_lane(id, 0), tile == 0, 0, lane == 0 ? 0 : -1, at_lane(rank, 0)};
     uint64_t same = __ballot(lane < rs.T);
     for (int b = 0; b < 11; ++b) {
       const bool one = (id >> b) & 1;
@@ -172,26 +184,35 @@ __device__ __forceinline__ Tile find_tile(const AdapterArgs& d, const RowSet& rs
     const int nth = lanes_under(same);
     uint64_t lead = __ballot(lane < rs.T && nth % M == 0);
     for (int i = 0; i < tile; ++i) lead &= lead - 1;
-    if (!lead) return {n, 0, 0, -1, 0, 0.0f};
+    if (!lead) return {n, 0, 0, -1, 0};
     const int at = __builtin_ctzll(lead);
     const int a = at_lane(id, at), n0 = at_lane(nth, at);
     const uint64_t mine = __ballot(lane < rs.T && id == a && nth >= n0 && nth < n0 + M);
     const int cnt = __popcll(mine), bit = nth_bit(mine, M);
-    return {a, cnt, 0, lane < cnt ? bit : -1, at_lane(rank, at), at_lane_f(scale, at)};
+    return {a, cnt, 0, lane < cnt ? bit : -1, at_lane(rank, at)};
   }
   if (tile >= rs.tiles) {
-    const int t0 = (tile - rs.tiles) * M, t = t0 + lane;
+    const int t0 = min((tile - rs.tiles) * M, rs.T), t = t0 + lane;
     const int id = rs.ids[min(t, rs.T - 1)];
     const uint64_t mine = __ballot(lane < M && t < rs.T && (unsigned)id >= (unsigned)n);
     const int cnt = __popcll(mine), bit = nth_bit(mine, M);
-    return {n, cnt, 0, lane < cnt ? t0 + bit : -1, 0, 0.0f};
+    return {n, cnt, 0, lane < cnt ? t0 + bit : -1, 0};
+  }
+  int used = 0;
+  for (int a0 = 0; a0 < n && n > 64; a0 += 64) {
+    int first, count;
+    group_of(rs, a0 + lane, n, &first, &count);
+    used += at_lane(wave_prefix((count + M - 1) / M), 63);
   }
   for (int a0 = 0, done = 0; a0 < n; a0 += 64) {
     int first, count;
     group_of(rs, a0 + lane, n, &first, &count);
     const int rank = rank_of(d, min(a0 + lane, n - 1));
-    const float scale = d.scale[min(a0 + lane, n - 1)];
     const int nt = (count + M - 1) / M, incl = wave_prefix(nt);
+    if (a0 == 0) {
+      tile = tile_of_place(tile, min(n > 64 ? used : at_lane(incl, 63), rs.tiles));
+      if (tile < 0) break;
+    }
     const uint64_t past = __ballot(incl > tile - done);
     if (past) {
       const int at = __builtin_ctzll(past);
@@ -199,22 +220,12 @@ __device__ __forceinline__ Tile find_tile(const AdapterArgs& d, const RowSet& rs
       const int i0 = at_lane(first, at) + j * M, cnt = min(M, at_lane(count, at) - j * M);
       int row = rs.pairs[min(i0 + lane, rs.T - 1)];
       if (lane >= cnt || (unsigned)row >= (unsigned)rs.T) row = -1;
-      return {a0 + at, cnt, i0, row, at_lane(rank, at), at_lane_f(scale, at)};
+      return {a0 + at, cnt, i0, row, at_lane(rank, at)};
     }
     done += at_lane(incl, 63);
   }
-  return {n, 0, 0, -1, 0, 0.0f};
+  return {n, 0, 0, -1, 0};
 }
-
-// A tile as a workgroup holds it in LDS, and as the first launch of a pass
-// leaves it in workspace for the second.
-struct SharedTile {
-  int a, cnt, first, rank;
-  float scale;
-  int pad[3];
-  int row[32];
-};
-constexpr int kTileWords = sizeof(SharedTile) / 4;
 
 // find_tile by the first wavefront; stored to *keep where given.  Ends with a
 // barrier.
@@ -224,13 +235,12 @@ __device__ __forceinline__ void share_tile(SharedTile* s, const AdapterArgs& d, 
   if (threadIdx.x < 64) {
     const Tile t = find_tile<M>(d, rs, tile);
     const auto put = [&](SharedTile* o) {
-      if (threadIdx.x < 32) o->row[threadIdx.x] = t.row;
+      o->row[threadIdx.x] = t.row;
       if (threadIdx.x == 0) {
         o->a = t.a;
         o->cnt = t.cnt;
         o->first = t.first;
         o->rank = t.rank;
-        o->scale = t.scale;
       }
     };
     put(s);
@@ -301,73 +311,72 @@ __device__ __forceinline__ v8_t<DT> read_across(const typename Mat<DT>::elem* lo
   return __builtin_bit_cast(v8_t<DT>, v);
 }
 
-// Sums acc over the workgroup's W wavefronts into wavefront 0, pairwise.
-// red: W / 2 * NF fragments.
-template <int W, int NF>
-__device__ __forceinline__ void reduce_waves(f32x4 (&acc)[NF], f32x4* red, int wave, int lane) {
-#pragma unroll
-  for (int h = W / 2; h >= 1; h /= 2) {
-    if (wave >= h && wave < 2 * h) {
-#pragma unroll
-      for (int f = 0; f < NF; ++f) red[((wave - h) * NF + f) * 64 + lane] = acc[f];
-    }
-    __syncthreads();
-    if (wave < h) {
-#pragma unroll
-      for (int f = 0; f < NF; ++f) acc[f] += red[(wave * NF + f) * 64 + lane];
-    }
-    __syncthreads();
-  }
-}
-
-constexpr int cmax(int a, int b) { return a > b ? a : b; }
-
 constexpr int kRowThreads = 512;
 constexpr int kRowWaves = kRowThreads / kWave;
 
+// What k_rows leaves: fragments by bands of 16 of a tile's 64 rows and blocks of
+// 32 r.
+struct RowsOut {
+  float* sums;       // small batches: u [S][T][R] by row; else v [T][R] in the sorted order, or u by row (or NULL)
+  const float* u;    // backward: the forward pass's u, copied to
+  float* u_sorted;   //   [T][R] in the sorted order
+  u32x4* frag;       // [tiles][4][blocks][2 pieces][64]: contraction over r
+  float* scale;      // [tiles][4][blocks][16]: what the products are multiplied by
+  int blocks;
+};
+
 // The long sums over a tile's rows: u[t][r] = <A_a[r], x[t]> (ACROSS false), or
-// v[t][r] = s_a sum_c dy[t][c] B_a[c][r] (ACROSS), of one segment of the columns
-// (blockIdx.y of gridDim.y), split again over the wavefronts.  u: [S][T][R] by
-// row; v: the same in the sorted order, and a copy of the forward pass's u in
-// that order.
+// v[t][r] = s_a sum_c dy[t][c] B_a[c][r] (ACROSS), for MT bands of rows and one
+// block of r (blockIdx.y) per workgroup; the columns are split over its
+// wavefronts, and in small batches over blockIdx.z first.  Splitting r instead
+// of the columns reads x once per block but leaves whole sums, which are split
+// into fragments here, once.
 // Memory is read 128 contiguous bytes per row (8 lanes side by side: lanes that
 // follow the fragments' layout, each in a row of its own, cost the address unit
 // four times as many cycles); a wavefront's own LDS turns that into fragments,
-// the next step's loads in flight meanwhile.
-template <int DT, int MT, int RT, bool ACROSS>
-__global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, const void* x, int64_t ldx, float* out,
-                                                     bool zero_none, const float* u, float* u_sorted) {
+// the next steps' loads in flight meanwhile.
+template <int DT, int MT, int RT, bool ACROSS, bool SMALL>
+__global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, const void* x, int64_t ldx, RowsOut out) {
   typedef typename Mat<DT>::elem E;
-  constexpr int M = MT * 16, W = RT * 16;
-  constexpr int KS = RT == 8 ? 32 : 64, NH = KS / 32;  // columns per step
-  constexpr int XV = KS / 8, XS = KS + 8;              // x's rows in LDS: vectors, stride
+  constexpr int M = MT * 16, W = RT * 16, NF = MT * RT;
+  constexpr int KS = 64, XV = KS / 8, XS = KS + 8;  // columns per step; x's rows in LDS: vectors, stride
   constexpr int FR = ACROSS ? KS : W, FV = ACROSS ? W / 8 : XV, FS = ACROSS ? W + 8 : XS;  // the factor's
   constexpr int XL = M * XV / 64, FL = FR * FV / 64;   // loads per lane
   constexpr int kStage = (M * XS + FR * FS) * 2;
+  static_assert(kStage >= NF * 1024, "a wavefront's sums fit its stage");
   __shared__ SharedTile st;
-  __shared__ __align__(16) char lds[cmax(kRowWaves * kStage, kRowWaves / 2 * MT * RT * 1024)];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
-  if ((int)blockIdx.x >= rs.tiles && blockIdx.y) return;
-  share_tile<M>(&st, d, rs, blockIdx.x, blockIdx.y ? nullptr : rs.kept + blockIdx.x);
-  const int a = __builtin_amdgcn_readfirstlane(st.a), cnt = __builtin_amdgcn_readfirstlane(st.cnt);
-  if (!cnt) return;
-  float* o = out + (size_t)blockIdx.y * rs.T * d.R;
-  if (a == d.n) {
-    if (zero_none)
-      for (int i = threadIdx.x; i < cnt * d.R; i += kRowThreads) o[(size_t)st.row[i / d.R] * d.R + i % d.R] = 0.0f;
+  __shared__ __align__(16) char lds[kRowWaves * kStage];
+  __shared__ __align__(16) float vs[SMALL ? 1 : M][W + 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
+  const int tile = blockIdx.x, t0 = SMALL ? 0 : blockIdx.z * M, r0 = blockIdx.y * W;
+  share_tile<SMALL ? kSmallM : kM>(&st, d, rs, tile, r0 == 0 && blockIdx.z == 0 ? rs.kept + tile : nullptr);
+  const int a = __builtin_amdgcn_readfirstlane(st.a), cnt = __builtin_amdgcn_readfirstlane(st.cnt) - t0;
+  if (cnt <= 0 || a == d.n) return;
+  const int rk = __builtin_amdgcn_readfirstlane(st.rank) - r0, R = d.R, C = ACROSS ? d.N : d.K;
+  const int* strow = st.row + t0;
+  const int first = st.first + t0;
+  if (ACROSS)  // this block's columns of u
+    for (int i = tid; i < min(cnt, M) * (W / 4); i += kRowThreads) {
+      const int t = i / (W / 4), r = r0 + i % (W / 4) * 4;
+      if (r < R) {
+        f32x4 v = *(const f32x4*)(out.u + (size_t)max(strow[t], 0) * R + r);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = r - r0 + c < rk && strow[t] >= 0 ? v[c] : 0.0f;
+        *(f32x4*)(out.u_sorted + (size_t)(first + t) * R + r) = v;
+      }
+    }
+  if (rk <= 0) {
+    if (!ACROSS && !SMALL && out.sums)
+      for (int i = tid; i < min(cnt, M) * (W / 4); i += kRowThreads) {
+        const int t = i / (W / 4), r = r0 + i % (W / 4) * 4;
+        if (strow[t] >= 0 && r < R) *(f32x4*)(out.sums + (size_t)strow[t] * R + r) = f32x4{0, 0, 0, 0};
+      }
     return;
   }
-  const int rk = __builtin_amdgcn_readfirstlane(st.rank), C = ACROSS ? d.N : d.K;
   const bool whole = rk % 8 == 0;
-  if (ACROSS && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < cnt * (d.R / 4); i += kRowThreads) {
-      const int t = i / (d.R / 4), r = i % (d.R / 4) * 4;
-      f32x4 v = *(const f32x4*)(u + (size_t)max(st.row[t], 0) * d.R + r);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = r + c < rk && st.row[t] >= 0 ? v[c] : 0.0f;
-      *(f32x4*)(u_sorted + (size_t)(st.first + t) * d.R + r) = v;
-    }
-  const int steps = (C + KS - 1) / KS, parts = gridDim.y * kRowWaves, part = blockIdx.y * kRowWaves + wave;
+  const float f = ACROSS || !SMALL ? d.scale[a] : 1.0f;
+  const int steps = (C + KS - 1) / KS, parts = (SMALL ? gridDim.z : 1) * kRowWaves;
+  const int part = (SMALL ? blockIdx.z : 0) * kRowWaves + wave;
   const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
   E* xs = (E*)(lds + wave * kStage);
   E* fs = xs + M * XS;
@@ -376,25 +385,26 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
   bool xok[XL];
 #pragma unroll
   for (int i = 0; i < XL; ++i) {
-    const int r = st.row[(lane + 64 * i) / XV];
+    const int r = strow[(lane + 64 * i) / XV];
     xok[i] = r >= 0;
     xrow[i] = (const E*)x + (size_t)max(r, 0) * ldx;
   }
-  const E* fbase = (const E*)(ACROSS ? d.b : d.a) + (size_t)a * d.R * C;
-  u32x4 xn[2][XL], fn[2][FL];  // the next two steps
+  const E* fbase = (const E*)(ACROSS ? d.b : d.a) + (size_t)a * R * C + (size_t)r0 * (ACROSS ? 1 : C);
+  constexpr int DEPTH = XL + FL <= 4 ? 4 : 2;
+  u32x4 xn[DEPTH][XL], fn[DEPTH][FL];  // the next steps
   const auto fetch = [&](int s, u32x4 (&xn)[XL], u32x4 (&fn)[FL]) {
     const int c = s * KS + xc < C ? s * KS + xc : 0;
 #pragma unroll
     for (int i = 0; i < FL; ++i) {
       const int row = (lane + 64 * i) / FV, fc = (lane + 64 * i) % FV * 8;
-      const uint32_t at = ACROSS ? (uint32_t)min(s * KS + row, C - 1) * d.R + (fc < rk ? fc : 0)
+      const uint32_t at = ACROSS ? (uint32_t)min(s * KS + row, C - 1) * R + (fc < rk ? fc : 0)
                                  : (uint32_t)(row < rk ? row : 0) * C + c;
       fn[i] = load8<DT>(fbase, at);
     }
 #pragma unroll
     for (int i = 0; i < XL; ++i) xn[i] = load8<DT>(xrow[i], c);
   };
-  f32x4 acc[MT * RT] = {};
+  f32x4 acc[NF] = {};
   const auto step = [&](int s, u32x4 (&xn)[XL], u32x4 (&fn)[FL]) {
     const bool cok = s * KS + xc < C;
 #pragma unroll
@@ -405,10 +415,10 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
       const u32x4 v = ACROSS ? keep_upto(fn[i], s * KS + row < C ? rk - fc : 0, whole) : keep(fn[i], row < rk && cok);
       *(u32x4*)(fs + row * FS + fc) = v;
     }
-    if (s + 2 < s1) fetch(s + 2, xn, fn);
+    if (s + DEPTH < s1) fetch(s + DEPTH, xn, fn);
     lds_order();
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
+    for (int h = 0; h < KS / 32; ++h) {
       v8_t<DT> xf[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) xf[m] = *(const v8_t<DT>*)(xs + (m * 16 + li) * XS + h * 32 + g * 8);
@@ -427,37 +437,66 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
     }
     lds_order();
   };
-  if (s0 < s1) fetch(s0, xn[0], fn[0]);
-  if (s0 + 1 < s1) fetch(s0 + 1, xn[1], fn[1]);
-  for (int s = s0; s < s1; s += 2) {
-    step(s, xn[0], fn[0]);
-    if (s + 1 < s1) step(s + 1, xn[1], fn[1]);
+#pragma unroll
+  for (int k = 0; k < DEPTH; ++k)
+    if (s0 + k < s1) fetch(s0 + k, xn[k], fn[k]);
+  for (int s = s0; s < s1; s += DEPTH) {
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k)
+      if (s + k < s1) step(s + k, xn[k], fn[k]);
   }
+  // the wavefronts' sums, added in order
+#pragma unroll
+  for (int q = 0; q < NF; ++q) *(f32x4*)(lds + wave * kStage + (q * 64 + lane) * 16) = acc[q];
   __syncthreads();
-  reduce_waves<kRowWaves, MT * RT>(acc, (f32x4*)lds, wave, lane);
-  if (wave == 0) {
-    const float f = st.scale;
+  if (tid < NF * 64) {
+    f32x4 s = *(const f32x4*)(lds + tid * 16);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int t = m * 16 + li, row = ACROSS ? (t < cnt ? st.first + t : -1) : st.row[t];
+    for (int w = 1; w < kRowWaves; ++w) s += *(const f32x4*)(lds + w * kStage + tid * 16);
+    if (ACROSS) s *= f;
+    const int q = tid / 64, t = q / RT * 16 + li, c = q % RT * 16 + g * 4, r = r0 + c;
+    const int row = ACROSS ? (t < cnt ? first + t : -1) : strow[t];
+    if ((SMALL || out.sums) && row >= 0 && r < R)
+      *(f32x4*)(out.sums + ((size_t)(SMALL ? blockIdx.z : 0) * rs.T + row) * R + r) = s;
+    if (!SMALL) *(f32x4*)&vs[t][c] = s;
+  }
+  if (SMALL) return;
+  __syncthreads();
+  constexpr int BW = (RT + 1) / 2;  // blocks of 32 r here
+  if (wave < MT * BW) {
+    const int t = wave / BW * 16 + li, b = wave % BW;
+    float v[8], top = 0.0f;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int c = r * 16 + g * 4;
-        if (row >= 0 && c < d.R) *(f32x4*)(o + (size_t)row * d.R + c) = ACROSS ? acc[m * RT + r] * f : acc[m * RT + r];
-      }
+    for (int i = 0; i < 8; ++i) {
+      v[i] = RT > 1 || g < 2 ? vs[t][b * 32 + g * 8 + i] : 0.0f;
+      top = fmaxf(top, finite_abs(v[i]));
     }
+    top = fmaxf(top, __builtin_bit_cast(float, partner<16>(__builtin_bit_cast(int, top))));
+    top = fmaxf(top, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, top))));
+    const int e = scale_exp<DT>(top);
+    v8_t<DT> h[2];
+    split_pieces<DT, 2>(v, e, h);
+    const size_t at = ((size_t)tile * 4 + t0 / 16 + wave / BW) * out.blocks + blockIdx.y * BW + b;
+    out.frag[(at * 2 + 0) * 64 + lane] = __builtin_bit_cast(u32x4, h[0]);
+    out.frag[(at * 2 + 1) * 64 + lane] = __builtin_bit_cast(u32x4, h[1]);
+    // below 2^-126 this factor loses bits of results that are far below the
+    // 16-bit types' smallest step
+    if (g == 0) out.scale[at * 16 + li] = __builtin_amdgcn_ldexpf(ACROSS ? 1.0f : f, -e);
   }
 }
 
 constexpr int kOutThreads = 256;
 constexpr int kOutWaves = kOutThreads / kWave;
 
-// LDS of a tile's u or v on its way to fragments.
-template <int M, int RB>
+// ---------------------------------------------------------------------------
+// Second launch of the forward pass.
+// ---------------------------------------------------------------------------
+// LDS of a small tile's u on its way to fragments.
+template <int RB>
 struct RowPack {
-  float v[M][RB * 32 + 4];
-  alignas(16) float scale[M];      // what the products are multiplied by
-  u32x4 frag[M / 16 * RB][2][64];  // contraction over r, two pieces
+  float v[kSmallM][RB * 32 + 4];
+  alignas(16) float scale[kSmallM];
+  u32x4 frag[RB][2][64];
 };
 
 // p[0] + p[stride] + ... (S of them), in that order, four loads in flight.
@@ -474,168 +513,268 @@ __device__ __forceinline__ f32x4 sum_segments(const float* p, size_t stride, int
   return v;
 }
 
-// Sums the S segments of a tile's rows (also written to u, where given), and
-// splits them into fragments: a wavefront per fragment.  SORTED: part is in the
-// sorted order.  Ends with a barrier.
-template <int DT, int M, int RB, bool SORTED>
-__device__ __forceinline__ void pack_rows(RowPack<M, RB>* p, const SharedTile& st, const float* part, int S, int T, int R,
+// Sums the S segments of a small tile's rows (also written to u, where given),
+// and splits them into fragments.  Ends with a barrier.
+template <int DT, int RB>
+__device__ __forceinline__ void pack_rows(RowPack<RB>* p, const SharedTile& st, const float* part, int S, int T, int R,
                                           float f, float* u) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
   const int rk = st.rank;
 #pragma unroll
-  for (int i0 = 0; i0 < M * RB * 8; i0 += kOutThreads) {
+  for (int i0 = 0; i0 < kSmallM * RB * 8; i0 += kOutThreads) {
     const int i = i0 + tid, t = i / (RB * 8), r = i % (RB * 8) * 4;
-    if (M * RB * 8 % kOutThreads && i >= M * RB * 8) break;
-    const int row = SORTED ? (t < st.cnt ? st.first + t : -1) : st.row[t];
+    if (kSmallM * RB * 8 % kOutThreads && i >= kSmallM * RB * 8) break;
+    const int row = st.row[t];
     f32x4 v = {0, 0, 0, 0};
     if (row >= 0 && r < rk) v = sum_segments(part + (size_t)row * R + r, (size_t)T * R, S);
     *(f32x4*)&p->v[t][r] = v;
     if (u && row >= 0 && r < R) *(f32x4*)(u + (size_t)row * R + r) = v;
   }
   __syncthreads();
+  if (wave < RB) {
+    const int b = wave;
+    float v[8], top = 0.0f;
 #pragma unroll
-  for (int unit0 = 0; unit0 < M / 16 * RB; unit0 += kOutWaves) {
-    const int unit = unit0 + wave;
-    if (M / 16 * RB % kOutWaves && unit >= M / 16 * RB) break;
-    const int t = unit / RB * 16 + li, b = unit % RB;
-    float v[8];
+    for (int i = 0; i < 8; ++i) v[i] = p->v[li][b * 32 + g * 8 + i];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p->v[t][b * 32 + g * 8 + i];
-    int e = 0;
-    if (DT == MOE_T_F16) {
-      float top = 0.0f;
+    for (int c = 0; c < RB * 8; c += 4) {  // a quarter of the row per lane group
+      const f32x4 w = *(const f32x4*)&p->v[li][g * RB * 8 + c];
 #pragma unroll
-      for (int c = 0; c < RB * 8; c += 4) {  // a quarter of the row per lane group
-        const f32x4 w = *(const f32x4*)&p->v[t][g * RB * 8 + c];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, finite_abs(w[i]));
-      }
-      top = fmaxf(top, __builtin_bit_cast(float, partner<16>(__builtin_bit_cast(int, top))));
-      top = fmaxf(top, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, top))));
-      e = scale_exp<DT>(top);
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, finite_abs(w[i]));
     }
+    top = fmaxf(top, __builtin_bit_cast(float, partner<16>(__builtin_bit_cast(int, top))));
+    top = fmaxf(top, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, top))));
+    const int e = scale_exp<DT>(top);
     v8_t<DT> h[2];
     split_pieces<DT, 2>(v, e, h);
-    p->frag[unit][0][lane] = __builtin_bit_cast(u32x4, h[0]);
-    p->frag[unit][1][lane] = __builtin_bit_cast(u32x4, h[1]);
-    // below 2^-126 this factor loses bits of results that are far below the
-    // 16-bit types' smallest step
-    if (b == 0 && g == 0) p->scale[t] = __builtin_amdgcn_ldexpf(f, -e);
+    p->frag[b][0][lane] = __builtin_bit_cast(u32x4, h[0]);
+    p->frag[b][1][lane] = __builtin_bit_cast(u32x4, h[1]);
+    if (b == 0 && g == 0) p->scale[li] = __builtin_amdgcn_ldexpf(f, -e);
   }
   __syncthreads();
 }
 
-constexpr int kExpandCols = kOutWaves * 128;  // columns of a workgroup's pass
+// Column 8 i + q of 128 is lane i's column of product q, so that a lane ends
+// with 8 consecutive columns and 16 lanes with 256 contiguous bytes of a row.
+// B's rows pass through LDS, row 8 i + q at place 16 q + i (fragment reads then
+// meet no bank conflict).
+__device__ __forceinline__ int place_of(int n) { return n % 8 * 16 + n / 8; }
 
-// y[t] = add[t] + s_a B_a u[t] for a tile's rows and a run of columns, 128
-// columns at a time per wavefront.  Column 8 i + q of the 128 is lane i's
-// column of product q, so that a lane ends with 8 consecutive columns and 16
-// lanes with 256 contiguous bytes of a row.  B's rows pass through LDS, row
-// 8 i + q at place 16 q + i (fragment reads then meet no bank conflict).
-template <int DT, int MT, int RT>
-__global__ __launch_bounds__(kOutThreads) void k_expand(AdapterArgs d, RowSet rs, const float* part, int S, float* u,
-                                                       const void* add, int64_t ldadd, void* y, int64_t ldy, int passes) {
+// y[t] = add[t] + s_a B_a u[t] for a small tile's rows, 128 columns per
+// wavefront.
+template <int DT, int RT>
+__global__ __launch_bounds__(kOutThreads) void k_expand_small(AdapterArgs d, RowSet rs, const float* part, int S, float* u,
+                                                             const void* add, int64_t ldadd, void* y, int64_t ldy) {
   typedef typename Mat<DT>::elem E;
-  constexpr int M = MT * 16, RB = (RT + 1) / 2, VR = RT == 1 ? 2 : 4, BL = 128 * VR / 64, BS = VR * 8 + 8;
+  constexpr int RB = (RT + 1) / 2, VR = RT == 1 ? 2 : 4, BL = 128 * VR / 64, BS = VR * 8 + 8;
   __shared__ SharedTile st;
-  __shared__ RowPack<M, RB> pk;
+  __shared__ RowPack<RB> pk;
   __shared__ __align__(16) E lds[kOutWaves][128 * BS];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
-  if ((int)blockIdx.x >= rs.tiles) {  // rows without an adapter: one workgroup takes all columns
-    if (blockIdx.y) return;
-    passes = (d.N + kExpandCols - 1) / kExpandCols;
-  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
   take_tile(&st, rs.kept + blockIdx.x);
   if (!__builtin_amdgcn_readfirstlane(st.cnt)) return;
   const int rk = __builtin_amdgcn_readfirstlane(st.rank), a = min(__builtin_amdgcn_readfirstlane(st.a), d.n - 1);
   const bool whole = rk % 8 == 0;
   E* bs = lds[wave];
   const E* bbase = (const E*)d.b + (size_t)a * d.N * d.R;
+  const int n0 = (blockIdx.y * kOutWaves + wave) * 128, c = n0 + li * 8;
   if (RT == 1) {  // rank 16 fills half of the contraction; the other half reads zeros
 #pragma unroll
     for (int i = 0; i < 2; ++i) *(u32x4*)(bs + (lane + 64 * i) * BS + 16) = u32x4{0, 0, 0, 0};
   }
   u32x4 bn[BL];
-  const auto fetch = [&](int n0, int b) {
+  const auto fetch = [&](int b) {
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
       const int v = lane + 64 * i, r = b * 32 + v % VR * 8;
       bn[i] = load8<DT>(bbase, (uint32_t)min(n0 + v / VR, d.N - 1) * d.R + (r < rk ? r : 0));
     }
   };
-  const int first = (blockIdx.y * passes * kOutWaves + wave) * 128;
-  fetch(first, 0);
-  const E* addrow[MT][4];
+  fetch(0);
+  u32x4 av[4] = {};
+  int row[4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int i = 0; i < 4; ++i) {
+    row[i] = st.row[g * 4 + i];
+    if (add) av[i] = load8<DT>((const E*)add + (size_t)max(row[i], 0) * ldadd, c < d.N ? c : 0);
+  }
+  const float f0 = rk ? d.scale[a] : 0.0f;
+  pack_rows<DT, RB>(&pk, st, part, S, rs.T, d.R, f0, blockIdx.y == 0 ? u : nullptr);
+  f32x4 acc[8] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) addrow[m][i] = (const E*)add + (size_t)max(st.row[m * 16 + g * 4 + i], 0) * ldadd;
-  u32x4 av[MT][4] = {};
-  const auto fetch_add = [&](int n0) {
-    const int c = n0 + li * 8 < d.N ? n0 + li * 8 : 0;
+  for (int b = 0; b < RB; ++b) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < BL; ++i) {
+      const int v = lane + 64 * i, r = b * 32 + v % VR * 8;
+      *(u32x4*)(bs + place_of(v / VR) * BS + v % VR * 8) = keep_upto(bn[i], rk - r, whole);
+    }
+    lds_order();
+    if (b + 1 < RB) fetch(b + 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) av[m][i] = load8<DT>(addrow[m][i], c);
+    for (int q = 0; q < 8; ++q) {
+      const v8_t<DT> bf = *(const v8_t<DT>*)(bs + (q * 16 + li) * BS + (RT == 1 ? min(g, 2) : g) * 8);
+      acc[q] = Mat<DT>::mma(as_frag<DT>(pk.frag[b][0][lane]), bf, acc[q]);
+      acc[q] = Mat<DT>::mma(as_frag<DT>(pk.frag[b][1][lane]), bf, acc[q]);
+    }
+    lds_order();
+  }
+  const f32x4 f = *(const f32x4*)&pk.scale[g * 4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float o[8];
+    unpack_vec<DT>(av[i], o);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) o[q] = fmaf(acc[q][i], f[i], o[q]);
+    if (row[i] >= 0 && c < d.N) *(u32x4*)((E*)y + (size_t)row[i] * ldy + c) = pack_vec<DT>(o);
+  }
+}
+
+// Rows without an adapter (tile >= rs.tiles): out = add or zeros, u = 0.
+template <int DT>
+__device__ __forceinline__ void copy_none(SharedTile* st, const AdapterArgs& d, const RowSet& rs, int tile, const void* add,
+                                          int64_t ldadd, void* out, int64_t ldo, int C, float* u) {
+  typedef typename Mat<DT>::elem E;
+  share_tile<kM>(st, d, rs, tile, nullptr);
+  const int cnt = st->cnt, nv = C / 8;
+  for (int i = threadIdx.x; i < cnt * nv; i += kOutThreads) {
+    const int row = st->row[i / nv], c = i % nv * 8;
+    u32x4 v = {0, 0, 0, 0};
+    if (add) v = *(const u32x4*)((const E*)add + (size_t)row * ldadd + c);
+    *(u32x4*)((E*)out + (size_t)row * ldo + c) = v;
+  }
+  if (u)
+    for (int i = threadIdx.x; i < cnt * d.R; i += kOutThreads) u[(size_t)st->row[i / d.R] * d.R + i % d.R] = 0.0f;
+}
+
+constexpr int kCols = 128;  // columns that a workgroup of the second launch takes at a time
+
+// The second launch of either pass, for a tile's rows and `passes` runs of 128
+// columns: out[t] = add[t] + F v[t], with F = B_a times s_a (forward: rows of
+// F in memory, v = u) or A_a^T (ACROSS: columns of F).  A band of 16 rows per
+// wavefront, F's part shared in LDS, in two buffers: the next run's F and add
+// load while this one is worked on.  Column 8 i + q of a run is lane i's
+// column of product q (place_of); where the contraction runs across the rows
+// of A, LDS holds their columns in that order, and 16 lanes read product q's
+// across.
+template <int DT, int RT, bool ACROSS>
+__global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs, const u32x4* frag, const float* scale,
+                                                       const void* add, int64_t ldadd, void* out, int64_t ldo, float* u,
+                                                       int passes) {
+  typedef typename Mat<DT>::elem E;
+  constexpr int W = RT * 16, RB = (RT + 1) / 2, FL = W * kCols / 8 / kOutThreads;
+  constexpr int FV = ACROSS ? kCols / 8 : W / 8;                 // vectors of a row of F
+  constexpr int FS = ACROSS ? kCols + 16 : W + 8;                // LDS row stride
+  constexpr int FR = ACROSS ? RB * 32 : kCols;                   // LDS rows
+  __shared__ SharedTile st;
+  __shared__ __align__(16) E lds[2][FR * FS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
+  const int C = ACROSS ? d.K : d.N, R = d.R;
+  if (blockIdx.y == gridDim.y - 1) {  // the tiles of rows without an adapter
+    if ((int)blockIdx.x * kM < rs.T) copy_none<DT>(&st, d, rs, rs.tiles + blockIdx.x, add, ldadd, out, ldo, C, u);
+    return;
+  }
+  take_tile(&st, rs.kept + blockIdx.x);
+  const int cnt = __builtin_amdgcn_readfirstlane(st.cnt);
+  if (!cnt) return;
+  const int rk = __builtin_amdgcn_readfirstlane(st.rank), a = __builtin_amdgcn_readfirstlane(st.a);
+  const bool whole = rk % 8 == 0, mine = wave * 16 < cnt;
+  const E* fbase = (const E*)(ACROSS ? d.a : d.b) + (size_t)a * R * C;
+  u32x4 fn[FL], vf[RB][2], av[4] = {};
+  const auto fetch = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < FL; ++i) {
+      const int v = tid + kOutThreads * i, row = v / FV, c = v % FV * 8;
+      if (ACROSS) fn[i] = load8<DT>(fbase, (uint32_t)(row < rk ? row : 0) * C + (c0 + c < C ? c0 + c : 0));
+      else fn[i] = load8<DT>(fbase, (uint32_t)min(c0 + row, C - 1) * R + (c < rk ? c : 0));
+    }
   };
-  if (add) fetch_add(first);
-  pack_rows<DT, M, RB, false>(&pk, st, part, S, rs.T, d.R, st.scale, blockIdx.y == 0 ? u : nullptr);
-  for (int q0 = 0; q0 < passes; ++q0) {
-    const int n0 = first + q0 * kExpandCols, c = n0 + li * 8;
-    if (n0 >= d.N) break;
-    f32x4 acc[MT][8] = {};
+  const int first = blockIdx.y * passes * kCols;
+  fetch(first);
+  const size_t band = ((size_t)blockIdx.x * 4 + wave) * RB;
+  f32x4 sc[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    // (blocks past the rank, and bands past the rows, hold anything: not used)
+    vf[b][0] = frag[((band + b) * 2 + 0) * 64 + lane];
+    vf[b][1] = frag[((band + b) * 2 + 1) * 64 + lane];
+    sc[b] = *(const f32x4*)(scale + (band + b) * 16 + g * 4);
+  }
+  int row[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) row[i] = st.row[wave * 16 + g * 4 + i];
+  const auto fetch_add = [&](int c0) {
+    const int c = c0 + li * 8 < C ? c0 + li * 8 : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) av[i] = load8<DT>((const E*)add + (size_t)max(row[i], 0) * ldadd, c);
+  };
+  if (add && mine) fetch_add(first);
+  if (ACROSS && RT == 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *(u32x4*)(lds[i] + (tid / 16 + 16) * FS + tid % 16 * 8) = u32x4{0, 0, 0, 0};
+  }
+  constexpr bool kOneScale = DT == MOE_T_BF16 || RB == 1;  // else the blocks' powers of two differ
+  for (int p = 0; p < passes; ++p) {
+    const int c0 = first + p * kCols, c = c0 + li * 8;
+    if (c0 >= C) break;
+    E* fs = lds[p & 1];
+#pragma unroll
+    for (int i = 0; i < FL; ++i) {
+      const int v = tid + kOutThreads * i, frow = v / FV, fc = v % FV * 8;
+      if (ACROSS) {
+        const v8_t<DT> w = as_frag<DT>(keep(fn[i], frow < rk && c0 + fc < C));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) fs[frow * FS + q * 16 + fc / 8] = w[q];
+      } else {
+        *(u32x4*)(fs + place_of(frow) * FS + fc) = keep_upto(fn[i], rk - fc, whole);
+      }
+    }
+    if (p + 1 < passes) fetch(c0 + kCols);
+    __syncthreads();
+    if (!mine) continue;
+    f32x4 tot[8] = {};
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-#pragma unroll
-      for (int i = 0; i < BL; ++i) {
-        const int v = lane + 64 * i, n = v / VR, r = b * 32 + v % VR * 8;
-        *(u32x4*)(bs + (n % 8 * 16 + n / 8) * BS + v % VR * 8) = keep_upto(bn[i], rk - r, whole);
-      }
-      lds_order();
-      if (b + 1 < RB) fetch(n0, b + 1);
-      else if (q0 + 1 < passes) fetch(n0 + kExpandCols, 0);
-      v8_t<DT> uf[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) uf[m][h] = as_frag<DT>(pk.frag[m * RB + b][h][lane]);
+      if (b * 32 >= rk) break;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const v8_t<DT> bf = *(const v8_t<DT>*)(bs + (q * 16 + li) * BS + (RT == 1 ? min(g, 2) : g) * 8);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          acc[m][q] = Mat<DT>::mma(uf[m][0], bf, acc[m][q]);
-          acc[m][q] = Mat<DT>::mma(uf[m][1], bf, acc[m][q]);
+        v8_t<DT> ff = {};
+        if (ACROSS) {
+          const E* at = fs + (b * 32 + g * 8 + (li >> 2)) * FS + q * 16 + (li & 3) * 4;
+          ff = read_across<DT>(at, at + 4 * FS);
+        } else if (RT > 1 || g < 2) {
+          ff = *(const v8_t<DT>*)(fs + (q * 16 + li) * FS + b * 32 + g * 8);
         }
-      }
-      lds_order();
-    }
+        f32x4 s = kOneScale ? tot[q] : f32x4{0, 0, 0, 0};
+        s = Mat<DT>::mma(as_frag<DT>(vf[b][0]), ff, s);
+        s = Mat<DT>::mma(as_frag<DT>(vf[b][1]), ff, s);
+        if (kOneScale) tot[q] = s;
+        else
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const f32x4 f = *(const f32x4*)&pk.scale[m * 16 + g * 4];
-      int row[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = st.row[m * 16 + g * 4 + i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float o[8];
-        unpack_vec<DT>(av[m][i], o);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) o[q] = fmaf(acc[m][q][i], f[i], o[q]);
-        if (row[i] >= 0 && c < d.N) *(u32x4*)((E*)y + (size_t)row[i] * ldy + c) = pack_vec<DT>(o);
+          for (int i = 0; i < 4; ++i) tot[q][i] = fmaf(s[i], sc[b][i], tot[q][i]);
       }
     }
-    if (add && q0 + 1 < passes) fetch_add(n0 + kExpandCols);
+    u32x4 res[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float o[8];
+      unpack_vec<DT>(av[i], o);
+      const float f = rk ? sc[0][i] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = kOneScale ? fmaf(tot[q][i], f, o[q]) : o[q] + tot[q][i];
+      res[i] = pack_vec<DT>(o);
+    }
+    if (add && p + 1 < passes) fetch_add(c0 + kCols);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row[i] >= 0 && c < C) *(u32x4*)((E*)out + (size_t)row[i] * ldo + c) = res[i];
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward pass: k_rows<ACROSS> forms v, k_grad_out dx, dA and dB, and
-// k_grad_sum adds the partial dA and dB of adapters whose rows several
+// Backward pass: k_rows<ACROSS> forms v, k_spread<ACROSS> dx, k_outer dA and
+// dB, and k_grad_sum adds the partial dA and dB of adapters whose rows several
 // workgroups took.
 // ---------------------------------------------------------------------------
-constexpr int kGradM = 32;  // rows per tile
-
 // Pieces of a factor of a weight gradient (an fp32 output).
 template <int DT>
 constexpr int kGradPieces = DT == MOE_T_F16 ? 2 : 3;
@@ -669,205 +808,105 @@ __device__ __forceinline__ Item find_item(const RowSet& rs, int n, int item, int
   return {n, 0, 0, -1};
 }
 
-constexpr int kStride = 72;                  // elements of an LDS row of 64 columns
-constexpr int kOutCols = kOutWaves * 64;     // columns of a workgroup
-constexpr int kDxStride = 68;                // floats of an LDS row of 64 results
+constexpr int cmin(int a, int b) { return a < b ? a : b; }
 
-// Rows of the weight gradients' factor held as fragments at a time.
-template <int DT, int RT>
-constexpr int kChunkTiles = RT == 1 ? 8 : RT == 2 ? 4 : RT == 4 ? 2 : 1;
+constexpr int kGradM = 32;                // rows taken at a time
+constexpr int kStride = 72;               // elements of an LDS row of 64 columns
+constexpr int kOutCols = kOutWaves * 64;  // columns of a workgroup
+constexpr int kOuterThreads = 512;        // two wavefronts per 64 columns: they take tiles in turn
+constexpr int kOuterWaves = kOuterThreads / kWave;
 
-template <int DT, int RT>
-struct GradLds {
-  static constexpr int RB = (RT + 1) / 2;
-  struct Dx {
-    SharedTile st;
-    RowPack<kGradM, RB> pk;
-    union {
-      typename Mat<DT>::elem rows[32 * kStride];
-      float out[kGradM * kDxStride];
-    } w[kOutWaves];
-  };
-  struct Outer {
-    float top[kOutWaves];
-    u32x4 frag[kChunkTiles<DT, RT>][RT][kGradPieces<DT>][64];
-    typename Mat<DT>::elem rows[kOutWaves][kGradM * kStride];
-  };
-  union {
-    Dx dx;
-    Outer o;
-  };
-  __device__ GradLds() {}
+// 32-row tiles of v or u held as fragments at a time (a multiple of 4).
+template <int RT>
+constexpr int kChunkTiles = RT <= 2 ? 8 : 4;
+
+struct OuterArgs {
+  const float *u, *v;  // [T][R] in the sorted order
+  int items, G, slots;
+  const void *x, *dy;
+  int64_t ldx, lddy;
+  float *d_a, *d_b, *sums;  // sums: [slots][R K + R N], partial results
 };
-
-// dx of a tile's rows, 64 columns at a time per wavefront: rows of A through
-// LDS, 32 at a time; the results go back through LDS so that 8 lanes finish
-// 128 contiguous bytes of a row.
-template <int DT, int RT>
-__device__ __forceinline__ void grad_dx(GradLds<DT, RT>& lds, const AdapterArgs& d, const RowSet& rs, const float* v, int S,
-                                        int tile, int chunk, int passes, const void* add, int64_t ldadd, void* dx,
-                                        int64_t lddx) {
-  typedef typename Mat<DT>::elem E;
-  constexpr int RB = (RT + 1) / 2, MT = kGradM / 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
-  auto& L = lds.dx;
-  if (tile >= rs.tiles) {  // rows without an adapter: one workgroup takes all columns
-    if (chunk) return;
-    passes = (d.K + kOutCols - 1) / kOutCols;
-    share_tile<kGradM>(&L.st, d, rs, tile, nullptr);
-  } else {
-    take_tile(&L.st, rs.kept + tile);
-  }
-  if (!__builtin_amdgcn_readfirstlane(L.st.cnt)) return;
-  const int rk = __builtin_amdgcn_readfirstlane(L.st.rank), a = min(__builtin_amdgcn_readfirstlane(L.st.a), d.n - 1);
-  E* stage = L.w[wave].rows;
-  float* out = L.w[wave].out;
-  const E* abase = (const E*)d.a + (size_t)a * d.R * d.K;
-  u32x4 an[4];
-  const auto fetch = [&](int k0, int b) {
-    const int k = k0 + lane % 8 * 8 < d.K ? k0 + lane % 8 * 8 : 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = b * 32 + lane / 8 + 8 * i;
-      an[i] = load8<DT>(abase, (uint32_t)(r < rk ? r : 0) * d.K + k);
-    }
-  };
-  const int first = (chunk * passes * kOutWaves + wave) * 64;
-  fetch(first, 0);
-  int row[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) row[i] = L.st.row[lane / 8 + 8 * i];
-  u32x4 av[4] = {};
-  const auto fetch_add = [&](int k0) {
-    const int k = k0 + lane % 8 * 8 < d.K ? k0 + lane % 8 * 8 : 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) av[i] = load8<DT>((const E*)add + (size_t)max(row[i], 0) * ldadd, k);
-  };
-  if (add) fetch_add(first);
-  pack_rows<DT, kGradM, RB, true>(&L.pk, L.st, v, S, rs.T, d.R, 1.0f, nullptr);
-  for (int q0 = 0; q0 < passes; ++q0) {
-    const int k0 = first + q0 * kOutCols, c = k0 + lane % 8 * 8;
-    if (k0 >= d.K) break;
-    f32x4 acc[MT][4] = {};
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lane / 8 + 8 * i;
-        *(u32x4*)(stage + r * kStride + lane % 8 * 8) = keep(an[i], b * 32 + r < rk && c < d.K);
-      }
-      lds_order();
-      if (b + 1 < RB) fetch(k0, b + 1);
-      else if (q0 + 1 < passes) fetch(k0 + kOutCols, 0);
-      v8_t<DT> vf[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) vf[m][h] = as_frag<DT>(L.pk.frag[m * RB + b][h][lane]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const E* p = stage + (g * 8 + (li >> 2)) * kStride + q * 16 + (li & 3) * 4;
-        const v8_t<DT> af = read_across<DT>(p, p + 4 * kStride);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          acc[m][q] = Mat<DT>::mma(af, vf[m][0], acc[m][q]);
-          acc[m][q] = Mat<DT>::mma(af, vf[m][1], acc[m][q]);
-        }
-      }
-      lds_order();
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) *(f32x4*)(out + (m * 16 + li) * kDxStride + q * 16 + g * 4) = acc[m][q];
-    lds_order();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = lane / 8 + 8 * i;
-      const f32x4* r = (const f32x4*)(out + t * kDxStride + lane % 8 * 8);
-      const f32x4 lo = r[0], hi = r[1];
-      float o[8];
-      unpack_vec<DT>(av[i], o);
-      const float f = L.pk.scale[t];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        o[q] = fmaf(lo[q], f, o[q]);
-        o[4 + q] = fmaf(hi[q], f, o[4 + q]);
-      }
-      if (row[i] >= 0 && c < d.K) *(u32x4*)((E*)dx + (size_t)row[i] * lddx + c) = pack_vec<DT>(o);
-    }
-    lds_order();
-    if (add && q0 + 1 < passes) fetch_add(k0 + kOutCols);
-  }
-}
 
 // A weight gradient's 64 columns per wavefront over an item's rows: the rows
 // of x (dA = sum_t v x^T) or dy (TR: dB = s_a sum_t dy u^T) pass through LDS, 32
-// at a time, against v or u (in the sorted order), which the workgroup holds as
-// fragments for a few tiles at a time.  In binary16 those share one power of
-// two, the smallest so far; where a chunk brings a smaller one, the sums are
-// rescaled.
+// at a time, two such tiles in flight per wavefront, against v or u, which the workgroup
+// holds as fragments for a few tiles at a time.  In binary16 those share one
+// power of two, the smallest so far; where a chunk brings a smaller one, the
+// sums are rescaled.
+template <int DT, int RT>
+struct OuterLds {
+  float top[kOuterWaves];
+  int ids[2][kChunkTiles<RT> * kGradM];  // rows of this chunk and of the next
+  union {
+    struct {
+      u32x4 frag[kChunkTiles<RT>][RT][kGradPieces<DT>][64];
+      typename Mat<DT>::elem rows[kOuterWaves][kGradM * kStride];
+    };
+    f32x4 half[kOutWaves][4 * cmin(RT, 4)][64];  // the second wavefronts' sums (of up to 4 r tiles)
+  };
+};
+
 template <int DT, int RT, bool TR>
-__device__ __forceinline__ void grad_outer(GradLds<DT, RT>& lds, const AdapterArgs& d, const RowSet& rs, const float* v,
-                                           int S, int item, int G, int chunk, const void* x, int64_t ldx, float* out,
-                                           float* sums, int slots) {
+__device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArgs& d, const RowSet& rs, const OuterArgs& ga,
+                                           int item, int chunk) {
   typedef typename Mat<DT>::elem E;
-  constexpr int NP = kGradPieces<DT>, CT = kChunkTiles<DT, RT>, UW = (CT * RT + kOutWaves - 1) / kOutWaves;
-  auto& L = lds.o;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
-  const int C = TR ? d.N : d.K, c0 = chunk * kOutCols + wave * 64;
-  const Item it = find_item(rs, d.n, item, G);  // by every wavefront: no barrier
-  if (it.a >= d.n || it.slot >= slots) return;  // (past the slots: only for groups that overlap)
+  constexpr int NP = kGradPieces<DT>, CT = kChunkTiles<RT>, UW = (CT * RT + kOuterWaves - 1) / kOuterWaves;
+  constexpr int CR = CT * kGradM;  // rows of a chunk
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
+  const int C = TR ? d.N : d.K, c0 = chunk * kOutCols + wave % kOutWaves * 64, half = wave / kOutWaves;
+  const float* v = TR ? ga.u : ga.v;
+  const E* x = (const E*)(TR ? ga.dy : ga.x);
+  const int64_t ldx = TR ? ga.lddy : ga.ldx;
+  const Item it = find_item(rs, d.n, item, ga.G);  // by every wavefront: no barrier
+  if (it.a >= d.n || it.slot >= ga.slots) return;  // (past the slots: only for groups that overlap)
   const int rk = rank_of(d, it.a), tiles = rk ? (it.cnt + kGradM - 1) / kGradM : 0;
   E* stage = L.rows[wave];
   const int col = c0 + lane % 8 * 8, colc = col < C ? col : 0;
-  int ids[4], next[4];  // rows of the tile in `rows`, and of the one after it
-  const auto fetch_ids = [&](int j) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = j * kGradM + lane / 8 + 8 * q;
-      const int r = rs.pairs[min(it.first + i, rs.T - 1)];
-      next[q] = i < it.cnt && (unsigned)r < (unsigned)rs.T ? r : -1;
-    }
+  const auto fetch_id = [&](int j0) {  // this thread's row of a chunk
+    const int i = j0 * kGradM + tid;
+    const int r = rs.pairs[min(it.first + min(i, it.cnt), rs.T - 1)];
+    return i < it.cnt && (unsigned)r < (unsigned)rs.T ? r : -1;
   };
-  u32x4 rows[4];
-  const auto fetch = [&](int j) {
+  const auto id_of = [&](int j, int q) { return L.ids[j / CT & 1][j % CT * kGradM + lane / 8 + 8 * q]; };
+  u32x4 rows[2][4];  // the next two tiles
+  const auto fetch = [&](int j, u32x4 (&rows)[4]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      ids[q] = next[q];
-      rows[q] = load8<DT>((const E*)x + (size_t)max(ids[q], 0) * ldx, colc);
-    }
-    if (j + 1 < tiles) fetch_ids(j + 1);
+    for (int q = 0; q < 4; ++q) rows[q] = load8<DT>(x + (size_t)max(id_of(j, q), 0) * ldx, colc);
   };
   // this wavefront's part of a chunk of v: unit -> tile unit / RT, r tile unit % RT
   float w[UW][8];
   const auto fetch_v = [&](int j0) {
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
-      const int unit = min(wave + k * kOutWaves, CT * RT - 1), r = min(unit % RT * 16 + li, d.R - 1);
+      const int unit = min(wave + k * kOuterWaves, CT * RT - 1), r = min(unit % RT * 16 + li, d.R - 1);
       const int i = (j0 + unit / RT) * kGradM + g * 8;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float* p = v + (size_t)(it.first + min(i + q, it.cnt - 1)) * d.R + r;
-        float s = p[0];
-        for (int k2 = 1; k2 < S; ++k2) s += p[(size_t)k2 * rs.T * d.R];
-        w[k][q] = s;
-      }
+      for (int q = 0; q < 8; ++q) w[k][q] = v[(size_t)(it.first + min(i + q, it.cnt - 1)) * d.R + r];
     }
   };
   f32x4 acc[4][RT] = {};
   int e = 0;
   bool any = false;
+  int id = -1;
   if (tiles) {
-    fetch_ids(0);
+    const int id0 = tid < CR ? fetch_id(0) : -1;
     fetch_v(0);
-    fetch(0);
+    id = tid < CR ? fetch_id(CT) : -1;
+    if (tid < CR) {
+      L.ids[0][tid] = id0;
+      L.ids[1][tid] = id;
+    }
+    __syncthreads();
+    fetch(half, rows[0]);
+    fetch(half + 2, rows[1]);
+    id = tid < CR ? fetch_id(2 * CT) : -1;
   }
   for (int j0 = 0; j0 < tiles; j0 += CT) {
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
-      const int unit = wave + k * kOutWaves, r = unit % RT * 16 + li, i = (j0 + unit / RT) * kGradM + g * 8;
+      const int unit = wave + k * kOuterWaves, r = unit % RT * 16 + li, i = (j0 + unit / RT) * kGradM + g * 8;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         w[k][q] = unit < CT * RT && r < rk && i + q < it.cnt ? w[k][q] : 0.0f;
@@ -877,9 +916,15 @@ __device__ __forceinline__ void grad_outer(GradLds<DT, RT>& lds, const AdapterAr
     if (DT == MOE_T_F16) {
       top = __builtin_bit_cast(float, wave_max_u32(__builtin_bit_cast(uint32_t, top)));
       if (lane == 0) L.top[wave] = top;
-      __syncthreads();  // also: the last chunk's fragments have been read
+    }
+    __syncthreads();  // also: the last chunk's fragments and ids have been read
+    if (j0 && tid < CR) {  // the next chunk's rows; and ask for those after
+      L.ids[j0 / CT + 1 & 1][tid] = id;
+      id = fetch_id(j0 + 2 * CT);
+    }
+    if (DT == MOE_T_F16) {
 #pragma unroll
-      for (int q = 0; q < kOutWaves; ++q) top = fmaxf(top, L.top[q]);
+      for (int q = 0; q < kOuterWaves; ++q) top = fmaxf(top, L.top[q]);
       if (top > 0.0f) {
         const int en = any ? min(e, scale_exp<DT>(top)) : scale_exp<DT>(top);
         if (any && en < e) {
@@ -892,12 +937,10 @@ __device__ __forceinline__ void grad_outer(GradLds<DT, RT>& lds, const AdapterAr
         e = en;
         any = true;
       }
-    } else {
-      __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
-      const int unit = wave + k * kOutWaves;
+      const int unit = wave + k * kOuterWaves;
       if (unit < CT * RT) {
         v8_t<DT> p[NP];
         split_pieces<DT, NP>(w[k], e, p);
@@ -907,11 +950,11 @@ __device__ __forceinline__ void grad_outer(GradLds<DT, RT>& lds, const AdapterAr
     }
     __syncthreads();
     if (j0 + CT < tiles) fetch_v(j0 + CT);
-    for (int j = j0; j < min(j0 + CT, tiles); ++j) {
+    const auto tile = [&](int j, u32x4 (&rows)[4]) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *(u32x4*)(stage + (lane / 8 + 8 * q) * kStride + lane % 8 * 8) = keep(rows[q], ids[q] >= 0 && col < C);
-      if (j + 1 < tiles) fetch(j + 1);
+        *(u32x4*)(stage + (lane / 8 + 8 * q) * kStride + lane % 8 * 8) = keep(rows[q], id_of(j, q) >= 0 && col < C);
+      if (j + 4 < tiles) fetch(j + 4, rows);
       lds_order();
       v8_t<DT> xf[4];
 #pragma unroll
@@ -928,11 +971,36 @@ __device__ __forceinline__ void grad_outer(GradLds<DT, RT>& lds, const AdapterAr
           for (int q = 0; q < 4; ++q) acc[q][r] = TR ? Mat<DT>::mma(vf, xf[q], acc[q][r]) : Mat<DT>::mma(xf[q], vf, acc[q][r]);
         }
       lds_order();
+    };
+    const int j1 = min(j0 + CT, tiles);
+    for (int j = j0 + half; j < j1; j += 4) {
+      tile(j, rows[0]);
+      if (j + 2 < j1) tile(j + 2, rows[1]);
     }
   }
-  if (c0 >= C) return;
+  // the two wavefronts of each 64 columns, 4 r tiles at a time
+#pragma unroll
+  for (int r0 = 0; r0 < RT; r0 += 4) {
+    constexpr int RH = RT < 4 ? RT : 4;
+    __syncthreads();
+    if (half) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int r = 0; r < RH; ++r) L.half[wave % kOutWaves][q * RH + r][lane] = acc[q][r0 + r];
+    }
+    __syncthreads();
+    if (!half) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int r = 0; r < RH; ++r) acc[q][r0 + r] += L.half[wave][q * RH + r][lane];
+    }
+  }
+  if (half || c0 >= C) return;
   const size_t per = (size_t)d.R * (d.K + d.N);
-  float* o = it.slot >= 0 ? sums + it.slot * per + (TR ? (size_t)d.R * d.K : 0) : out + (size_t)it.a * d.R * C;
+  float* out = TR ? ga.d_b : ga.d_a;
+  float* o = it.slot >= 0 ? ga.sums + it.slot * per + (TR ? (size_t)d.R * d.K : 0) : out + (size_t)it.a * d.R * C;
   const float f = __builtin_amdgcn_ldexpf(TR ? d.scale[it.a] : 1.0f, -e);
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -948,31 +1016,14 @@ __device__ __forceinline__ void grad_outer(GradLds<DT, RT>& lds, const AdapterAr
     }
 }
 
-struct GradArgs {
-  const float *u, *v;  // [T][R], [S][T][R], in the sorted order
-  int S, items, G, slots, dx_passes;
-  const void *x, *dy, *add;
-  int64_t ldx, lddy, ldadd, lddx;
-  void* dx;
-  float *d_a, *d_b, *sums;
-};
-
-// Workgroups [0, nA) take dA, [nA, nA + nB) dB, the rest dx.
+// Workgroups [0, nA) take dA, the rest dB.
 template <int DT, int RT>
-__global__ __launch_bounds__(kOutThreads) void k_grad_out(AdapterArgs d, RowSet rs, GradArgs ga) {
-  __shared__ GradLds<DT, RT> lds;
-  const int ka = (d.K + kOutCols - 1) / kOutCols, kb = (d.N + kOutCols - 1) / kOutCols;
-  int b = blockIdx.x;
-  if (b < ga.items * ka)
-    return grad_outer<DT, RT, false>(lds, d, rs, ga.v, ga.S, b / ka, ga.G, b % ka, ga.x, ga.ldx, ga.d_a, ga.sums, ga.slots);
-  b -= ga.items * ka;
-  if (b < ga.items * kb)
-    return grad_outer<DT, RT, true>(lds, d, rs, ga.u, 1, b / kb, ga.G, b % kb, ga.dy, ga.lddy, ga.d_b, ga.sums, ga.slots);
-  b -= ga.items * kb;
-  const int kx = (ka + ga.dx_passes - 1) / ga.dx_passes;
-  const bool none = b >= rs.tiles * kx;
-  grad_dx<DT, RT>(lds, d, rs, ga.v, ga.S, none ? b - rs.tiles * (kx - 1) : b / kx, none ? 0 : b % kx, ga.dx_passes, ga.add,
-                  ga.ldadd, ga.dx, ga.lddx);
+__global__ __launch_bounds__(kOuterThreads) void k_outer(AdapterArgs d, RowSet rs, OuterArgs ga) {
+  __shared__ OuterLds<DT, RT> lds;
+  const int ka = (d.K + kOutCols - 1) / kOutCols, kb = (d.N + kOutCols - 1) / kOutCols, nA = ga.items * ka;
+  const int b = blockIdx.x;
+  if (b < nA) grad_outer<DT, RT, false>(lds, d, rs, ga, b / ka, b % ka);
+  else grad_outer<DT, RT, true>(lds, d, rs, ga, (b - nA) / kb, (b - nA) % kb);
 }
 
 // Sums the partial gradients of adapters that have several.
@@ -1026,36 +1077,36 @@ int check_adapter_ptrs(const moe_adapters_t* d) {
   return MOE_OK;
 }
 
-constexpr int kSmallRows = 64;      // rows that a workgroup groups by itself
-constexpr int kSegment = 512;       // columns per K-segment of a small batch
-constexpr int kWanted = 256;        // workgroups of k_rows that run at once
-constexpr int kWantedOut = 512;     // workgroups of the second launch that do
+constexpr int kSmallRows = 64;   // rows that a workgroup groups by itself
+constexpr int kSegment = 1024;   // columns per K-segment of a small batch: two steps of every wavefront
+constexpr int kWideRows = 4096;  // rows from which k_rows takes 64 r at a time
+constexpr int kSpreadGroups = 512;  // workgroups of k_spread below which none takes more than one run
+constexpr int kWanted = 256;     // workgroups of k_outer that fill the GPU
 
 // Matrix fragments of a rank: 1, 2, 4 or 8 of 16.
 int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
 struct AdapterPlan {
-  bool small;         // forward: grouped by the workgroups, 16-row tiles
-  int M, tiles, all;  // forward: rows per tile, bound on tiles of adapters, and with the others
-  int S;              // forward: K-segments
-  int gtiles, gS, G, items, slots;  // backward
-  size_t kept, part, v, u, sums;    // partial u; partial v, sorted u, partial dA and dB
+  bool small;             // forward: 16-row tiles that the workgroups find from ids
+  int tiles;              // bound on tiles of adapters (a multiple of kXcds, and no less than T / kM)
+  int stiles, S;          // small: tiles, K-segments
+  int rb;                 // blocks of 32 r
+  int G, items, slots;    // k_outer
+  size_t kept, part, frag, scale, v, u, sums;
   size_t offsets, pairs, pos, sort, total;
 };
 
 AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
   AdapterPlan p{};
   p.small = T <= kSmallRows;
-  p.M = p.small ? 16 : 32;
-  p.tiles = (int)std::min<int64_t>(T, (int64_t)T / p.M + d.n + p.small);
-  p.all = p.tiles + (p.small ? 0 : ceil_div(T, p.M));
-  const auto segments = [](int width, int tiles) {
-    return std::max(1, std::min(ceil_div(width, kSegment), kWanted / std::max(1, tiles)));
-  };
-  p.S = p.small ? ceil_div(d.K, kSegment) : segments(d.K, ceil_div(T, p.M) + d.n / 2);
-  p.gS = segments(d.N, ceil_div(T, kGradM) + d.n / 2);
-  p.gtiles = (int)std::min<int64_t>(T, (int64_t)T / kGradM + d.n);
-  p.G = std::max(256, ceil_div(T, 32 * kGradM) * kGradM);
+  p.tiles = ceil_div(std::min(T, T / kM + d.n), kXcds) * kXcds;
+  p.stiles = std::min(T, T / kSmallM + d.n + 1);
+  p.S = ceil_div(d.K, kSegment);
+  p.rb = (rank_tiles(d.R) + 1) / 2;
+  // An adapter's rows go to one workgroup per 256 columns, or, where few
+  // adapters leave the GPU empty, to several (whose results are then added).
+  const int cols = ceil_div(d.K, kOutCols) + ceil_div(d.N, kOutCols), wanted = ceil_div(kWanted, cols);
+  p.G = d.n >= (wanted + 1) / 2 ? 2048 : std::max(256, ceil_div(T, wanted / d.n * kGradM) * kGradM);
   p.items = T / p.G + d.n;
   p.slots = T > p.G ? 2 * (T / p.G) : 0;
   size_t o = 0;
@@ -1068,15 +1119,14 @@ AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
   p.pairs = take((size_t)T * 4);
   p.pos = take((size_t)T * 4);
   p.sort = take(moe_sort_workspace_bytes(T, 1, d.n));
-  p.kept = take((size_t)std::max(p.all, p.gtiles) * sizeof(SharedTile));
-  const size_t common = o;
-  p.part = take((size_t)p.S * T * d.R * 4);
-  const size_t forward = o;
-  o = common;
-  p.v = take((size_t)p.gS * T * d.R * 4);
+  p.kept = take((size_t)std::max(p.tiles, p.stiles) * sizeof(SharedTile));
+  p.part = take(p.small ? (size_t)p.S * T * d.R * 4 : 0);
+  p.frag = take((size_t)p.tiles * 4 * p.rb * 2 * 1024);
+  p.scale = take((size_t)p.tiles * 4 * p.rb * 16 * 4);
+  p.v = take((size_t)T * d.R * 4);
   p.u = take((size_t)T * d.R * 4);
   p.sums = take((size_t)p.slots * d.R * ((size_t)d.K + d.N) * 4);
-  p.total = std::max(forward, o);
+  p.total = o;
   return p;
 }
 
@@ -1097,6 +1147,32 @@ void by_shape(const moe_adapters_t& d, F f) {
   };
   if (d.dtype == MOE_T_F16) ranks(Const<MOE_T_F16>{});
   else ranks(Const<MOE_T_BF16>{});
+}
+
+template <int DT, int RT, bool ACROSS>
+void launch_rows(const AdapterPlan& p, const AdapterArgs& g, const RowSet& rs, const void* x, int64_t ldx,
+                 const RowsOut& out, hipStream_t s) {
+  // Bands and fragments of r per workgroup: fewer workgroups re-read less, more
+  // fill the GPU.  k_rows at 6144 columns, rank 64 (mixed), bfloat16: 1,801 rows
+  // 14.4 us as below, 16.6 with one band and 64 r, 17.7 with one band and 32 r,
+  // 18.6 with two bands and 64 r; 7,204 rows 30.7 us as below, 37.8 with 32 r,
+  // 32.6 with four bands and 32 r.  Rank 16, 1,801 rows: 9.7 us, 11.8 with two bands.
+  constexpr int BT = RT < 2 ? RT : 2, WT = RT < 4 ? RT : 4, MT = RT == 1 ? 1 : 2;
+  if (!ACROSS && p.small)
+    k_rows<DT, 1, BT, ACROSS, true><<<dim3(p.stiles, ceil_div(g.R, BT * 16), p.S), kRowThreads, 0, s>>>(g, rs, x, ldx, out);
+  else if (rs.T < kWideRows)
+    k_rows<DT, MT, BT, ACROSS, false><<<dim3(p.tiles, ceil_div(g.R, BT * 16), 4 / MT), kRowThreads, 0, s>>>(g, rs, x, ldx, out);
+  else
+    k_rows<DT, 2, WT, ACROSS, false><<<dim3(p.tiles, ceil_div(g.R, WT * 16), 2), kRowThreads, 0, s>>>(g, rs, x, ldx, out);
+}
+
+template <int DT, int RT, bool ACROSS>
+void launch_spread(const AdapterPlan& p, const AdapterArgs& g, const RowSet& rs, int width, const u32x4* frag,
+                   const float* scale, const void* add, int64_t ldadd, void* out, int64_t ldo, float* u, hipStream_t s) {
+  const int runs = ceil_div(width, kCols);
+  const int passes = std::max(1, std::min(runs, (int)((int64_t)p.tiles * runs / kSpreadGroups)));
+  k_spread<DT, RT, ACROSS><<<dim3(p.tiles, ceil_div(runs, passes) + 1), kOutThreads, 0, s>>>(
+      g, rs, frag, scale, add, ldadd, out, ldo, u, passes);
 }
 
 }  // namespace
@@ -1128,32 +1204,31 @@ int moe_adapter_forward(const moe_adapters_t* d, const void* x, int64_t ldx, int
   const hipStream_t s = (hipStream_t)stream;
   const AdapterArgs g{d->a, d->b, d->scale, d->ranks, d->n, d->K, d->N, d->R};
   char* w = (char*)ws;
-  RowSet rs{ids, nullptr, nullptr, (SharedTile*)(w + p.kept), T, p.tiles};
-  if (!p.small) {
-    if (!offsets) {
-      int32_t *o = (int32_t*)(w + p.offsets), *q = (int32_t*)(w + p.pairs);
-      if (launch_sort(ids, T, 1, d->n, 1, T, o, q, (int32_t*)(w + p.pos), w + p.sort, s) != hipSuccess) return MOE_E_HIP;
-      offsets = o;
-      pairs = q;
-    }
-    rs.offsets = offsets;
-    rs.pairs = pairs;
+  u32x4* frag = (u32x4*)(w + p.frag);
+  float* scale = (float*)(w + p.scale);
+  SharedTile* kept = (SharedTile*)(w + p.kept);
+  if (p.small) {
+    const RowSet rs{ids, nullptr, nullptr, kept, T, p.stiles};
+    float* part = (float*)(w + p.part);
+    by_shape(*d, [&](auto dt, auto rt) {
+      constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
+      launch_rows<DT, RT, false>(p, g, rs, x, ldx, RowsOut{part, nullptr, nullptr, frag, scale, p.rb}, s);
+      k_expand_small<DT, RT><<<dim3(p.stiles, ceil_div(d->N, kOutWaves * kCols)), kOutThreads, 0, s>>>(
+          g, rs, part, p.S, u, add, ldadd, y, ldy);
+    });
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
   }
-  const bool direct = p.S == 1 && u;  // the only segment is u itself
-  float* part = direct ? u : (float*)(w + p.part);
-  const int cols = ceil_div(d->N, kExpandCols);
-  const int passes = std::min(cols, ceil_div((int64_t)p.tiles * cols, kWantedOut));
+  if (!offsets) {
+    int32_t *o = (int32_t*)(w + p.offsets), *q = (int32_t*)(w + p.pairs);
+    if (launch_sort(ids, T, 1, d->n, 1, T, o, q, (int32_t*)(w + p.pos), w + p.sort, s) != hipSuccess) return MOE_E_HIP;
+    offsets = o;
+    pairs = q;
+  }
+  const RowSet rs{ids, offsets, pairs, kept, T, p.tiles};
   by_shape(*d, [&](auto dt, auto rt) {
     constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-    const dim3 g1(p.all, p.S), g2(p.all, ceil_div(cols, passes));
-    float* uo = direct ? nullptr : u;
-    if (p.small) {
-      k_rows<DT, 1, RT, false><<<g1, kRowThreads, 0, s>>>(g, rs, x, ldx, part, direct, nullptr, nullptr);
-      k_expand<DT, 1, RT><<<g2, kOutThreads, 0, s>>>(g, rs, part, p.S, uo, add, ldadd, y, ldy, passes);
-    } else {
-      k_rows<DT, 2, RT, false><<<g1, kRowThreads, 0, s>>>(g, rs, x, ldx, part, direct, nullptr, nullptr);
-      k_expand<DT, 2, RT><<<g2, kOutThreads, 0, s>>>(g, rs, part, p.S, uo, add, ldadd, y, ldy, passes);
-    }
+    launch_rows<DT, RT, false>(p, g, rs, x, ldx, RowsOut{u, nullptr, nullptr, frag, scale, p.rb}, s);
+    launch_spread<DT, RT, false>(p, g, rs, d->N, frag, scale, add, ldadd, y, ldy, u, s);
   });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
@@ -1183,17 +1258,16 @@ int moe_adapter_backward(const moe_adapters_t* d, const void* dy, int64_t lddy, 
     offsets = o;
     pairs = q;
   }
-  const RowSet rs{ids, offsets, pairs, (SharedTile*)(w + p.kept), T, p.gtiles};
-  const int ka = ceil_div(d->K, kOutCols), kb = ceil_div(d->N, kOutCols);
-  const int passes = std::min(ka, std::max(1, ceil_div((int64_t)p.gtiles * ka, kWantedOut)));
-  float *v = (float*)(w + p.v), *us = (float*)(w + p.u), *sums = (float*)(w + p.sums);
-  const GradArgs ga{us, v,   p.gS, p.items, p.G,  p.slots, passes, x,   dy,
-                    add, ldx, lddy, ldadd,   lddx, dx,      d_a,    d_b, sums};
-  const int dx_groups = dx && T ? p.gtiles * ceil_div(ka, passes) + ceil_div(T, kGradM) : 0;
+  u32x4* frag = (u32x4*)(w + p.frag);
+  float *scale = (float*)(w + p.scale), *v = (float*)(w + p.v), *us = (float*)(w + p.u), *sums = (float*)(w + p.sums);
+  const RowSet rs{ids, offsets, pairs, (SharedTile*)(w + p.kept), T, p.tiles};
+  const OuterArgs ga{us, v, p.items, p.G, p.slots, x, dy, ldx, lddy, d_a, d_b, sums};
+  const int cols = ceil_div(d->K, kOutCols) + ceil_div(d->N, kOutCols);
   by_shape(*d, [&](auto dt, auto rt) {
     constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-    if (T) k_rows<DT, 2, RT, true><<<dim3(p.gtiles, p.gS), kRowThreads, 0, s>>>(g, rs, dy, lddy, v, false, u, us);
-    k_grad_out<DT, RT><<<p.items * (ka + kb) + dx_groups, kOutThreads, 0, s>>>(g, rs, ga);
+    if (T) launch_rows<DT, RT, true>(p, g, rs, dy, lddy, RowsOut{v, u, us, frag, scale, p.rb}, s);
+    if (T && dx) launch_spread<DT, RT, true>(p, g, rs, d->K, frag, scale, add, ldadd, dx, lddx, nullptr, s);
+    k_outer<DT, RT><<<p.items * cols, kOuterThreads, 0, s>>>(g, rs, ga);
   });
   if (p.slots) k_grad_sum<<<dim3(d->n, 64), 256, 0, s>>>(g, rs, sums, p.slots, p.G, d_a, d_b);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
