@@ -59,16 +59,25 @@ __global__ __launch_bounds__(kThreads) void k_route_dots(RouteArgs a, int range,
   constexpr int L = kLanes<CW>, P = 64 / L;  // lanes per slot, slots per step
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / L, cl = lane % L;
   const int c0 = blockIdx.x * CW, nv = a.H / 8, cv = min(c0 / 8 + cl, nv - 1);
-  load_slice<CW>(a, c0, w);
-  __syncthreads();
   const int n = a.T * a.k, p1 = min((int)(blockIdx.y + 1) * range * a.k, n);
   float* out = zpart + (size_t)blockIdx.x * n;
-  for (int base = blockIdx.y * range * a.k + wave * 64; base < p1; base += kWaves * 64) {
-    int e = a.idx[min(base + lane, n - 1)];
-    if ((unsigned)e >= (unsigned)a.E) e = 0;  // dropped: the sum is not used
+  u32x4 next[L];
+  int en = 0;
+  const auto fetch = [&](int base) {
+    en = a.idx[min(base + lane, n - 1)];
+#pragma unroll
+    for (int s = 0; s < L; ++s) next[s] = a.x[(size_t)token_of(a, min(base + s * P + sub, n - 1)) * nv + cv];
+  };
+  const int first = blockIdx.y * range * a.k + wave * 64;
+  if (first < p1) fetch(first);
+  load_slice<CW>(a, c0, w);
+  __syncthreads();
+  for (int base = first; base < p1; base += kWaves * 64) {
+    const int e = (unsigned)en < (unsigned)a.E ? en : 0;  // dropped: the sum is not used
     u32x4 xv[L];
 #pragma unroll
-    for (int s = 0; s < L; ++s) xv[s] = a.x[(size_t)token_of(a, min(base + s * P + sub, n - 1)) * nv + cv];
+    for (int s = 0; s < L; ++s) xv[s] = next[s];
+    if (base + kWaves * 64 < p1) fetch(base + kWaves * 64);
     float mine = 0.0f;
 #pragma unroll
     for (int s = 0; s < L; ++s) {
@@ -92,12 +101,63 @@ __global__ __launch_bounds__(kThreads) void k_route_dots(RouteArgs a, int range,
   }
 }
 
+// Work items of the weights' gradient: up to kItemRows sorted rows of one
+// expert (an expert without rows has one, which writes zeros).
+constexpr int kItemRows = 128;
+struct Item {
+  int e, r0, r1;  // e < 0: none
+  int slot;       // partial sum it writes, or -1: the result itself
+  int parts;      // the expert's items, in its first one (else 0)
+};
+
+// Fills items[0, most) from the groups; one workgroup of 256 threads.
+__device__ __forceinline__ void make_items(const int32_t* offsets, int E, int rows, int most, int per, Item* items) {
+  __shared__ int sums[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int at = 0, slots = 0;
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    const int e = e0 + tid;
+    int r0 = 0, r1 = 0;
+    if (e < E) {
+      r0 = min(max(0, offsets[e]), rows);
+      r1 = max(r0, min(rows, offsets[e + 1]));
+    }
+    const int parts = (int)(((int64_t)r1 - r0 + per - 1) / per), ni = e < E ? max(1, parts) : 0, ns = parts > 1 ? parts : 0;
+    int ii = ni, is = ns;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int oi = __shfl_up(ii, d), os = __shfl_up(is, d);
+      ii += lane >= d ? oi : 0;
+      is += lane >= d ? os : 0;
+    }
+    if (lane == 63) {
+      sums[0][wave] = ii;
+      sums[1][wave] = is;
+    }
+    __syncthreads();
+    int i0 = at + ii - ni, s0 = slots + is - ns;
+    for (int w = 0; w < 4; ++w) {
+      i0 += w < wave ? sums[0][w] : 0;
+      s0 += w < wave ? sums[1][w] : 0;
+      at += sums[0][w];
+      slots += sums[1][w];
+    }
+    for (int j = 0; j < ni; ++j)
+      if (i0 + j < most)
+        items[i0 + j] = {e, r0 + j * per, j + 1 < ni ? r0 + (j + 1) * per : r1, ns ? s0 + j : -1, j ? 0 : parts};
+    __syncthreads();
+  }
+  for (int i = at + tid; i < most; i += 256) items[i] = {-1, 0, 0, -1, 0};
+}
+
 // dz of every slot from the partial logits: 64 / k tokens per workgroup, four
-// threads per slot over the slices.
+// threads per slot over the slices.  The last workgroup makes the items of the
+// launch after next.
 constexpr int kSlotThreads = 256;
 __global__ __launch_bounds__(kSlotThreads) void k_route_slots(RouteArgs a, int slices, const float* zpart, const float* br,
-                                                             const float* dw, float* dz) {
+                                                             const float* dw, float* dz, const int32_t* offsets, int rows,
+                                                             int most, int per_item, Item* items) {
   __shared__ float part[4][64], sg[64], gw[64];
+  if (blockIdx.x == gridDim.x - 1) return make_items(offsets, a.E, rows, most, per_item, items);
   const int l = threadIdx.x & 63, q = threadIdx.x >> 6, n = a.T * a.k, per = 64 / a.k;
   const int p0 = blockIdx.x * per * a.k, np = min(per * a.k, n - p0), p = min(p0 + l, n - 1);
   float z = 0.0f;
@@ -138,30 +198,39 @@ __global__ __launch_bounds__(kThreads) void k_route_dx(RouteArgs a, int range, c
   constexpr int L = kLanes<CW>, P = 64 / L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / L, cl = lane % L;
   const int c0 = blockIdx.x * CW, nv = a.H / 8, cv = c0 / 8 + cl;
+  const int n = a.T * a.k, t1 = min((int)(blockIdx.y + 1) * range, a.T), cc = min(cv, nv - 1);
+  int en = -1;  // the next L slots of this lane's token: one per lane
+  float dn = 0.0f;
+  const auto fetch = [&](int base, int j0) {
+    const int p = min(min(base + sub, a.T - 1) * a.k + j0 + cl, n - 1);
+    en = a.idx[p];
+    dn = dz[p];
+    if (j0 + cl >= a.k || (unsigned)en >= (unsigned)a.E) en = -1;
+  };
+  const int first = blockIdx.y * range + wave * P;
+  if (first < t1) fetch(first, 0);
   load_slice<CW>(a, c0, w);
   __syncthreads();
-  const int n = a.T * a.k, t1 = min((int)(blockIdx.y + 1) * range, a.T);
-  for (int base = blockIdx.y * range + wave * P; base < t1; base += kWaves * P) {
-    const int t = base + sub, tt = min(t, a.T - 1), cc = min(cv, nv - 1);
+  for (int base = first; base < t1; base += kWaves * P) {
+    const int t = base + sub;
     float acc[8] = {};
-    if (add) unpack_vec<DT>(add[(size_t)tt * nv + cc], acc);
+    if (add) unpack_vec<DT>(add[(size_t)min(t, a.T - 1) * nv + cc], acc);
     for (int j0 = 0; j0 < a.k; j0 += L) {
-      const int p = min(tt * a.k + j0 + cl, n - 1);
-      int e = a.idx[p];
-      float d = dz[p];
-      if (j0 + cl >= a.k || (unsigned)e >= (unsigned)a.E) e = -1;
+      const int e = en;
+      const float d = dn;
+      if (j0 + L < a.k) fetch(base, j0 + L);
+      else if (base + kWaves * P < t1) fetch(base + kWaves * P, 0);
 #pragma unroll
       for (int j = 0; j < L; ++j) {
         const int ej = __shfl(e, sub * L + j);
         const float dj = __shfl(d, sub * L + j);
         const float* r = w + max(ej, 0) * (CW + 4) + cl * 8;
-        const f32x4 lo = *(const f32x4*)r, hi = *(const f32x4*)(r + 4);
-        if (ej >= 0) {
+        f32x4 lo = *(const f32x4*)r, hi = *(const f32x4*)(r + 4);
+        if (ej < 0) lo = hi = f32x4{0, 0, 0, 0};  // (dz is 0 for dropped slots)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            acc[c] = fmaf(dj, lo[c], acc[c]);
-            acc[4 + c] = fmaf(dj, hi[c], acc[4 + c]);
-          }
+        for (int c = 0; c < 4; ++c) {
+          acc[c] = fmaf(dj, lo[c], acc[c]);
+          acc[4 + c] = fmaf(dj, hi[c], acc[4 + c]);
         }
       }
     }
@@ -233,63 +302,126 @@ __global__ __launch_bounds__(kThreads) void k_route_grad_tokens(RouteArgs a, con
   }
 }
 
-// dWr[e] = sum over the expert's rows of dz x[t], and db[e]: a workgroup per
-// expert and 512 columns, a thread per 8 columns, the rows split over its
-// wavefronts, 8 in flight for each.
-constexpr int kSumThreads = 512;
-template <int DT>
-__global__ __launch_bounds__(kSumThreads) void k_route_weights(const u32x4* x, int nv, int E, int k, uint32_t per_k,
-                                                              const float* dz, const int32_t* offsets, const int32_t* pairs,
-                                                              int rows, int n, float* dwr, float* db) {
-  constexpr int W = kSumThreads / kWave, U = 8;
-  __shared__ f32x4 red[W][2][64];
+// dWr[e] = sum over an item's rows of dz x[t], and db[e]: a workgroup per item
+// and Q * 256 columns.  Half a wavefront takes a row (a lane 8 columns of each
+// 256), the rows are split over the W wavefronts, 8 KB or more in flight for
+// each.  With 8 runs of columns a die takes one of them, so that its L2 keeps
+// that part of x over all experts.  items == NULL: an expert each.
+template <int DT, int W, int Q>
+__global__ __launch_bounds__(W * kWave) void k_route_weights(const u32x4* x, int nv, int E, uint32_t per_k, const float* dz,
+                                                            const int32_t* offsets, const int32_t* pairs, int rows, int n,
+                                                            const Item* items, int chunks, float* dwr, float* db,
+                                                            float* sums, float* bsums, int slots) {
+  constexpr int U = Q == 1 ? 8 : Q == 2 ? 6 : 4;  // rows in flight per half
+  __shared__ f32x4 red[W][Q][2][32];
   __shared__ float bred[W];
-  const int e = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.x * 64 + lane;
-  const int r0 = min(max(0, offsets[e]), rows), r1 = max(r0, min(rows, offsets[e + 1]));
-  const int ic = min(i, nv - 1), cnt = r1 - r0;
-  const int a0 = r0 + (int)((int64_t)cnt * wave / W), a1 = r0 + (int)((int64_t)cnt * (wave + 1) / W);
-  float acc[8] = {}, sum = 0.0f;
+  const int j = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  Item it;
+  if (items) {
+    it = items[j];
+  } else {
+    it.e = j;
+    it.r0 = min(max(0, offsets[it.e]), rows);
+    it.r1 = max(it.r0, min(rows, offsets[it.e + 1]));
+    it.slot = -1;
+    it.parts = 0;
+  }
+  if (it.e < 0 || it.slot >= slots) return;  // (past the slots: only for groups that overlap)
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, l = lane & 31;
+  int cc[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) cc[q] = min((chunk * Q + q) * 32 + l, nv - 1);
+  const int cnt = it.r1 - it.r0;
+  const int a0 = it.r0 + cnt * wave / W, a1 = it.r0 + cnt * (wave + 1) / W;
+  float acc[Q][8] = {};
+  float sum = 0.0f;
   for (int b0 = a0; b0 < a1; b0 += 64) {  // 64 slots: a lane each
     const int rr = b0 + lane;
-    int p = rr < a1 ? pairs[rr] : -1;
+    const int p = rr < a1 ? pairs[rr] : -1;
     const bool ok = (unsigned)p < (unsigned)n;
     const float d = ok ? dz[p] : 0.0f;
     sum += d;
     int t = ok ? p : 0;
     if (per_k) t = (int)__umulhi((uint32_t)t, per_k);
+    if (!ok) t = -1;
     const int m = min(64, a1 - b0);
-    const uint64_t used = __ballot(ok);
-    for (int s = 0; s < m; s += U) {
-      u32x4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = x[(size_t)__builtin_amdgcn_readlane(t, min(s + u, 63)) * nv + ic];
+    for (int s = 0; s < m; s += 2 * U) {
+      u32x4 v[U][Q];
+      int tt[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (!(used >> min(s + u, 63) & 1)) continue;  // padding: x is not used
-        const float du = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, d), min(s + u, 63)));
-        float f[8];
-        unpack_vec<DT>(v[u], f);
+        tt[u] = __shfl(t, min(s + 2 * u + half, 63));
+        const u32x4* row = x + (size_t)max(tt[u], 0) * nv;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = fmaf(du, f[c], acc[c]);
+        for (int q = 0; q < Q; ++q) v[u][q] = row[cc[q]];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float du = __shfl(d, min(s + 2 * u + half, 63));
+        if (s + 2 * u + half < m && tt[u] >= 0) {  // else padding: x is not used
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            float f[8];
+            unpack_vec<DT>(v[u][q], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[q][i] = fmaf(du, f[i], acc[q][i]);
+          }
+        }
       }
     }
   }
-  red[wave][0][lane] = f32x4{acc[0], acc[1], acc[2], acc[3]};
-  red[wave][1][lane] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      acc[q][i] += __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, acc[q][i])));
+    if (!half) {
+      red[wave][q][0][l] = f32x4{acc[q][0], acc[q][1], acc[q][2], acc[q][3]};
+      red[wave][q][1][l] = f32x4{acc[q][4], acc[q][5], acc[q][6], acc[q][7]};
+    }
+  }
   sum = wave_sum_f32(sum);
   if (lane == 0) bred[wave] = sum;
   __syncthreads();
-  if (threadIdx.x < 128) {
-    const int h = threadIdx.x & 1, l = threadIdx.x >> 1, c = blockIdx.x * 64 + l;
-    f32x4 s = red[0][h][l];
+  float* o = it.slot >= 0 ? sums + (size_t)it.slot * nv * 8 : dwr + (size_t)it.e * nv * 8;
+  for (int i = threadIdx.x; i < Q * 64; i += W * kWave) {  // 4 columns each, in their order
+    const int q = i / 64, c = i % 64 / 2, h = i & 1, col = (chunk * Q + q) * 32 + c;
+    f32x4 s = red[0][q][h][c];
 #pragma unroll
-    for (int w = 1; w < W; ++w) s += red[w][h][l];
-    if (c < nv) *(f32x4*)(dwr + ((size_t)e * nv + c) * 8 + h * 4) = s;
+    for (int w = 1; w < W; ++w) s += red[w][q][h][c];
+    if (col < nv) *(f32x4*)(o + (size_t)col * 8 + h * 4) = s;
   }
-  if (threadIdx.x == 0 && blockIdx.x == 0) {
+  if (threadIdx.x == 0 && chunk == 0) {
     float s = 0.0f;
     for (int w = 0; w < W; ++w) s += bred[w];
-    db[e] = s;
+    (it.slot >= 0 ? bsums[it.slot] : db[it.e]) = s;
+  }
+}
+
+// Adds the partial sums of experts that have several (in consecutive slots).
+__global__ __launch_bounds__(256) void k_route_sum(const Item* items, int H, const float* sums, const float* bsums, int slots,
+                                                  float* dwr, float* db) {
+  const Item it = items[blockIdx.x];
+  if (it.e < 0 || it.parts < 2) return;
+  const int m = min(it.parts, slots - it.slot), i = blockIdx.y * 256 + threadIdx.x;
+  if (m <= 0) return;
+  if (i < H / 4) {
+    const f32x4* p = (const f32x4*)(sums + (size_t)it.slot * H) + i;
+    f32x4 s = {0, 0, 0, 0};
+    for (int j = 0; j < m; j += 8) {
+      f32x4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = p[(size_t)min(j + k, m - 1) * (H / 4)];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (j + k < m) s += v[k];
+    }
+    *(f32x4*)(dwr + (size_t)it.e * H + i * 4) = s;
+  }
+  if (i == 0) {
+    float s = 0.0f;
+    for (int j = 0; j < m; ++j) s += bsums[it.slot + j];
+    db[it.e] = s;
   }
 }
 
@@ -309,17 +441,33 @@ constexpr int kSliceGroups = 512;  // workgroups of the slice kernels
 struct RoutePlan {
   bool gather;  // few slots: rows of Wr gathered
   int slices, ranges, range;
-  size_t dz, z, total;
+  int per_item, items, slots;  // of the weights' gradient (bounds)
+  size_t dz, z, item, sums, bsums, total;
 };
-RoutePlan route_plan(int T, int k, int E, int H) {
+RoutePlan route_plan(int T, int k, int E, int H, int rows) {
   RoutePlan p{};
   p.gather = (int64_t)T * k <= E;
   p.slices = ceil_div(H, E <= kWideSlice ? 64 : 32);
   p.ranges = std::max(1, std::min(kSliceGroups / p.slices, ceil_div(T, 32)));
   p.range = ceil_div(std::max(T, 1), p.ranges);
-  p.dz = 0;
-  p.z = round256(std::max<size_t>(4, (size_t)T * k * 4));
-  p.total = p.z + (p.gather ? 0 : round256((size_t)p.slices * T * k * 4));
+  // (a batch of few tokens leaves no expert many rows, unless tokens name it twice)
+  p.per_item = T <= kItemRows ? std::max(1, rows) : kItemRows;
+  p.items = E + rows / p.per_item;
+  p.slots = rows > p.per_item ? 2 * (rows / p.per_item) : 0;
+  size_t o = 0;
+  const auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += round256(bytes);
+    return at;
+  };
+  p.dz = take(std::max<size_t>(4, (size_t)T * k * 4));
+  if (!p.gather) {
+    p.z = take((size_t)p.slices * T * k * 4);
+    p.item = take((size_t)p.items * sizeof(Item));
+    p.sums = take((size_t)p.slots * H * 4);
+    p.bsums = take((size_t)p.slots * 4);
+  }
+  p.total = o;
   return p;
 }
 
@@ -333,7 +481,7 @@ extern "C" {
 
 size_t moe_route_backward_workspace_bytes(int32_t T, int32_t k, int32_t n_experts, int32_t H, int32_t rows) {
   if (check_shape(T, k, n_experts, H, rows) != MOE_OK) return 0;
-  return route_plan(T, k, n_experts, H).total;
+  return route_plan(T, k, n_experts, H, rows).total;
 }
 
 int moe_route_backward(const void* x, int32_t dtype, int32_t T, int32_t H, int32_t n_experts, int32_t k,
@@ -348,21 +496,24 @@ int moe_route_backward(const void* x, int32_t dtype, int32_t T, int32_t H, int32
     return MOE_E_INVAL;
   if (T && (bad(x, 16) || bad(dx, 16) || (add && !aligned_to(add, 16)) || bad(topk_idx, 4) || bad(dw, 4)))
     return MOE_E_INVAL;
-  const RoutePlan p = route_plan(T, k, n_experts, H);
+  const RoutePlan p = route_plan(T, k, n_experts, H, rows);
   if (ws_bytes < p.total) return MOE_E_WORKSPACE;
   const uint32_t per_k = k == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + k - 1) / k);
   const RouteArgs a{(const u32x4*)x, router_w, topk_idx, T, H, n_experts, k, per_k};
-  const int nv = H / 8, n = T * k;
+  const int n = T * k;
   float *dz = (float*)((char*)ws + p.dz), *z = (float*)((char*)ws + p.z);
   const hipStream_t s = (hipStream_t)stream;
   const u32x4* addv = (const u32x4*)add;
   u32x4* dxv = (u32x4*)dx;
-  const dim3 grid(p.slices, p.ranges), sums(ceil_div(nv, 64), n_experts);
+  const dim3 grid(p.slices, p.ranges);
+  Item* items = p.gather || T == 0 ? nullptr : (Item*)((char*)ws + p.item);
+  float *sums = (float*)((char*)ws + p.sums), *bsums = (float*)((char*)ws + p.bsums);
   const auto run = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     const auto slices = [&](auto dots, auto to_dx) {
       dots<<<grid, kThreads, 0, s>>>(a, p.range, z);
-      k_route_slots<<<ceil_div(T, 64 / k), kSlotThreads, 0, s>>>(a, p.slices, z, router_b, dw, dz);
+      k_route_slots<<<ceil_div(T, 64 / k) + 1, kSlotThreads, 0, s>>>(a, p.slices, z, router_b, dw, dz, offsets, rows, p.items,
+                                                                     p.per_item, items);
       to_dx<<<grid, kThreads, 0, s>>>(a, p.range, dz, addv, dxv);
     };
     if (T && p.gather) k_route_grad_tokens<DT><<<T, kThreads, 0, s>>>(a, router_b, dw, addv, dxv, dz);
@@ -370,8 +521,23 @@ int moe_route_backward(const void* x, int32_t dtype, int32_t T, int32_t H, int32
     else if (T && n_experts <= 256) slices(k_route_dots<DT, 256, 64>, k_route_dx<DT, 256, 64>);
     else if (T && n_experts <= kWideSlice) slices(k_route_dots<DT, kWideSlice, 64>, k_route_dx<DT, kWideSlice, 64>);
     else if (T) slices(k_route_dots<DT, kMaxExperts, 32>, k_route_dx<DT, kMaxExperts, 32>);
-    k_route_weights<DT><<<sums, kSumThreads, 0, s>>>((const u32x4*)x, nv, n_experts, k, per_k, dz, offsets, pairs, rows, n,
-                                                    d_router_w, d_router_b);
+    const auto weights = [&](auto kernel, int W, int Q) {
+      const int chunks = ceil_div(H, 256 * Q);
+      kernel<<<(items ? p.items : n_experts) * chunks, W * kWave, 0, s>>>((const u32x4*)x, H / 8, n_experts, per_k, dz, offsets,
+                                                                        pairs, rows, n, items, chunks, d_router_w, d_router_b,
+                                                                        sums, bsums, items ? p.slots : 0);
+    };
+    // An eighth of the width per workgroup where that is 256 to 768 columns; two
+    // wavefronts and 128 rows at most: 2,048 tokens, top-8 of 256, 6144 wide, a
+    // skewed router: 20 us (64 rows: 19, but twice the partial sums; 256: 26; one
+    // wavefront 24, eight and 512 rows 32).
+    const int runs = ceil_div(H, 8 * 256);
+    if (runs == 1) weights(k_route_weights<DT, 2, 1>, 2, 1);
+    else if (runs == 2) weights(k_route_weights<DT, 2, 2>, 2, 2);
+    else weights(k_route_weights<DT, 2, 3>, 2, 3);
+    if (items && p.slots)
+      k_route_sum<<<dim3(p.items, ceil_div(H, 1024)), 256, 0, s>>>(items, H, sums, bsums, p.slots, d_router_w,
+                                                                  d_router_b);
   };
   if (dtype == MOE_T_F16) run(std::integral_constant<int, MOE_T_F16>{});
   else run(std::integral_constant<int, MOE_T_BF16>{});
