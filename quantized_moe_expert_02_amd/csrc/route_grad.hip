@@ -27,77 +27,95 @@ struct RouteArgs {
   const float* wr;
   const int32_t* idx;
   int T, H, E, k;
-  uint32_t per_k;  // ceil(2^32 / k): p / k by multiplication (exact for p < 2^27, k <= 32), 0 for k = 1
 };
 
-__device__ __forceinline__ int token_of(const RouteArgs& a, int p) {
-  return a.per_k ? (int)__umulhi((uint32_t)p, a.per_k) : p;
-}
-
-// All experts' columns [c0, c0 + CW) of Wr into LDS rows of CW + 4 floats;
-// columns past H are zero.
+// All experts' columns [c0, c0 + CW) of Wr into LDS rows; columns past H are
+// zero, and so is one row more, which dropped slots read.
 template <int CW>
 __device__ __forceinline__ void load_slice(const RouteArgs& a, int c0, float* w) {
-  constexpr int V = CW / 4;
-  for (int i = threadIdx.x; i < a.E * V; i += kThreads) {
-    const int e = i / V, c = i % V * 4;
-    f32x4 v = {0, 0, 0, 0};
-    if (c0 + c < a.H) v = *(const f32x4*)(a.wr + (size_t)e * a.H + c0 + c);
-    *(f32x4*)(w + e * (CW + 4) + c) = v;
+  constexpr int V = CW / 4, U = 9;  // loads in flight (all of them for 256 experts)
+  const int n = (a.E + 1) * V;
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+    f32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads, e = min(i / V, a.E - 1), c = c0 + i % V * 4;
+      v[u] = *(const f32x4*)(a.wr + (size_t)e * a.H + (c < a.H ? c : 0));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= a.E * V || c0 + i % V * 4 >= a.H) v[u] = f32x4{0, 0, 0, 0};
+      if (i < n) *(f32x4*)(w + i * 4) = v[u];
+    }
   }
 }
 
-// Lanes that share a row of a slice, 8 columns each, and rows per wavefront.
+// A row of a slice is shared by CW / 8 lanes, 8 columns each.  A lane reads its
+// 8 as two 16-byte halves, and lanes of odd rows take the second half first:
+// two neighbouring rows then cover different LDS banks, whichever experts they
+// are.
 template <int CW>
 constexpr int kLanes = CW / 8;
 
-// Partial logits [slices][T k]: a group of CW / 8 lanes per slot, 64 slots per
-// turn of a wavefront.
+// The slots of the token that a lane group works on, L at a time, one per lane:
+// the experts' places in LDS.
+template <int CW>
+__device__ __forceinline__ int slot_place(const RouteArgs& a, int t, int j) {
+  int e = a.idx[min(min(t, a.T - 1) * a.k + j, a.T * a.k - 1)];
+  if (j >= a.k || (unsigned)e >= (unsigned)a.E) e = a.E;
+  return e * CW;
+}
+
+// Partial logits [slices][T k], 64 / L tokens per turn of a wavefront.
 template <int DT, int EC, int CW>
 __global__ __launch_bounds__(kThreads) void k_route_dots(RouteArgs a, int range, float* zpart) {
-  __shared__ __align__(16) float w[EC * (CW + 4)];  // E <= EC
-  constexpr int L = kLanes<CW>, P = 64 / L;  // lanes per slot, slots per step
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / L, cl = lane % L;
-  const int c0 = blockIdx.x * CW, nv = a.H / 8, cv = min(c0 / 8 + cl, nv - 1);
-  const int n = a.T * a.k, p1 = min((int)(blockIdx.y + 1) * range * a.k, n);
-  float* out = zpart + (size_t)blockIdx.x * n;
-  u32x4 next[L];
-  int en = 0;
-  const auto fetch = [&](int base) {
-    en = a.idx[min(base + lane, n - 1)];
-#pragma unroll
-    for (int s = 0; s < L; ++s) next[s] = a.x[(size_t)token_of(a, min(base + s * P + sub, n - 1)) * nv + cv];
-  };
-  const int first = blockIdx.y * range * a.k + wave * 64;
-  if (first < p1) fetch(first);
+  __shared__ __align__(16) float w[(EC + 1) * CW];  // E <= EC
+  constexpr int L = kLanes<CW>, P = 64 / L;  // lanes per token, tokens per turn
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / L, cl = lane % L, odd = sub & 1;
+  const int c0 = blockIdx.x * CW, nv = a.H / 8, cv = c0 / 8 + cl;
+  const int n = a.T * a.k, t1 = min((int)(blockIdx.y + 1) * range, a.T), first = blockIdx.y * range + wave * P;
+  u32x4 xn = {0, 0, 0, 0};
+  int pn = 0;
+  const auto fetch_x = [&](int base) { xn = a.x[(size_t)min(base + sub, a.T - 1) * nv + min(cv, nv - 1)]; };
+  if (first < t1) {
+    fetch_x(first);
+    pn = slot_place<CW>(a, first + sub, cl);
+  }
   load_slice<CW>(a, c0, w);
   __syncthreads();
-  for (int base = first; base < p1; base += kWaves * 64) {
-    const int e = (unsigned)en < (unsigned)a.E ? en : 0;  // dropped: the sum is not used
-    u32x4 xv[L];
-#pragma unroll
-    for (int s = 0; s < L; ++s) xv[s] = next[s];
-    if (base + kWaves * 64 < p1) fetch(base + kWaves * 64);
-    float mine = 0.0f;
-#pragma unroll
-    for (int s = 0; s < L; ++s) {
-      const float* r = w + __shfl(e, s * P + sub) * (CW + 4) + cl * 8;
-      const f32x4 lo = *(const f32x4*)r, hi = *(const f32x4*)(r + 4);
-      if (c0 + CW > a.H && c0 / 8 + cl >= nv) xv[s] = u32x4{0, 0, 0, 0};  // past the last column
-      float f[8];
-      unpack_vec<DT>(xv[s], f);
-      float z = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) z = fmaf(f[c], lo[c], z);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) z = fmaf(f[4 + c], hi[c], z);
-      z += __builtin_bit_cast(float, partner<1>(__builtin_bit_cast(int, z)));
-      z += __builtin_bit_cast(float, partner<2>(__builtin_bit_cast(int, z)));
-      if (L == 8) z += __builtin_bit_cast(float, partner<4>(__builtin_bit_cast(int, z)));
-      if (cl == s) mine = z;  // slot base + s P + sub
+  const float *wa = w + cl * 8 + odd * 4, *wb = w + cl * 8 + 4 - odd * 4;
+  float* out = zpart + (size_t)blockIdx.x * n;
+  for (int base = first; base < t1; base += kWaves * P) {
+    const int t = base + sub;
+    float f[8];
+    {
+      u32x4 x = cv < nv ? xn : u32x4{0, 0, 0, 0};
+      if (odd) x = u32x4{x[2], x[3], x[0], x[1]};
+      unpack_vec<DT>(x, f);
     }
-    const int p = base + cl * P + sub;
-    if (p < p1) out[p] = mine;
+    if (base + kWaves * P < t1) fetch_x(base + kWaves * P);
+    for (int j0 = 0; j0 < a.k; j0 += L) {
+      const int place = pn;
+      if (j0 + L < a.k) pn = slot_place<CW>(a, t, j0 + L + cl);
+      else if (base + kWaves * P < t1) pn = slot_place<CW>(a, t + kWaves * P, cl);
+      float mine = 0.0f;
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        const int at = __shfl(place, sub * L + j);
+        const f32x4 r0 = *(const f32x4*)(wa + at), r1 = *(const f32x4*)(wb + at);
+        float z = f[0] * r0[0];
+#pragma unroll
+        for (int c = 1; c < 4; ++c) z = fmaf(f[c], r0[c], z);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z = fmaf(f[4 + c], r1[c], z);
+        z += __builtin_bit_cast(float, partner<1>(__builtin_bit_cast(int, z)));
+        z += __builtin_bit_cast(float, partner<2>(__builtin_bit_cast(int, z)));
+        if (L == 8) z += __builtin_bit_cast(float, partner<4>(__builtin_bit_cast(int, z)));
+        if (cl == j) mine = z;
+      }
+      if (t < t1 && j0 + cl < a.k) out[(size_t)t * a.k + j0 + cl] = mine;
+    }
   }
 }
 
@@ -190,49 +208,57 @@ __global__ __launch_bounds__(kSlotThreads) void k_route_slots(RouteArgs a, int s
   if (l < np) dz[p] = ok ? w * (1.0f / (1.0f + expf(z))) * (g - m) : 0.0f;
 }
 
-// dx[t] = add[t] + sum_j dz_j Wr[e_j], 64 columns of 8 tokens (32 of 16) per
-// turn of a wavefront.
+// dx[t] = add[t] + sum_j dz_j Wr[e_j], as k_route_dots.
 template <int DT, int EC, int CW>
 __global__ __launch_bounds__(kThreads) void k_route_dx(RouteArgs a, int range, const float* dz, const u32x4* add, u32x4* dx) {
-  __shared__ __align__(16) float w[EC * (CW + 4)];  // E <= EC
+  __shared__ __align__(16) float w[(EC + 1) * CW];
   constexpr int L = kLanes<CW>, P = 64 / L;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / L, cl = lane % L;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / L, cl = lane % L, odd = sub & 1;
   const int c0 = blockIdx.x * CW, nv = a.H / 8, cv = c0 / 8 + cl;
-  const int n = a.T * a.k, t1 = min((int)(blockIdx.y + 1) * range, a.T), cc = min(cv, nv - 1);
-  int en = -1;  // the next L slots of this lane's token: one per lane
+  const int n = a.T * a.k, t1 = min((int)(blockIdx.y + 1) * range, a.T), first = blockIdx.y * range + wave * P;
+  u32x4 an = {0, 0, 0, 0};
+  int pn = 0;
   float dn = 0.0f;
-  const auto fetch = [&](int base, int j0) {
-    const int p = min(min(base + sub, a.T - 1) * a.k + j0 + cl, n - 1);
-    en = a.idx[p];
-    dn = dz[p];
-    if (j0 + cl >= a.k || (unsigned)en >= (unsigned)a.E) en = -1;
+  const auto fetch_add = [&](int base) { an = add[(size_t)min(base + sub, a.T - 1) * nv + min(cv, nv - 1)]; };
+  const auto fetch = [&](int t, int j) {
+    pn = slot_place<CW>(a, t, j);
+    dn = dz[min(min(t, a.T - 1) * a.k + j, n - 1)];
+    if (j >= a.k) dn = 0.0f;
   };
-  const int first = blockIdx.y * range + wave * P;
-  if (first < t1) fetch(first, 0);
+  if (first < t1) {
+    if (add) fetch_add(first);
+    fetch(first + sub, cl);
+  }
   load_slice<CW>(a, c0, w);
   __syncthreads();
+  const float *wa = w + cl * 8 + odd * 4, *wb = w + cl * 8 + 4 - odd * 4;
   for (int base = first; base < t1; base += kWaves * P) {
     const int t = base + sub;
-    float acc[8] = {};
-    if (add) unpack_vec<DT>(add[(size_t)min(t, a.T - 1) * nv + cc], acc);
+    float acc[8];
+    unpack_vec<DT>(an, acc);
+    if (add && base + kWaves * P < t1) fetch_add(base + kWaves * P);
+    f32x4 s0 = {0, 0, 0, 0}, s1 = s0;
     for (int j0 = 0; j0 < a.k; j0 += L) {
-      const int e = en;
+      const int place = pn;
       const float d = dn;
-      if (j0 + L < a.k) fetch(base, j0 + L);
-      else if (base + kWaves * P < t1) fetch(base + kWaves * P, 0);
+      if (j0 + L < a.k) fetch(t, j0 + L + cl);
+      else if (base + kWaves * P < t1) fetch(t + kWaves * P, cl);
 #pragma unroll
       for (int j = 0; j < L; ++j) {
-        const int ej = __shfl(e, sub * L + j);
+        const int at = __shfl(place, sub * L + j);
         const float dj = __shfl(d, sub * L + j);
-        const float* r = w + max(ej, 0) * (CW + 4) + cl * 8;
-        f32x4 lo = *(const f32x4*)r, hi = *(const f32x4*)(r + 4);
-        if (ej < 0) lo = hi = f32x4{0, 0, 0, 0};  // (dz is 0 for dropped slots)
+        const f32x4 r0 = *(const f32x4*)(wa + at), r1 = *(const f32x4*)(wb + at);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          acc[c] = fmaf(dj, lo[c], acc[c]);
-          acc[4 + c] = fmaf(dj, hi[c], acc[4 + c]);
+          s0[c] = fmaf(dj, r0[c], s0[c]);
+          s1[c] = fmaf(dj, r1[c], s1[c]);
         }
       }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      acc[c] += odd ? s1[c] : s0[c];
+      acc[4 + c] += odd ? s0[c] : s1[c];
     }
     if (t < t1 && cv < nv) dx[(size_t)t * nv + cv] = pack_vec<DT>(acc);
   }
@@ -498,8 +524,9 @@ int moe_route_backward(const void* x, int32_t dtype, int32_t T, int32_t H, int32
     return MOE_E_INVAL;
   const RoutePlan p = route_plan(T, k, n_experts, H, rows);
   if (ws_bytes < p.total) return MOE_E_WORKSPACE;
+  // p / k by multiplication with ceil(2^32 / k): exact for p < 2^27, k <= 32; 0 for k = 1
   const uint32_t per_k = k == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + k - 1) / k);
-  const RouteArgs a{(const u32x4*)x, router_w, topk_idx, T, H, n_experts, k, per_k};
+  const RouteArgs a{(const u32x4*)x, router_w, topk_idx, T, H, n_experts, k};
   const int n = T * k;
   float *dz = (float*)((char*)ws + p.dz), *z = (float*)((char*)ws + p.z);
   const hipStream_t s = (hipStream_t)stream;
