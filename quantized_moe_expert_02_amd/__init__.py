@@ -120,7 +120,7 @@ def lib():
         L.moe_tier_sync.argtypes = [P, P]
         L.moe_tier_sync.restype = ctypes.c_int
         i64 = ctypes.c_int64
-        A = ctypes.POINTER(MoeAdapters)
+        A = P  # const moe_adapters_t*: a MoeAdapters by reference, or its bytes
         L.moe_sort_rows.argtypes = [i32, i32, i32, i32]
         L.moe_sort_rows.restype = i64
         L.moe_sort_workspace_bytes.argtypes = [i32, i32, i32]

@@ -3,13 +3,16 @@ a shared projection, forward and backward.  Checks and marshalling only, as in
 dispatch.py; x, dy, add and out may be row-strided views (last stride 1)."""
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import Optional
 
 import torch
 
-from . import MoeAdapters, lib
+from . import lib
 from .dispatch import _F32, _I32, _check, _ptr, _rows_dtype, _run
+
+
+_ADAPTERS = struct.Struct("@PPPPiiiii").pack
 
 
 def _check_rows(name, t, dtype, shape, dev):
@@ -38,9 +41,10 @@ def _adapters(x, a, b, scale, ranks, ids, order):
         off, pairs = order["offsets"], order["pairs"]
         _check("order: offsets", off, _I32, (n + 1,), dev)
         _check("order: pairs", pairs, _I32, (T,), dev)
-    d = MoeAdapters(a.data_ptr(), b.data_ptr(), scale.data_ptr(), _ptr(ranks), n, K, N, R, code)
-    ws = torch.empty(lib().moe_adapter_workspace_bytes(ctypes.byref(d), T), dtype=torch.uint8, device=dev)
-    return d, dev, T, off, pairs, ws
+    # a moe_adapters_t
+    d = _ADAPTERS(a.data_ptr(), b.data_ptr(), scale.data_ptr(), 0 if ranks is None else ranks.data_ptr(), n, K, N, R, code)
+    ws = torch.empty(lib().moe_adapter_workspace_bytes(d, T), dtype=torch.uint8, device=dev)
+    return d, dev, T, n, K, N, R, off, pairs, ws
 
 
 def moe_adapter_forward(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, scale: torch.Tensor,
@@ -51,18 +55,18 @@ def moe_adapter_forward(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: 
     ranks int32 [n]: each adapter's rank where below R; add [T][N] (may be
     `out`); order: moe_sort(ids[:, None], n) where the caller has it.
     save_u: returns (y, u) with u = a[i] @ x[t] fp32 [T][R] for the backward."""
-    d, dev, T, off, pairs, ws = _adapters(x, a, b, scale, ranks, ids, order)
-    ldx = _check_rows("x", x, x.dtype, (T, d.K), dev)
-    ldadd = 0 if add is None else _check_rows("add", add, x.dtype, (T, d.N), dev)
+    d, dev, T, n, K, N, R, off, pairs, ws = _adapters(x, a, b, scale, ranks, ids, order)
+    ldx = _check_rows("x", x, x.dtype, (T, K), dev)
+    ldadd = 0 if add is None else _check_rows("add", add, x.dtype, (T, N), dev)
     made = [ws]
     if out is None:
-        out = torch.empty((T, d.N), dtype=x.dtype, device=dev)
+        out = torch.empty((T, N), dtype=x.dtype, device=dev)
         made.append(out)
-    ldy = _check_rows("out", out, x.dtype, (T, d.N), dev)
-    u = torch.empty((T, d.R), dtype=_F32, device=dev) if save_u else None
+    ldy = _check_rows("out", out, x.dtype, (T, N), dev)
+    u = torch.empty((T, R), dtype=_F32, device=dev) if save_u else None
     if save_u:
         made.append(u)
-    _run(lib().moe_adapter_forward, dev, stream, made, ctypes.byref(d), x.data_ptr(), ldx, T, ids.data_ptr(),
+    _run(lib().moe_adapter_forward, dev, stream, made, d, x.data_ptr(), ldx, T, ids.data_ptr(),
          _ptr(off), _ptr(pairs), _ptr(add), ldadd, out.data_ptr(), ldy, _ptr(u), ws.data_ptr(), ws.numel())
     return (out, u) if save_u else out
 
@@ -72,17 +76,17 @@ def moe_adapter_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, a: 
                          add: Optional[torch.Tensor] = None, order=None, need_dx: bool = True, stream=None):
     """(dx [T][K] or None, da fp32 [n][R][K], db fp32 [n][N][R]) for dy [T][N];
     u from the forward call; add [T][K] is added to dx."""
-    d, dev, T, off, pairs, ws = _adapters(x, a, b, scale, ranks, ids, order)
-    ldx = _check_rows("x", x, x.dtype, (T, d.K), dev)
-    lddy = _check_rows("dy", dy, x.dtype, (T, d.N), dev)
-    _check("u", u, _F32, (T, d.R), dev)
-    ldadd = 0 if add is None else _check_rows("add", add, x.dtype, (T, d.K), dev)
+    d, dev, T, n, K, N, R, off, pairs, ws = _adapters(x, a, b, scale, ranks, ids, order)
+    ldx = _check_rows("x", x, x.dtype, (T, K), dev)
+    lddy = _check_rows("dy", dy, x.dtype, (T, N), dev)
+    _check("u", u, _F32, (T, R), dev)
+    ldadd = 0 if add is None else _check_rows("add", add, x.dtype, (T, K), dev)
     if add is not None and not need_dx:
         raise ValueError("add: there is no dx to add it to")
-    dx = torch.empty((T, d.K), dtype=x.dtype, device=dev) if need_dx else None
-    da = torch.empty((d.n, d.R, d.K), dtype=_F32, device=dev)
-    db = torch.empty((d.n, d.N, d.R), dtype=_F32, device=dev)
-    _run(lib().moe_adapter_backward, dev, stream, [ws, da, db] + ([dx] if need_dx else []), ctypes.byref(d),
+    dx = torch.empty((T, K), dtype=x.dtype, device=dev) if need_dx else None
+    da = torch.empty((n, R, K), dtype=_F32, device=dev)
+    db = torch.empty((n, N, R), dtype=_F32, device=dev)
+    _run(lib().moe_adapter_backward, dev, stream, [ws, da, db] + ([dx] if need_dx else []), d,
          dy.data_ptr(), lddy, x.data_ptr(), ldx, u.data_ptr(), T, ids.data_ptr(), _ptr(off), _ptr(pairs), _ptr(add),
-         ldadd, _ptr(dx), d.K, da.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel())
+         ldadd, _ptr(dx), K, da.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel())
     return dx, da, db

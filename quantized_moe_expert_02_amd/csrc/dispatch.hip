@@ -161,9 +161,99 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx,
   }
 }
 
+// Sort and rows of a small batch in one launch (align 1, up to kSmallSlots
+// slots): every workgroup sorts all slots for itself, then lays out its part of
+// one token's row; the first one also writes the order.
+constexpr int kSmallSlots = 1024;
+constexpr int kRowThreads = 256;
+
+__global__ __launch_bounds__(kRowThreads) void k_dispatch_small(const u32x4* x, int T, int nv, const int32_t* idx, int k,
+                                                                int E, int bits, u32x4* xs, int32_t* offsets,
+                                                                int32_t* pairs, int32_t* pos) {
+  constexpr int W = kRowThreads / kWave, C = kSmallSlots / kRowThreads;
+  __shared__ uint16_t wc[C * W][kMaxExperts];  // slots of each expert in each 64 slots, then those before
+  __shared__ int start[kMaxExperts + 1], wsum[W], place[kSmallSlots];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = T * k, t = blockIdx.x;
+  const int i = blockIdx.y * kRowThreads + tid;
+  u32x4 v = {0, 0, 0, 0};
+  if (i < nv) v = x[(size_t)t * nv + i];
+  int ids[C], ranks[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) ids[c] = c * kRowThreads + tid < n ? idx[c * kRowThreads + tid] : -1;
+  const int chunks = (n + 63) / 64;
+  for (int c = tid; c < chunks * E; c += kRowThreads) wc[c / E][c % E] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c * kRowThreads >= n) break;
+    const bool ok = (unsigned)ids[c] < (unsigned)E;
+    const uint64_t m = match_id(ids[c], ok, bits);
+    ranks[c] = lanes_below(m);
+    if (ok && ranks[c] == 0) wc[c * W + wave][ids[c]] = (uint16_t)__popcll(m);
+  }
+  __syncthreads();
+  const int per = (E + kRowThreads - 1) / kRowThreads;  // experts of this thread
+  int total[kMaxExperts / kRowThreads], mine = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxExperts / kRowThreads; ++q) {
+    total[q] = 0;
+    const int e = tid * per + q;
+    if (q < per && e < E)
+      for (int c = 0; c < chunks; ++c) {
+        const int s = wc[c][e];
+        wc[c][e] = (uint16_t)total[q];
+        total[q] += s;
+      }
+    mine += total[q];
+  }
+  int incl = mine;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    incl += lane >= d ? o : 0;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int at = incl - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    at += w < wave ? wsum[w] : 0;
+    all += wsum[w];
+  }
+#pragma unroll
+  for (int q = 0; q < kMaxExperts / kRowThreads; ++q) {
+    const int e = tid * per + q;
+    if (q < per && e < E) start[e] = at;
+    at += total[q];
+  }
+  if (tid == 0) start[E] = all;
+  __syncthreads();
+  const bool writes = blockIdx.x == 0 && blockIdx.y == 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int s = c * kRowThreads + tid;
+    if (s >= n) continue;
+    const bool ok = (unsigned)ids[c] < (unsigned)E;
+    const int r = ok ? start[ids[c]] + wc[c * W + wave][ids[c]] + ranks[c] : -1;
+    place[s] = r;
+    if (writes) {
+      pos[s] = r;
+      if (ok) pairs[r] = s;
+      if (s >= all) pairs[s] = -1;
+    }
+  }
+  if (writes)
+    for (int e = tid; e <= E; e += kRowThreads) offsets[e] = start[e];
+  __syncthreads();
+  if (i >= nv) return;
+  for (int j = 0; j < k; ++j) {
+    const int r = place[t * k + j];
+    if (r >= 0) xs[(size_t)r * nv + i] = v;
+  }
+  for (int r = all + t; r < n; r += T) xs[(size_t)r * nv + i] = u32x4{0, 0, 0, 0};
+}
+
 // xs[pos(t,j)] = x[t], token by token, 16-byte vectors; workgroups past the
 // tokens' zero the rows that hold no slot.
-constexpr int kRowThreads = 256;
 constexpr int kPadRows = 64;  // rows looked over by one zeroing workgroup
 
 __device__ __forceinline__ void zero_pad_rows(const int32_t* pairs, int rows, int part, u32x4* out, int nv) {
@@ -335,10 +425,16 @@ int moe_dispatch(const void* x, int32_t dtype, int32_t T, int32_t H, const int32
   st = check_sort_shape(T, k, n_experts, align);
   if (st != MOE_OK) return st;
   if (T && (bad(x, 16) || bad(xs, 16))) return MOE_E_INVAL;
+  const int nv = (int)((size_t)H * elem_bytes(dtype) / 16), n = T * k;
+  if (T && align == 1 && n <= kSmallSlots) {
+    if (bad(offsets, 4) || bad(topk_idx, 4) || bad(pairs, 4) || bad(pos, 4)) return MOE_E_INVAL;
+    k_dispatch_small<<<dim3(T, (nv + kRowThreads - 1) / kRowThreads), kRowThreads, 0, (hipStream_t)stream>>>(
+        (const u32x4*)x, T, nv, topk_idx, k, n_experts, id_bits(n_experts), (u32x4*)xs, offsets, pairs, pos);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+  }
   st = moe_sort(topk_idx, T, k, n_experts, align, offsets, pairs, pos, ws, ws_bytes, stream);
   if (st != MOE_OK || T == 0) return st;
   const int rows = (int)moe_sort_rows(T, k, n_experts, align);
-  const int nv = (int)((size_t)H * elem_bytes(dtype) / 16);
   k_scatter_rows<<<T + (rows + kPadRows - 1) / kPadRows, kRowThreads, 0, (hipStream_t)stream>>>(
       (const u32x4*)x, T, nv, k, rows, pos, pairs, (u32x4*)xs);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;

@@ -38,20 +38,27 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# The raw handle and device index, without the objects that torch.cuda wraps
+# around them: a small call's time is mostly its host side.
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _run(fn, dev, stream, made, *args):
     """Calls a C entry point on `dev` and `stream`; `made` are the tensors
     allocated here, kept from reuse until that stream has passed the call."""
-    if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if handle != torch.cuda.current_stream(dev).cuda_stream:
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
+    index = dev.index
+    handle = _current_stream(index)
+    if stream is not None:
+        given = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if given != handle:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(given, device=dev)
             s.wait_stream(torch.cuda.current_stream(dev))  # the allocator may hand out memory still in use there
             for t in made:
                 if t is not None:
                     t.record_stream(s)
-    if dev.index == torch.cuda.current_device():
+            handle = given
+    if index == _current_device():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):

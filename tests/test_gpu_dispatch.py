@@ -111,7 +111,8 @@ def test_sort_any_index(T, k, E):
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("T,k,E,align,drop,H", [
     (0, 2, 8, 1, 0.0, 64), (1, 8, 256, 1, 0.0, 6144), (1, 1, 1, 1, 1.0, 8), (7, 3, 5, 8, 0.3, 24), (33, 8, 40, 1, 0.0, 2056),
-    (129, 8, 64, 16, 0.2, 264), (700, 6, 100, 1, 0.1, 520), (41, 32, 33, 64, 0.5, 40)])
+    (129, 8, 64, 16, 0.2, 264), (700, 6, 100, 1, 0.1, 520), (41, 32, 33, 64, 0.5, 40), (128, 8, 1024, 1, 0.2, 72),
+    (1024, 1, 300, 1, 0.0, 8), (341, 3, 3, 1, 0.9, 4104)])
 def test_dispatch_and_gradient(dtype, T, k, E, align, drop, H):
     _log("dispatch", dtype, T, k, E, align, drop, H)
     idx = make_idx(T, k, E, drop, 2000 + T)
