@@ -60,10 +60,10 @@ def moe_adapter_forward(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: 
     ldadd = 0 if add is None else _check_rows("add", add, x.dtype, (T, N), dev)
     made = [ws]
     if out is None:
-        out = torch.empty((T, N), dtype=x.dtype, device=dev)
+        out = x.new_empty((T, N))
         made.append(out)
     ldy = _check_rows("out", out, x.dtype, (T, N), dev)
-    u = torch.empty((T, R), dtype=_F32, device=dev) if save_u else None
+    u = scale.new_empty((T, R)) if save_u else None
     if save_u:
         made.append(u)
     _run(lib().moe_adapter_forward, dev, stream, made, d, x.data_ptr(), ldx, T, ids.data_ptr(),
@@ -83,9 +83,9 @@ def moe_adapter_backward(dy: torch.Tensor, x: torch.Tensor, u: torch.Tensor, a: 
     ldadd = 0 if add is None else _check_rows("add", add, x.dtype, (T, K), dev)
     if add is not None and not need_dx:
         raise ValueError("add: there is no dx to add it to")
-    dx = torch.empty((T, K), dtype=x.dtype, device=dev) if need_dx else None
-    da = torch.empty((n, R, K), dtype=_F32, device=dev)
-    db = torch.empty((n, N, R), dtype=_F32, device=dev)
+    dx = x.new_empty((T, K)) if need_dx else None
+    da = scale.new_empty((n, R, K))
+    db = scale.new_empty((n, N, R))
     _run(lib().moe_adapter_backward, dev, stream, [ws, da, db] + ([dx] if need_dx else []), d,
          dy.data_ptr(), lddy, x.data_ptr(), ldx, u.data_ptr(), T, ids.data_ptr(), _ptr(off), _ptr(pairs), _ptr(add),
          ldadd, _ptr(dx), K, da.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel())

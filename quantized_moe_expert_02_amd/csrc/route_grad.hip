@@ -264,30 +264,43 @@ __global__ __launch_bounds__(kThreads) void k_route_dx(RouteArgs a, int range, c
   }
 }
 
-// The same three steps for few slots, whose rows of Wr are gathered directly:
-// one workgroup per token.
+// The same three steps for few tokens, whose rows of Wr are gathered directly:
+// one workgroup per token, a wavefront per slot and then a thread per 8 columns.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_route_grad_tokens(RouteArgs a, const float* br, const float* dw, const u32x4* add,
                                                                 u32x4* dx, float* dz_out) {
+  constexpr int U = 4;  // vectors, or slots, in flight
   __shared__ float z[kMaxTopK], dz[kMaxTopK];
   __shared__ int ex[kMaxTopK];
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, k = a.k, nv = a.H / 8;
   const u32x4* xt = a.x + (size_t)t * nv;
+  const f32x4* w4 = (const f32x4*)a.wr;
   for (int j = wave; j < k; j += kWaves) {
     const int e = a.idx[(size_t)t * k + j];
     const bool ok = (unsigned)e < (unsigned)a.E;
+    const f32x4* r = w4 + (size_t)(ok ? e : 0) * nv * 2;
     float s = 0.0f;
-    if (ok)
-      for (int i = lane; i < nv; i += 64) {
-        float f[8];
-        unpack_vec<DT>(xt[i], f);
-        const f32x4* r = (const f32x4*)(a.wr + ((size_t)e * nv + i) * 8);
-        const f32x4 lo = r[0], hi = r[1];
+    for (int i0 = lane; i0 < nv; i0 += 64 * U) {
+      u32x4 x[U];
+      f32x4 lo[U], hi[U];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s = fmaf(f[c], lo[c], s);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s = fmaf(f[4 + c], hi[c], s);
+      for (int u = 0; u < U; ++u) {
+        const int i = min(i0 + 64 * u, nv - 1);
+        x[u] = xt[i];
+        lo[u] = r[i * 2];
+        hi[u] = r[i * 2 + 1];
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + 64 * u >= nv) continue;
+        float f[8];
+        unpack_vec<DT>(x[u], f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s = fmaf(f[c], lo[u][c], s);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s = fmaf(f[4 + c], hi[u][c], s);
+      }
+    }
     s = wave_sum_f32(s);
     if (lane == 0) {
       ex[j] = ok ? e : -1;
@@ -313,15 +326,23 @@ __global__ __launch_bounds__(kThreads) void k_route_grad_tokens(RouteArgs a, con
   for (int i = tid; i < nv; i += kThreads) {
     float acc[8] = {};
     if (add) unpack_vec<DT>(add[(size_t)t * nv + i], acc);
-    for (int j = 0; j < k; ++j) {
-      if (ex[j] < 0) continue;
-      const f32x4* r = (const f32x4*)(a.wr + ((size_t)ex[j] * nv + i) * 8);
-      const f32x4 lo = r[0], hi = r[1];
-      const float d = dz[j];
+    for (int j0 = 0; j0 < k; j0 += U) {
+      f32x4 lo[U], hi[U];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        acc[c] = fmaf(d, lo[c], acc[c]);
-        acc[4 + c] = fmaf(d, hi[c], acc[4 + c]);
+      for (int u = 0; u < U; ++u) {
+        const f32x4* r = w4 + ((size_t)max(ex[min(j0 + u, k - 1)], 0) * nv + i) * 2;
+        lo[u] = r[0];
+        hi[u] = r[1];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j0 + u >= k || ex[j0 + u] < 0) continue;
+        const float d = dz[j0 + u];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[c] = fmaf(d, lo[u][c], acc[c]);
+          acc[4 + c] = fmaf(d, hi[u][c], acc[4 + c]);
+        }
       }
     }
     dx[(size_t)t * nv + i] = pack_vec<DT>(acc);
@@ -462,17 +483,18 @@ int check_shape(int32_t T, int32_t k, int32_t E, int32_t H, int32_t rows) {
 }
 
 constexpr int kWideSlice = 512;    // experts up to which a slice has 64 columns
+constexpr int kGatherTokens = 256;  // tokens up to which rows of Wr are gathered
 constexpr int kSliceGroups = 512;  // workgroups of the slice kernels
 
 struct RoutePlan {
-  bool gather;  // few slots: rows of Wr gathered
+  bool gather;  // few tokens: rows of Wr gathered
   int slices, ranges, range;
   int per_item, items, slots;  // of the weights' gradient (bounds)
   size_t dz, z, item, sums, bsums, total;
 };
 RoutePlan route_plan(int T, int k, int E, int H, int rows) {
   RoutePlan p{};
-  p.gather = (int64_t)T * k <= E;
+  p.gather = T <= kGatherTokens;
   p.slices = ceil_div(H, E <= kWideSlice ? 64 : 32);
   p.ranges = std::max(1, std::min(kSliceGroups / p.slices, ceil_div(T, 32)));
   p.range = ceil_div(std::max(T, 1), p.ranges);

@@ -83,9 +83,7 @@ def _sort_buffers(topk_idx, n_experts, align):
     dev = topk_idx.device
     _check("topk_idx", topk_idx, _I32, (T, k), dev)
     rows = moe_sort_rows(T, k, n_experts, align)
-    offsets = torch.empty(n_experts + 1, dtype=_I32, device=dev)
-    pairs = torch.empty(rows, dtype=_I32, device=dev)
-    pos = torch.empty((T, k), dtype=_I32, device=dev)
+    offsets, pairs, pos = topk_idx.new_empty(n_experts + 1), topk_idx.new_empty(rows), torch.empty_like(topk_idx)
     need = lib().moe_sort_workspace_bytes(T, k, n_experts)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     return T, k, dev, rows, offsets, pairs, pos, ws
@@ -107,7 +105,7 @@ def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, n_experts: int, align:
     T, k, dev, rows, offsets, pairs, pos, ws = _sort_buffers(topk_idx, n_experts, align)
     H = x.shape[1]
     _check("x", x, x.dtype, (T, H), dev)
-    xs = torch.empty((rows, H), dtype=x.dtype, device=dev)
+    xs = x.new_empty((rows, H))
     _run(lib().moe_dispatch, dev, stream, (xs, offsets, pairs, pos, ws), x.data_ptr(), code, T, H,
          topk_idx.data_ptr(), k, n_experts, align, xs.data_ptr(), offsets.data_ptr(), pairs.data_ptr(),
          pos.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
@@ -126,7 +124,7 @@ def _gather_args(name, o, pos, add, out):
         _check("add", add, o.dtype, (T, H), dev)
     made = ()
     if out is None:
-        out = torch.empty((T, H), dtype=o.dtype, device=dev)
+        out = o.new_empty((T, H))
         made = (out,)
     else:
         _check("out", out, o.dtype, (T, H), dev)
@@ -166,7 +164,7 @@ def moe_combine_backward(dy: torch.Tensor, o: torch.Tensor, topk_w: torch.Tensor
     _check("pos", pos, _I32, (T, k), dev)
     _check("pairs", pairs, _I32, (rows,), dev)
     d_o = torch.empty_like(o)
-    dw = torch.empty((T, k), dtype=_F32, device=dev)
+    dw = torch.empty_like(topk_w)
     _run(lib().moe_combine_backward, dev, stream, (d_o, dw), dy.data_ptr(), o.data_ptr(), code, rows, H,
          topk_w.data_ptr(), pos.data_ptr(), pairs.data_ptr(), T, k, d_o.data_ptr(), dw.data_ptr())
     return d_o, dw
@@ -195,9 +193,7 @@ def moe_route_backward(x: torch.Tensor, router_w: torch.Tensor, router_b: Option
     _check("pairs", pairs, _I32, (rows,), dev)
     if add is not None:
         _check("add", add, x.dtype, (T, H), dev)
-    dx = torch.empty((T, H), dtype=x.dtype, device=dev)
-    dwr = torch.empty((E, H), dtype=_F32, device=dev)
-    db = torch.empty(E, dtype=_F32, device=dev)
+    dx, dwr, db = torch.empty_like(x), torch.empty_like(router_w), router_w.new_empty(E)
     ws = torch.empty(lib().moe_route_backward_workspace_bytes(T, k, E, H, rows), dtype=torch.uint8, device=dev)
     _run(lib().moe_route_backward, dev, stream, (dx, dwr, db, ws), x.data_ptr(), code, T, H, E, k,
          router_w.data_ptr(), _ptr(router_b), topk_idx.data_ptr(), dw.data_ptr(), offsets.data_ptr(),
