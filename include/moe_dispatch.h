@@ -63,7 +63,7 @@ typedef enum { MOE_T_F16 = 0, MOE_T_BF16 = 1, MOE_T_F32 = 2 } moe_dtype_t;
 int64_t moe_sort_rows(int32_t T, int32_t k, int32_t n_experts, int32_t align);
 
 /* Bytes of scratch memory that moe_sort and moe_dispatch need.  0 where they
- * need none (up to 8,192 slots: ws may be NULL) and for an unsupported shape. */
+ * need none (up to 32,768 slots: ws may be NULL) and for an unsupported shape. */
 size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t n_experts);
 
 /* Sorts the slots of topk_idx (int32 [T][k]) by expert.

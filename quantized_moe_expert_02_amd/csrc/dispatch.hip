@@ -11,7 +11,8 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortMaxBlocks = 128;
-constexpr int kSortOne = 8;  // up to this many times 1,024 slots one workgroup sorts alone, in one launch
+constexpr int kSortOne = 4;       // up to this many times 1,024 slots one workgroup sorts alone
+constexpr int kSortRead = 32768;  // up to this many slots each workgroup counts all of them by itself, in one launch
 
 // Slots per workgroup (a multiple of kSortThreads) and number of workgroups.
 struct SortSplit {
@@ -60,7 +61,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const int32_t* idx,
 // derives expert e's place from all workgroups' counts; then the slots are
 // walked 1,024 at a time: a wavefront ranks its 64 slots by matching ids, and
 // thread e turns the wavefronts' counts of expert e into places.  ONE: a single
-// workgroup, which counts by itself and holds its slots in registers.
+// workgroup, which holds its slots in registers.  cnt == NULL: every workgroup
+// counts all slots by itself (reading them again costs less than a launch).
 template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx, int n, int E, int bits, int align,
                                                              int rows, int per_block, const int32_t* cnt,
@@ -87,6 +89,27 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx,
       same[c] = __popcll(m);
       if (ok && ranks[c] == 0) atomicAdd(&h[ids[c]], same[c]);
     }
+    __syncthreads();
+    total = tid < E ? h[tid] : 0;
+  } else if (!cnt) {
+    int* h = wc[0];
+    h[tid] = 0;
+    __syncthreads();
+    const auto count = [&](int from, int to) {
+      for (int i0 = from + tid; i0 < to; i0 += 8 * kSortThreads) {
+        int e[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) e[u] = idx[min(i0 + u * kSortThreads, n - 1)];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (i0 + u * kSortThreads < to && (unsigned)e[u] < (unsigned)E) atomicAdd(&h[e[u]], 1);
+      }
+    };
+    count(0, (int)lo);
+    __syncthreads();
+    before = tid < E ? h[tid] : 0;
+    __syncthreads();
+    count((int)lo, n);
     __syncthreads();
     total = tid < E ? h[tid] : 0;
   } else if (tid < E) {
@@ -254,13 +277,15 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch_small(const u32x4* x, 
 
 // xs[pos(t,j)] = x[t], token by token, 16-byte vectors; workgroups past the
 // tokens' zero the rows that hold no slot.
-constexpr int kPadRows = 64;  // rows looked over by one zeroing workgroup
+constexpr int kPadRows = 256;  // rows looked over by one zeroing workgroup
 
 __device__ __forceinline__ void zero_pad_rows(const int32_t* pairs, int rows, int part, u32x4* out, int nv) {
-  const int r0 = part * kPadRows, r1 = min(r0 + kPadRows, rows);
-  for (int r = r0; r < r1; ++r)
-    if (pairs[r] < 0)
-      for (int i = threadIdx.x; i < nv; i += kRowThreads) out[(size_t)r * nv + i] = u32x4{0, 0, 0, 0};
+  const int lane = threadIdx.x & 63, r0 = part * kPadRows + (threadIdx.x >> 6) * 64, r = r0 + lane;
+  uint64_t pad = __ballot(r < rows && pairs[min(r, rows - 1)] < 0);  // a wavefront looks over 64 rows
+  for (; pad; pad &= pad - 1) {
+    u32x4* o = out + (size_t)(r0 + __builtin_ctzll(pad)) * nv;
+    for (int i = lane; i < nv; i += 64) o[i] = u32x4{0, 0, 0, 0};
+  }
 }
 
 __global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, int T, int nv, int k, int rows,
@@ -277,7 +302,9 @@ __global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, in
   }
 }
 
-// y[t] = add[t] + sum_j w[t][j] o[pos(t,j)] (w == NULL: all ones), slots in order.
+// y[t] = add[t] + sum_j w[t][j] o[pos(t,j)] (w == NULL: all ones), slots in
+// order, 8 rows in flight.
+constexpr int kSlotsAtOnce = 8;
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int rows, int nv, const float* w,
                                                             const int32_t* pos, int k, const u32x4* add, u32x4* y) {
@@ -286,55 +313,91 @@ __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int 
   if (i >= nv) return;
   float acc[VE] = {};
   if (add) unpack_vec<DT>(add[(size_t)t * nv + i], acc);
-  for (int j = 0; j < k; ++j) {
-    const int r = pos[(size_t)t * k + j];
-    if ((unsigned)r >= (unsigned)rows) continue;
-    float f[VE];
-    unpack_vec<DT>(o[(size_t)r * nv + i], f);
-    const float wj = w ? w[(size_t)t * k + j] : 1.0f;
+  constexpr int S = kSlotsAtOnce;
+  for (int j0 = 0; j0 < k; j0 += S) {
+    int r[S];
+    float wj[S];
+    u32x4 v[S];
 #pragma unroll
-    for (int c = 0; c < VE; ++c) acc[c] = fmaf(wj, f[c], acc[c]);
+    for (int j = 0; j < S; ++j) {
+      const int p = t * k + min(j0 + j, k - 1);
+      r[j] = pos[p];
+      if (j0 + j >= k || (unsigned)r[j] >= (unsigned)rows) r[j] = -1;
+      wj[j] = w ? w[p] : 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < S; ++j)
+      if (r[j] >= 0) v[j] = o[(size_t)r[j] * nv + i];  // (uniform)
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      if (r[j] < 0) continue;
+      float f[VE];
+      unpack_vec<DT>(v[j], f);
+#pragma unroll
+      for (int c = 0; c < VE; ++c) acc[c] = fmaf(wj[j], f[c], acc[c]);
+    }
   }
   y[(size_t)t * nv + i] = pack_vec<DT>(acc);
 }
 
 // d_o[pos(t,j)] = w dy[t]; dw[t][j] = <dy[t], o[pos(t,j)]>.  One workgroup per
-// token; the workgroups past the tokens' zero padding rows.
+// token, 8 slots at a time: their rows of o in flight together.  The workgroups
+// past the tokens' zero padding rows.
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, const u32x4* o, int rows, int nv,
                                                               const float* w, const int32_t* pos,
                                                               const int32_t* pairs, int T, int k, u32x4* d_o,
                                                               float* dw) {
-  constexpr int VE = kVec<DT>;
-  __shared__ float part[kRowThreads / kWave];
-  const int t = blockIdx.x;
+  constexpr int VE = kVec<DT>, S = kSlotsAtOnce, W = kRowThreads / kWave;
+  __shared__ float part[W][S];
+  const int t = blockIdx.x, tid = threadIdx.x;
   if (t >= T) return zero_pad_rows(pairs, rows, t - T, d_o, nv);
-  for (int j = 0; j < k; ++j) {
-    const int r = pos[(size_t)t * k + j];
-    float dot = 0.0f;
-    if ((unsigned)r < (unsigned)rows) {
-      const float wj = w[(size_t)t * k + j];
-      for (int i = threadIdx.x; i < nv; i += kRowThreads) {
-        float g[VE], f[VE];
-        unpack_vec<DT>(dy[(size_t)t * nv + i], g);
-        unpack_vec<DT>(o[(size_t)r * nv + i], f);
+  for (int j0 = 0; j0 < k; j0 += S) {
+    int r[S];
+    float wj[S], dot[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      const int p = t * k + min(j0 + j, k - 1);
+      r[j] = pos[p];
+      if (j0 + j >= k || (unsigned)r[j] >= (unsigned)rows) r[j] = -1;
+      wj[j] = w[p];
+      dot[j] = 0.0f;
+    }
+    for (int i = tid; i < nv; i += kRowThreads) {
+      const u32x4 gv = dy[(size_t)t * nv + i];
+      u32x4 v[S];
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+        if (r[j] >= 0) v[j] = o[(size_t)r[j] * nv + i];  // (uniform)
+      float g[VE];
+      unpack_vec<DT>(gv, g);
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        if (r[j] < 0) continue;
+        float f[VE], q[VE];
+        unpack_vec<DT>(v[j], f);
 #pragma unroll
         for (int c = 0; c < VE; ++c) {
-          dot = fmaf(g[c], f[c], dot);
-          g[c] *= wj;
+          dot[j] = fmaf(g[c], f[c], dot[j]);
+          q[c] = g[c] * wj[j];
         }
-        d_o[(size_t)r * nv + i] = pack_vec<DT>(g);
+        d_o[(size_t)r[j] * nv + i] = pack_vec<DT>(q);
       }
     }
-    dot = wave_sum_f32(dot);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float s = 0.0f;
-      for (int q = 0; q < kRowThreads / kWave; ++q) s += part[q];
-      dw[(size_t)t * k + j] = s;
+#pragma unroll
+    for (int j = 0; j < S; ++j) dot[j] = wave_sum_f32(dot[j]);
+    if ((tid & 63) == 0) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) part[tid >> 6][j] = dot[j];
     }
     __syncthreads();
+    if (tid < S && j0 + tid < k) {
+      float s = part[0][tid];
+#pragma unroll
+      for (int q = 1; q < W; ++q) s += part[q][tid];
+      dw[(size_t)t * k + j0 + tid] = s;
+    }
+    if (j0 + S < k) __syncthreads();
   }
 }
 
@@ -375,7 +438,8 @@ hipError_t launch_sort(const int32_t* idx, int T, int k, int E, int align, int r
     k_sort_place<true><<<1, kSortThreads, 0, s>>>(idx, n, E, id_bits(E), align, rows, sp.per_block, cnt, offsets, pairs,
                                                  pos);
   } else {
-    k_sort_count<<<sp.blocks, kSortThreads, 0, s>>>(idx, n, E, sp.per_block, cnt);
+    if (n > kSortRead) k_sort_count<<<sp.blocks, kSortThreads, 0, s>>>(idx, n, E, sp.per_block, cnt);
+    else cnt = nullptr;
     k_sort_place<false><<<sp.blocks, kSortThreads, 0, s>>>(idx, n, E, id_bits(E), align, rows, sp.per_block, cnt, offsets,
                                                           pairs, pos);
   }
@@ -398,7 +462,7 @@ int64_t moe_sort_rows(int32_t T, int32_t k, int32_t n_experts, int32_t align) {
 size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t n_experts) {
   if (check_sort_shape(T, k, n_experts, 1) != MOE_OK) return 0;
   const int blocks = sort_split((int64_t)T * k).blocks;
-  return blocks > 1 ? round256((size_t)blocks * n_experts * 4) : 0;
+  return blocks > 1 && (int64_t)T * k > kSortRead ? round256((size_t)blocks * n_experts * 4) : 0;
 }
 
 int moe_sort(const int32_t* topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t align, int32_t* offsets,

@@ -33,7 +33,7 @@ def test_sort_rows(L):
     for bad in ((-1, 1, 8), (1, 0, 8), (1, 9, 8), (1, 1, 0), (1, 1, 1025), (1, 33, 64), (1 << 29, 4, 8)):
         assert L.moe_sort_workspace_bytes(*bad) == 0
     assert L.moe_sort_workspace_bytes(4, 2, 8) == 0  # one workgroup sorts them without any
-    assert L.moe_sort_workspace_bytes(5000, 2, 8) > 0
+    assert L.moe_sort_workspace_bytes(50000, 2, 8) > 0
 
 
 def _expect(fn, good, changes):
@@ -45,7 +45,7 @@ def _expect(fn, good, changes):
 
 
 def test_sort_refuses(L):
-    good = dict(idx=P, T=5000, k=2, E=8, align=1, offsets=P, pairs=P, pos=P, ws=P, ws_bytes=1 << 20, stream=None)
+    good = dict(idx=P, T=50000, k=2, E=8, align=1, offsets=P, pairs=P, pos=P, ws=P, ws_bytes=1 << 20, stream=None)
     _expect(L.moe_sort, good, [
         ("idx", None, INVAL), ("idx", P + 2, INVAL), ("T", -1, INVAL), ("T", 1 << 30, UNSUPPORTED), ("k", 0, INVAL), ("k", 9, INVAL),
         ("E", 0, INVAL), ("E", 1025, UNSUPPORTED), ("align", 0, INVAL), ("align", 1025, INVAL), ("offsets", None, INVAL),
@@ -54,7 +54,7 @@ def test_sort_refuses(L):
 
 
 def test_dispatch_refuses(L):
-    good = dict(x=P, dtype=0, T=5000, H=64, idx=P, k=2, E=8, align=1, xs=P, offsets=P, pairs=P, pos=P, ws=P, ws_bytes=1 << 20,
+    good = dict(x=P, dtype=0, T=50000, H=64, idx=P, k=2, E=8, align=1, xs=P, offsets=P, pairs=P, pos=P, ws=P, ws_bytes=1 << 20,
                 stream=None)
     _expect(L.moe_dispatch, good, [
         ("x", None, INVAL), ("x", P + 8, INVAL), ("xs", None, INVAL), ("xs", P + 4, INVAL), ("dtype", 3, INVAL),
