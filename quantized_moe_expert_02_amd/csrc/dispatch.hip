@@ -188,37 +188,37 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx,
 // slots): every workgroup sorts all slots for itself, then lays out its part of
 // one token's row; the first one also writes the order.
 constexpr int kSmallSlots = 1024;
-constexpr int kRowThreads = 256;
+constexpr int kSmallThreads = 256;
 
-__global__ __launch_bounds__(kRowThreads) void k_dispatch_small(const u32x4* x, int T, int nv, const int32_t* idx, int k,
+__global__ __launch_bounds__(kSmallThreads) void k_dispatch_small(const u32x4* x, int T, int nv, const int32_t* idx, int k,
                                                                 int E, int bits, u32x4* xs, int32_t* offsets,
                                                                 int32_t* pairs, int32_t* pos) {
-  constexpr int W = kRowThreads / kWave, C = kSmallSlots / kRowThreads;
+  constexpr int W = kSmallThreads / kWave, C = kSmallSlots / kSmallThreads;
   __shared__ uint16_t wc[C * W][kMaxExperts];  // slots of each expert in each 64 slots, then those before
   __shared__ int start[kMaxExperts + 1], wsum[W], place[kSmallSlots];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = T * k, t = blockIdx.x;
-  const int i = blockIdx.y * kRowThreads + tid;
+  const int i = blockIdx.y * kSmallThreads + tid;
   u32x4 v = {0, 0, 0, 0};
   if (i < nv) v = x[(size_t)t * nv + i];
   int ids[C], ranks[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) ids[c] = c * kRowThreads + tid < n ? idx[c * kRowThreads + tid] : -1;
+  for (int c = 0; c < C; ++c) ids[c] = c * kSmallThreads + tid < n ? idx[c * kSmallThreads + tid] : -1;
   const int chunks = (n + 63) / 64;
-  for (int c = tid; c < chunks * E; c += kRowThreads) wc[c / E][c % E] = 0;
+  for (int c = tid; c < chunks * E; c += kSmallThreads) wc[c / E][c % E] = 0;
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if (c * kRowThreads >= n) break;
+    if (c * kSmallThreads >= n) break;
     const bool ok = (unsigned)ids[c] < (unsigned)E;
     const uint64_t m = match_id(ids[c], ok, bits);
     ranks[c] = lanes_below(m);
     if (ok && ranks[c] == 0) wc[c * W + wave][ids[c]] = (uint16_t)__popcll(m);
   }
   __syncthreads();
-  const int per = (E + kRowThreads - 1) / kRowThreads;  // experts of this thread
-  int total[kMaxExperts / kRowThreads], mine = 0;
+  const int per = (E + kSmallThreads - 1) / kSmallThreads;  // experts of this thread
+  int total[kMaxExperts / kSmallThreads], mine = 0;
 #pragma unroll
-  for (int q = 0; q < kMaxExperts / kRowThreads; ++q) {
+  for (int q = 0; q < kMaxExperts / kSmallThreads; ++q) {
     total[q] = 0;
     const int e = tid * per + q;
     if (q < per && e < E)
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch_small(const u32x4* x, 
     all += wsum[w];
   }
 #pragma unroll
-  for (int q = 0; q < kMaxExperts / kRowThreads; ++q) {
+  for (int q = 0; q < kMaxExperts / kSmallThreads; ++q) {
     const int e = tid * per + q;
     if (q < per && e < E) start[e] = at;
     at += total[q];
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch_small(const u32x4* x, 
   const bool writes = blockIdx.x == 0 && blockIdx.y == 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int s = c * kRowThreads + tid;
+    const int s = c * kSmallThreads + tid;
     if (s >= n) continue;
     const bool ok = (unsigned)ids[c] < (unsigned)E;
     const int r = ok ? start[ids[c]] + wc[c * W + wave][ids[c]] + ranks[c] : -1;
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch_small(const u32x4* x, 
     }
   }
   if (writes)
-    for (int e = tid; e <= E; e += kRowThreads) offsets[e] = start[e];
+    for (int e = tid; e <= E; e += kSmallThreads) offsets[e] = start[e];
   __syncthreads();
   if (i >= nv) return;
   for (int j = 0; j < k; ++j) {
@@ -276,11 +276,11 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch_small(const u32x4* x, 
 }
 
 // xs[pos(t,j)] = x[t], token by token, 16-byte vectors; workgroups past the
-// tokens' zero the rows that hold no slot.
-constexpr int kPadRows = 256;  // rows looked over by one zeroing workgroup
+// tokens' zero the rows that hold no slot, a row per thread looked over.
+constexpr int kRowThreads = 256;  // most threads of a workgroup of the row kernels
 
 __device__ __forceinline__ void zero_pad_rows(const int32_t* pairs, int rows, int part, u32x4* out, int nv) {
-  const int lane = threadIdx.x & 63, r0 = part * kPadRows + (threadIdx.x >> 6) * 64, r = r0 + lane;
+  const int lane = threadIdx.x & 63, r0 = part * blockDim.x + (threadIdx.x & ~63u), r = r0 + lane;
   uint64_t pad = __ballot(r < rows && pairs[min(r, rows - 1)] < 0);  // a wavefront looks over 64 rows
   for (; pad; pad &= pad - 1) {
     u32x4* o = out + (size_t)(r0 + __builtin_ctzll(pad)) * nv;
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, in
   const int t = blockIdx.x;
   if (t >= T) return zero_pad_rows(pairs, rows, t - T, xs, nv);
   const int32_t* p = pos + (size_t)t * k;
-  for (int i = threadIdx.x; i < nv; i += kRowThreads) {
+  for (int i = threadIdx.x; i < nv; i += blockDim.x) {
     const u32x4 v = x[(size_t)t * nv + i];
     for (int j = 0; j < k; ++j) {
       const int r = p[j];
@@ -305,11 +305,18 @@ __global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, in
 // y[t] = add[t] + sum_j w[t][j] o[pos(t,j)] (w == NULL: all ones), slots in
 // order, 8 rows in flight.
 constexpr int kSlotsAtOnce = 8;
-template <int DT>
+
+// Rows of o that are read once: past the last-level cache (256 MB) they are
+// read without a place in it.
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_row(const u32x4* p) {
+  return STREAM ? __builtin_nontemporal_load(p) : *p;
+}
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int rows, int nv, const float* w,
                                                             const int32_t* pos, int k, const u32x4* add, u32x4* y) {
   constexpr int VE = kVec<DT>;
-  const int t = blockIdx.x, i = blockIdx.y * kRowThreads + threadIdx.x;
+  const int t = blockIdx.x, i = blockIdx.y * blockDim.x + threadIdx.x;
   if (i >= nv) return;
   float acc[VE] = {};
   if (add) unpack_vec<DT>(add[(size_t)t * nv + i], acc);
@@ -327,7 +334,7 @@ __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int 
     }
 #pragma unroll
     for (int j = 0; j < S; ++j)
-      if (r[j] >= 0) v[j] = o[(size_t)r[j] * nv + i];  // (uniform)
+      if (r[j] >= 0) v[j] = load_row<STREAM>(o + (size_t)r[j] * nv + i);  // (uniform)
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       if (r[j] < 0) continue;
@@ -343,7 +350,7 @@ __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int 
 // d_o[pos(t,j)] = w dy[t]; dw[t][j] = <dy[t], o[pos(t,j)]>.  One workgroup per
 // token, 8 slots at a time: their rows of o in flight together.  The workgroups
 // past the tokens' zero padding rows.
-template <int DT>
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, const u32x4* o, int rows, int nv,
                                                               const float* w, const int32_t* pos,
                                                               const int32_t* pairs, int T, int k, u32x4* d_o,
@@ -363,12 +370,12 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, c
       wj[j] = w[p];
       dot[j] = 0.0f;
     }
-    for (int i = tid; i < nv; i += kRowThreads) {
+    for (int i = tid; i < nv; i += blockDim.x) {
       const u32x4 gv = dy[(size_t)t * nv + i];
       u32x4 v[S];
 #pragma unroll
       for (int j = 0; j < S; ++j)
-        if (r[j] >= 0) v[j] = o[(size_t)r[j] * nv + i];  // (uniform)
+        if (r[j] >= 0) v[j] = load_row<STREAM>(o + (size_t)r[j] * nv + i);  // (uniform)
       float g[VE];
       unpack_vec<DT>(gv, g);
 #pragma unroll
@@ -393,12 +400,21 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, c
     __syncthreads();
     if (tid < S && j0 + tid < k) {
       float s = part[0][tid];
-#pragma unroll
-      for (int q = 1; q < W; ++q) s += part[q][tid];
+      for (int q = 1; q < (int)blockDim.x / kWave; ++q) s += part[q][tid];
       dw[(size_t)t * k + j0 + tid] = s;
     }
     if (j0 + S < k) __syncthreads();
   }
+}
+
+constexpr size_t kStream = (size_t)112 << 20;  // bytes of o from which it is streamed
+
+// Threads of a row kernel's workgroup: the row's vectors in as few equal parts as
+// 256 threads allow (a 257-vector row: two parts of 192 threads).
+int row_parts(int nv) { return (nv + kRowThreads - 1) / kRowThreads; }
+int row_threads(int nv) {
+  const int parts = row_parts(nv);
+  return ((nv + parts - 1) / parts + kWave - 1) / kWave * kWave;
 }
 
 int id_bits(int E) {
@@ -492,14 +508,15 @@ int moe_dispatch(const void* x, int32_t dtype, int32_t T, int32_t H, const int32
   const int nv = (int)((size_t)H * elem_bytes(dtype) / 16), n = T * k;
   if (T && align == 1 && n <= kSmallSlots) {
     if (bad(offsets, 4) || bad(topk_idx, 4) || bad(pairs, 4) || bad(pos, 4)) return MOE_E_INVAL;
-    k_dispatch_small<<<dim3(T, (nv + kRowThreads - 1) / kRowThreads), kRowThreads, 0, (hipStream_t)stream>>>(
+    k_dispatch_small<<<dim3(T, (nv + kSmallThreads - 1) / kSmallThreads), kSmallThreads, 0, (hipStream_t)stream>>>(
         (const u32x4*)x, T, nv, topk_idx, k, n_experts, id_bits(n_experts), (u32x4*)xs, offsets, pairs, pos);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
   }
   st = moe_sort(topk_idx, T, k, n_experts, align, offsets, pairs, pos, ws, ws_bytes, stream);
   if (st != MOE_OK || T == 0) return st;
   const int rows = (int)moe_sort_rows(T, k, n_experts, align);
-  k_scatter_rows<<<T + (rows + kPadRows - 1) / kPadRows, kRowThreads, 0, (hipStream_t)stream>>>(
+  const int threads = row_threads(nv);
+  k_scatter_rows<<<T + (rows + threads - 1) / threads, threads, 0, (hipStream_t)stream>>>(
       (const u32x4*)x, T, nv, k, rows, pos, pairs, (u32x4*)xs);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
@@ -509,14 +526,18 @@ static int gather_sum(const void* o, int32_t dtype, int32_t rows, int32_t H, con
   if (T == 0) return MOE_OK;
   if ((rows && bad(o, 16)) || bad(pos, 4) || bad(y, 16) || (add && !aligned_to(add, 16))) return MOE_E_INVAL;
   const int nv = (int)((size_t)H * elem_bytes(dtype) / 16);
-  const dim3 grid(T, (nv + kRowThreads - 1) / kRowThreads);
+  const dim3 grid(T, row_parts(nv));
+  const int threads = row_threads(nv);
   const auto launch = [&](auto kernel) {
-    kernel<<<grid, kRowThreads, 0, (hipStream_t)stream>>>((const u32x4*)o, rows, nv, w, pos, k, (const u32x4*)add,
+    kernel<<<grid, threads, 0, (hipStream_t)stream>>>((const u32x4*)o, rows, nv, w, pos, k, (const u32x4*)add,
                                                          (u32x4*)y);
   };
-  if (dtype == MOE_T_F16) launch(k_gather_sum<MOE_T_F16>);
-  else if (dtype == MOE_T_BF16) launch(k_gather_sum<MOE_T_BF16>);
-  else launch(k_gather_sum<MOE_T_F32>);
+  // 6144 wide, top-8, binary16, plain and streamed: 101 MB of rows 23.1 and 22.5 us, 201 MB 46.8 and 42.9, 403 MB 99.8 and
+  // 84.4; 25 MB 7.0 and 7.9.
+  const bool stream_rows = (size_t)T * k * nv * 16 >= kStream;
+  if (dtype == MOE_T_F16) stream_rows ? launch(k_gather_sum<MOE_T_F16, true>) : launch(k_gather_sum<MOE_T_F16, false>);
+  else if (dtype == MOE_T_BF16) stream_rows ? launch(k_gather_sum<MOE_T_BF16, true>) : launch(k_gather_sum<MOE_T_BF16, false>);
+  else stream_rows ? launch(k_gather_sum<MOE_T_F32, true>) : launch(k_gather_sum<MOE_T_F32, false>);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
@@ -547,14 +568,18 @@ int moe_combine_backward(const void* dy, const void* o, int32_t dtype, int32_t r
   if (T && (bad(dy, 16) || bad(topk_w, 4) || bad(pos, 4) || bad(dw, 4))) return MOE_E_INVAL;
   if (rows && (bad(o, 16) || bad(d_o, 16) || bad(pairs, 4))) return MOE_E_INVAL;
   const int nv = (int)((size_t)H * elem_bytes(dtype) / 16);
-  const int grid = T + (rows + kPadRows - 1) / kPadRows;
+  const int threads = row_threads(nv), grid = T + (rows + threads - 1) / threads;
   const auto launch = [&](auto kernel) {
-    kernel<<<grid, kRowThreads, 0, (hipStream_t)stream>>>((const u32x4*)dy, (const u32x4*)o, rows, nv, topk_w, pos,
+    kernel<<<grid, threads, 0, (hipStream_t)stream>>>((const u32x4*)dy, (const u32x4*)o, rows, nv, topk_w, pos,
                                                          pairs, T, k, (u32x4*)d_o, dw);
   };
-  if (dtype == MOE_T_F16) launch(k_combine_grad<MOE_T_F16>);
-  else if (dtype == MOE_T_BF16) launch(k_combine_grad<MOE_T_BF16>);
-  else launch(k_combine_grad<MOE_T_F32>);
+  // Plain and streamed, as there: 101 MB of rows 37.2 and 36.4 us, 134 MB (padded) 70.7 and 64.0, 201 MB 81.6 and 66.7,
+  // 403 MB 168 and 157; 50 MB 18.2 and 20.0.
+  const bool stream_rows = (size_t)T * k * nv * 16 >= kStream;
+  if (dtype == MOE_T_F16) stream_rows ? launch(k_combine_grad<MOE_T_F16, true>) : launch(k_combine_grad<MOE_T_F16, false>);
+  else if (dtype == MOE_T_BF16)
+    stream_rows ? launch(k_combine_grad<MOE_T_BF16, true>) : launch(k_combine_grad<MOE_T_BF16, false>);
+  else stream_rows ? launch(k_combine_grad<MOE_T_F32, true>) : launch(k_combine_grad<MOE_T_F32, false>);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
