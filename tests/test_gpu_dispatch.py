@@ -289,6 +289,15 @@ def test_route_gradient(dtype, T, k, E, align, drop, H, bias):
         assert bool(((ga.double().cpu() - ref).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T,k,E,align,drop,H,bias", [
+    (513, 4, 9, 16, 0.2, 264, True), (700, 8, 256, 1, 0.1, 2048, True), (600, 32, 300, 64, 0.3, 136, False),
+    (1025, 3, 65, 8, 0.0, 72, True), (900, 1, 512, 1, 0.2, 1544, True), (2049, 5, 257, 1, 0.9, 64, False)])
+def test_route_gradient_of_many_tokens(dtype, T, k, E, align, drop, H, bias):
+    """More tokens than rows of the router's weights are gathered for, over each range of experts."""
+    test_route_gradient(dtype, T, k, E, align, drop, H, bias)
+
+
 def test_route_gradient_against_differences():
     T, k, E, H = 12, 3, 7, 48
     _log("route grad differences")
