@@ -318,52 +318,63 @@ constexpr int kRowWaves = kRowThreads / kWave;
 // 32 r.
 struct RowsOut {
   float* sums;       // small batches: u [S][T][R] by row; else v [T][R] in the sorted order, or u by row (or NULL)
-  const float* u;    // backward: the forward pass's u, copied to
-  float* u_sorted;   //   [T][R] in the sorted order
   u32x4* frag;       // [tiles][4][blocks][2 pieces][64]: contraction over r
   float* scale;      // [tiles][4][blocks][16]: what the products are multiplied by
   int blocks;
+  const float* u;    // backward, where given: the forward pass's u, copied to
+  float* u_sorted;   //   [T][R] in the sorted order
+};
+
+template <int MT, int RT, bool ACROSS>
+struct RowsLds {
+  static constexpr int M = MT * 16, W = RT * 16;
+  static constexpr int KS = 64, XV = KS / 8, XS = KS + 8;  // columns per step; x's rows in LDS: vectors, stride
+  static constexpr int FR = ACROSS ? KS : W, FV = ACROSS ? W / 8 : XV, FS = ACROSS ? W + 8 : XS;  // the factor's
+  static constexpr int kStage = (M * XS + FR * FS) * 2;
+  static_assert(kStage >= MT * RT * 1024, "a wavefront's sums fit its stage");
+  SharedTile st;
+  alignas(16) char lds[kRowWaves * kStage];
+  alignas(16) float vs[M][W + 4];
 };
 
 // The long sums over a tile's rows: u[t][r] = <A_a[r], x[t]> (ACROSS false), or
-// v[t][r] = s_a sum_c dy[t][c] B_a[c][r] (ACROSS), for MT bands of rows and one
-// block of r (blockIdx.y) per workgroup; the columns are split over its
-// wavefronts, and in small batches over blockIdx.z first.  Splitting r instead
-// of the columns reads x once per block but leaves whole sums, which are split
-// into fragments here, once.
+// v[t][r] = s_a sum_c dy[t][c] B_a[c][r] (ACROSS), for MT bands of rows (z) and
+// one block of r (y) per workgroup; the columns are split over its wavefronts,
+// and in small batches over zs segments (z) first.  Splitting r instead of the
+// columns reads x once per block but leaves whole sums, which are split into
+// fragments here, once.
 // Memory is read 128 contiguous bytes per row (8 lanes side by side: lanes that
 // follow the fragments' layout, each in a row of its own, cost the address unit
 // four times as many cycles); a wavefront's own LDS turns that into fragments,
 // the next steps' loads in flight meanwhile.
+// 2,048 rows of 6144 binary16, rank 16: 10.3 us, of which 1.2 find the tile, 3.5
+// pass until the first steps have their data, 3.0 take the other two thirds, 1.0
+// join and split the sums, the rest is the launch.  1,801 rows, rank 64: 14.3 us;
+// its 120 workgroups are bound by what a CU loads (64 bytes a cycle), and more of
+// them load more in all (the choice at RowsShape); 1,024 threads each: 15.2.
 template <int DT, int MT, int RT, bool ACROSS, bool SMALL>
-__global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, const void* x, int64_t ldx, RowsOut out) {
+__device__ __forceinline__ void rows_body(RowsLds<MT, RT, ACROSS>& L, const AdapterArgs& d, const RowSet& rs, const void* x,
+                                          int64_t ldx, const RowsOut& out, int tile, int y, int z, int zs) {
   typedef typename Mat<DT>::elem E;
-  constexpr int M = MT * 16, W = RT * 16, NF = MT * RT;
-  constexpr int KS = 64, XV = KS / 8, XS = KS + 8;  // columns per step; x's rows in LDS: vectors, stride
-  constexpr int FR = ACROSS ? KS : W, FV = ACROSS ? W / 8 : XV, FS = ACROSS ? W + 8 : XS;  // the factor's
+  typedef RowsLds<MT, RT, ACROSS> Lds;
+  constexpr int M = Lds::M, W = Lds::W, NF = MT * RT, KS = Lds::KS, XV = Lds::XV, XS = Lds::XS, FR = Lds::FR, FV = Lds::FV,
+                FS = Lds::FS, kStage = Lds::kStage;
   constexpr int XL = M * XV / 64, FL = FR * FV / 64;   // loads per lane
-  constexpr int kStage = (M * XS + FR * FS) * 2;
-  static_assert(kStage >= NF * 1024, "a wavefront's sums fit its stage");
-  __shared__ SharedTile st;
-  __shared__ __align__(16) char lds[kRowWaves * kStage];
-  __shared__ __align__(16) float vs[SMALL ? 1 : M][W + 4];
+  SharedTile& st = L.st;
+  char* lds = L.lds;
+  auto& vs = L.vs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x, t0 = SMALL ? 0 : blockIdx.z * M, r0 = blockIdx.y * W;
-  share_tile<SMALL ? kSmallM : kM>(&st, d, rs, tile, r0 == 0 && blockIdx.z == 0 ? rs.kept + tile : nullptr);
+  const int t0 = SMALL ? 0 : z * M, r0 = y * W;
+  share_tile<SMALL ? kSmallM : kM>(&st, d, rs, tile, r0 == 0 && z == 0 ? rs.kept + tile : nullptr);
   const int a = __builtin_amdgcn_readfirstlane(st.a), cnt = __builtin_amdgcn_readfirstlane(st.cnt) - t0;
   if (cnt <= 0 || a == d.n) return;
   const int rk = __builtin_amdgcn_readfirstlane(st.rank) - r0, R = d.R, C = ACROSS ? d.N : d.K;
   const int* strow = st.row + t0;
   const int first = st.first + t0;
-  if (ACROSS)  // this block's columns of u
+  if (ACROSS && out.u)  // this block's columns of u
     for (int i = tid; i < min(cnt, M) * (W / 4); i += kRowThreads) {
       const int t = i / (W / 4), r = r0 + i % (W / 4) * 4;
-      if (r < R) {
-        f32x4 v = *(const f32x4*)(out.u + (size_t)max(strow[t], 0) * R + r);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = r - r0 + c < rk && strow[t] >= 0 ? v[c] : 0.0f;
-        *(f32x4*)(out.u_sorted + (size_t)(first + t) * R + r) = v;
-      }
+      if (r < R) *(f32x4*)(out.u_sorted + (size_t)(first + t) * R + r) = *(const f32x4*)(out.u + (size_t)max(strow[t], 0) * R + r);
     }
   if (rk <= 0) {
     if (!ACROSS && !SMALL && out.sums)
@@ -375,8 +386,8 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
   }
   const bool whole = rk % 8 == 0;
   const float f = ACROSS || !SMALL ? d.scale[a] : 1.0f;
-  const int steps = (C + KS - 1) / KS, parts = (SMALL ? gridDim.z : 1) * kRowWaves;
-  const int part = (SMALL ? blockIdx.z : 0) * kRowWaves + wave;
+  const int steps = (C + KS - 1) / KS, parts = (SMALL ? zs : 1) * kRowWaves;
+  const int part = (SMALL ? z : 0) * kRowWaves + wave;
   const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
   E* xs = (E*)(lds + wave * kStage);
   E* fs = xs + M * XS;
@@ -457,7 +468,7 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
     const int q = tid / 64, t = q / RT * 16 + li, c = q % RT * 16 + g * 4, r = r0 + c;
     const int row = ACROSS ? (t < cnt ? first + t : -1) : strow[t];
     if ((SMALL || out.sums) && row >= 0 && r < R)
-      *(f32x4*)(out.sums + ((size_t)(SMALL ? blockIdx.z : 0) * rs.T + row) * R + r) = s;
+      *(f32x4*)(out.sums + ((size_t)(SMALL ? z : 0) * rs.T + row) * R + r) = s;
     if (!SMALL) *(f32x4*)&vs[t][c] = s;
   }
   if (SMALL) return;
@@ -476,13 +487,19 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
     const int e = scale_exp<DT>(top);
     v8_t<DT> h[2];
     split_pieces<DT, 2>(v, e, h);
-    const size_t at = ((size_t)tile * 4 + t0 / 16 + wave / BW) * out.blocks + blockIdx.y * BW + b;
+    const size_t at = ((size_t)tile * 4 + t0 / 16 + wave / BW) * out.blocks + y * BW + b;
     out.frag[(at * 2 + 0) * 64 + lane] = __builtin_bit_cast(u32x4, h[0]);
     out.frag[(at * 2 + 1) * 64 + lane] = __builtin_bit_cast(u32x4, h[1]);
     // below 2^-126 this factor loses bits of results that are far below the
     // 16-bit types' smallest step
     if (g == 0) out.scale[at * 16 + li] = __builtin_amdgcn_ldexpf(ACROSS ? 1.0f : f, -e);
   }
+}
+
+template <int DT, int MT, int RT, bool ACROSS, bool SMALL>
+__global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, const void* x, int64_t ldx, RowsOut out) {
+  __shared__ RowsLds<MT, RT, ACROSS> lds;
+  rows_body<DT, MT, RT, ACROSS, SMALL>(lds, d, rs, x, ldx, out, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z);
 }
 
 constexpr int kOutThreads = 256;
@@ -561,7 +578,9 @@ __device__ __forceinline__ void pack_rows(RowPack<RB>* p, const SharedTile& st, 
 __device__ __forceinline__ int place_of(int n) { return n % 8 * 16 + n / 8; }
 
 // y[t] = add[t] + s_a B_a u[t] for a small tile's rows, 128 columns per
-// wavefront.
+// wavefront.  Bound by a chain of waits: the tile, the sums of u's segments, one
+// run of B.  One token, 6144 wide, rank 16: 4.8 us (k_rows 4.2); 48 requests of 32
+// adapters of rank up to 64, 6144 to 2048: 6.7 (8.6, for 11 MB of factors).
 template <int DT, int RT>
 __global__ __launch_bounds__(kOutThreads) void k_expand_small(AdapterArgs d, RowSet rs, const float* part, int S, float* u,
                                                              const void* add, int64_t ldadd, void* y, int64_t ldy) {
@@ -648,6 +667,26 @@ __device__ __forceinline__ void copy_none(SharedTile* st, const AdapterArgs& d, 
 
 constexpr int kCols = 128;  // columns that a workgroup of the second launch takes at a time
 
+struct SpreadArgs {
+  const u32x4* frag;
+  const float* scale;
+  const void* add;
+  int64_t ldadd;
+  void* out;
+  int64_t ldo;
+  float* u;      // forward: zeros for the rows without an adapter (or NULL)
+  int passes;    // runs of 128 columns per workgroup
+  int columns;   // workgroups of a tile; as many follow for the rows without an adapter, of which the first takes all
+};
+template <int DT, int RT, bool ACROSS>
+struct SpreadLds {
+  static constexpr int W = RT * 16, RB = (RT + 1) / 2;
+  static constexpr int FS = ACROSS ? kCols + 16 : W + 8;   // row stride
+  static constexpr int FR = ACROSS ? RB * 32 : kCols;      // rows
+  SharedTile st;
+  alignas(16) typename Mat<DT>::elem f[2][FR * FS];        // in turn
+};
+
 // The second launch of either pass, for a tile's rows and `passes` runs of 128
 // columns: out[t] = add[t] + F v[t], with F = B_a times s_a (forward: rows of
 // F in memory, v = u) or A_a^T (ACROSS: columns of F).  A band of 16 rows per
@@ -656,24 +695,29 @@ constexpr int kCols = 128;  // columns that a workgroup of the second launch tak
 // column of product q (place_of); where the contraction runs across the rows
 // of A, LDS holds their columns in that order, and 16 lanes read product q's
 // across.
+// Bound by memory, once the first run's data are there: 1,801 rows of 6144
+// bfloat16, rank 64: 12.7 us for 44 MB of add and y (3.5 TB/s); 7,204 rows 40.3
+// (4.4 TB/s).
 template <int DT, int RT, bool ACROSS>
-__global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs, const u32x4* frag, const float* scale,
-                                                       const void* add, int64_t ldadd, void* out, int64_t ldo, float* u,
-                                                       int passes) {
+__device__ __forceinline__ void spread_body(SpreadLds<DT, RT, ACROSS>& L, const AdapterArgs& d, const RowSet& rs,
+                                            const SpreadArgs& sa, int tile, int chunk) {
   typedef typename Mat<DT>::elem E;
-  constexpr int W = RT * 16, RB = (RT + 1) / 2, FL = W * kCols / 8 / kOutThreads;
-  constexpr int FV = ACROSS ? kCols / 8 : W / 8;                 // vectors of a row of F
-  constexpr int FS = ACROSS ? kCols + 16 : W + 8;                // LDS row stride
-  constexpr int FR = ACROSS ? RB * 32 : kCols;                   // LDS rows
-  __shared__ SharedTile st;
-  __shared__ __align__(16) E lds[2][FR * FS];
+  typedef SpreadLds<DT, RT, ACROSS> Lds;
+  constexpr int W = Lds::W, RB = Lds::RB, FS = Lds::FS, FL = W * kCols / 8 / kOutThreads;
+  constexpr int FV = ACROSS ? kCols / 8 : W / 8;           // vectors of a row of F
+  SharedTile& st = L.st;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
-  const int C = ACROSS ? d.K : d.N, R = d.R;
-  if (blockIdx.y == gridDim.y - 1) {  // the tiles of rows without an adapter
-    if ((int)blockIdx.x * kM < rs.T) copy_none<DT>(&st, d, rs, rs.tiles + blockIdx.x, add, ldadd, out, ldo, C, u);
+  const int C = ACROSS ? d.K : d.N, R = d.R, passes = sa.passes;
+  const u32x4* frag = sa.frag;
+  const float* scale = sa.scale;
+  const void* add = sa.add;
+  void* out = sa.out;
+  const int64_t ldadd = sa.ldadd, ldo = sa.ldo;
+  if (chunk == sa.columns) {  // the tiles of rows without an adapter
+    if (tile * kM < rs.T) copy_none<DT>(&st, d, rs, rs.tiles + tile, add, ldadd, out, ldo, C, sa.u);
     return;
   }
-  take_tile(&st, rs.kept + blockIdx.x);
+  take_tile(&st, rs.kept + tile);
   const int cnt = __builtin_amdgcn_readfirstlane(st.cnt);
   if (!cnt) return;
   const int rk = __builtin_amdgcn_readfirstlane(st.rank), a = __builtin_amdgcn_readfirstlane(st.a);
@@ -688,9 +732,9 @@ __global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs
       else fn[i] = load8<DT>(fbase, (uint32_t)min(c0 + row, C - 1) * R + (c < rk ? c : 0));
     }
   };
-  const int first = blockIdx.y * passes * kCols;
+  const int first = chunk * passes * kCols;
   fetch(first);
-  const size_t band = ((size_t)blockIdx.x * 4 + wave) * RB;
+  const size_t band = ((size_t)tile * 4 + wave) * RB;
   f32x4 sc[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
@@ -710,13 +754,12 @@ __global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs
   if (add && mine) fetch_add(first);
   if (ACROSS && RT == 1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) *(u32x4*)(lds[i] + (tid / 16 + 16) * FS + tid % 16 * 8) = u32x4{0, 0, 0, 0};
+    for (int i = 0; i < 2; ++i) *(u32x4*)(L.f[i] + (tid / 16 + 16) * FS + tid % 16 * 8) = u32x4{0, 0, 0, 0};
   }
   constexpr bool kOneScale = DT == MOE_T_BF16 || RB == 1;  // else the blocks' powers of two differ
   for (int p = 0; p < passes; ++p) {
     const int c0 = first + p * kCols, c = c0 + li * 8;
-    if (c0 >= C) break;
-    E* fs = lds[p & 1];
+    E* fs = L.f[p & 1];
 #pragma unroll
     for (int i = 0; i < FL; ++i) {
       const int v = tid + kOutThreads * i, frow = v / FV, fc = v % FV * 8;
@@ -730,7 +773,7 @@ __global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs
     }
     if (p + 1 < passes) fetch(c0 + kCols);
     __syncthreads();
-    if (!mine) continue;
+    if (!mine || c0 >= C) continue;
     f32x4 tot[8] = {};
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
@@ -770,10 +813,21 @@ __global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs
   }
 }
 
+template <int DT, int RT, bool ACROSS>
+__global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs, SpreadArgs sa) {
+  __shared__ SpreadLds<DT, RT, ACROSS> lds;
+  spread_body<DT, RT, ACROSS>(lds, d, rs, sa, blockIdx.x, blockIdx.y);
+}
+
 // ---------------------------------------------------------------------------
-// Backward pass: k_rows<ACROSS> forms v, k_spread<ACROSS> dx, k_outer dA and
-// dB, and k_grad_sum adds the partial dA and dB of adapters whose rows several
-// workgroups took.
+// Backward pass, in two launches or three (kMergeTiles): k_grad_first forms v
+// and, on the CUs that leaves free, dB, and k_grad_second dx and dA; or k_rows
+// forms v, k_spread dx, and k_grad_weights dA and dB.  k_grad_sum adds the
+// partial dA and dB of adapters whose rows several workgroups took.
+// 2,048 rows of 4 adapters, 6144 wide: rank 16, binary16 15.2, 14.6 and 4.2 us for
+// 3 passes over 25 MB and partial sums of 9; rank 64, bfloat16 16.1, 12.2 and 34.6,
+// the last for making three pieces of each value of u and v in every workgroup,
+// between barriers.
 // ---------------------------------------------------------------------------
 // Pieces of a factor of a weight gradient (an fp32 output).
 template <int DT>
@@ -813,45 +867,47 @@ constexpr int cmin(int a, int b) { return a < b ? a : b; }
 constexpr int kGradM = 32;                // rows taken at a time
 constexpr int kStride = 72;               // elements of an LDS row of 64 columns
 constexpr int kOutCols = kOutWaves * 64;  // columns of a workgroup
-constexpr int kOuterThreads = 512;        // two wavefronts per 64 columns: they take tiles in turn
-constexpr int kOuterWaves = kOuterThreads / kWave;
 
 // 32-row tiles of v or u held as fragments at a time (a multiple of 4).
 template <int RT>
 constexpr int kChunkTiles = RT <= 2 ? 8 : 4;
 
 struct OuterArgs {
-  const float *u, *v;  // [T][R] in the sorted order
+  const float *u, *v;  // [T][R]; v in the sorted order, u too where two launches follow k_rows
   int items, G, slots;
   const void *x, *dy;
   int64_t ldx, lddy;
   float *d_a, *d_b, *sums;  // sums: [slots][R K + R N], partial results
 };
 
-// A weight gradient's 64 columns per wavefront over an item's rows: the rows
-// of x (dA = sum_t v x^T) or dy (TR: dB = s_a sum_t dy u^T) pass through LDS, 32
-// at a time, two such tiles in flight per wavefront, against v or u, which the workgroup
-// holds as fragments for a few tiles at a time.  In binary16 those share one
-// power of two, the smallest so far; where a chunk brings a smaller one, the
-// sums are rescaled.
-template <int DT, int RT>
+template <int DT, int RT, int H>
 struct OuterLds {
-  float top[kOuterWaves];
+  float top[kOutWaves * H];
   int ids[2][kChunkTiles<RT> * kGradM];  // rows of this chunk and of the next
   union {
     struct {
       u32x4 frag[kChunkTiles<RT>][RT][kGradPieces<DT>][64];
-      typename Mat<DT>::elem rows[kOuterWaves][kGradM * kStride];
+      typename Mat<DT>::elem rows[kOutWaves * H][kGradM * kStride];
     };
-    f32x4 half[kOutWaves][4 * cmin(RT, 4)][64];  // the second wavefronts' sums (of up to 4 r tiles)
+    f32x4 half[H == 2 ? kOutWaves : 1][4 * cmin(RT, 4)][64];  // the second wavefronts' sums (of up to 4 r tiles)
   };
 };
 
-template <int DT, int RT, bool TR>
-__device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArgs& d, const RowSet& rs, const OuterArgs& ga,
+// A weight gradient's 64 columns per wavefront (H == 2: per two, which take
+// tiles in turn) over an item's rows: the rows of x (dA = sum_t v x^T) or dy (TR:
+// dB = s_a sum_t dy u^T) pass through LDS, 32 at a time, two such tiles in flight
+// per wavefront, against v or u (IDS: in the order of arrival), which the
+// workgroup holds as fragments for a chunk of tiles at a time.  In binary16 those
+// share one power of two, the smallest so far; where a chunk brings a smaller
+// one, the sums are rescaled.
+// Rank 16, 6144 wide: the 256 rows of a chunk take 4.0 us on 192 workgroups, 6.3
+// TB/s; 3.9 us pass before the first.  Four tiles in flight instead of two: no
+// change.
+template <int DT, int RT, int H, bool TR, bool IDS>
+__device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const AdapterArgs& d, const RowSet& rs, const OuterArgs& ga,
                                            int item, int chunk) {
   typedef typename Mat<DT>::elem E;
-  constexpr int NP = kGradPieces<DT>, CT = kChunkTiles<RT>, UW = (CT * RT + kOuterWaves - 1) / kOuterWaves;
+  constexpr int NP = kGradPieces<DT>, CT = kChunkTiles<RT>, WV = kOutWaves * H, UW = (CT * RT + WV - 1) / WV;
   constexpr int CR = CT * kGradM;  // rows of a chunk
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
   const int C = TR ? d.N : d.K, c0 = chunk * kOutCols + wave % kOutWaves * 64, half = wave / kOutWaves;
@@ -868,7 +924,8 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
     const int r = rs.pairs[min(it.first + min(i, it.cnt), rs.T - 1)];
     return i < it.cnt && (unsigned)r < (unsigned)rs.T ? r : -1;
   };
-  const auto id_of = [&](int j, int q) { return L.ids[j / CT & 1][j % CT * kGradM + lane / 8 + 8 * q]; };
+  const auto id_at = [&](int i) { return L.ids[i / CR & 1][i % CR]; };  // row of place i, this chunk or the next
+  const auto id_of = [&](int j, int q) { return id_at(j * kGradM + lane / 8 + 8 * q); };
   u32x4 rows[2][4];  // the next two tiles
   const auto fetch = [&](int j, u32x4 (&rows)[4]) {
 #pragma unroll
@@ -879,10 +936,11 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
   const auto fetch_v = [&](int j0) {
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
-      const int unit = min(wave + k * kOuterWaves, CT * RT - 1), r = min(unit % RT * 16 + li, d.R - 1);
+      const int unit = min(wave + k * WV, CT * RT - 1), r = min(unit % RT * 16 + li, d.R - 1);
       const int i = (j0 + unit / RT) * kGradM + g * 8;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) w[k][q] = v[(size_t)(it.first + min(i + q, it.cnt - 1)) * d.R + r];
+      for (int q = 0; q < 8; ++q)
+        w[k][q] = v[(size_t)(IDS ? max(id_at(i + q), 0) : it.first + min(i + q, it.cnt - 1)) * d.R + r];
     }
   };
   f32x4 acc[4][RT] = {};
@@ -891,25 +949,26 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
   int id = -1;
   if (tiles) {
     const int id0 = tid < CR ? fetch_id(0) : -1;
-    fetch_v(0);
+    if (!IDS) fetch_v(0);
     id = tid < CR ? fetch_id(CT) : -1;
     if (tid < CR) {
       L.ids[0][tid] = id0;
       L.ids[1][tid] = id;
     }
     __syncthreads();
+    if (IDS) fetch_v(0);
     fetch(half, rows[0]);
-    fetch(half + 2, rows[1]);
+    fetch(half + H, rows[1]);
     id = tid < CR ? fetch_id(2 * CT) : -1;
   }
   for (int j0 = 0; j0 < tiles; j0 += CT) {
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
-      const int unit = wave + k * kOuterWaves, r = unit % RT * 16 + li, i = (j0 + unit / RT) * kGradM + g * 8;
+      const int unit = wave + k * WV, r = unit % RT * 16 + li, i = (j0 + unit / RT) * kGradM + g * 8;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        w[k][q] = unit < CT * RT && r < rk && i + q < it.cnt ? w[k][q] : 0.0f;
+        w[k][q] = unit < CT * RT && r < rk && (IDS ? id_at(min(i + q, j0 * kGradM + CR - 1)) >= 0 : i + q < it.cnt) ? w[k][q] : 0.0f;
         top = fmaxf(top, finite_abs(w[k][q]));
       }
     }
@@ -924,7 +983,7 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
     }
     if (DT == MOE_T_F16) {
 #pragma unroll
-      for (int q = 0; q < kOuterWaves; ++q) top = fmaxf(top, L.top[q]);
+      for (int q = 0; q < WV; ++q) top = fmaxf(top, L.top[q]);
       if (top > 0.0f) {
         const int en = any ? min(e, scale_exp<DT>(top)) : scale_exp<DT>(top);
         if (any && en < e) {
@@ -940,7 +999,7 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
     }
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
-      const int unit = wave + k * kOuterWaves;
+      const int unit = wave + k * WV;
       if (unit < CT * RT) {
         v8_t<DT> p[NP];
         split_pieces<DT, NP>(w[k], e, p);
@@ -954,7 +1013,7 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *(u32x4*)(stage + (lane / 8 + 8 * q) * kStride + lane % 8 * 8) = keep(rows[q], id_of(j, q) >= 0 && col < C);
-      if (j + 4 < tiles) fetch(j + 4, rows);
+      if (j + 2 * H < tiles) fetch(j + 2 * H, rows);
       lds_order();
       v8_t<DT> xf[4];
 #pragma unroll
@@ -973,14 +1032,14 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
       lds_order();
     };
     const int j1 = min(j0 + CT, tiles);
-    for (int j = j0 + half; j < j1; j += 4) {
+    for (int j = j0 + half; j < j1; j += 2 * H) {
       tile(j, rows[0]);
-      if (j + 2 < j1) tile(j + 2, rows[1]);
+      if (j + H < j1) tile(j + H, rows[1]);
     }
   }
   // the two wavefronts of each 64 columns, 4 r tiles at a time
 #pragma unroll
-  for (int r0 = 0; r0 < RT; r0 += 4) {
+  for (int r0 = 0; r0 < (H == 2 ? RT : 0); r0 += 4) {
     constexpr int RH = RT < 4 ? RT : 4;
     __syncthreads();
     if (half) {
@@ -1016,17 +1075,50 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT>& L, const AdapterArg
     }
 }
 
-// Workgroups [0, nA) take dA, the rest dB.
-template <int DT, int RT>
-__global__ __launch_bounds__(kOuterThreads) void k_outer(AdapterArgs d, RowSet rs, OuterArgs ga) {
-  __shared__ OuterLds<DT, RT> lds;
-  const int ka = (d.K + kOutCols - 1) / kOutCols, kb = (d.N + kOutCols - 1) / kOutCols, nA = ga.items * ka;
+// Workgroups [0, rows_groups) form v (tile, block of r, bands: as k_rows), the
+// rest dB.
+template <int DT, int MT, int BT, int RT>
+__global__ __launch_bounds__(kRowThreads) void k_grad_first(AdapterArgs d, RowSet rs, const void* dy, int64_t lddy, RowsOut out,
+                                                           int blocks, int rows_groups, OuterArgs ga) {
+  __shared__ union Lds {
+    RowsLds<MT, BT, true> rows;
+    OuterLds<DT, RT, 2> outer;
+    __device__ Lds() {}
+  } lds;
   const int b = blockIdx.x;
-  if (b < nA) grad_outer<DT, RT, false>(lds, d, rs, ga, b / ka, b % ka);
-  else grad_outer<DT, RT, true>(lds, d, rs, ga, (b - nA) / kb, (b - nA) % kb);
+  if (b < rows_groups) {
+    const int y = b / rs.tiles;
+    return rows_body<DT, MT, BT, true, false>(lds.rows, d, rs, dy, lddy, out, b % rs.tiles, y % blocks, y / blocks, 1);
+  }
+  const int kb = (d.N + kOutCols - 1) / kOutCols;
+  grad_outer<DT, RT, 2, true, true>(lds.outer, d, rs, ga, (b - rows_groups) / kb, (b - rows_groups) % kb);
 }
 
-// Sums the partial gradients of adapters that have several.
+// Workgroups [0, nA) take dA, the rest dx.
+template <int DT, int RT>
+__global__ __launch_bounds__(kOutThreads) void k_grad_second(AdapterArgs d, RowSet rs, SpreadArgs sa, OuterArgs ga) {
+  __shared__ union Lds {
+    SpreadLds<DT, RT, true> spread;
+    OuterLds<DT, RT, 1> outer;
+    __device__ Lds() {}
+  } lds;
+  const int ka = (d.K + kOutCols - 1) / kOutCols, nA = ga.items * ka, b = blockIdx.x;
+  if (b < nA) grad_outer<DT, RT, 1, false, false>(lds.outer, d, rs, ga, b / ka, b % ka);
+  else spread_body<DT, RT, true>(lds.spread, d, rs, sa, (b - nA) % rs.tiles, (b - nA) / rs.tiles);
+}
+
+// Workgroups [0, nA) take dA, the rest dB.
+template <int DT, int RT>
+__global__ __launch_bounds__(2 * kOutThreads) void k_grad_weights(AdapterArgs d, RowSet rs, OuterArgs ga) {
+  __shared__ OuterLds<DT, RT, 2> lds;
+  const int ka = (d.K + kOutCols - 1) / kOutCols, kb = (d.N + kOutCols - 1) / kOutCols, nA = ga.items * ka;
+  const int b = blockIdx.x;
+  if (b < nA) grad_outer<DT, RT, 2, false, false>(lds, d, rs, ga, b / ka, b % ka);
+  else grad_outer<DT, RT, 2, true, false>(lds, d, rs, ga, (b - nA) / kb, (b - nA) % kb);
+}
+
+// Sums the partial gradients of adapters that have several, in their order (4 to
+// 6 us, mostly the launch).
 __global__ __launch_bounds__(256) void k_grad_sum(AdapterArgs d, RowSet rs, const float* part, int slots, int G,
                                                   float* d_a, float* d_b) {
   const int a = blockIdx.x, lane = threadIdx.x & 63;
@@ -1047,8 +1139,7 @@ __global__ __launch_bounds__(256) void k_grad_sum(AdapterArgs d, RowSet rs, cons
   if (mine <= 0) return;
   const size_t na = (size_t)d.R * d.K / 4, nb = (size_t)d.R * d.N / 4;
   for (size_t i = (size_t)blockIdx.y * 256 + threadIdx.x; i < na + nb; i += (size_t)gridDim.y * 256) {
-    f32x4 s = {0, 0, 0, 0};
-    for (int j = 0; j < mine; ++j) s += ((const f32x4*)part)[(size_t)(slot + j) * (na + nb) + i];
+    const f32x4 s = sum_segments(part + ((size_t)slot * (na + nb) + i) * 4, (na + nb) * 4, mine);
     if (i < na) ((f32x4*)d_a)[(size_t)a * na + i] = s;
     else ((f32x4*)d_b)[(size_t)a * nb + i - na] = s;
   }
@@ -1077,11 +1168,25 @@ int check_adapter_ptrs(const moe_adapters_t* d) {
   return MOE_OK;
 }
 
-constexpr int kSmallRows = 64;   // rows that a workgroup groups by itself
-constexpr int kSegment = 1024;   // columns per K-segment of a small batch: two steps of every wavefront
-constexpr int kWideRows = 4096;  // rows from which k_rows takes 64 r at a time
-constexpr int kSpreadGroups = 512;  // workgroups of k_spread below which none takes more than one run
-constexpr int kWanted = 256;     // workgroups of k_outer that fill the GPU
+// Rows that each workgroup groups by itself, in tiles of 16: so, and sorted
+// first, 6144 wide: one row 9.0 and 15.0 us, 48 rows of 32 adapters 15.2 and 21.0, 64
+// rows of 4 13.0 and 21.1.  (64: a lane each.)
+constexpr int kSmallRows = 64;
+// Columns per K-segment of a small batch: two steps of every wavefront.  Those
+// three calls with half as many 9.1, 16.7 and 13.0, with twice as many 9.2, 13.8, 13.8.
+constexpr int kSegment = 1024;
+constexpr int kWideRows = 4096;  // rows from which k_rows takes 64 r at a time (RowsShape)
+constexpr int kWanted = 256;     // workgroups of k_grad_weights that fill the GPU
+// Rank fragments up to which the gradients take two launches.  Two and three
+// launches, 6144 wide, 4 adapters: 2,048 rows rank 16 34.0 and 39.7 us, rank 32 45.3
+// and 47.1, rank 64 78.8 and 63.0 (the kernels' register and LDS needs add up);
+// 8,000 rows, 2048 to 6144 wide, rank 16 63 and 93; 200 rows, 2048 wide 13.0 and
+// 15.4.
+constexpr int kMergeTiles = 2;
+// Workgroups of k_spread below which none takes more than one run.  1,801 and
+// 7,204 rows of 6144, rank 64: 12.6 and 40.3 us; 256: 15.2 and 52.9; 1,024: 12.8 and
+// 41.6; one run each: 12.8 and 42.1.
+constexpr int kSpreadGroups = 512;
 
 // Matrix fragments of a rank: 1, 2, 4 or 8 of 16.
 int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
@@ -1091,7 +1196,7 @@ struct AdapterPlan {
   int tiles;              // bound on tiles of adapters (a multiple of kXcds, and no less than T / kM)
   int stiles, S;          // small: tiles, K-segments
   int rb;                 // blocks of 32 r
-  int G, items, slots;    // k_outer
+  int G, items, slots;    // weight gradients
   size_t kept, part, frag, scale, v, u, sums;
   size_t offsets, pairs, pos, sort, total;
 };
@@ -1103,10 +1208,15 @@ AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
   p.stiles = std::min(T, T / kSmallM + d.n + 1);
   p.S = ceil_div(d.K, kSegment);
   p.rb = (rank_tiles(d.R) + 1) / 2;
-  // An adapter's rows go to one workgroup per 256 columns, or, where few
-  // adapters leave the GPU empty, to several (whose results are then added).
-  const int cols = ceil_div(d.K, kOutCols) + ceil_div(d.N, kOutCols), wanted = ceil_div(kWanted, cols);
-  p.G = d.n >= (wanted + 1) / 2 ? 2048 : std::max(256, ceil_div(T, wanted / d.n * kGradM) * kGradM);
+  // Rows of an adapter per workgroup of its weight gradients: more leave the
+  // last one working alone, fewer cost partial sums (R (K + N) floats each).
+  // Rank 16, 4 adapters: 2,048 rows of 6144 34.0 us with 256, 40.4 with 512, 51.5 with
+  // 1,024; 8,000 rows, 2048 to 6144 wide 63.0, 67.0, 81.2.  Above rank 32 a workgroup takes whole
+  // adapters where there are enough of them to fill the GPU: rank 64, 2,048 rows
+  // of 4 adapters 63 us, in parts of 512 rows 71; of one adapter 67 in parts of 352.
+  const int tiles = rank_tiles(d.R), cols = ceil_div(d.K, kOutCols) + ceil_div(d.N, kOutCols), wanted = ceil_div(kWanted, cols);
+  if (tiles <= kMergeTiles) p.G = std::max(256, ceil_div(T, 64 * kGradM) * kGradM);
+  else p.G = d.n >= (wanted + 1) / 2 ? 2048 : std::max(256, ceil_div(T, wanted / d.n * kGradM) * kGradM);
   p.items = T / p.G + d.n;
   p.slots = T > p.G ? 2 * (T / p.G) : 0;
   size_t o = 0;
@@ -1124,7 +1234,7 @@ AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
   p.frag = take((size_t)p.tiles * 4 * p.rb * 2 * 1024);
   p.scale = take((size_t)p.tiles * 4 * p.rb * 16 * 4);
   p.v = take((size_t)T * d.R * 4);
-  p.u = take((size_t)T * d.R * 4);
+  p.u = take(tiles > kMergeTiles ? (size_t)T * d.R * 4 : 0);
   p.sums = take((size_t)p.slots * d.R * ((size_t)d.K + d.N) * 4);
   p.total = o;
   return p;
@@ -1149,15 +1259,21 @@ void by_shape(const moe_adapters_t& d, F f) {
   else ranks(Const<MOE_T_BF16>{});
 }
 
+// Bands and fragments of r per workgroup of k_rows: fewer workgroups re-read
+// less, more fill the GPU.  At 6144 columns, rank 64 (mixed), bfloat16: 1,801
+// rows 14.4 us with two bands and 32 r, 16.6 with one band and 64 r, 17.7 with
+// one band and 32 r, 18.6 with two bands and 64 r; 7,204 rows 30.7 us with two
+// bands and 64 r, 37.8 with 32 r, 32.6 with four bands and 32 r.  Rank 16, 1,801
+// rows: 9.7 us with one band, 11.8 with two.
+template <int RT>
+struct RowsShape {
+  static constexpr int BT = RT < 2 ? RT : 2, WT = RT < 4 ? RT : 4, MT = RT == 1 ? 1 : 2;
+};
+
 template <int DT, int RT, bool ACROSS>
 void launch_rows(const AdapterPlan& p, const AdapterArgs& g, const RowSet& rs, const void* x, int64_t ldx,
                  const RowsOut& out, hipStream_t s) {
-  // Bands and fragments of r per workgroup: fewer workgroups re-read less, more
-  // fill the GPU.  k_rows at 6144 columns, rank 64 (mixed), bfloat16: 1,801 rows
-  // 14.4 us as below, 16.6 with one band and 64 r, 17.7 with one band and 32 r,
-  // 18.6 with two bands and 64 r; 7,204 rows 30.7 us as below, 37.8 with 32 r,
-  // 32.6 with four bands and 32 r.  Rank 16, 1,801 rows: 9.7 us, 11.8 with two bands.
-  constexpr int BT = RT < 2 ? RT : 2, WT = RT < 4 ? RT : 4, MT = RT == 1 ? 1 : 2;
+  constexpr int BT = RowsShape<RT>::BT, WT = RowsShape<RT>::WT, MT = RowsShape<RT>::MT;
   if (!ACROSS && p.small)
     k_rows<DT, 1, BT, ACROSS, true><<<dim3(p.stiles, ceil_div(g.R, BT * 16), p.S), kRowThreads, 0, s>>>(g, rs, x, ldx, out);
   else if (rs.T < kWideRows)
@@ -1166,13 +1282,24 @@ void launch_rows(const AdapterPlan& p, const AdapterArgs& g, const RowSet& rs, c
     k_rows<DT, 2, WT, ACROSS, false><<<dim3(p.tiles, ceil_div(g.R, WT * 16), 2), kRowThreads, 0, s>>>(g, rs, x, ldx, out);
 }
 
-template <int DT, int RT, bool ACROSS>
-void launch_spread(const AdapterPlan& p, const AdapterArgs& g, const RowSet& rs, int width, const u32x4* frag,
-                   const float* scale, const void* add, int64_t ldadd, void* out, int64_t ldo, float* u, hipStream_t s) {
+template <int DT, int RT>
+void launch_grad_first(const AdapterPlan& p, const AdapterArgs& g, const RowSet& rs, const void* dy, int64_t lddy,
+                       const RowsOut& out, const OuterArgs& ga, hipStream_t s) {
+  constexpr int BT = RowsShape<RT>::BT, WT = RowsShape<RT>::WT, MT = RowsShape<RT>::MT;
+  const int kb = ceil_div(g.N, kOutCols);
+  const auto launch = [&](auto kernel, int mt, int bt) {
+    const int blocks = ceil_div(g.R, bt * 16), rows = rs.T ? p.tiles * blocks * (4 / mt) : 0;
+    kernel<<<rows + p.items * kb, kRowThreads, 0, s>>>(g, rs, dy, lddy, out, blocks, rows, ga);
+  };
+  if (rs.T < kWideRows) launch(k_grad_first<DT, MT, BT, RT>, MT, BT);
+  else launch(k_grad_first<DT, 2, WT, RT>, 2, WT);
+}
+
+// Runs of columns per workgroup of the second launch, and workgroups per tile.
+void split_runs(const AdapterPlan& p, int width, SpreadArgs* sa) {
   const int runs = ceil_div(width, kCols);
-  const int passes = std::max(1, std::min(runs, (int)((int64_t)p.tiles * runs / kSpreadGroups)));
-  k_spread<DT, RT, ACROSS><<<dim3(p.tiles, ceil_div(runs, passes) + 1), kOutThreads, 0, s>>>(
-      g, rs, frag, scale, add, ldadd, out, ldo, u, passes);
+  sa->passes = std::max(1, std::min(runs, (int)((int64_t)p.tiles * runs / kSpreadGroups)));
+  sa->columns = ceil_div(runs, sa->passes);
 }
 
 }  // namespace
@@ -1212,7 +1339,7 @@ int moe_adapter_forward(const moe_adapters_t* d, const void* x, int64_t ldx, int
     float* part = (float*)(w + p.part);
     by_shape(*d, [&](auto dt, auto rt) {
       constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-      launch_rows<DT, RT, false>(p, g, rs, x, ldx, RowsOut{part, nullptr, nullptr, frag, scale, p.rb}, s);
+      launch_rows<DT, RT, false>(p, g, rs, x, ldx, RowsOut{part, frag, scale, p.rb, nullptr, nullptr}, s);
       k_expand_small<DT, RT><<<dim3(p.stiles, ceil_div(d->N, kOutWaves * kCols)), kOutThreads, 0, s>>>(
           g, rs, part, p.S, u, add, ldadd, y, ldy);
     });
@@ -1225,10 +1352,12 @@ int moe_adapter_forward(const moe_adapters_t* d, const void* x, int64_t ldx, int
     pairs = q;
   }
   const RowSet rs{ids, offsets, pairs, kept, T, p.tiles};
+  SpreadArgs sa{frag, scale, add, ldadd, y, ldy, u, 0, 0};
+  split_runs(p, d->N, &sa);
   by_shape(*d, [&](auto dt, auto rt) {
     constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-    launch_rows<DT, RT, false>(p, g, rs, x, ldx, RowsOut{u, nullptr, nullptr, frag, scale, p.rb}, s);
-    launch_spread<DT, RT, false>(p, g, rs, d->N, frag, scale, add, ldadd, y, ldy, u, s);
+    launch_rows<DT, RT, false>(p, g, rs, x, ldx, RowsOut{u, frag, scale, p.rb, nullptr, nullptr}, s);
+    k_spread<DT, RT, false><<<dim3(p.tiles, sa.columns + 1), kOutThreads, 0, s>>>(g, rs, sa);
   });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
@@ -1261,15 +1390,23 @@ int moe_adapter_backward(const moe_adapters_t* d, const void* dy, int64_t lddy, 
   u32x4* frag = (u32x4*)(w + p.frag);
   float *scale = (float*)(w + p.scale), *v = (float*)(w + p.v), *us = (float*)(w + p.u), *sums = (float*)(w + p.sums);
   const RowSet rs{ids, offsets, pairs, (SharedTile*)(w + p.kept), T, p.tiles};
-  const OuterArgs ga{us, v, p.items, p.G, p.slots, x, dy, ldx, lddy, d_a, d_b, sums};
-  const int cols = ceil_div(d->K, kOutCols) + ceil_div(d->N, kOutCols);
+  OuterArgs ga{u, v, p.items, p.G, p.slots, x, dy, ldx, lddy, d_a, d_b, sums};
+  SpreadArgs sa{frag, scale, add, ldadd, dx, lddx, nullptr, 0, 0};
+  split_runs(p, d->K, &sa);
   by_shape(*d, [&](auto dt, auto rt) {
     constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-    if (T) launch_rows<DT, RT, true>(p, g, rs, dy, lddy, RowsOut{v, u, us, frag, scale, p.rb}, s);
-    if (T && dx) launch_spread<DT, RT, true>(p, g, rs, d->K, frag, scale, add, ldadd, dx, lddx, nullptr, s);
-    k_outer<DT, RT><<<p.items * cols, kOuterThreads, 0, s>>>(g, rs, ga);
+    const int ka = p.items * ceil_div(d->K, kOutCols), kb = p.items * ceil_div(d->N, kOutCols);
+    if constexpr (RT <= kMergeTiles) {
+      launch_grad_first<DT, RT>(p, g, rs, dy, lddy, RowsOut{v, frag, scale, p.rb, nullptr, nullptr}, ga, s);
+      k_grad_second<DT, RT><<<ka + (dx && T ? p.tiles * (sa.columns + 1) : 0), kOutThreads, 0, s>>>(g, rs, sa, ga);
+    } else {
+      if (T) launch_rows<DT, RT, true>(p, g, rs, dy, lddy, RowsOut{v, frag, scale, p.rb, u, us}, s);
+      if (T && dx) k_spread<DT, RT, true><<<dim3(p.tiles, sa.columns + 1), kOutThreads, 0, s>>>(g, rs, sa);
+      ga.u = us;
+      k_grad_weights<DT, RT><<<ka + kb, 2 * kOutThreads, 0, s>>>(g, rs, ga);
+    }
   });
-  if (p.slots) k_grad_sum<<<dim3(d->n, 64), 256, 0, s>>>(g, rs, sums, p.slots, p.G, d_a, d_b);
+  if (p.slots) k_grad_sum<<<dim3(d->n, ceil_div((int64_t)d->R * (d->K + d->N), 2048)), 256, 0, s>>>(g, rs, sums, p.slots, p.G, d_a, d_b);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
