@@ -807,9 +807,10 @@ __device__ __forceinline__ void spread_body(SpreadLds<DT, RT, ACROSS>& L, const 
       res[i] = pack_vec<DT>(o);
     }
     if (add && p + 1 < passes) fetch_add(c0 + kCols);
+    // (past the L2s, whose dirty lines the launch's end would wait for)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (row[i] >= 0 && c < C) *(u32x4*)((E*)out + (size_t)row[i] * ldo + c) = res[i];
+      if (row[i] >= 0 && c < C) __builtin_nontemporal_store(res[i], (u32x4*)((E*)out + (size_t)row[i] * ldo + c));
   }
 }
 

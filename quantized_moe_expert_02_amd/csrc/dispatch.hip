@@ -1,6 +1,7 @@
 // Tokens sorted by expert, their rows laid out and combined, and the
 // gradients (include/moe_dispatch.h).
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.h"
 
@@ -11,8 +12,15 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortMaxBlocks = 128;
-constexpr int kSortOne = 4;       // up to this many times 1,024 slots one workgroup sorts alone
-constexpr int kSortRead = 32768;  // up to this many slots each workgroup counts all of them by itself, in one launch
+// Up to this many times 1,024 slots one workgroup sorts alone, each costing it
+// about 1.3 us: with 8 instead, 4,800 slots of 256 experts 8.9 us (5 workgroups: 6.0), 8,000
+// 12.8 (6.4).
+constexpr int kSortOne = 4;
+// Up to this many slots each workgroup counts all of them by itself, in one
+// launch.  One launch and two (whose gap costs 3 us on the host and about 1 on the
+// GPU): 4,800 slots 6.0 us and 7.8, 16,384 7.8 and 7.7, 32,768 10.6 and 8.7, 48,000
+// 12.3 and 11.2, 65,536 14.7 and 10.0.
+constexpr int kSortRead = 32768;
 
 // Slots per workgroup (a multiple of kSortThreads) and number of workgroups.
 struct SortSplit {
@@ -62,7 +70,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const int32_t* idx,
 // walked 1,024 at a time: a wavefront ranks its 64 slots by matching ids, and
 // thread e turns the wavefronts' counts of expert e into places.  ONE: a single
 // workgroup, which holds its slots in registers.  cnt == NULL: every workgroup
-// counts all slots by itself (reading them again costs less than a launch).
+// counts all slots by itself.  Bound by its chain of steps, not by its 3 words per
+// slot: 16,384 slots of 256 experts 7.8 us.
 template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx, int n, int E, int bits, int align,
                                                              int rows, int per_block, const int32_t* cnt,
@@ -186,7 +195,10 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(const int32_t* idx,
 
 // Sort and rows of a small batch in one launch (align 1, up to kSmallSlots
 // slots): every workgroup sorts all slots for itself, then lays out its part of
-// one token's row; the first one also writes the order.
+// one token's row; the first one also writes the order.  Bound by that chain of
+// steps: one token of 6144 binary16, top-8 of 256 3.8 us, 128 tokens 9.0.
+// So, and as sort and rows: 8 tokens 4.4 and 10.1 us, 50 5.9 and 10.7, 128 9.0 and
+// 11.9, 200 (1,600 slots) 17.6 and 13.6.
 constexpr int kSmallSlots = 1024;
 constexpr int kSmallThreads = 256;
 
@@ -275,43 +287,55 @@ __global__ __launch_bounds__(kSmallThreads) void k_dispatch_small(const u32x4* x
   for (int r = all + t; r < n; r += T) xs[(size_t)r * nv + i] = u32x4{0, 0, 0, 0};
 }
 
-// xs[pos(t,j)] = x[t], token by token, 16-byte vectors; workgroups past the
-// tokens' zero the rows that hold no slot, a row per thread looked over.
+// xs[pos(t,j)] = x[t], token by token, 16-byte vectors: x is read once.
+// Workgroups past the tokens' zero the rows that hold no slot, a row per thread
+// looked over.  Bound by the writes: 2,048 tokens of 6144 binary16, top-8: 36.1 us,
+// 6.3 TB/s (a fill of 2 GiB reaches 6.9).
 constexpr int kRowThreads = 256;  // most threads of a workgroup of the row kernels
 
+// Rows past the last-level cache (256 MB) are read and written without a place
+// in the caches.  Written so, they also leave no dirty lines in the dies' L2s,
+// which the end of the launch would wait for.
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_row(const u32x4* p) {
+  return STREAM ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_row(u32x4* p, u32x4 v) {
+  if (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+template <bool STREAM>
 __device__ __forceinline__ void zero_pad_rows(const int32_t* pairs, int rows, int part, u32x4* out, int nv) {
   const int lane = threadIdx.x & 63, r0 = part * blockDim.x + (threadIdx.x & ~63u), r = r0 + lane;
   uint64_t pad = __ballot(r < rows && pairs[min(r, rows - 1)] < 0);  // a wavefront looks over 64 rows
   for (; pad; pad &= pad - 1) {
     u32x4* o = out + (size_t)(r0 + __builtin_ctzll(pad)) * nv;
-    for (int i = lane; i < nv; i += 64) o[i] = u32x4{0, 0, 0, 0};
+    for (int i = lane; i < nv; i += 64) store_row<STREAM>(o + i, u32x4{0, 0, 0, 0});
   }
 }
 
+template <bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, int T, int nv, int k, int rows,
                                                               const int32_t* pos, const int32_t* pairs, u32x4* xs) {
   const int t = blockIdx.x;
-  if (t >= T) return zero_pad_rows(pairs, rows, t - T, xs, nv);
+  if (t >= T) return zero_pad_rows<STREAM>(pairs, rows, t - T, xs, nv);
   const int32_t* p = pos + (size_t)t * k;
   for (int i = threadIdx.x; i < nv; i += blockDim.x) {
     const u32x4 v = x[(size_t)t * nv + i];
     for (int j = 0; j < k; ++j) {
       const int r = p[j];
-      if (r >= 0) xs[(size_t)r * nv + i] = v;
+      if (r >= 0) store_row<STREAM>(xs + (size_t)r * nv + i, v);
     }
   }
 }
 
 // y[t] = add[t] + sum_j w[t][j] o[pos(t,j)] (w == NULL: all ones), slots in
-// order, 8 rows in flight.
+// order, 8 rows in flight.  Bound by reading o: 2,048 tokens of 6144 binary16,
+// top-8, with add: 42.8 us, 5.9 TB/s (a copy of 400 MB reaches 5.4); 8 tokens 3.5 us.
 constexpr int kSlotsAtOnce = 8;
 
-// Rows of o that are read once: past the last-level cache (256 MB) they are
-// read without a place in it.
-template <bool STREAM>
-__device__ __forceinline__ u32x4 load_row(const u32x4* p) {
-  return STREAM ? __builtin_nontemporal_load(p) : *p;
-}
 template <int DT, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int rows, int nv, const float* w,
                                                             const int32_t* pos, int k, const u32x4* add, u32x4* y) {
@@ -344,13 +368,14 @@ __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int 
       for (int c = 0; c < VE; ++c) acc[c] = fmaf(wj[j], f[c], acc[c]);
     }
   }
-  y[(size_t)t * nv + i] = pack_vec<DT>(acc);
+  store_row<STREAM>(y + (size_t)t * nv + i, pack_vec<DT>(acc));
 }
 
 // d_o[pos(t,j)] = w dy[t]; dw[t][j] = <dy[t], o[pos(t,j)]>.  One workgroup per
 // token, 8 slots at a time: their rows of o in flight together.  The workgroups
-// past the tokens' zero padding rows.
-template <int DT, bool STREAM>
+// past the tokens' zero padding rows.  Bound by reading o and writing d_o: 4,096
+// tokens of 2048 bfloat16, top-8, groups padded to 64: 63.5 us, 5.2 TB/s.
+template <int DT, bool STREAM_O, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, const u32x4* o, int rows, int nv,
                                                               const float* w, const int32_t* pos,
                                                               const int32_t* pairs, int T, int k, u32x4* d_o,
@@ -358,7 +383,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, c
   constexpr int VE = kVec<DT>, S = kSlotsAtOnce, W = kRowThreads / kWave;
   __shared__ float part[W][S];
   const int t = blockIdx.x, tid = threadIdx.x;
-  if (t >= T) return zero_pad_rows(pairs, rows, t - T, d_o, nv);
+  if (t >= T) return zero_pad_rows<STREAM>(pairs, rows, t - T, d_o, nv);
   for (int j0 = 0; j0 < k; j0 += S) {
     int r[S];
     float wj[S], dot[S];
@@ -375,7 +400,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, c
       u32x4 v[S];
 #pragma unroll
       for (int j = 0; j < S; ++j)
-        if (r[j] >= 0) v[j] = load_row<STREAM>(o + (size_t)r[j] * nv + i);  // (uniform)
+        if (r[j] >= 0) v[j] = load_row<STREAM_O>(o + (size_t)r[j] * nv + i);  // (uniform)
       float g[VE];
       unpack_vec<DT>(gv, g);
 #pragma unroll
@@ -388,7 +413,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, c
           dot[j] = fmaf(g[c], f[c], dot[j]);
           q[c] = g[c] * wj[j];
         }
-        d_o[(size_t)r[j] * nv + i] = pack_vec<DT>(q);
+        store_row<STREAM>(d_o + (size_t)r[j] * nv + i, pack_vec<DT>(q));
       }
     }
 #pragma unroll
@@ -407,7 +432,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, c
   }
 }
 
-constexpr size_t kStream = (size_t)112 << 20;  // bytes of o from which it is streamed
+constexpr size_t kStream = (size_t)112 << 20;  // bytes of rows from which they are streamed
 
 // Threads of a row kernel's workgroup: the row's vectors in as few equal parts as
 // 256 threads allow (a 257-vector row: two parts of 192 threads).
@@ -515,9 +540,15 @@ int moe_dispatch(const void* x, int32_t dtype, int32_t T, int32_t H, const int32
   st = moe_sort(topk_idx, T, k, n_experts, align, offsets, pairs, pos, ws, ws_bytes, stream);
   if (st != MOE_OK || T == 0) return st;
   const int rows = (int)moe_sort_rows(T, k, n_experts, align);
-  const int threads = row_threads(nv);
-  k_scatter_rows<<<T + (rows + threads - 1) / threads, threads, 0, (hipStream_t)stream>>>(
-      (const u32x4*)x, T, nv, k, rows, pos, pairs, (u32x4*)xs);
+  const int threads = row_threads(nv), grid = T + (rows + threads - 1) / threads;
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, threads, 0, (hipStream_t)stream>>>((const u32x4*)x, T, nv, k, rows, pos, pairs, (u32x4*)xs);
+  };
+  // 6144 wide, top-8, binary16, a call after another, plain and streamed: 50 MB of
+  // rows 18.8 us and 18.5, 88 MB 22.1 and 23.6, 118 MB 31.1 and 29.4, 147 MB 42.6 and
+  // 35.6, 201 MB 55.3 and 47.6.
+  if ((size_t)n * nv * 16 >= kStream) launch(k_scatter_rows<true>);
+  else launch(k_scatter_rows<false>);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
@@ -532,8 +563,9 @@ static int gather_sum(const void* o, int32_t dtype, int32_t rows, int32_t H, con
     kernel<<<grid, threads, 0, (hipStream_t)stream>>>((const u32x4*)o, rows, nv, w, pos, k, (const u32x4*)add,
                                                          (u32x4*)y);
   };
-  // 6144 wide, top-8, binary16, plain and streamed: 101 MB of rows 23.1 and 22.5 us, 201 MB 46.8 and 42.9, 403 MB 99.8 and
-  // 84.4; 25 MB 7.0 and 7.9.
+  // 6144 wide, top-8, binary16, plain and streamed: 101 MB of rows 23.1 and 22.5 us,
+  // 201 MB 46.8 and 42.9, 403 MB 99.8 and 84.4; 25 MB 7.0 and 7.9.  (201 MB, y
+  // written plainly and streamed: 42.8 and 40.4.)
   const bool stream_rows = (size_t)T * k * nv * 16 >= kStream;
   if (dtype == MOE_T_F16) stream_rows ? launch(k_gather_sum<MOE_T_F16, true>) : launch(k_gather_sum<MOE_T_F16, false>);
   else if (dtype == MOE_T_BF16) stream_rows ? launch(k_gather_sum<MOE_T_BF16, true>) : launch(k_gather_sum<MOE_T_BF16, false>);
@@ -573,13 +605,20 @@ int moe_combine_backward(const void* dy, const void* o, int32_t dtype, int32_t r
     kernel<<<grid, threads, 0, (hipStream_t)stream>>>((const u32x4*)dy, (const u32x4*)o, rows, nv, topk_w, pos,
                                                          pairs, T, k, (u32x4*)d_o, dw);
   };
-  // Plain and streamed, as there: 101 MB of rows 37.2 and 36.4 us, 134 MB (padded) 70.7 and 64.0, 201 MB 81.6 and 66.7,
-  // 403 MB 168 and 157; 50 MB 18.2 and 20.0.
-  const bool stream_rows = (size_t)T * k * nv * 16 >= kStream;
-  if (dtype == MOE_T_F16) stream_rows ? launch(k_combine_grad<MOE_T_F16, true>) : launch(k_combine_grad<MOE_T_F16, false>);
-  else if (dtype == MOE_T_BF16)
-    stream_rows ? launch(k_combine_grad<MOE_T_BF16, true>) : launch(k_combine_grad<MOE_T_BF16, false>);
-  else stream_rows ? launch(k_combine_grad<MOE_T_F32, true>) : launch(k_combine_grad<MOE_T_F32, false>);
+  // o is streamed where it and d_o together are that large, d_o where it is.  2048
+  // wide, top-8, binary16, a call after another, o of 33 MB plain 12.8 us, o streamed
+  // 14.9, both 15.1; 66 MB 26.5, 26.9, 27.2; 82 MB 36.1, 31.8, 34.4; 98 MB 44.6, 36.8,
+  // 41.5; 131 MB 56.2, 49.5, 49.3; 164 MB, both 63.9 and o 69.0.
+  const size_t bytes = (size_t)T * k * nv * 16;
+  const auto by_size = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (bytes >= kStream) launch(k_combine_grad<DT, true, true>);
+    else if (2 * bytes >= kStream) launch(k_combine_grad<DT, true, false>);
+    else launch(k_combine_grad<DT, false, false>);
+  };
+  if (dtype == MOE_T_F16) by_size(std::integral_constant<int, MOE_T_F16>{});
+  else if (dtype == MOE_T_BF16) by_size(std::integral_constant<int, MOE_T_BF16>{});
+  else by_size(std::integral_constant<int, MOE_T_F32>{});
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 

@@ -9,7 +9,8 @@
 // MB for 2,048 tokens, top-8, 6144 wide) out of the 6 MB of Wr.  The two steps
 // that gather Wr therefore run by column slice: a workgroup holds all experts'
 // 64 (32 above 512 experts) columns in LDS and takes a range of tokens, so
-// that Wr and x each cross the memory a few times only.
+// that Wr and x each cross the memory a few times only.  What bounds them is the
+// vector unit: 8 multiply-adds of a lane come with about 14 other instructions.
 #include <algorithm>
 #include <type_traits>
 
@@ -67,7 +68,8 @@ __device__ __forceinline__ int slot_place(const RouteArgs& a, int t, int j) {
   return e * CW;
 }
 
-// Partial logits [slices][T k], 64 / L tokens per turn of a wavefront.
+// Partial logits [slices][T k], 64 / L tokens per turn of a wavefront.  2,048
+// tokens, top-8 of 256, 6144 wide: 17 us, of which about 5 fill the slices.
 template <int DT, int EC, int CW>
 __global__ __launch_bounds__(kThreads) void k_route_dots(RouteArgs a, int range, float* zpart) {
   __shared__ __align__(16) float w[(EC + 1) * CW];  // E <= EC
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(kSlotThreads) void k_route_slots(RouteArgs a, int s
   if (l < np) dz[p] = ok ? w * (1.0f / (1.0f + expf(z))) * (g - m) : 0.0f;
 }
 
-// dx[t] = add[t] + sum_j dz_j Wr[e_j], as k_route_dots.
+// dx[t] = add[t] + sum_j dz_j Wr[e_j], as k_route_dots (17 us there).
 template <int DT, int EC, int CW>
 __global__ __launch_bounds__(kThreads) void k_route_dx(RouteArgs a, int range, const float* dz, const u32x4* add, u32x4* dx) {
   __shared__ __align__(16) float w[(EC + 1) * CW];
@@ -260,12 +262,15 @@ __global__ __launch_bounds__(kThreads) void k_route_dx(RouteArgs a, int range, c
       acc[c] += odd ? s1[c] : s0[c];
       acc[4 + c] += odd ? s0[c] : s1[c];
     }
-    if (t < t1 && cv < nv) dx[(size_t)t * nv + cv] = pack_vec<DT>(acc);
+    // (past the L2s, whose dirty lines the launch's end would wait for: 58.7 -> 56.5 us)
+    if (t < t1 && cv < nv) __builtin_nontemporal_store(pack_vec<DT>(acc), dx + (size_t)t * nv + cv);
   }
 }
 
 // The same three steps for few tokens, whose rows of Wr are gathered directly:
 // one workgroup per token, a wavefront per slot and then a thread per 8 columns.
+// Bound by three waits for memory in turn: 100 tokens, top-8 of 256, 6144 wide 10.5
+// us; 45 tokens, 2048 wide 5.5.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_route_grad_tokens(RouteArgs a, const float* br, const float* dw, const u32x4* add,
                                                                 u32x4* dx, float* dz_out) {

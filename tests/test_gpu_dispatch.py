@@ -187,6 +187,13 @@ def test_combine_and_gradient(dtype, T, k, E, align, drop, H):
     assert torch.equal(go.cpu()[~kept], torch.zeros_like(o[~kept]))
 
 
+@pytest.mark.parametrize("dtype,T,H", [(F16, 1010, 4096), (BF16, 1900, 4104), (F32, 470, 4096), (F32, 930, 4096)])
+def test_rows_past_the_caches(dtype, T, H):
+    """Rows of 64 MB, and of 125 MB: parts or all of them streamed."""
+    test_combine_and_gradient(dtype, T, 8, 64, 16, 0.02, H)
+    test_dispatch_and_gradient(dtype, T, 8, 64, 16, 0.02, H)
+
+
 def test_combine_is_its_gradients_adjoint():
     """Differences: the combine is linear in o and in w, so moving either along
     a direction changes <dy, y> by the gradients' product with it."""
