@@ -939,6 +939,7 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const Adapter
     for (int k = 0; k < UW; ++k) {
       const int unit = min(wave + k * WV, CT * RT - 1), r = min(unit % RT * 16 + li, d.R - 1);
       const int i = (j0 + unit / RT) * kGradM + g * 8;
+      if (j0 + unit / RT >= tiles) break;
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         w[k][q] = v[(size_t)(IDS ? max(id_at(i + q), 0) : it.first + min(i + q, it.cnt - 1)) * d.R + r];
@@ -967,6 +968,7 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const Adapter
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
       const int unit = wave + k * WV, r = unit % RT * 16 + li, i = (j0 + unit / RT) * kGradM + g * 8;
+      if (j0 + unit / RT >= tiles) break;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         w[k][q] = unit < CT * RT && r < rk && (IDS ? id_at(min(i + q, j0 * kGradM + CR - 1)) >= 0 : i + q < it.cnt) ? w[k][q] : 0.0f;
@@ -1001,7 +1003,7 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const Adapter
 #pragma unroll
     for (int k = 0; k < UW; ++k) {
       const int unit = wave + k * WV;
-      if (unit < CT * RT) {
+      if (unit < CT * RT && j0 + unit / RT < tiles) {
         v8_t<DT> p[NP];
         split_pieces<DT, NP>(w[k], e, p);
 #pragma unroll
@@ -1215,9 +1217,10 @@ AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
   // 1,024; 8,000 rows, 2048 to 6144 wide 63.0, 67.0, 81.2.  Above rank 32 a workgroup takes whole
   // adapters where there are enough of them to fill the GPU: rank 64, 2,048 rows
   // of 4 adapters 63 us, in parts of 512 rows 71; of one adapter 67 in parts of 352.
+  // (Up to 256 rows are not split: the sum would cost a launch.)
   const int tiles = rank_tiles(d.R), cols = ceil_div(d.K, kOutCols) + ceil_div(d.N, kOutCols), wanted = ceil_div(kWanted, cols);
   if (tiles <= kMergeTiles) p.G = std::max(256, ceil_div(T, 64 * kGradM) * kGradM);
-  else p.G = d.n >= (wanted + 1) / 2 ? 2048 : std::max(256, ceil_div(T, wanted / d.n * kGradM) * kGradM);
+  else p.G = d.n >= (wanted + 1) / 2 ? 2048 : std::max(T <= 256 ? 256 : 128, ceil_div(T, wanted / d.n * kGradM) * kGradM);
   p.items = T / p.G + d.n;
   p.slots = T > p.G ? 2 * (T / p.G) : 0;
   size_t o = 0;

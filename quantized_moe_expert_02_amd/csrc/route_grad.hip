@@ -130,9 +130,12 @@ struct Item {
   int parts;      // the expert's items, in its first one (else 0)
 };
 
-// Fills items[0, most) from the groups; one workgroup of 256 threads.
-__device__ __forceinline__ void make_items(const int32_t* offsets, int E, int rows, int most, int per, Item* items) {
-  __shared__ int sums[2][4];
+// Fills items[0, most) from the groups; one workgroup of 256 threads.  The
+// experts' first items and slots first, then a thread looks up each item's expert.
+struct ItemLds {
+  int item[kMaxExperts], slot[kMaxExperts], r0[kMaxExperts], r1[kMaxExperts], sums[2][4];
+};
+__device__ __forceinline__ void make_items(ItemLds& L, const int32_t* offsets, int E, int rows, int most, int per, Item* items) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int at = 0, slots = 0;
   for (int e0 = 0; e0 < E; e0 += 256) {
@@ -150,23 +153,40 @@ __device__ __forceinline__ void make_items(const int32_t* offsets, int E, int ro
       is += lane >= d ? os : 0;
     }
     if (lane == 63) {
-      sums[0][wave] = ii;
-      sums[1][wave] = is;
+      L.sums[0][wave] = ii;
+      L.sums[1][wave] = is;
     }
     __syncthreads();
     int i0 = at + ii - ni, s0 = slots + is - ns;
     for (int w = 0; w < 4; ++w) {
-      i0 += w < wave ? sums[0][w] : 0;
-      s0 += w < wave ? sums[1][w] : 0;
-      at += sums[0][w];
-      slots += sums[1][w];
+      i0 += w < wave ? L.sums[0][w] : 0;
+      s0 += w < wave ? L.sums[1][w] : 0;
+      at += L.sums[0][w];
+      slots += L.sums[1][w];
     }
-    for (int j = 0; j < ni; ++j)
-      if (i0 + j < most)
-        items[i0 + j] = {e, r0 + j * per, j + 1 < ni ? r0 + (j + 1) * per : r1, ns ? s0 + j : -1, j ? 0 : parts};
+    if (e < E) {
+      L.item[e] = i0;
+      L.slot[e] = s0;
+      L.r0[e] = r0;
+      L.r1[e] = r1;
+    }
     __syncthreads();
   }
-  for (int i = at + tid; i < most; i += 256) items[i] = {-1, 0, 0, -1, 0};
+  for (int i = tid; i < most; i += 256) {
+    Item it = {-1, 0, 0, -1, 0};
+    if (i < at) {
+      int lo = 0, hi = E;  // L.item[lo] <= i < L.item[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (L.item[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      const int r0 = L.r0[lo], r1 = L.r1[lo];
+      const int j = i - L.item[lo], parts = (int)(((int64_t)r1 - r0 + per - 1) / per), from = r0 + j * per;
+      it = {lo, from, min(r1, from + per), parts > 1 ? L.slot[lo] + j : -1, j ? 0 : parts};
+    }
+    items[i] = it;
+  }
 }
 
 // dz of every slot from the partial logits: 64 / k tokens per workgroup, four
@@ -176,8 +196,15 @@ constexpr int kSlotThreads = 256;
 __global__ __launch_bounds__(kSlotThreads) void k_route_slots(RouteArgs a, int slices, const float* zpart, const float* br,
                                                              const float* dw, float* dz, const int32_t* offsets, int rows,
                                                              int most, int per_item, Item* items) {
-  __shared__ float part[4][64], sg[64], gw[64];
-  if (blockIdx.x == gridDim.x - 1) return make_items(offsets, a.E, rows, most, per_item, items);
+  __shared__ union {
+    ItemLds items;
+    struct {
+      float part[4][64], sg[64], gw[64];
+    };
+  } L;
+  auto& part = L.part;
+  float *sg = L.sg, *gw = L.gw;
+  if (blockIdx.x == gridDim.x - 1) return make_items(L.items, offsets, a.E, rows, most, per_item, items);
   const int l = threadIdx.x & 63, q = threadIdx.x >> 6, n = a.T * a.k, per = 64 / a.k;
   const int p0 = blockIdx.x * per * a.k, np = min(per * a.k, n - p0), p = min(p0 + l, n - 1);
   float z = 0.0f;
@@ -459,21 +486,23 @@ __global__ __launch_bounds__(256) void k_route_sum(const Item* items, int H, con
   if (m <= 0) return;
   if (i < H / 4) {
     const f32x4* p = (const f32x4*)(sums + (size_t)it.slot * H) + i;
+    constexpr int U = 8;  // in flight
     f32x4 s = {0, 0, 0, 0};
-    for (int j = 0; j < m; j += 8) {
-      f32x4 v[8];
+    for (int j = 0; j < m; j += U) {
+      f32x4 v[U];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = p[(size_t)min(j + k, m - 1) * (H / 4)];
+      for (int k = 0; k < U; ++k) v[k] = p[(size_t)min(j + k, m - 1) * (H / 4)];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < U; ++k)
         if (j + k < m) s += v[k];
     }
     *(f32x4*)(dwr + (size_t)it.e * H + i * 4) = s;
   }
-  if (i == 0) {
+  if (i < 64) {
     float s = 0.0f;
-    for (int j = 0; j < m; ++j) s += bsums[it.slot + j];
-    db[it.e] = s;
+    for (int j = i; j < m; j += 64) s += bsums[it.slot + j];
+    s = wave_sum_f32(s);
+    if (i == 0) db[it.e] = s;
   }
 }
 
