@@ -1179,7 +1179,7 @@ constexpr int kSmallRows = 64;
 // three calls with half as many 9.1, 16.7 and 13.0, with twice as many 9.2, 13.8, 13.8.
 constexpr int kSegment = 1024;
 constexpr int kWideRows = 4096;  // rows from which k_rows takes 64 r at a time (RowsShape)
-constexpr int kWanted = 256;     // workgroups of k_grad_weights that fill the GPU
+constexpr int kWanted = 256;     // workgroups of k_grad_weights, one per CU
 // Rank fragments up to which the gradients take two launches.  Two and three
 // launches, 6144 wide, 4 adapters: 2,048 rows rank 16 34.0 and 39.7 us, rank 32 45.3
 // and 47.1, rank 64 78.8 and 63.0 (the kernels' register and LDS needs add up);
@@ -1214,13 +1214,16 @@ AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
   // Rows of an adapter per workgroup of its weight gradients: more leave the
   // last one working alone, fewer cost partial sums (R (K + N) floats each).
   // Rank 16, 4 adapters: 2,048 rows of 6144 34.0 us with 256, 40.4 with 512, 51.5 with
-  // 1,024; 8,000 rows, 2048 to 6144 wide 63.0, 67.0, 81.2.  Above rank 32 a workgroup takes whole
-  // adapters where there are enough of them to fill the GPU: rank 64, 2,048 rows
-  // of 4 adapters 63 us, in parts of 512 rows 71; of one adapter 67 in parts of 352.
-  // (Up to 256 rows are not split: the sum would cost a launch.)
-  const int tiles = rank_tiles(d.R), cols = ceil_div(d.K, kOutCols) + ceil_div(d.N, kOutCols), wanted = ceil_div(kWanted, cols);
+  // 1,024; 8,000 rows, 2048 to 6144 wide 63.0, 67.0, 81.2.  Above rank 32 a CU holds
+  // one workgroup, so a launch has no more than there are CUs, or one per adapter
+  // where that is more: rank 64, 2,048 rows of 6144 of 4 adapters whole 63 us, in parts
+  // of 512 71; of one adapter whole 93, in parts of 512 57, of 352 67; 4,000 rows of
+  // 2048 of 4 adapters whole 76, in parts of 352 45.  (Up to 256 rows are not split:
+  // the sum would cost a launch.)
+  const int tiles = rank_tiles(d.R), cols = ceil_div(d.K, kOutCols) + ceil_div(d.N, kOutCols), wanted = kWanted / cols;
   if (tiles <= kMergeTiles) p.G = std::max(256, ceil_div(T, 64 * kGradM) * kGradM);
-  else p.G = d.n >= (wanted + 1) / 2 ? 2048 : std::max(T <= 256 ? 256 : 128, ceil_div(T, wanted / d.n * kGradM) * kGradM);
+  else if (wanted <= d.n) p.G = 2048;
+  else p.G = std::min(2048, std::max(T <= 256 ? 256 : 128, ceil_div(T, (wanted - d.n) * kGradM) * kGradM));
   p.items = T / p.G + d.n;
   p.slots = T > p.G ? 2 * (T / p.G) : 0;
   size_t o = 0;
