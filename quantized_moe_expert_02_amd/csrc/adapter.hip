@@ -696,8 +696,7 @@ struct SpreadLds {
 // of A, LDS holds their columns in that order, and 16 lanes read product q's
 // across.
 // Bound by memory, once the first run's data are there: 1,801 rows of 6144
-// bfloat16, rank 64: 12.7 us for 44 MB of add and y (3.5 TB/s); 7,204 rows 40.3
-// (4.4 TB/s).
+// bfloat16, rank 64: 11.7 us for 44 MB of add and y (3.8 TB/s).
 template <int DT, int RT, bool ACROSS>
 __device__ __forceinline__ void spread_body(SpreadLds<DT, RT, ACROSS>& L, const AdapterArgs& d, const RowSet& rs,
                                             const SpreadArgs& sa, int tile, int chunk) {
@@ -825,8 +824,8 @@ __global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs
 // and, on the CUs that leaves free, dB, and k_grad_second dx and dA; or k_rows
 // forms v, k_spread dx, and k_grad_weights dA and dB.  k_grad_sum adds the
 // partial dA and dB of adapters whose rows several workgroups took.
-// 2,048 rows of 4 adapters, 6144 wide: rank 16, binary16 15.2, 14.6 and 4.2 us for
-// 3 passes over 25 MB and partial sums of 9; rank 64, bfloat16 16.1, 12.2 and 34.6,
+// 2,048 rows of 4 adapters, 6144 wide: rank 16, binary16 15.1, 14.0 and 4.2 us for
+// 4 passes over 25 MB and partial sums of 7; rank 64, bfloat16 16.1, 9.9 and 35.5,
 // the last for making three pieces of each value of u and v in every workgroup,
 // between barriers.
 // ---------------------------------------------------------------------------

@@ -289,8 +289,8 @@ __global__ __launch_bounds__(kSmallThreads) void k_dispatch_small(const u32x4* x
 
 // xs[pos(t,j)] = x[t], token by token, 16-byte vectors: x is read once.
 // Workgroups past the tokens' zero the rows that hold no slot, a row per thread
-// looked over.  Bound by the writes: 2,048 tokens of 6144 binary16, top-8: 36.1 us,
-// 6.3 TB/s (a fill of 2 GiB reaches 6.9).
+// looked over.  Bound by the writes: 2,048 tokens of 6144 binary16, top-8: 40.4 us,
+// 5.6 TB/s (a fill of 2 GiB reaches 6.9, a copy of 400 MB 5.4).
 constexpr int kRowThreads = 256;  // most threads of a workgroup of the row kernels
 
 // Rows past the last-level cache (256 MB) are read and written without a place
@@ -333,7 +333,8 @@ __global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, in
 
 // y[t] = add[t] + sum_j w[t][j] o[pos(t,j)] (w == NULL: all ones), slots in
 // order, 8 rows in flight.  Bound by reading o: 2,048 tokens of 6144 binary16,
-// top-8, with add: 42.8 us, 5.9 TB/s (a copy of 400 MB reaches 5.4); 8 tokens 3.5 us.
+// top-8, with add: 40.5 us, 6.2 TB/s; 8 tokens 3.6 us; 1,501 tokens of 2056 bfloat16,
+// top-6, without weights: 9.0 us, 4.3 TB/s.
 constexpr int kSlotsAtOnce = 8;
 
 template <int DT, bool STREAM>
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(kRowThreads) void k_gather_sum(const u32x4* o, int 
 // d_o[pos(t,j)] = w dy[t]; dw[t][j] = <dy[t], o[pos(t,j)]>.  One workgroup per
 // token, 8 slots at a time: their rows of o in flight together.  The workgroups
 // past the tokens' zero padding rows.  Bound by reading o and writing d_o: 4,096
-// tokens of 2048 bfloat16, top-8, groups padded to 64: 63.5 us, 5.2 TB/s.
+// tokens of 2048 bfloat16, top-8, groups padded to 64: 69.6 us, 5.1 TB/s.
 template <int DT, bool STREAM_O, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, const u32x4* o, int rows, int nv,
                                                               const float* w, const int32_t* pos,
