@@ -325,7 +325,10 @@ struct RowsOut {
   float* u_sorted;   //   [T][R] in the sorted order
 };
 
-template <int MT, int RT, bool ACROSS>
+constexpr int cmin(int a, int b) { return a < b ? a : b; }
+
+// (BYTES: no fewer for the wavefronts together, for what follows in k_small.)
+template <int MT, int RT, bool ACROSS, int BYTES = 0>
 struct RowsLds {
   static constexpr int M = MT * 16, W = RT * 16;
   static constexpr int KS = 64, XV = KS / 8, XS = KS + 8;  // columns per step; x's rows in LDS: vectors, stride
@@ -333,7 +336,7 @@ struct RowsLds {
   static constexpr int kStage = (M * XS + FR * FS) * 2;
   static_assert(kStage >= MT * RT * 1024, "a wavefront's sums fit its stage");
   SharedTile st;
-  alignas(16) char lds[kRowWaves * kStage];
+  alignas(16) char lds[kRowWaves * kStage < BYTES ? BYTES : kRowWaves * kStage];
   alignas(16) float vs[M][W + 4];
 };
 
@@ -352,11 +355,11 @@ struct RowsLds {
 // join and split the sums, the rest is the launch.  1,801 rows, rank 64: 14.3 us;
 // its 120 workgroups are bound by what a CU loads (64 bytes a cycle), and more of
 // them load more in all (the choice at RowsShape); 1,024 threads each: 15.2.
-template <int DT, int MT, int RT, bool ACROSS, bool SMALL>
-__device__ __forceinline__ void rows_body(RowsLds<MT, RT, ACROSS>& L, const AdapterArgs& d, const RowSet& rs, const void* x,
+// FUSED: the tile is in L already, and the sums stay in L.vs.
+template <int DT, int MT, int RT, bool ACROSS, bool SMALL, bool FUSED = false, typename Lds>
+__device__ __forceinline__ void rows_body(Lds& L, const AdapterArgs& d, const RowSet& rs, const void* x,
                                           int64_t ldx, const RowsOut& out, int tile, int y, int z, int zs) {
   typedef typename Mat<DT>::elem E;
-  typedef RowsLds<MT, RT, ACROSS> Lds;
   constexpr int M = Lds::M, W = Lds::W, NF = MT * RT, KS = Lds::KS, XV = Lds::XV, XS = Lds::XS, FR = Lds::FR, FV = Lds::FV,
                 FS = Lds::FS, kStage = Lds::kStage;
   constexpr int XL = M * XV / 64, FL = FR * FV / 64;   // loads per lane
@@ -365,7 +368,7 @@ __device__ __forceinline__ void rows_body(RowsLds<MT, RT, ACROSS>& L, const Adap
   auto& vs = L.vs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
   const int t0 = SMALL ? 0 : z * M, r0 = y * W;
-  share_tile<SMALL ? kSmallM : kM>(&st, d, rs, tile, r0 == 0 && z == 0 ? rs.kept + tile : nullptr);
+  if (!FUSED) share_tile<SMALL ? kSmallM : kM>(&st, d, rs, tile, r0 == 0 && z == 0 ? rs.kept + tile : nullptr);
   const int a = __builtin_amdgcn_readfirstlane(st.a), cnt = __builtin_amdgcn_readfirstlane(st.cnt) - t0;
   if (cnt <= 0 || a == d.n) return;
   const int rk = __builtin_amdgcn_readfirstlane(st.rank) - r0, R = d.R, C = ACROSS ? d.N : d.K;
@@ -467,9 +470,9 @@ __device__ __forceinline__ void rows_body(RowsLds<MT, RT, ACROSS>& L, const Adap
     if (ACROSS) s *= f;
     const int q = tid / 64, t = q / RT * 16 + li, c = q % RT * 16 + g * 4, r = r0 + c;
     const int row = ACROSS ? (t < cnt ? first + t : -1) : strow[t];
-    if ((SMALL || out.sums) && row >= 0 && r < R)
+    if (!FUSED && (SMALL || out.sums) && row >= 0 && r < R)
       *(f32x4*)(out.sums + ((size_t)(SMALL ? z : 0) * rs.T + row) * R + r) = s;
-    if (!SMALL) *(f32x4*)&vs[t][c] = s;
+    if (!SMALL || FUSED) *(f32x4*)&vs[t][c] = s;
   }
   if (SMALL) return;
   __syncthreads();
@@ -579,7 +582,7 @@ __device__ __forceinline__ int place_of(int n) { return n % 8 * 16 + n / 8; }
 
 // y[t] = add[t] + s_a B_a u[t] for a small tile's rows, 128 columns per
 // wavefront.  Bound by a chain of waits: the tile, the sums of u's segments, one
-// run of B.  One token, 6144 wide, rank 16: 4.8 us (k_rows 4.2); 48 requests of 32
+// run of B.  One token, 6144 wide, rank 16: 5.0 us (k_rows 4.0); 48 requests of 32
 // adapters of rank up to 64, 6144 to 2048: 6.7 (8.6, for 11 MB of factors).
 template <int DT, int RT>
 __global__ __launch_bounds__(kOutThreads) void k_expand_small(AdapterArgs d, RowSet rs, const float* part, int S, float* u,
@@ -644,6 +647,96 @@ __global__ __launch_bounds__(kOutThreads) void k_expand_small(AdapterArgs d, Row
     unpack_vec<DT>(av[i], o);
 #pragma unroll
     for (int q = 0; q < 8; ++q) o[q] = fmaf(acc[q][i], f[i], o[q]);
+    if (row[i] >= 0 && c < d.N) *(u32x4*)((E*)y + (size_t)row[i] * ldy + c) = pack_vec<DT>(o);
+  }
+}
+
+// Both products of a small tile in one launch, 128 columns of y per wavefront:
+// every workgroup forms the tile's u for itself.  That costs the GPU about what
+// the launch between did, and spares the host that launch (kSmallElems).  Bound by
+// the same chain of waits: one token, 6144 wide, rank 16: 9.3 us.
+template <int DT, int RT>
+__global__ __launch_bounds__(kRowThreads) void k_small(AdapterArgs d, RowSet rs, const void* x, int64_t ldx, float* u,
+                                                      const void* add, int64_t ldadd, void* y, int64_t ldy) {
+  typedef typename Mat<DT>::elem E;
+  constexpr int RB = (RT + 1) / 2, VR = RT == 1 ? 2 : 4, BL = 128 * VR / 64, BS = VR * 8 + 8;
+  __shared__ RowsLds<1, RT, false, kRowWaves * 128 * BS * 2> L;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
+  share_tile<kSmallM>(&L.st, d, rs, blockIdx.x, nullptr);
+  if (!__builtin_amdgcn_readfirstlane(L.st.cnt)) return;
+  const int rk = __builtin_amdgcn_readfirstlane(L.st.rank), a = min(__builtin_amdgcn_readfirstlane(L.st.a), d.n - 1);
+  const bool whole = rk % 8 == 0;
+  const E* bbase = (const E*)d.b + (size_t)a * d.N * d.R;
+  const int n0 = (blockIdx.y * kRowWaves + wave) * 128, c = n0 + li * 8;
+  u32x4 bn[RB][BL], av[4] = {};
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      const int v = lane + 64 * i, r = b * 32 + v % VR * 8;
+      bn[b][i] = load8<DT>(bbase, (uint32_t)min(n0 + v / VR, d.N - 1) * d.R + (r < rk ? r : 0));
+    }
+  int row[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    row[i] = L.st.row[g * 4 + i];
+    if (add) av[i] = load8<DT>((const E*)add + (size_t)max(row[i], 0) * ldadd, c < d.N ? c : 0);
+  }
+  if (rk > 0) rows_body<DT, 1, RT, false, true, true>(L, d, rs, x, ldx, RowsOut{}, 0, 0, 0, 1);
+  __syncthreads();
+  if (u && blockIdx.y == 0)
+    for (int i = tid; i < kSmallM * (d.R / 4); i += kRowThreads) {
+      const int t = i / (d.R / 4), r = i % (d.R / 4) * 4;
+      f32x4 v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = r + q < rk ? L.vs[t][r + q] : 0.0f;
+      if (L.st.row[t] >= 0) *(f32x4*)(u + (size_t)L.st.row[t] * d.R + r) = v;
+    }
+  // this wavefront's fragments of u
+  float v[RB][8], top = 0.0f;
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = b * 32 + g * 8 + i;
+      v[b][i] = (RT > 1 || g < 2) && r < rk ? L.vs[li][r] : 0.0f;
+      top = fmaxf(top, finite_abs(v[b][i]));
+    }
+  top = fmaxf(top, __builtin_bit_cast(float, partner<16>(__builtin_bit_cast(int, top))));
+  top = fmaxf(top, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, top))));
+  const int e = scale_exp<DT>(top);
+  const float sc = __builtin_amdgcn_ldexpf(rk ? d.scale[a] : 0.0f, -e);
+  E* bs = (E*)L.lds + wave * 128 * BS;
+  if (RT == 1) {  // rank 16 fills half of the contraction; the other half reads zeros
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *(u32x4*)(bs + (lane + 64 * i) * BS + 16) = u32x4{0, 0, 0, 0};
+  }
+  f32x4 acc[8] = {};
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    v8_t<DT> h[2];
+    split_pieces<DT, 2>(v[b], e, h);
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      const int k = lane + 64 * i, r = b * 32 + k % VR * 8;
+      *(u32x4*)(bs + place_of(k / VR) * BS + k % VR * 8) = keep_upto(bn[b][i], rk - r, whole);
+    }
+    lds_order();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const v8_t<DT> bf = *(const v8_t<DT>*)(bs + (q * 16 + li) * BS + (RT == 1 ? min(g, 2) : g) * 8);
+      acc[q] = Mat<DT>::mma(h[0], bf, acc[q]);
+      acc[q] = Mat<DT>::mma(h[1], bf, acc[q]);
+    }
+    lds_order();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f = __shfl(sc, g * 4 + i);
+    float o[8];
+    unpack_vec<DT>(av[i], o);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) o[q] = fmaf(acc[q][i], f, o[q]);
     if (row[i] >= 0 && c < d.N) *(u32x4*)((E*)y + (size_t)row[i] * ldy + c) = pack_vec<DT>(o);
   }
 }
@@ -861,8 +954,6 @@ __device__ __forceinline__ Item find_item(const RowSet& rs, int n, int item, int
   }
   return {n, 0, 0, -1};
 }
-
-constexpr int cmin(int a, int b) { return a < b ? a : b; }
 
 constexpr int kGradM = 32;                // rows taken at a time
 constexpr int kStride = 72;               // elements of an LDS row of 64 columns
@@ -1170,10 +1261,19 @@ int check_adapter_ptrs(const moe_adapters_t* d) {
   return MOE_OK;
 }
 
-// Rows that each workgroup groups by itself, in tiles of 16: so, and sorted
-// first, 6144 wide: one row 9.0 and 15.0 us, 48 rows of 32 adapters 15.2 and 21.0, 64
-// rows of 4 13.0 and 21.1.  (64: a lane each.)
+// Rows that each workgroup groups by itself, in tiles of 16: so (in two launches),
+// and sorted first, 6144 wide: one row 9.0 and 15.0 us, 48 rows of 32 adapters 15.2
+// and 21.0, 64 rows of 4 13.0 and 21.1.  (64: a lane each.)
 constexpr int kSmallRows = 64;
+// A small batch takes one launch (k_small) up to rank 64 where its workgroups load
+// up to so many elements of x and A each, and fit the GPU at once.  Calls so and in
+// two launches, of which 3.4 us are the second one's host time (GPU alone in
+// brackets): rank 16, 6144 wide 13.0 and 15.9 us (9.3 and 9.1); rank 32, 2048 wide 13.0
+// and 15.9 (8.6 and 10.3), 6144 wide 12.8 and 15.8 (11.8 and 10.4); rank 16, 10240 wide
+// 13.0 and 16.1 (12.0 and 10.0); rank 64, 6144 wide 18.4 and 15.7 (18.9 and 11.9).
+constexpr int kSmallTiles = 4;
+constexpr int kSmallElems = 5 << 16;
+constexpr int kSmallGroups = 256;
 // Columns per K-segment of a small batch: two steps of every wavefront.  Those
 // three calls with half as many 9.1, 16.7 and 13.0, with twice as many 9.2, 13.8, 13.8.
 constexpr int kSegment = 1024;
@@ -1345,6 +1445,13 @@ int moe_adapter_forward(const moe_adapters_t* d, const void* x, int64_t ldx, int
     float* part = (float*)(w + p.part);
     by_shape(*d, [&](auto dt, auto rt) {
       constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
+      if constexpr (RT <= kSmallTiles) {
+        const int groups = ceil_div(d->N, kRowWaves * kCols);
+        if (p.stiles * groups <= kSmallGroups && (int64_t)(kSmallM + RT * 16) * d->K <= kSmallElems) {
+          k_small<DT, RT><<<dim3(p.stiles, groups), kRowThreads, 0, s>>>(g, rs, x, ldx, u, add, ldadd, y, ldy);
+          return;
+        }
+      }
       launch_rows<DT, RT, false>(p, g, rs, x, ldx, RowsOut{part, frag, scale, p.rb, nullptr, nullptr}, s);
       k_expand_small<DT, RT><<<dim3(p.stiles, ceil_div(d->N, kOutWaves * kCols)), kOutThreads, 0, s>>>(
           g, rs, part, p.S, u, add, ldadd, y, ldy);

@@ -136,6 +136,15 @@ def test_adapter_of_many_rows(dtype, T, K, N, n, R, mixed, none, runs):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T,K,N,n,R,mixed,none,runs", [
+    (3, 20488, 136, 2, 16, False, 0.0, False), (20, 8200, 72, 4, 32, True, 0.2, False), (5, 8200, 264, 3, 64, True, 0.2, False),
+    (60, 136, 6144, 60, 8, False, 0.1, False), (64, 1032, 1416, 64, 40, True, 0.3, False), (17, 264, 2048, 1, 8, False, 0.0, False)])
+def test_adapter_of_few_rows(dtype, T, K, N, n, R, mixed, none, runs):
+    """Both sides of the rule for one launch or two, at each number of rank tiles."""
+    test_adapter(dtype, T, K, N, n, R, mixed, none, runs)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("T", [3, 200])
 def test_rows_of_wider_buffers(dtype, T):
     K, N, n, R = 264, 136, 3, 16
