@@ -104,8 +104,8 @@ struct SharedTile {
 };
 constexpr int kTileWords = sizeof(SharedTile) / 4;
 
-// Which rows a call has and how they are grouped.  offsets == NULL: at most
-// 64 rows, grouped by each workgroup itself from ids.
+// Which rows a call has and how they are grouped.  offsets == NULL: grouped by
+// each workgroup itself from ids (find_tile up to 64 rows, else group_tile).
 struct RowSet {
   const int32_t *ids, *offsets, *pairs;
   SharedTile* kept;  // [tiles]
@@ -170,7 +170,7 @@ template <int M>
 __device__ __forceinline__ Tile find_tile(const AdapterArgs& d, const RowSet& rs, int tile) {
   const int n = d.n;
   const int lane = threadIdx.x & 63;
-  if (!rs.offsets) {
+  if (M == kSmallM && !rs.offsets) {
     int id = rs.ids[min(lane, rs.T - 1)];
     if ((unsigned)id >= (unsigned)n) id = n;
     const int rank = id < n ? rank_of(d, min(id, n - 1)) : 0;
@@ -247,6 +247,74 @@ __device__ __forceinline__ void share_tile(SharedTile* s, const AdapterArgs& d, 
     if (keep) put(keep);
   }
   __syncthreads();
+}
+
+// A tile of kM rows from at most kGroupRows ids of at most 64 adapters, by a whole
+// workgroup of NT threads: it counts the adapters' rows, finds the tile's adapter,
+// and takes that one's rows by their place among them.  Ends with a barrier.
+// 1,801 rows of 8 adapters, 6144 wide, rank 64: 2 us longer than from a sorted
+// order, which takes 4 and a launch; calls 27.2 and 29.4 us, 200 rows 17.7 and 21.0,
+// 4,096 rows of 64 adapters 92.5 and 95.5.  (Of 300 adapters 31.8 and 24.2.)
+constexpr int kGroupRows = 4096;
+struct GroupLds {
+  int count[64];  // rows of each adapter
+  int per[64];    // rows of the tile's adapter in each 64
+};
+template <int NT>
+__device__ __forceinline__ void group_tile(SharedTile* s, const AdapterArgs& d, const RowSet& rs, int tile, GroupLds& L,
+                                           SharedTile* kept) {
+  constexpr int W = NT / 64, C = kGroupRows / NT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = d.n, bits = 32 - __clz(n);
+  int id[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) id[c] = rs.ids[min((c * W + wave) * 64 + lane, rs.T - 1)];
+  if (tid < 64) L.count[tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if ((c * W + wave) * 64 + lane >= rs.T || (unsigned)id[c] >= (unsigned)n) id[c] = -1;
+    if ((c * W + wave) * 64 >= rs.T) continue;
+    uint64_t same = __ballot(id[c] >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const bool one = (id[c] >> b) & 1;
+      const uint64_t v = __ballot(one);
+      same &= one ? v : ~v;
+    }
+    if (id[c] >= 0 && lanes_under(same) == 0) atomicAdd(&L.count[id[c]], (int)__popcll(same));
+  }
+  __syncthreads();
+  const int count = L.count[lane], nt = (count + kM - 1) / kM, incl = wave_prefix(nt), to = wave_prefix(count);
+  tile = tile_of_place(tile, min(at_lane(incl, 63), rs.tiles));
+  int a = n, cnt = 0, first = 0, j = 0;
+  const uint64_t past = __ballot(incl > tile);
+  if (tile >= 0 && past) {
+    a = __builtin_ctzll(past);
+    j = tile - at_lane(incl - nt, a);
+    cnt = min(kM, at_lane(count, a) - j * kM);
+    first = at_lane(to - count, a) + j * kM;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint64_t m = __ballot(id[c] == a);
+    if (lane == 0) L.per[c * W + wave] = (int)__popcll(m);
+  }
+  __syncthreads();
+  const int p = L.per[lane], before = wave_prefix(p) - p;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint64_t m = __ballot(id[c] == a);
+    const int r = __shfl(before, c * W + wave) + lanes_under(m) - j * kM;
+    if (id[c] == a && r >= 0 && r < cnt) s->row[r] = (c * W + wave) * 64 + lane;
+  }
+  if (tid < kM && tid >= cnt) s->row[tid] = -1;
+  if (tid == 0) {
+    s->a = a;
+    s->cnt = cnt;
+    s->first = first;
+    s->rank = a < n ? rank_of(d, a) : 0;
+  }
+  __syncthreads();
+  if (kept && tid < kTileWords) ((int*)kept)[tid] = ((const int*)s)[tid];
 }
 
 // The same from workspace.
@@ -368,7 +436,12 @@ __device__ __forceinline__ void rows_body(Lds& L, const AdapterArgs& d, const Ro
   auto& vs = L.vs;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
   const int t0 = SMALL ? 0 : z * M, r0 = y * W;
-  if (!FUSED) share_tile<SMALL ? kSmallM : kM>(&st, d, rs, tile, r0 == 0 && z == 0 ? rs.kept + tile : nullptr);
+  SharedTile* kept = r0 == 0 && z == 0 ? rs.kept + tile : nullptr;
+  if (!ACROSS && !SMALL && !rs.offsets) {
+    group_tile<kRowThreads>(&st, d, rs, tile, *(GroupLds*)lds, kept);
+  } else if (!FUSED) {
+    share_tile<SMALL ? kSmallM : kM>(&st, d, rs, tile, kept);
+  }
   const int a = __builtin_amdgcn_readfirstlane(st.a), cnt = __builtin_amdgcn_readfirstlane(st.cnt) - t0;
   if (cnt <= 0 || a == d.n) return;
   const int rk = __builtin_amdgcn_readfirstlane(st.rank) - r0, R = d.R, C = ACROSS ? d.N : d.K;
@@ -1458,7 +1531,7 @@ int moe_adapter_forward(const moe_adapters_t* d, const void* x, int64_t ldx, int
     });
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
   }
-  if (!offsets) {
+  if (!offsets && (T > kGroupRows || d->n > 64)) {
     int32_t *o = (int32_t*)(w + p.offsets), *q = (int32_t*)(w + p.pairs);
     if (launch_sort(ids, T, 1, d->n, 1, T, o, q, (int32_t*)(w + p.pos), w + p.sort, s) != hipSuccess) return MOE_E_HIP;
     offsets = o;

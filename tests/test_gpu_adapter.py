@@ -129,7 +129,7 @@ def test_adapter(dtype, T, K, N, n, R, mixed, none, runs):
 @pytest.mark.parametrize("T,K,N,n,R,mixed,none,runs", [
     (4500, 264, 136, 5, 24, True, 0.1, False), (4200, 136, 264, 3, 64, True, 0.0, True), (4097, 72, 80, 2, 128, False, 0.2, False),
     (1500, 264, 136, 1, 16, False, 0.0, False), (1500, 264, 136, 1, 72, False, 0.0, False), (3000, 64, 64, 70, 32, True, 0.3, True),
-    (5000, 40, 520, 1, 8, False, 0.0, True)])
+    (5000, 40, 520, 1, 8, False, 0.0, True), (4096, 72, 64, 64, 8, False, 0.3, False), (4095, 8, 72, 63, 24, True, 0.0, True)])
 def test_adapter_of_many_rows(dtype, T, K, N, n, R, mixed, none, runs):
     """Adapters whose gradients several workgroups sum, and row counts past the wide tiles' threshold."""
     test_adapter(dtype, T, K, N, n, R, mixed, none, runs)
