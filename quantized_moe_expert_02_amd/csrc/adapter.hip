@@ -420,9 +420,10 @@ struct RowsLds {
 // the next steps' loads in flight meanwhile.
 // 2,048 rows of 6144 binary16, rank 16: 10.3 us, of which 1.2 find the tile, 3.5
 // pass until the first steps have their data, 3.0 take the other two thirds, 1.0
-// join and split the sums, the rest is the launch.  1,801 rows, rank 64: 14.3 us;
-// its 120 workgroups are bound by what a CU loads (64 bytes a cycle), and more of
-// them load more in all (the choice at RowsShape); 1,024 threads each: 15.2.
+// join and split the sums, the rest is the launch.  1,801 rows, rank 64: 16.0 us, 1.7
+// of them grouping; its 120 workgroups are bound by what a CU loads (64 bytes a
+// cycle), and more of them load more in all (the choice at RowsShape); with 1,024
+// threads each 0.9 us longer.
 // FUSED: the tile is in L already, and the sums stay in L.vs.
 template <int DT, int MT, int RT, bool ACROSS, bool SMALL, bool FUSED = false, typename Lds>
 __device__ __forceinline__ void rows_body(Lds& L, const AdapterArgs& d, const RowSet& rs, const void* x,
@@ -542,6 +543,8 @@ __device__ __forceinline__ void rows_body(Lds& L, const AdapterArgs& d, const Ro
     for (int w = 1; w < kRowWaves; ++w) s += *(const f32x4*)(lds + w * kStage + tid * 16);
     if (ACROSS) s *= f;
     const int q = tid / 64, t = q / RT * 16 + li, c = q % RT * 16 + g * 4, r = r0 + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = c + i < rk ? s[i] : 0.0f;  // (zeros times an infinity otherwise)
     const int row = ACROSS ? (t < cnt ? first + t : -1) : strow[t];
     if (!FUSED && (SMALL || out.sums) && row >= 0 && r < R)
       *(f32x4*)(out.sums + ((size_t)(SMALL ? z : 0) * rs.T + row) * R + r) = s;
@@ -1227,16 +1230,20 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const Adapter
   float* out = TR ? ga.d_b : ga.d_a;
   float* o = it.slot >= 0 ? ga.sums + it.slot * per + (TR ? (size_t)d.R * d.K : 0) : out + (size_t)it.a * d.R * C;
   const float f = __builtin_amdgcn_ldexpf(TR ? d.scale[it.a] : 1.0f, -e);
+  // (past the rank: zeros, where the sums may hold zeros times an infinity)
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (TR) {  // [N][R]: a lane holds 4 consecutive r of one column
         const int n = c0 + q * 16 + li, rr = r * 16 + g * 4;
-        if (n < C && rr < d.R) *(f32x4*)(o + (size_t)n * d.R + rr) = acc[q][r] * f;
+        f32x4 v = acc[q][r] * f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = rr + i < rk ? v[i] : 0.0f;
+        if (n < C && rr < d.R) *(f32x4*)(o + (size_t)n * d.R + rr) = v;
       } else {  // [R][K]: 4 consecutive columns of one r
         const int k = c0 + g * 16 + q * 4, rr = r * 16 + li;
-        if (k < C && rr < d.R) *(f32x4*)(o + (size_t)rr * C + k) = acc[q][r] * f;
+        if (k < C && rr < d.R) *(f32x4*)(o + (size_t)rr * C + k) = rr < rk ? acc[q][r] * f : f32x4{0, 0, 0, 0};
       }
     }
 }

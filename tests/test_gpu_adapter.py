@@ -335,3 +335,25 @@ def test_binding_refuses():
                                 c["ids"], c["scale"])
     with pytest.raises(moe.MoeError):  # rows that start inside a vector
         moe.moe_adapter_forward(torch.zeros((4, 72), device=DEV).half()[:, 4:68], c["a"], c["b"], c["ids"], c["scale"])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T,K,R", [(3, 64, 64), (20, 8200, 64), (80, 64, 64), (80, 64, 128), (200, 64, 16)])
+def test_infinities_beside_a_lower_rank(dtype, T, K, R):
+    """What lies past an adapter's rank adds nothing, not even to a row that holds an infinity."""
+    _log("adapter infinity and rank", dtype, T, K, R)
+    N, rank = 40, 8
+    x = torch.ones((T, K), dtype=dtype, device=DEV)
+    a, b = torch.ones((1, R, K), dtype=dtype, device=DEV), torch.ones((1, N, R), dtype=dtype, device=DEV)
+    ids, scale = torch.zeros(T, dtype=torch.int32, device=DEV), torch.ones(1, device=DEV)
+    ranks = torch.tensor([rank], dtype=torch.int32, device=DEV)
+    x[1, 7] = float("inf")
+    y, u = moe.moe_adapter_forward(x, a / K, b, ids, scale, ranks=ranks, save_u=True)
+    assert bool((y[1] == float("inf")).all()) and bool(torch.isfinite(y[2:]).all())
+    assert bool((u[1, :rank] == float("inf")).all()) and bool((u[:, rank:] == 0).all())
+    dy = torch.ones((T, N), dtype=dtype, device=DEV)
+    dy[2, 3] = float("inf")
+    dx, da, db = moe.moe_adapter_backward(dy, torch.ones_like(x), torch.where(torch.isfinite(u), u, 1.0), a, b, ids, scale,
+                                          ranks=ranks)
+    assert bool((dx[2] == float("inf")).all()) and bool(torch.isfinite(dx[:2]).all())
+    assert bool((da[0, rank:] == 0).all()) and bool((db[0, :, rank:] == 0).all())
