@@ -167,6 +167,7 @@ def main():
     losses = train(layer, x, target, args.steps)
     print(f"loss {losses[0]:.3e} -> {losses[-1]:.3e} in {args.steps} steps of {args.tokens} tokens")
 
+    torch.manual_seed(3)
     n, rank = 4, 8  # four requests' adapters of ranks up to 8
     a, b = torch.randn((n, rank, dims.hidden)) / 16, torch.randn((n, dims.hidden, rank)) / 16
     ids = torch.tensor([0, 3, -1, 1, 0], dtype=torch.int32, device="cuda")

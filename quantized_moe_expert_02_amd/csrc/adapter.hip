@@ -451,7 +451,8 @@ __device__ __forceinline__ void rows_body(Lds& L, const AdapterArgs& d, const Ro
   if (ACROSS && out.u)  // this block's columns of u
     for (int i = tid; i < min(cnt, M) * (W / 4); i += kRowThreads) {
       const int t = i / (W / 4), r = r0 + i % (W / 4) * 4;
-      if (r < R) *(f32x4*)(out.u_sorted + (size_t)(first + t) * R + r) = *(const f32x4*)(out.u + (size_t)max(strow[t], 0) * R + r);
+      const f32x4 v = *(const f32x4*)(out.u + (size_t)max(strow[t], 0) * R + (r < R ? r : 0));
+      if (r < R) *(f32x4*)(out.u_sorted + (size_t)(first + t) * R + r) = v;
     }
   if (rk <= 0) {
     if (!ACROSS && !SMALL && out.sums)
@@ -1137,7 +1138,8 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const Adapter
       if (j0 + unit / RT >= tiles) break;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        w[k][q] = unit < CT * RT && r < rk && (IDS ? id_at(min(i + q, j0 * kGradM + CR - 1)) >= 0 : i + q < it.cnt) ? w[k][q] : 0.0f;
+        const bool row = IDS ? id_at(min(i + q, j0 * kGradM + CR - 1)) >= 0 : i + q < it.cnt;
+        w[k][q] = unit < CT * RT && r < rk && row ? w[k][q] : 0.0f;
         top = fmaxf(top, finite_abs(w[k][q]));
       }
     }
@@ -1599,7 +1601,9 @@ int moe_adapter_backward(const moe_adapters_t* d, const void* dy, int64_t lddy, 
       k_grad_weights<DT, RT><<<ka + kb, 2 * kOutThreads, 0, s>>>(g, rs, ga);
     }
   });
-  if (p.slots) k_grad_sum<<<dim3(d->n, ceil_div((int64_t)d->R * (d->K + d->N), 2048)), 256, 0, s>>>(g, rs, sums, p.slots, p.G, d_a, d_b);
+  if (p.slots)
+    k_grad_sum<<<dim3(d->n, ceil_div((int64_t)d->R * (d->K + d->N), 2048)), 256, 0, s>>>(g, rs, sums, p.slots, p.G, d_a,
+                                                                                         d_b);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
