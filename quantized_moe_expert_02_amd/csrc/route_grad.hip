@@ -189,6 +189,11 @@ __device__ __forceinline__ void make_items(ItemLds& L, const int32_t* offsets, i
   }
 }
 
+// sigmoid(z) e^-top for a token's kept slots, top being their largest logit or 0
+// if that is less: the factor cancels in w = s / sum s, and without it every s of
+// a token is 0 in fp32 where all its logits lie below about -88 (0 / 0).
+__device__ __forceinline__ float scaled_sigmoid(float z, float top) { return 1.0f / (expf(top) + expf(top - z)); }
+
 // dz of every slot from the partial logits: 64 / k tokens per workgroup, four
 // threads per slot over the slices.  The last workgroup makes the items of the
 // launch after next.
@@ -223,10 +228,14 @@ __global__ __launch_bounds__(kSlotThreads) void k_route_slots(RouteArgs a, int s
   const bool ok = l < np && (unsigned)e < (unsigned)a.E;
   z = (part[0][l] + part[1][l]) + (part[2][l] + part[3][l]);
   if (ok && br) z += br[e];
-  const float s = ok ? 1.0f / (1.0f + expf(-z)) : 0.0f, g = ok ? dw[p] : 0.0f;
-  sg[l] = s;
+  gw[l] = ok ? z : -INFINITY;
   __atomic_signal_fence(__ATOMIC_SEQ_CST);  // one wavefront from here on: LDS keeps its order
   const int first = l / a.k * a.k;
+  float top = -INFINITY;
+  for (int j = 0; j < a.k; ++j) top = fmaxf(top, gw[min(first + j, 63)]);
+  const float s = ok ? scaled_sigmoid(z, fminf(top, 0.0f)) : 0.0f, g = ok ? dw[p] : 0.0f;
+  sg[l] = s;
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
   float S = 0.0f;
   for (int j = 0; j < a.k; ++j) S += sg[min(first + j, 63)];
   const float w = ok ? s / S : 0.0f;
@@ -343,7 +352,8 @@ __global__ __launch_bounds__(kThreads) void k_route_grad_tokens(RouteArgs a, con
   if (wave == 0) {
     const bool ok = lane < k && ex[lane] >= 0;
     const float zj = ok ? z[lane] : 0.0f;
-    const float s = ok ? 1.0f / (1.0f + expf(-zj)) : 0.0f;
+    const float top = wave_max_f32(ok ? zj : -INFINITY);
+    const float s = ok ? scaled_sigmoid(zj, fminf(top, 0.0f)) : 0.0f;
     const float S = wave_sum_f32(s);
     const float w = ok ? s / S : 0.0f;
     const float g = ok ? dw[(size_t)t * k + lane] : 0.0f;

@@ -70,6 +70,17 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return v;
 }
 
+// Every lane ends with the wave-wide largest value (NaNs are passed over).
+__device__ __forceinline__ float wave_max_f32(float v) {
+  v = fmaxf(v, __builtin_bit_cast(float, partner<1>(__builtin_bit_cast(int, v))));
+  v = fmaxf(v, __builtin_bit_cast(float, partner<2>(__builtin_bit_cast(int, v))));
+  v = fmaxf(v, __builtin_bit_cast(float, partner<4>(__builtin_bit_cast(int, v))));
+  v = fmaxf(v, __builtin_bit_cast(float, partner<8>(__builtin_bit_cast(int, v))));
+  v = fmaxf(v, __builtin_bit_cast(float, partner<16>(__builtin_bit_cast(int, v))));
+  v = fmaxf(v, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, v))));
+  return v;
+}
+
 // Every lane ends with the wave-wide fp64 sum, added in a fixed butterfly order.
 __device__ __forceinline__ double wave_sum(double v) {
   v += partner_d<1>(v);
