@@ -93,8 +93,8 @@ int moe_combine(const void* o, int32_t dtype, int32_t rows, int32_t H, const flo
                 int32_t T, int32_t k, const void* add, void* y, void* stream);
 
 /* Gradients of moe_combine for dy [T][H]: d_o [rows][H] (zeros in rows whose
- * `pairs` entry is negative), dw fp32 [T][k] (0 for dropped slots).  pos and
- * pairs come from one moe_sort. */
+ * `pairs` entry is none of the T * k slots, or a slot that pos drops), dw fp32
+ * [T][k] (0 for dropped slots).  pos and pairs come from one moe_sort. */
 int moe_combine_backward(const void* dy, const void* o, int32_t dtype, int32_t rows, int32_t H,
                          const float* topk_w, const int32_t* pos, const int32_t* pairs, int32_t T, int32_t k,
                          void* d_o, float* dw, void* stream);

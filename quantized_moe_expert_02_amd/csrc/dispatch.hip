@@ -306,10 +306,15 @@ __device__ __forceinline__ void store_row(u32x4* p, u32x4 v) {
   else *p = v;
 }
 
+// Zeros the rows whose pair is none of the n slots, or (pos given) a slot that
+// lies elsewhere.
 template <bool STREAM>
-__device__ __forceinline__ void zero_pad_rows(const int32_t* pairs, int rows, int part, u32x4* out, int nv) {
+__device__ __forceinline__ void zero_pad_rows(const int32_t* pairs, const int32_t* pos, int rows, int n, int part, u32x4* out,
+                                              int nv) {
   const int lane = threadIdx.x & 63, r0 = part * blockDim.x + (threadIdx.x & ~63u), r = r0 + lane;
-  uint64_t pad = __ballot(r < rows && pairs[min(r, rows - 1)] < 0);  // a wavefront looks over 64 rows
+  const int p = pairs[min(r, rows - 1)];
+  const bool slot = (unsigned)p < (unsigned)n && (!pos || pos[p] == r);
+  uint64_t pad = __ballot(r < rows && !slot);  // a wavefront looks over 64 rows
   for (; pad; pad &= pad - 1) {
     u32x4* o = out + (size_t)(r0 + __builtin_ctzll(pad)) * nv;
     for (int i = lane; i < nv; i += 64) store_row<STREAM>(o + i, u32x4{0, 0, 0, 0});
@@ -320,7 +325,7 @@ template <bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void k_scatter_rows(const u32x4* x, int T, int nv, int k, int rows,
                                                               const int32_t* pos, const int32_t* pairs, u32x4* xs) {
   const int t = blockIdx.x;
-  if (t >= T) return zero_pad_rows<STREAM>(pairs, rows, t - T, xs, nv);
+  if (t >= T) return zero_pad_rows<STREAM>(pairs, nullptr, rows, T * k, t - T, xs, nv);
   const int32_t* p = pos + (size_t)t * k;
   for (int i = threadIdx.x; i < nv; i += blockDim.x) {
     const u32x4 v = x[(size_t)t * nv + i];
@@ -384,7 +389,7 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_grad(const u32x4* dy, c
   constexpr int VE = kVec<DT>, S = kSlotsAtOnce, W = kRowThreads / kWave;
   __shared__ float part[W][S];
   const int t = blockIdx.x, tid = threadIdx.x;
-  if (t >= T) return zero_pad_rows<STREAM>(pairs, rows, t - T, d_o, nv);
+  if (t >= T) return zero_pad_rows<STREAM>(pairs, pos, rows, T * k, t - T, d_o, nv);
   for (int j0 = 0; j0 < k; j0 += S) {
     int r[S];
     float wj[S], dot[S];
