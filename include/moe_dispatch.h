@@ -37,7 +37,9 @@
  *     offsets outside its range is treated as dropped and nothing outside the
  *     buffers is read or written.
  *   - Shapes: 1 <= k <= E, 0 <= T, 1 <= align <= 1024, else MOE_E_INVAL;
- *     T <= 2^20, k <= 32, E <= 1024 and H <= 65536, else MOE_E_UNSUPPORTED.
+ *     T <= 2^20, k <= 32, E <= 1024, H <= 65536, and in moe_combine_backward
+ *     and moe_route_backward rows <= 2^25 + 2^20 (no sort gives more), else
+ *     MOE_E_UNSUPPORTED.
  *     T == 0 launches nothing and returns MOE_OK, except where a call has an
  *     output that does not depend on T (offsets, d_o's padding rows, dWr, db),
  *     which is written.

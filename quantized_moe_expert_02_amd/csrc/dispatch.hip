@@ -602,6 +602,7 @@ int moe_combine_backward(const void* dy, const void* o, int32_t dtype, int32_t r
   int st = check_rows(dtype, T, H);
   if (st == MOE_OK) st = check_slots(T, k, rows);
   if (st != MOE_OK) return st;
+  if (rows > kMaxSorted) return MOE_E_UNSUPPORTED;
   if (T == 0 && rows == 0) return MOE_OK;
   if (T && (bad(dy, 16) || bad(topk_w, 4) || bad(pos, 4) || bad(dw, 4))) return MOE_E_INVAL;
   if (rows && (bad(o, 16) || bad(d_o, 16) || bad(pairs, 4))) return MOE_E_INVAL;

@@ -523,7 +523,7 @@ int check_shape(int32_t T, int32_t k, int32_t E, int32_t H, int32_t rows) {
   const int st = check_sort_shape(T, k, E, 1);
   if (st != MOE_OK) return st;
   if (H <= 0 || rows < 0) return MOE_E_INVAL;
-  return H % 8 || H > kMaxWidth ? MOE_E_UNSUPPORTED : MOE_OK;
+  return H % 8 || H > kMaxWidth || rows > kMaxSorted ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
 constexpr int kWideSlice = 512;    // experts up to which a slice has 64 columns

@@ -59,6 +59,9 @@ inline size_t elem_bytes(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
 // Limits of one call, which keep every launch below 2^32 threads.
 constexpr int32_t kMaxRows = 1 << 20;   // T
 constexpr int32_t kMaxWidth = 1 << 16;  // H, K, N
+// Rows of sorted buffers that a call writes by or walks: no sort gives more, and
+// with more the kernels' 32-bit row and item numbers could wrap.
+constexpr int32_t kMaxSorted = (1 << 25) + (1 << 20);
 
 // Shape of a sort: MOE_OK, MOE_E_INVAL or MOE_E_UNSUPPORTED.
 int check_sort_shape(int32_t T, int32_t k, int32_t E, int32_t align);
