@@ -1231,7 +1231,8 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const Adapter
   const size_t per = (size_t)d.R * (d.K + d.N);
   float* out = TR ? ga.d_b : ga.d_a;
   float* o = it.slot >= 0 ? ga.sums + it.slot * per + (TR ? (size_t)d.R * d.K : 0) : out + (size_t)it.a * d.R * C;
-  const float f = __builtin_amdgcn_ldexpf(TR ? d.scale[it.a] : 1.0f, -e);
+  // (without rows: zero, whatever the scale)
+  const float f = tiles ? __builtin_amdgcn_ldexpf(TR ? d.scale[it.a] : 1.0f, -e) : 0.0f;
   // (past the rank: zeros, where the sums may hold zeros times an infinity)
 #pragma unroll
   for (int r = 0; r < RT; ++r)
