@@ -13,8 +13,9 @@
  *
  * Conventions are those of moe_dispatch.h.  Rows and adapters are binary16 or
  * bfloat16 (one moe_dtype_t for all); products are exact, sums are held in
- * fp32, outputs are rounded once.  x, dy, y, dx and add may have rows of a
- * wider buffer (ld: elements from row to row, a multiple of 8).
+ * fp32, outputs are rounded once.  An infinity in any operand, or a product past
+ * fp32's range, gives the infinity or NaN of the formula.  x, dy, y, dx and add may
+ * have rows of a wider buffer (ld: elements from row to row, a multiple of 8).
  */
 #ifndef MOE_ADAPTER_H
 #define MOE_ADAPTER_H

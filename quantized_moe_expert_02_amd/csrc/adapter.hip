@@ -18,6 +18,11 @@ namespace moe {
 
 namespace {
 
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+
 // Matrix instructions of the two row types.
 template <int DT>
 struct Mat;
@@ -51,11 +56,12 @@ using v8_t = typename Mat<DT>::v8;
 // ---------------------------------------------------------------------------
 constexpr int kTopExp = 13;
 
-// Power of two that scales a largest magnitude `top` as above (0 for 0).
+// Power of two that scales a largest magnitude `top` as above (0 for 0).  Up to
+// 2^140, which keeps every bit of subnormal values and has an inverse.
 template <int DT>
 __device__ __forceinline__ int scale_exp(float top) {
   if (DT == MOE_T_BF16 || top == 0.0f) return 0;
-  return kTopExp + 1 - __builtin_amdgcn_frexp_expf(top);
+  return min(kTopExp + 1 - __builtin_amdgcn_frexp_expf(top), 140);
 }
 
 __device__ __forceinline__ float finite_abs(float v) {
@@ -63,14 +69,19 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a < INFINITY ? a : 0.0f;  // NaN too
 }
 
-template <int DT, int NP>
+// SIGN: the first piece is 0 only for 0, else at least the type's smallest step.
+template <int DT, int NP, bool SIGN>
 __device__ __forceinline__ void split_pieces(const float (&v)[8], int e, v8_t<DT> (&p)[NP]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float rest = DT == MOE_T_F16 ? __builtin_amdgcn_ldexpf(v[i], e) : v[i];
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-      const typename Mat<DT>::elem h = (typename Mat<DT>::elem)rest;
+      typename Mat<DT>::elem h = (typename Mat<DT>::elem)rest;
+      if (SIGN && q == 0) {
+        const uint16_t bits = __builtin_bit_cast(uint16_t, h);
+        h = __builtin_bit_cast(typename Mat<DT>::elem, (uint16_t)(bits | (rest != 0.0f && !(bits & 0x7FFF) ? 1 : 0)));
+      }
       p[q][i] = h;
       const float f = (float)h;
       rest = fabsf(f) < INFINITY ? rest - f : 0.0f;  // an infinity or NaN stays in the first piece
@@ -87,6 +98,43 @@ struct AdapterArgs {
 
 __device__ __forceinline__ int rank_of(const AdapterArgs& d, int a) {
   return d.ranks ? min(max(d.ranks[a], 0), d.R) : d.R;
+}
+
+// Where the other factor is infinite the pieces' products cannot be added: a
+// second piece of 0 or of the other sign gives NaN beside the first one's infinity.
+// (In bfloat16 so can pieces whose products pass fp32's range.)  A result that is
+// NaN is therefore formed again from the first pieces alone, which hold the
+// values' signs, infinities and NaNs, and stays NaN only where the formula's is.
+// Finite results never take that path and pay for looking for NaNs, 0 to 0.5 us of
+// a forward call and 0 to 1 us of a backward one (1,801 rows of 6144, rank 64 27.0 ->
+// 27.4; gradients of 2,048, rank 16 31.2 -> 31.5, rank 64 60.8 -> 61.8).
+__device__ __forceinline__ bool has_nan(f32x4 v) {
+  return __builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3]);
+}
+
+// v, with what is NaN in it taken from `by`.
+__device__ __forceinline__ f32x4 replace_nan(f32x4 v, f32x4 by) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = v[i] == v[i] ? v[i] : by[i];
+  return v;
+}
+
+// The same for all of a lane's sums where the wavefront has a NaN: first(q) forms
+// sums q again.  (One at a time, in a loop: that path must not cost the others
+// registers.)
+template <typename F>
+__device__ __forceinline__ void redo_nan(f32x4 (&acc)[8], F first) {
+  bool nan = false;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) nan |= has_nan(acc[q]);
+  const int n = __ballot(nan) ? 8 : 0;
+#pragma unroll 1
+  for (int q = 0; q < n; ++q) {
+    const f32x4 v = first(q);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k == q) acc[k] = replace_nan(acc[k], v);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -148,6 +196,12 @@ __device__ __forceinline__ int wave_prefix(int v) {
 }
 
 __device__ __forceinline__ int at_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// A value that is the same in every lane, in a scalar register (stores that follow
+// then wait for its load once, not each for all that is in flight).
+__device__ __forceinline__ float uniform(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
 
 // One adapter's group of rows, bounds checked.
 __device__ __forceinline__ void group_of(const RowSet& rs, int a, int n, int* first, int* count) {
@@ -566,7 +620,7 @@ __device__ __forceinline__ void rows_body(Lds& L, const AdapterArgs& d, const Ro
     top = fmaxf(top, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, top))));
     const int e = scale_exp<DT>(top);
     v8_t<DT> h[2];
-    split_pieces<DT, 2>(v, e, h);
+    split_pieces<DT, 2, true>(v, e, h);
     const size_t at = ((size_t)tile * 4 + t0 / 16 + wave / BW) * out.blocks + y * BW + b;
     out.frag[(at * 2 + 0) * 64 + lane] = __builtin_bit_cast(u32x4, h[0]);
     out.frag[(at * 2 + 1) * 64 + lane] = __builtin_bit_cast(u32x4, h[1]);
@@ -584,6 +638,9 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
 
 constexpr int kOutThreads = 256;
 constexpr int kOutWaves = kOutThreads / kWave;
+// Wavefronts per SIMD that the second launches keep registers for, where their
+// LDS leaves room for as many workgroups.
+constexpr int out_waves(int RT) { return RT <= 4 ? 3 : 2; }
 
 // ---------------------------------------------------------------------------
 // Second launch of the forward pass.
@@ -643,7 +700,7 @@ __device__ __forceinline__ void pack_rows(RowPack<RB>* p, const SharedTile& st, 
     top = fmaxf(top, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, top))));
     const int e = scale_exp<DT>(top);
     v8_t<DT> h[2];
-    split_pieces<DT, 2>(v, e, h);
+    split_pieces<DT, 2, true>(v, e, h);
     p->frag[b][0][lane] = __builtin_bit_cast(u32x4, h[0]);
     p->frag[b][1][lane] = __builtin_bit_cast(u32x4, h[1]);
     if (b == 0 && g == 0) p->scale[li] = __builtin_amdgcn_ldexpf(f, -e);
@@ -662,8 +719,9 @@ __device__ __forceinline__ int place_of(int n) { return n % 8 * 16 + n / 8; }
 // run of B.  One token, 6144 wide, rank 16: 5.0 us (k_rows 4.0); 48 requests of 32
 // adapters of rank up to 64, 6144 to 2048: 6.7 (8.6, for 11 MB of factors).
 template <int DT, int RT>
-__global__ __launch_bounds__(kOutThreads) void k_expand_small(AdapterArgs d, RowSet rs, const float* part, int S, float* u,
-                                                             const void* add, int64_t ldadd, void* y, int64_t ldy) {
+__global__ __launch_bounds__(kOutThreads, out_waves(RT)) void k_expand_small(AdapterArgs d, RowSet rs, const float* part, int S,
+                                                                            float* u, const void* add, int64_t ldadd, void* y,
+                                                                            int64_t ldy) {
   typedef typename Mat<DT>::elem E;
   constexpr int RB = (RT + 1) / 2, VR = RT == 1 ? 2 : 4, BL = 128 * VR / 64, BS = VR * 8 + 8;
   __shared__ SharedTile st;
@@ -699,24 +757,41 @@ __global__ __launch_bounds__(kOutThreads) void k_expand_small(AdapterArgs d, Row
   }
   const float f0 = rk ? d.scale[a] : 0.0f;
   pack_rows<DT, RB>(&pk, st, part, S, rs.T, d.R, f0, blockIdx.y == 0 ? u : nullptr);
-  f32x4 acc[8] = {};
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
+  const auto stage = [&](int b) {
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
       const int v = lane + 64 * i, r = b * 32 + v % VR * 8;
       *(u32x4*)(bs + place_of(v / VR) * BS + v % VR * 8) = keep_upto(bn[i], rk - r, whole);
     }
     lds_order();
+  };
+  const auto factor = [&](int q) { return *(const v8_t<DT>*)(bs + (q * 16 + li) * BS + (RT == 1 ? min(g, 2) : g) * 8); };
+  f32x4 acc[8] = {};
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    stage(b);
     if (b + 1 < RB) fetch(b + 1);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const v8_t<DT> bf = *(const v8_t<DT>*)(bs + (q * 16 + li) * BS + (RT == 1 ? min(g, 2) : g) * 8);
+      const v8_t<DT> bf = factor(q);
       acc[q] = Mat<DT>::mma(as_frag<DT>(pk.frag[b][0][lane]), bf, acc[q]);
       acc[q] = Mat<DT>::mma(as_frag<DT>(pk.frag[b][1][lane]), bf, acc[q]);
     }
     lds_order();
   }
+  redo_nan(acc, [&](int q) {
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int b = 0; b < RB; ++b) {
+      if (RB > 1) {
+        fetch(b);
+        stage(b);
+      }
+      v = Mat<DT>::mma(as_frag<DT>(pk.frag[b][0][lane]), factor(q), v);
+      lds_order();
+    }
+    return v;
+  });
   const f32x4 f = *(const f32x4*)&pk.scale[g * 4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -746,13 +821,15 @@ __global__ __launch_bounds__(kRowThreads) void k_small(AdapterArgs d, RowSet rs,
   const E* bbase = (const E*)d.b + (size_t)a * d.N * d.R;
   const int n0 = (blockIdx.y * kRowWaves + wave) * 128, c = n0 + li * 8;
   u32x4 bn[RB][BL], av[4] = {};
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
+  const auto fetch = [&](int b, u32x4 (&bn)[BL]) {
 #pragma unroll
     for (int i = 0; i < BL; ++i) {
       const int v = lane + 64 * i, r = b * 32 + v % VR * 8;
-      bn[b][i] = load8<DT>(bbase, (uint32_t)min(n0 + v / VR, d.N - 1) * d.R + (r < rk ? r : 0));
+      bn[i] = load8<DT>(bbase, (uint32_t)min(n0 + v / VR, d.N - 1) * d.R + (r < rk ? r : 0));
     }
+  };
+#pragma unroll
+  for (int b = 0; b < RB; ++b) fetch(b, bn[b]);
   int row[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -771,14 +848,19 @@ __global__ __launch_bounds__(kRowThreads) void k_small(AdapterArgs d, RowSet rs,
     }
   // this wavefront's fragments of u
   float v[RB][8], top = 0.0f;
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
+  const auto fetch_u = [&](int b, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = b * 32 + g * 8 + i;
-      v[b][i] = (RT > 1 || g < 2) && r < rk ? L.vs[li][r] : 0.0f;
-      top = fmaxf(top, finite_abs(v[b][i]));
+      v[i] = (RT > 1 || g < 2) && r < rk ? L.vs[li][r] : 0.0f;
     }
+  };
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    fetch_u(b, v[b]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(v[b][i]));
+  }
   top = fmaxf(top, __builtin_bit_cast(float, partner<16>(__builtin_bit_cast(int, top))));
   top = fmaxf(top, __builtin_bit_cast(float, partner<32>(__builtin_bit_cast(int, top))));
   const int e = scale_exp<DT>(top);
@@ -788,25 +870,47 @@ __global__ __launch_bounds__(kRowThreads) void k_small(AdapterArgs d, RowSet rs,
 #pragma unroll
     for (int i = 0; i < 2; ++i) *(u32x4*)(bs + (lane + 64 * i) * BS + 16) = u32x4{0, 0, 0, 0};
   }
+  const auto stage = [&](int b, const u32x4 (&bn)[BL]) {
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      const int k = lane + 64 * i, r = b * 32 + k % VR * 8;
+      *(u32x4*)(bs + place_of(k / VR) * BS + k % VR * 8) = keep_upto(bn[i], rk - r, whole);
+    }
+    lds_order();
+  };
+  const auto factor = [&](int q) { return *(const v8_t<DT>*)(bs + (q * 16 + li) * BS + (RT == 1 ? min(g, 2) : g) * 8); };
   f32x4 acc[8] = {};
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     v8_t<DT> h[2];
-    split_pieces<DT, 2>(v[b], e, h);
-#pragma unroll
-    for (int i = 0; i < BL; ++i) {
-      const int k = lane + 64 * i, r = b * 32 + k % VR * 8;
-      *(u32x4*)(bs + place_of(k / VR) * BS + k % VR * 8) = keep_upto(bn[b][i], rk - r, whole);
-    }
-    lds_order();
+    split_pieces<DT, 2, false>(v[b], e, h);
+    stage(b, bn[b]);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const v8_t<DT> bf = *(const v8_t<DT>*)(bs + (q * 16 + li) * BS + (RT == 1 ? min(g, 2) : g) * 8);
+      const v8_t<DT> bf = factor(q);
       acc[q] = Mat<DT>::mma(h[0], bf, acc[q]);
       acc[q] = Mat<DT>::mma(h[1], bf, acc[q]);
     }
     lds_order();
   }
+  redo_nan(acc, [&](int q) {
+    f32x4 s = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int b = 0; b < RB; ++b) {
+      float u[8];
+      fetch_u(b, u);
+      v8_t<DT> h[1];
+      split_pieces<DT, 1, true>(u, e, h);
+      if (RB > 1) {
+        u32x4 bn[BL];
+        fetch(b, bn);
+        stage(b, bn);
+      }
+      s = Mat<DT>::mma(h[0], factor(q), s);
+      lds_order();
+    }
+    return s;
+  });
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float f = __shfl(sc, g * 4 + i);
@@ -943,19 +1047,23 @@ __device__ __forceinline__ void spread_body(SpreadLds<DT, RT, ACROSS>& L, const 
     if (p + 1 < passes) fetch(c0 + kCols);
     __syncthreads();
     if (!mine || c0 >= C) continue;
+    const auto factor = [&](int b, int q) {
+      v8_t<DT> ff = {};
+      if (ACROSS) {
+        const E* at = fs + (b * 32 + g * 8 + (li >> 2)) * FS + q * 16 + (li & 3) * 4;
+        ff = read_across<DT>(at, at + 4 * FS);
+      } else if (RT > 1 || g < 2) {
+        ff = *(const v8_t<DT>*)(fs + (q * 16 + li) * FS + b * 32 + g * 8);
+      }
+      return ff;
+    };
     f32x4 tot[8] = {};
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
       if (b * 32 >= rk) break;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        v8_t<DT> ff = {};
-        if (ACROSS) {
-          const E* at = fs + (b * 32 + g * 8 + (li >> 2)) * FS + q * 16 + (li & 3) * 4;
-          ff = read_across<DT>(at, at + 4 * FS);
-        } else if (RT > 1 || g < 2) {
-          ff = *(const v8_t<DT>*)(fs + (q * 16 + li) * FS + b * 32 + g * 8);
-        }
+        const v8_t<DT> ff = factor(b, q);
         f32x4 s = kOneScale ? tot[q] : f32x4{0, 0, 0, 0};
         s = Mat<DT>::mma(as_frag<DT>(vf[b][0]), ff, s);
         s = Mat<DT>::mma(as_frag<DT>(vf[b][1]), ff, s);
@@ -965,6 +1073,17 @@ __device__ __forceinline__ void spread_body(SpreadLds<DT, RT, ACROSS>& L, const 
           for (int i = 0; i < 4; ++i) tot[q][i] = fmaf(s[i], sc[b][i], tot[q][i]);
       }
     }
+    redo_nan(tot, [&](int q) {
+      f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        if (b * 32 >= rk) break;
+        const f32x4 s = Mat<DT>::mma(as_frag<DT>(vf[b][0]), factor(b, q), kOneScale ? v : f32x4{0, 0, 0, 0});
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = kOneScale ? s[i] : fmaf(s[i], sc[b][i], v[i]);
+      }
+      return v;
+    });
     u32x4 res[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -984,7 +1103,7 @@ __device__ __forceinline__ void spread_body(SpreadLds<DT, RT, ACROSS>& L, const 
 }
 
 template <int DT, int RT, bool ACROSS>
-__global__ __launch_bounds__(kOutThreads) void k_spread(AdapterArgs d, RowSet rs, SpreadArgs sa) {
+__global__ __launch_bounds__(kOutThreads, out_waves(RT)) void k_spread(AdapterArgs d, RowSet rs, SpreadArgs sa) {
   __shared__ SpreadLds<DT, RT, ACROSS> lds;
   spread_body<DT, RT, ACROSS>(lds, d, rs, sa, blockIdx.x, blockIdx.y);
 }
@@ -1052,6 +1171,7 @@ template <int DT, int RT, int H>
 struct OuterLds {
   float top[kOutWaves * H];
   int ids[2][kChunkTiles<RT> * kGradM];  // rows of this chunk and of the next
+  int redo;                              // whether a result is NaN
   union {
     struct {
       u32x4 frag[kChunkTiles<RT>][RT][kGradPieces<DT>][64];
@@ -1075,7 +1195,7 @@ template <int DT, int RT, int H, bool TR, bool IDS>
 __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const AdapterArgs& d, const RowSet& rs, const OuterArgs& ga,
                                            int item, int chunk) {
   typedef typename Mat<DT>::elem E;
-  constexpr int NP = kGradPieces<DT>, CT = kChunkTiles<RT>, WV = kOutWaves * H, UW = (CT * RT + WV - 1) / WV;
+  constexpr int CT = kChunkTiles<RT>, WV = kOutWaves * H, UW = (CT * RT + WV - 1) / WV;
   constexpr int CR = CT * kGradM;  // rows of a chunk
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, g = lane >> 4;
   const int C = TR ? d.N : d.K, c0 = chunk * kOutCols + wave % kOutWaves * 64, half = wave / kOutWaves;
@@ -1112,143 +1232,163 @@ __device__ __forceinline__ void grad_outer(OuterLds<DT, RT, H>& L, const Adapter
         w[k][q] = v[(size_t)(IDS ? max(id_at(i + q), 0) : it.first + min(i + q, it.cnt - 1)) * d.R + r];
     }
   };
-  f32x4 acc[4][RT] = {};
-  int e = 0;
-  bool any = false;
-  int id = -1;
-  if (tiles) {
-    const int id0 = tid < CR ? fetch_id(0) : -1;
-    if (!IDS) fetch_v(0);
-    id = tid < CR ? fetch_id(CT) : -1;
-    if (tid < CR) {
-      L.ids[0][tid] = id0;
-      L.ids[1][tid] = id;
-    }
-    __syncthreads();
-    if (IDS) fetch_v(0);
-    fetch(half, rows[0]);
-    fetch(half + H, rows[1]);
-    id = tid < CR ? fetch_id(2 * CT) : -1;
-  }
-  for (int j0 = 0; j0 < tiles; j0 += CT) {
-    float top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < UW; ++k) {
-      const int unit = wave + k * WV, r = unit % RT * 16 + li, i = (j0 + unit / RT) * kGradM + g * 8;
-      if (j0 + unit / RT >= tiles) break;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const bool row = IDS ? id_at(min(i + q, j0 * kGradM + CR - 1)) >= 0 : i + q < it.cnt;
-        w[k][q] = unit < CT * RT && r < rk && row ? w[k][q] : 0.0f;
-        top = fmaxf(top, finite_abs(w[k][q]));
+  const auto pass = [&](auto first) {  // first: from the first pieces alone, for the results that are NaN; whether some are
+    constexpr bool FIRST = decltype(first)::value;
+    constexpr int NP = FIRST ? 1 : kGradPieces<DT>;
+    f32x4 acc[4][RT] = {};
+    int e = 0;
+    bool any = false;
+    int id = -1;
+    if (tiles) {
+      const int id0 = tid < CR ? fetch_id(0) : -1;
+      if (!IDS) fetch_v(0);
+      id = tid < CR ? fetch_id(CT) : -1;
+      if (tid < CR) {
+        L.ids[0][tid] = id0;
+        L.ids[1][tid] = id;
       }
+      __syncthreads();
+      if (IDS) fetch_v(0);
+      fetch(half, rows[0]);
+      fetch(half + H, rows[1]);
+      id = tid < CR ? fetch_id(2 * CT) : -1;
     }
-    if (DT == MOE_T_F16) {
-      top = __builtin_bit_cast(float, wave_max_u32(__builtin_bit_cast(uint32_t, top)));
-      if (lane == 0) L.top[wave] = top;
-    }
-    __syncthreads();  // also: the last chunk's fragments and ids have been read
-    if (j0 && tid < CR) {  // the next chunk's rows; and ask for those after
-      L.ids[j0 / CT + 1 & 1][tid] = id;
-      id = fetch_id(j0 + 2 * CT);
-    }
-    if (DT == MOE_T_F16) {
+    for (int j0 = 0; j0 < tiles; j0 += CT) {
+      float top = 0.0f;
 #pragma unroll
-      for (int q = 0; q < WV; ++q) top = fmaxf(top, L.top[q]);
-      if (top > 0.0f) {
-        const int en = any ? min(e, scale_exp<DT>(top)) : scale_exp<DT>(top);
-        if (any && en < e) {
-          const float f = __builtin_amdgcn_ldexpf(1.0f, en - e);
+      for (int k = 0; k < UW; ++k) {
+        const int unit = wave + k * WV, r = unit % RT * 16 + li, i = (j0 + unit / RT) * kGradM + g * 8;
+        if (j0 + unit / RT >= tiles) break;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) acc[q][r] *= f;
+        for (int q = 0; q < 8; ++q) {
+          const bool row = IDS ? id_at(min(i + q, j0 * kGradM + CR - 1)) >= 0 : i + q < it.cnt;
+          w[k][q] = unit < CT * RT && r < rk && row ? w[k][q] : 0.0f;
+          top = fmaxf(top, finite_abs(w[k][q]));
         }
-        e = en;
-        any = true;
+      }
+      if (DT == MOE_T_F16) {
+        top = __builtin_bit_cast(float, wave_max_u32(__builtin_bit_cast(uint32_t, top)));
+        if (lane == 0) L.top[wave] = top;
+      }
+      __syncthreads();  // also: the last chunk's fragments and ids have been read
+      if (j0 && tid < CR) {  // the next chunk's rows; and ask for those after
+        L.ids[j0 / CT + 1 & 1][tid] = id;
+        id = fetch_id(j0 + 2 * CT);
+      }
+      if (DT == MOE_T_F16) {
+#pragma unroll
+        for (int q = 0; q < WV; ++q) top = fmaxf(top, L.top[q]);
+        if (top > 0.0f) {
+          const int en = any ? min(e, scale_exp<DT>(top)) : scale_exp<DT>(top);
+          if (any && en < e) {
+            const float f = __builtin_amdgcn_ldexpf(1.0f, max(en - e, -126));  // (not 0: the sums may be infinite)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int r = 0; r < RT; ++r) acc[q][r] *= f;
+          }
+          e = en;
+          any = true;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < UW; ++k) {
+        const int unit = wave + k * WV;
+        if (unit < CT * RT && j0 + unit / RT < tiles) {
+          v8_t<DT> p[NP];
+          split_pieces<DT, NP, FIRST>(w[k], e, p);
+#pragma unroll
+          for (int q = 0; q < NP; ++q) L.frag[unit / RT][unit % RT][q][lane] = __builtin_bit_cast(u32x4, p[q]);
+        }
+      }
+      __syncthreads();
+      if (j0 + CT < tiles) fetch_v(j0 + CT);
+      const auto tile = [&](int j, u32x4 (&rows)[4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(u32x4*)(stage + (lane / 8 + 8 * q) * kStride + lane % 8 * 8) = keep(rows[q], id_of(j, q) >= 0 && col < C);
+        if (j + 2 * H < tiles) fetch(j + 2 * H, rows);
+        lds_order();
+        v8_t<DT> xf[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const E* p = stage + (g * 8 + (li >> 2)) * kStride + (TR ? q * 16 + (li & 3) * 4 : (li & 3) * 16 + q * 4);
+          xf[q] = read_across<DT>(p, p + 4 * kStride);
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const v8_t<DT> vf = as_frag<DT>(L.frag[j - j0][r][p][lane]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q][r] = TR ? Mat<DT>::mma(vf, xf[q], acc[q][r]) : Mat<DT>::mma(xf[q], vf, acc[q][r]);
+          }
+        lds_order();
+      };
+      const int j1 = min(j0 + CT, tiles);
+      for (int j = j0 + half; j < j1; j += 2 * H) {
+        tile(j, rows[0]);
+        if (j + H < j1) tile(j + H, rows[1]);
       }
     }
+    // the two wavefronts of each 64 columns, 4 r tiles at a time
 #pragma unroll
-    for (int k = 0; k < UW; ++k) {
-      const int unit = wave + k * WV;
-      if (unit < CT * RT && j0 + unit / RT < tiles) {
-        v8_t<DT> p[NP];
-        split_pieces<DT, NP>(w[k], e, p);
+    for (int r0 = 0; r0 < (H == 2 ? RT : 0); r0 += 4) {
+      constexpr int RH = RT < 4 ? RT : 4;
+      __syncthreads();
+      if (half) {
 #pragma unroll
-        for (int q = 0; q < NP; ++q) L.frag[unit / RT][unit % RT][q][lane] = __builtin_bit_cast(u32x4, p[q]);
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int r = 0; r < RH; ++r) L.half[wave % kOutWaves][q * RH + r][lane] = acc[q][r0 + r];
+      }
+      __syncthreads();
+      if (!half) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int r = 0; r < RH; ++r) acc[q][r0 + r] += L.half[wave][q * RH + r][lane];
       }
     }
-    __syncthreads();
-    if (j0 + CT < tiles) fetch_v(j0 + CT);
-    const auto tile = [&](int j, u32x4 (&rows)[4]) {
+    bool nan = false;
+    if (half || c0 >= C) return nan;
+    const size_t per = (size_t)d.R * (d.K + d.N);
+    float* out = TR ? ga.d_b : ga.d_a;
+    float* o = it.slot >= 0 ? ga.sums + it.slot * per + (TR ? (size_t)d.R * d.K : 0) : out + (size_t)it.a * d.R * C;
+    // (without rows: zero, whatever the scale)
+    const float f = uniform(tiles ? __builtin_amdgcn_ldexpf(TR ? d.scale[it.a] : 1.0f, -e) : 0.0f);
+    const auto put = [&](float* p, f32x4 v) {
+      if (FIRST) {
+        v = replace_nan(*(const f32x4*)p, v);
+      } else {
+        nan |= has_nan(v);
+      }
+      *(f32x4*)p = v;
+    };
+    // (past the rank: zeros, where the sums may hold zeros times an infinity)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(u32x4*)(stage + (lane / 8 + 8 * q) * kStride + lane % 8 * 8) = keep(rows[q], id_of(j, q) >= 0 && col < C);
-      if (j + 2 * H < tiles) fetch(j + 2 * H, rows);
-      lds_order();
-      v8_t<DT> xf[4];
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const E* p = stage + (g * 8 + (li >> 2)) * kStride + (TR ? q * 16 + (li & 3) * 4 : (li & 3) * 16 + q * 4);
-        xf[q] = read_across<DT>(p, p + 4 * kStride);
-      }
+        if (TR) {  // [N][R]: a lane holds 4 consecutive r of one column
+          const int n = c0 + q * 16 + li, rr = r * 16 + g * 4;
+          f32x4 v = acc[q][r] * f;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const v8_t<DT> vf = as_frag<DT>(L.frag[j - j0][r][p][lane]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[q][r] = TR ? Mat<DT>::mma(vf, xf[q], acc[q][r]) : Mat<DT>::mma(xf[q], vf, acc[q][r]);
+          for (int i = 0; i < 4; ++i) v[i] = rr + i < rk ? v[i] : 0.0f;
+          if (n < C && rr < d.R) put(o + (size_t)n * d.R + rr, v);
+        } else {  // [R][K]: 4 consecutive columns of one r
+          const int k = c0 + g * 16 + q * 4, rr = r * 16 + li;
+          if (k < C && rr < d.R) put(o + (size_t)rr * C + k, rr < rk ? acc[q][r] * f : f32x4{0, 0, 0, 0});
         }
-      lds_order();
-    };
-    const int j1 = min(j0 + CT, tiles);
-    for (int j = j0 + half; j < j1; j += 2 * H) {
-      tile(j, rows[0]);
-      if (j + H < j1) tile(j + H, rows[1]);
-    }
-  }
-  // the two wavefronts of each 64 columns, 4 r tiles at a time
-#pragma unroll
-  for (int r0 = 0; r0 < (H == 2 ? RT : 0); r0 += 4) {
-    constexpr int RH = RT < 4 ? RT : 4;
-    __syncthreads();
-    if (half) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int r = 0; r < RH; ++r) L.half[wave % kOutWaves][q * RH + r][lane] = acc[q][r0 + r];
-    }
-    __syncthreads();
-    if (!half) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int r = 0; r < RH; ++r) acc[q][r0 + r] += L.half[wave][q * RH + r][lane];
-    }
-  }
-  if (half || c0 >= C) return;
-  const size_t per = (size_t)d.R * (d.K + d.N);
-  float* out = TR ? ga.d_b : ga.d_a;
-  float* o = it.slot >= 0 ? ga.sums + it.slot * per + (TR ? (size_t)d.R * d.K : 0) : out + (size_t)it.a * d.R * C;
-  // (without rows: zero, whatever the scale)
-  const float f = tiles ? __builtin_amdgcn_ldexpf(TR ? d.scale[it.a] : 1.0f, -e) : 0.0f;
-  // (past the rank: zeros, where the sums may hold zeros times an infinity)
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (TR) {  // [N][R]: a lane holds 4 consecutive r of one column
-        const int n = c0 + q * 16 + li, rr = r * 16 + g * 4;
-        f32x4 v = acc[q][r] * f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = rr + i < rk ? v[i] : 0.0f;
-        if (n < C && rr < d.R) *(f32x4*)(o + (size_t)n * d.R + rr) = v;
-      } else {  // [R][K]: 4 consecutive columns of one r
-        const int k = c0 + g * 16 + q * 4, rr = r * 16 + li;
-        if (k < C && rr < d.R) *(f32x4*)(o + (size_t)rr * C + k) = rr < rk ? acc[q][r] * f : f32x4{0, 0, 0, 0};
       }
-    }
+    return nan;
+  };
+  if (tid == 0) L.redo = 0;
+  const bool nan = pass(Const<false>{});
+  if (!tiles) return;
+  if (__ballot(nan) && lane == 0) L.redo = 1;
+  __syncthreads();
+  if (L.redo) pass(Const<true>{});
 }
 
 // Workgroups [0, rows_groups) form v (tile, block of r, bands: as k_rows), the
@@ -1272,7 +1412,7 @@ __global__ __launch_bounds__(kRowThreads) void k_grad_first(AdapterArgs d, RowSe
 
 // Workgroups [0, nA) take dA, the rest dx.
 template <int DT, int RT>
-__global__ __launch_bounds__(kOutThreads) void k_grad_second(AdapterArgs d, RowSet rs, SpreadArgs sa, OuterArgs ga) {
+__global__ __launch_bounds__(kOutThreads, out_waves(RT)) void k_grad_second(AdapterArgs d, RowSet rs, SpreadArgs sa, OuterArgs ga) {
   __shared__ union Lds {
     SpreadLds<DT, RT, true> spread;
     OuterLds<DT, RT, 1> outer;
@@ -1430,10 +1570,6 @@ AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
 }
 
 // Calls f with the type and the number of rank fragments as constants.
-template <int V>
-struct Const {
-  static constexpr int value = V;
-};
 template <typename F>
 void by_shape(const moe_adapters_t& d, F f) {
   const auto ranks = [&](auto dt) {
