@@ -135,7 +135,8 @@ struct Item {
 struct ItemLds {
   int item[kMaxExperts], slot[kMaxExperts], r0[kMaxExperts], r1[kMaxExperts], sums[2][4];
 };
-__device__ __forceinline__ void make_items(ItemLds& L, const int32_t* offsets, int E, int rows, int most, int per, Item* items) {
+__device__ __forceinline__ void make_items(ItemLds& L, const int32_t* offsets, int E, int rows, int most, Item* items) {
+  constexpr int per = kItemRows;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int at = 0, slots = 0;
   for (int e0 = 0; e0 < E; e0 += 256) {
@@ -200,7 +201,7 @@ __device__ __forceinline__ float scaled_sigmoid(float z, float top) { return 1.0
 constexpr int kSlotThreads = 256;
 __global__ __launch_bounds__(kSlotThreads) void k_route_slots(RouteArgs a, int slices, const float* zpart, const float* br,
                                                              const float* dw, float* dz, const int32_t* offsets, int rows,
-                                                             int most, int per_item, Item* items) {
+                                                             int most, Item* items) {
   __shared__ union {
     ItemLds items;
     struct {
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(kSlotThreads) void k_route_slots(RouteArgs a, int s
   } L;
   auto& part = L.part;
   float *sg = L.sg, *gw = L.gw;
-  if (blockIdx.x == gridDim.x - 1) return make_items(L.items, offsets, a.E, rows, most, per_item, items);
+  if (blockIdx.x == gridDim.x - 1) return make_items(L.items, offsets, a.E, rows, most, items);
   const int l = threadIdx.x & 63, q = threadIdx.x >> 6, n = a.T * a.k, per = 64 / a.k;
   const int p0 = blockIdx.x * per * a.k, np = min(per * a.k, n - p0), p = min(p0 + l, n - 1);
   float z = 0.0f;
@@ -539,7 +540,7 @@ constexpr int kSliceGroups = 512;  // workgroups of the slice kernels
 struct RoutePlan {
   bool gather;  // few tokens: rows of Wr gathered
   int slices, ranges, range;
-  int per_item, items, slots;  // of the weights' gradient (bounds)
+  int items, slots;  // of the weights' gradient (bounds; none where rows are gathered)
   size_t dz, z, item, sums, bsums, total;
 };
 RoutePlan route_plan(int T, int k, int E, int H, int rows) {
@@ -548,10 +549,6 @@ RoutePlan route_plan(int T, int k, int E, int H, int rows) {
   p.slices = ceil_div(H, E <= kWideSlice ? 64 : 32);
   p.ranges = std::max(1, std::min(kSliceGroups / p.slices, ceil_div(T, 32)));
   p.range = ceil_div(std::max(T, 1), p.ranges);
-  // (a batch of few tokens leaves no expert many rows, unless tokens name it twice)
-  p.per_item = T <= kItemRows ? std::max(1, rows) : kItemRows;
-  p.items = E + rows / p.per_item;
-  p.slots = rows > p.per_item ? 2 * (rows / p.per_item) : 0;
   size_t o = 0;
   const auto take = [&o](size_t bytes) {
     const size_t at = o;
@@ -560,6 +557,8 @@ RoutePlan route_plan(int T, int k, int E, int H, int rows) {
   };
   p.dz = take(std::max<size_t>(4, (size_t)T * k * 4));
   if (!p.gather) {
+    p.items = E + rows / kItemRows;
+    p.slots = 2 * (rows / kItemRows);
     p.z = take((size_t)p.slices * T * k * 4);
     p.item = take((size_t)p.items * sizeof(Item));
     p.sums = take((size_t)p.slots * H * 4);
@@ -605,14 +604,14 @@ int moe_route_backward(const void* x, int32_t dtype, int32_t T, int32_t H, int32
   const u32x4* addv = (const u32x4*)add;
   u32x4* dxv = (u32x4*)dx;
   const dim3 grid(p.slices, p.ranges);
-  Item* items = p.gather || T == 0 ? nullptr : (Item*)((char*)ws + p.item);
+  Item* items = p.gather ? nullptr : (Item*)((char*)ws + p.item);
   float *sums = (float*)((char*)ws + p.sums), *bsums = (float*)((char*)ws + p.bsums);
   const auto run = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     const auto slices = [&](auto dots, auto to_dx) {
       dots<<<grid, kThreads, 0, s>>>(a, p.range, z);
       k_route_slots<<<ceil_div(T, 64 / k) + 1, kSlotThreads, 0, s>>>(a, p.slices, z, router_b, dw, dz, offsets, rows, p.items,
-                                                                     p.per_item, items);
+                                                                     items);
       to_dx<<<grid, kThreads, 0, s>>>(a, p.range, dz, addv, dxv);
     };
     if (T && p.gather) k_route_grad_tokens<DT><<<T, kThreads, 0, s>>>(a, router_b, dw, addv, dxv, dz);
