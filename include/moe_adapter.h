@@ -53,7 +53,8 @@ size_t moe_adapter_workspace_bytes(const moe_adapters_t* d, int32_t T);
  *   without an adapter), which the backward call takes;
  *   offsets, pairs: moe_sort of ids as [T][1] with n experts and align 1, or
  *   both NULL: the call groups the rows itself (a caller with several
- *   projections per step sorts once and passes the result to each). */
+ *   projections per step sorts once and passes the result to each).  (Of a row
+ *   with an adapter that they do not name, y, u and dx are not written.) */
 int moe_adapter_forward(const moe_adapters_t* d, const void* x, int64_t ldx, int32_t T, const int32_t* ids,
                         const int32_t* offsets, const int32_t* pairs, const void* add, int64_t ldadd, void* y,
                         int64_t ldy, float* u, void* ws, size_t ws_bytes, void* stream);
