@@ -176,25 +176,6 @@ struct Tile {
   int a, cnt, first, row, rank;  // row: this lane's
 };
 
-__device__ __forceinline__ int lanes_under(uint64_t m) {
-  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-}
-
-// Inclusive sum over the wavefront's lanes (all active): row shifts, then the
-// rows' ends broadcast on.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int add_shifted(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_prefix(int v) {
-  v = add_shifted<0x111, 0xF>(v);  // row_shr:1
-  v = add_shifted<0x112, 0xF>(v);  // row_shr:2
-  v = add_shifted<0x114, 0xF>(v);  // row_shr:4
-  v = add_shifted<0x118, 0xF>(v);  // row_shr:8
-  v = add_shifted<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
-  return add_shifted<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
-}
-
 __device__ __forceinline__ int at_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 // A value that is the same in every lane, in a scalar register (stores that follow
@@ -235,7 +216,7 @@ __device__ __forceinline__ Tile find_tile(const AdapterArgs& d, const RowSet& rs
       const uint64_t v = __ballot(one);
       same &= one ? v : ~v;
     }
-    const int nth = lanes_under(same);
+    const int nth = lanes_below(same);
     uint64_t lead = __ballot(lane < rs.T && nth % M == 0);
     for (int i = 0; i < tile; ++i) lead &= lead - 1;
     if (!lead) return {n, 0, 0, -1, 0};
@@ -256,13 +237,13 @@ __device__ __forceinline__ Tile find_tile(const AdapterArgs& d, const RowSet& rs
   for (int a0 = 0; a0 < n && n > 64; a0 += 64) {
     int first, count;
     group_of(rs, a0 + lane, n, &first, &count);
-    used += at_lane(wave_prefix((count + M - 1) / M), 63);
+    used += at_lane(wave_inclusive_scan((count + M - 1) / M), 63);
   }
   for (int a0 = 0, done = 0; a0 < n; a0 += 64) {
     int first, count;
     group_of(rs, a0 + lane, n, &first, &count);
     const int rank = rank_of(d, min(a0 + lane, n - 1));
-    const int nt = (count + M - 1) / M, incl = wave_prefix(nt);
+    const int nt = (count + M - 1) / M, incl = wave_inclusive_scan(nt);
     if (a0 == 0) {
       tile = tile_of_place(tile, min(n > 64 ? used : at_lane(incl, 63), rs.tiles));
       if (tile < 0) break;
@@ -334,10 +315,10 @@ __device__ __forceinline__ void group_tile(SharedTile* s, const AdapterArgs& d, 
       const uint64_t v = __ballot(one);
       same &= one ? v : ~v;
     }
-    if (id[c] >= 0 && lanes_under(same) == 0) atomicAdd(&L.count[id[c]], (int)__popcll(same));
+    if (id[c] >= 0 && lanes_below(same) == 0) atomicAdd(&L.count[id[c]], (int)__popcll(same));
   }
   __syncthreads();
-  const int count = L.count[lane], nt = (count + kM - 1) / kM, incl = wave_prefix(nt), to = wave_prefix(count);
+  const int count = L.count[lane], nt = (count + kM - 1) / kM, incl = wave_inclusive_scan(nt), to = wave_inclusive_scan(count);
   tile = tile_of_place(tile, min(at_lane(incl, 63), rs.tiles));
   int a = n, cnt = 0, first = 0, j = 0;
   const uint64_t past = __ballot(incl > tile);
@@ -353,11 +334,11 @@ __device__ __forceinline__ void group_tile(SharedTile* s, const AdapterArgs& d, 
     if (lane == 0) L.per[c * W + wave] = (int)__popcll(m);
   }
   __syncthreads();
-  const int p = L.per[lane], before = wave_prefix(p) - p;
+  const int p = L.per[lane], before = wave_inclusive_scan(p) - p;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const uint64_t m = __ballot(id[c] == a);
-    const int r = __shfl(before, c * W + wave) + lanes_under(m) - j * kM;
+    const int r = __shfl(before, c * W + wave) + lanes_below(m) - j * kM;
     if (id[c] == a && r >= 0 && r < cnt) s->row[r] = (c * W + wave) * 64 + lane;
   }
   if (tid < kM && tid >= cnt) s->row[tid] = -1;
@@ -1137,7 +1118,7 @@ __device__ __forceinline__ Item find_item(const RowSet& rs, int n, int item, int
     group_of(rs, a0 + lane, n, &first, &count);
     const int parts = (count + G - 1) / G, ni = a0 + lane < n ? max(1, parts) : 0;
     const int ns = parts > 1 ? parts : 0;
-    const int incl = wave_prefix(ni), is = wave_prefix(ns);
+    const int incl = wave_inclusive_scan(ni), is = wave_inclusive_scan(ns);
     const uint64_t past = __ballot(incl > item - done);
     if (past) {
       const int at = __builtin_ctzll(past);
@@ -1443,7 +1424,7 @@ __global__ __launch_bounds__(256) void k_grad_sum(AdapterArgs d, RowSet rs, cons
     int first, count;
     group_of(rs, a0 + lane, d.n, &first, &count);
     const int parts = (count + G - 1) / G, ns = parts > 1 ? parts : 0;
-    const int incl = wave_prefix(ns);
+    const int incl = wave_inclusive_scan(ns);
     if (a - a0 < 64) {
       slot += at_lane(incl - ns, a - a0);
       mine = at_lane(ns, a - a0);
@@ -1464,7 +1445,6 @@ __global__ __launch_bounds__(256) void k_grad_sum(AdapterArgs d, RowSet rs, cons
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-inline bool bad(const void* p, unsigned align) { return !p || !aligned_to(p, align); }
 inline bool bad_ld(int64_t ld, int width) { return ld < width || ld % 8; }
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 

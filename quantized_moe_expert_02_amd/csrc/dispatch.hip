@@ -45,10 +45,6 @@ __device__ __forceinline__ uint64_t match_id(int id, bool ok, int bits) {
   return m;
 }
 
-__device__ __forceinline__ int lanes_below(uint64_t m) {
-  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-}
-
 // Per-workgroup expert counts, [blocks][E].
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(const int32_t* idx, int n, int E, int per_block,
                                                              int32_t* cnt) {
@@ -465,8 +461,6 @@ int check_slots(int32_t T, int32_t k, int32_t rows) {
   if (T < 0 || k < 1 || rows < 0) return MOE_E_INVAL;
   return k > kMaxTopK ? MOE_E_UNSUPPORTED : MOE_OK;
 }
-
-inline bool bad(const void* p, unsigned align) { return !p || !aligned_to(p, align); }
 
 }  // namespace
 

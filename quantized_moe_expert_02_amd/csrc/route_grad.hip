@@ -517,7 +517,6 @@ __global__ __launch_bounds__(256) void k_route_sum(const Item* items, int H, con
   }
 }
 
-inline bool bad(const void* p, unsigned align) { return !p || !aligned_to(p, align); }
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int check_shape(int32_t T, int32_t k, int32_t E, int32_t H, int32_t rows) {

@@ -52,7 +52,13 @@ __device__ __forceinline__ u32x4 pack_vec(const float (&f)[kVec<DT>]) {
   return __builtin_bit_cast(u32x4, r);
 }
 
+// Lanes of m below this one.
+__device__ __forceinline__ int lanes_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
 inline bool aligned_to(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline bool bad(const void* p, unsigned align) { return !p || !aligned_to(p, align); }
 inline size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 inline size_t elem_bytes(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
 
