@@ -12,8 +12,11 @@
  * at or past r_a are not used, and their gradients are zero.
  *
  * Conventions are those of moe_dispatch.h.  Rows and adapters are binary16 or
- * bfloat16 (one moe_dtype_t for all); products are exact, sums are held in
- * fp32, outputs are rounded once.  An infinity in any operand, or a product past
+ * bfloat16 (one moe_dtype_t for all); products of theirs are exact, sums, u and v
+ * among them, are held in fp32, outputs are rounded once.  As factors in their
+ * turn u and v count to 22 bits in binary16 (no finer than 2^-38 of the largest of
+ * the row, or in d_a and d_b of the adapter's rows), and in bfloat16 to 16 bits in y
+ * and dx and to 24 in d_a and d_b.  An infinity in any operand, or a product past
  * fp32's range, gives the infinity or NaN of the formula.  x, dy, y, dx and add may
  * have rows of a wider buffer (ld: elements from row to row, a multiple of 8).
  */

@@ -29,7 +29,8 @@
  *     pairs, offsets, dw, db) 4-byte aligned, router_w and its gradient 16.
  *   - Workspaces need no initial contents and 16-byte alignment; calls that
  *     overlap in time must not share one.
- *   - Sums are held in fp32 and rounded once to the rows' type.  Infinities
+ *   - Sums are held in fp32 (the router's logits too, which moe_route forms
+ *     in fp64) and rounded once to the rows' type.  Infinities
  *     and NaNs propagate as the formulas say; rows of dropped slots and
  *     padding rows are never read.  Bitwise the same at every call (no
  *     floating-point atomics).

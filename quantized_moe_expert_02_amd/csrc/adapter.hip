@@ -49,10 +49,11 @@ using v8_t = typename Mat<DT>::v8;
 // ---------------------------------------------------------------------------
 // fp32 factors on 16-bit matrix instructions.  u and v are sums and are not
 // rounded to 16 bits: a value is carried as a sum of 16-bit pieces, each the
-// rounded rest of the ones before (two binary16 pieces hold 22 bits, two
-// bfloat16 16 bits, three 24).  binary16 lacks fp32's range, so values are
-// first scaled by a power of two per row (or per tile, where the contraction
-// runs over rows) that brings the largest finite one to 2^13.
+// rounded rest of the ones before (two binary16 pieces hold 22 bits and no less
+// than 2^-38 of the scale's largest, two bfloat16 16 bits, three 24).  binary16
+// lacks fp32's range, so values are first scaled by a power of two per row (or per
+// tile, where the contraction runs over rows) that brings the largest finite one
+// to 2^13.
 // ---------------------------------------------------------------------------
 constexpr int kTopExp = 13;
 
@@ -288,8 +289,8 @@ __device__ __forceinline__ void share_tile(SharedTile* s, const AdapterArgs& d, 
 // workgroup of NT threads: it counts the adapters' rows, finds the tile's adapter,
 // and takes that one's rows by their place among them.  Ends with a barrier.
 // 1,801 rows of 8 adapters, 6144 wide, rank 64: 2 us longer than from a sorted
-// order, which takes 4 and a launch; calls 27.2 and 29.4 us, 200 rows 17.7 and 21.0,
-// 4,096 rows of 64 adapters 92.5 and 95.5.  (Of 300 adapters 31.8 and 24.2.)
+// order, which takes 4 and a launch; calls 27.4 and 29.5 us, 200 rows of 2048, rank 16
+// 17.4 and 20.5, 4,096 rows of 64 adapters 84 and 87.  (Of 300 adapters 31.8 and 24.2.)
 constexpr int kGroupRows = 4096;
 struct GroupLds {
   int count[64];  // rows of each adapter
@@ -455,7 +456,7 @@ struct RowsLds {
 // the next steps' loads in flight meanwhile.
 // 2,048 rows of 6144 binary16, rank 16: 10.3 us, of which 1.2 find the tile, 3.5
 // pass until the first steps have their data, 3.0 take the other two thirds, 1.0
-// join and split the sums, the rest is the launch.  1,801 rows, rank 64: 16.0 us, 1.7
+// join and split the sums, the rest is the launch.  1,801 rows, rank 64: 16.4 us, 1.7
 // of them grouping; its 120 workgroups are bound by what a CU loads (64 bytes a
 // cycle), and more of them load more in all (the choice at RowsShape); with 1,024
 // threads each 0.9 us longer.
@@ -619,8 +620,10 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(AdapterArgs d, RowSet rs, 
 
 constexpr int kOutThreads = 256;
 constexpr int kOutWaves = kOutThreads / kWave;
-// Wavefronts per SIMD that the second launches keep registers for, where their
-// LDS leaves room for as many workgroups.
+// Wavefronts per SIMD that the second launches are held to.  Calls so and without:
+// 1,801 rows of 6144, rank 64 27.4 and 29.7 us, 2,048 rows, rank 32 26.1 and 28.0,
+// gradients of rank 16 31.5 and 34.0, but 4,096 rows of 64 adapters 84 and 79.  (4 at
+// rank 64 is more than the registers: 31.9 us for the first.)
 constexpr int out_waves(int RT) { return RT <= 4 ? 3 : 2; }
 
 // ---------------------------------------------------------------------------
@@ -698,7 +701,7 @@ __device__ __forceinline__ int place_of(int n) { return n % 8 * 16 + n / 8; }
 // y[t] = add[t] + s_a B_a u[t] for a small tile's rows, 128 columns per
 // wavefront.  Bound by a chain of waits: the tile, the sums of u's segments, one
 // run of B.  One token, 6144 wide, rank 16: 5.0 us (k_rows 4.0); 48 requests of 32
-// adapters of rank up to 64, 6144 to 2048: 6.7 (8.6, for 11 MB of factors).
+// adapters of rank up to 64, 6144 to 2048: 6.5 (7.2, for 11 MB of factors).
 template <int DT, int RT>
 __global__ __launch_bounds__(kOutThreads, out_waves(RT)) void k_expand_small(AdapterArgs d, RowSet rs, const float* part, int S,
                                                                             float* u, const void* add, int64_t ldadd, void* y,
@@ -787,7 +790,7 @@ __global__ __launch_bounds__(kOutThreads, out_waves(RT)) void k_expand_small(Ada
 // Both products of a small tile in one launch, 128 columns of y per wavefront:
 // every workgroup forms the tile's u for itself.  That costs the GPU about what
 // the launch between did, and spares the host that launch (kSmallElems).  Bound by
-// the same chain of waits: one token, 6144 wide, rank 16: 9.3 us.
+// the same chain of waits: one token, 6144 wide, rank 16: 9.5 us.
 template <int DT, int RT>
 __global__ __launch_bounds__(kRowThreads) void k_small(AdapterArgs d, RowSet rs, const void* x, int64_t ldx, float* u,
                                                       const void* add, int64_t ldadd, void* y, int64_t ldy) {
@@ -951,7 +954,7 @@ struct SpreadLds {
 // of A, LDS holds their columns in that order, and 16 lanes read product q's
 // across.
 // Bound by memory, once the first run's data are there: 1,801 rows of 6144
-// bfloat16, rank 64: 11.7 us for 44 MB of add and y (3.8 TB/s).
+// bfloat16, rank 64: 11.9 us for 44 MB of add and y (3.7 TB/s).
 template <int DT, int RT, bool ACROSS>
 __device__ __forceinline__ void spread_body(SpreadLds<DT, RT, ACROSS>& L, const AdapterArgs& d, const RowSet& rs,
                                             const SpreadArgs& sa, int tile, int chunk) {
@@ -1094,8 +1097,8 @@ __global__ __launch_bounds__(kOutThreads, out_waves(RT)) void k_spread(AdapterAr
 // and, on the CUs that leaves free, dB, and k_grad_second dx and dA; or k_rows
 // forms v, k_spread dx, and k_grad_weights dA and dB.  k_grad_sum adds the
 // partial dA and dB of adapters whose rows several workgroups took.
-// 2,048 rows of 4 adapters, 6144 wide: rank 16, binary16 15.1, 14.0 and 4.2 us for
-// 4 passes over 25 MB and partial sums of 7; rank 64, bfloat16 16.1, 9.9 and 35.5,
+// 2,048 rows of 4 adapters, 6144 wide: rank 16, binary16 15.3, 13.7 and 4.2 us for
+// 4 passes over 25 MB and partial sums of 7; rank 64, bfloat16 16.4, 10.1 and 36.1,
 // the last for making three pieces of each value of u and v in every workgroup,
 // between barriers.
 // ---------------------------------------------------------------------------
@@ -1471,9 +1474,9 @@ constexpr int kSmallRows = 64;
 // A small batch takes one launch (k_small) up to rank 64 where its workgroups load
 // up to so many elements of x and A each, and fit the GPU at once.  Calls so and in
 // two launches, of which 3.4 us are the second one's host time (GPU alone in
-// brackets): rank 16, 6144 wide 13.0 and 15.9 us (9.3 and 9.1); rank 32, 2048 wide 13.0
-// and 15.9 (8.6 and 10.3), 6144 wide 12.8 and 15.8 (11.8 and 10.4); rank 16, 10240 wide
-// 13.0 and 16.1 (12.0 and 10.0); rank 64, 6144 wide 18.4 and 15.7 (18.9 and 11.9).
+// brackets): rank 16, 6144 wide 12.9 and 16.0 us (9.5 and 8.9); rank 32, 2048 wide 12.9
+// and 15.8 (7.3 and 8.6), 6144 wide 12.9 and 15.9 (11.4 and 9.6); rank 16, 10240 wide
+// 12.9 and 15.9 (11.7 and 9.1); rank 64, 6144 wide 16.3 and 15.9 (16.6 and 10.1).
 constexpr int kSmallTiles = 4;
 constexpr int kSmallElems = 5 << 16;
 constexpr int kSmallGroups = 256;
@@ -1483,14 +1486,14 @@ constexpr int kSegment = 1024;
 constexpr int kWideRows = 4096;  // rows from which k_rows takes 64 r at a time (RowsShape)
 constexpr int kWanted = 256;     // workgroups of k_grad_weights, one per CU
 // Rank fragments up to which the gradients take two launches.  Two and three
-// launches, 6144 wide, 4 adapters: 2,048 rows rank 16 34.0 and 39.7 us, rank 32 45.3
-// and 47.1, rank 64 78.8 and 63.0 (the kernels' register and LDS needs add up);
-// 8,000 rows, 2048 to 6144 wide, rank 16 63 and 93; 200 rows, 2048 wide 13.0 and
-// 15.4.
+// launches, 6144 wide, 4 adapters: 2,048 rows rank 16 31.4 and 36.5 us, rank 32 40.5
+// and 44.3, rank 64 69.0 and 60.5 (the kernels' register and LDS needs add up);
+// 8,000 rows, 2048 to 6144 wide, rank 16 65 and 93; 200 rows, 2048 wide 19.6 and
+// 22.6.
 constexpr int kMergeTiles = 2;
-// Workgroups of k_spread below which none takes more than one run.  1,801 and
-// 7,204 rows of 6144, rank 64: 12.6 and 40.3 us; 256: 15.2 and 52.9; 1,024: 12.8 and
-// 41.6; one run each: 12.8 and 42.1.
+// Workgroups of k_spread below which none takes more than one run.  Calls of 1,801
+// and 7,204 rows of 6144, rank 64: 27.4 and 83.3 us; 256: 29.7 and 93.4; 1,024: 27.8
+// and 83.9; one run each: 27.7 and 85.3.
 constexpr int kSpreadGroups = 512;
 
 // Matrix fragments of a rank: 1, 2, 4 or 8 of 16.
@@ -1515,12 +1518,12 @@ AdapterPlan adapter_plan(const moe_adapters_t& d, int T) {
   p.rb = (rank_tiles(d.R) + 1) / 2;
   // Rows of an adapter per workgroup of its weight gradients: more leave the
   // last one working alone, fewer cost partial sums (R (K + N) floats each).
-  // Rank 16, 4 adapters: 2,048 rows of 6144 34.0 us with 256, 40.4 with 512, 51.5 with
-  // 1,024; 8,000 rows, 2048 to 6144 wide 63.0, 67.0, 81.2.  Above rank 32 a CU holds
+  // Rank 16, 4 adapters: 2,048 rows of 6144 31.4 us with 256, 39.0 with 512, 51.9 with
+  // 1,024; 8,000 rows, 2048 to 6144 wide 64.7, 70.5, 86.3.  Above rank 32 a CU holds
   // one workgroup, so a launch has no more than there are CUs, or one per adapter
-  // where that is more: rank 64, 2,048 rows of 6144 of 4 adapters whole 63 us, in parts
-  // of 512 71; of one adapter whole 93, in parts of 512 57, of 352 67; 4,000 rows of
-  // 2048 of 4 adapters whole 76, in parts of 352 45.  (Up to 256 rows are not split:
+  // where that is more: rank 64, 2,048 rows of 6144 of 4 adapters whole 62 us, in parts
+  // of 512 64; of one adapter whole 97, in parts of 512 55, of 352 66; 4,000 rows of
+  // 2048 of 4 adapters whole 81, in parts of 512 47, of 352 44.  (Up to 256 rows are not split:
   // the sum would cost a launch.)
   const int tiles = rank_tiles(d.R), cols = ceil_div(d.K, kOutCols) + ceil_div(d.N, kOutCols), wanted = kWanted / cols;
   if (tiles <= kMergeTiles) p.G = std::max(256, ceil_div(T, 64 * kGradM) * kGradM);

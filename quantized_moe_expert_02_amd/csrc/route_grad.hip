@@ -528,11 +528,12 @@ int check_shape(int32_t T, int32_t k, int32_t E, int32_t H, int32_t rows) {
 
 constexpr int kWideSlice = 512;    // experts up to which a slice has 64 columns
 // Tokens up to which rows of Wr are gathered, in two launches instead of five.
-// Gathered and by slices, top-8 of 256, even router: 100 tokens, 6144 wide 18.2
-// and 22.9 us; 512 tokens 26.0 and 30.2, 2048 wide 13.5 and 20.5; 800 tokens 37.8
-// and 38.7, 17.1 and 23.1.  A skewed router (zipf 1.1) leaves an expert's rows to
-// one workgroup: 512 tokens 38.5 and 38.2, 21.9 and 24.6; 800 tokens 56.5 and 41.2,
-// 32.6 and 26.9.
+// Calls gathered and by slices, 6144 wide, even router: 512 tokens, 2 of 8 experts
+// 19.5 and 28.3 us, 8 of 64 21.1 and 27.0, 8 of 256 24.9 and 27.4 (800 tokens 37.8 and
+// 38.7); 100 tokens 17 and 27; 2048 wide, 512 tokens 17 and 27 with any.  A skewed
+// router (zipf 1.1) leaves an expert's rows to one workgroup: 300 tokens, 8 of 64
+// experts 26.6 and 28.0, 8 of 256 27.6 and 29.2, 512 tokens 25.5 and 28.4, 35.6 and 30.4,
+// 36.5 and 33.1 (800 tokens 56.5 and 41.2), 2048 wide 17.4, 20.7, 21.4 and 27.5.
 constexpr int kGatherTokens = 512;
 constexpr int kSliceGroups = 512;  // workgroups of the slice kernels
 
