@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import MOE_E_INVAL, MOE_OK, MoeError, lib
+from . import MOE_OK, MoeError, lib
 
 MOE_T_F16, MOE_T_BF16, MOE_T_F32 = 0, 1, 2
 _DTYPES = {torch.float16: MOE_T_F16, torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_F32}
@@ -70,8 +70,8 @@ def _run(fn, dev, stream, made, *args):
 def moe_sort_rows(T: int, k: int, n_experts: int, align: int = 1) -> int:
     """Rows of the expert-sorted buffers."""
     n = int(lib().moe_sort_rows(T, k, n_experts, align))
-    if n < 0:
-        raise MoeError(MOE_E_INVAL, "moe_sort_rows")
+    if n < 0:  # (the size query has no status; the sort checks the shape before anything else)
+        raise MoeError(lib().moe_sort(None, T, k, n_experts, align, None, None, None, None, 0, None), "moe_sort_rows")
     return n
 
 

@@ -1,5 +1,5 @@
-"""Most rows of the expert-sorted buffers that the gradients take: decided on
-the host before any launch (no GPU needed)."""
+"""Most rows of the expert-sorted buffers that the gradients take, and the status of
+shapes that the binding refuses: decided on the host before any launch (no GPU needed)."""
 import os
 
 import pytest
@@ -38,3 +38,11 @@ def test_the_most_is_accepted(L):
         need = L.moe_route_backward_workspace_bytes(T, 2, 8, 64, MOST)
         assert need > 0
         assert L.moe_route_backward(P, 0, T, 64, 8, 2, P, None, P, P, P, P, MOST, None, P, P, P, P, need - 1, None) == WORKSPACE
+
+
+@pytest.mark.parametrize("shape,status", [((1, 1, 2000, 1), UNSUPPORTED), ((1, 33, 64, 1), UNSUPPORTED), ((1 << 21, 1, 8, 1), UNSUPPORTED),
+                                          ((1, 9, 8, 1), -1), ((1, 1, 8, 0), -1), ((-1, 1, 8, 1), -1)])
+def test_binding_gives_the_status_of_a_refused_shape(L, shape, status):
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_sort_rows(*shape)
+    assert e.value.code == status
