@@ -29,7 +29,10 @@ EXPORTS = ("moe_packed_bytes", "moe_workspace_bytes", "moe_workspace_sync_bytes"
            "moe_tier_slot", "moe_tier_stats", "moe_tier_sync",
            "moe_sort_rows", "moe_sort_workspace_bytes", "moe_sort", "moe_dispatch", "moe_dispatch_backward",
            "moe_combine", "moe_combine_backward", "moe_route_backward_workspace_bytes", "moe_route_backward",
-           "moe_adapter_workspace_bytes", "moe_adapter_forward", "moe_adapter_backward")
+           "moe_adapter_workspace_bytes", "moe_adapter_forward", "moe_adapter_backward",
+           "moe_w4_packed_bytes", "moe_w4_pack", "moe_w4_unpack", "moe_w4_few_rows", "moe_w4_workspace_bytes",
+           "moe_w4_forward", "moe_w4_backward", "moe_distill_workspace_bytes", "moe_distill_forward",
+           "moe_distill_backward")
 MOE_TIER_LRU, MOE_TIER_HOT = 0, 1
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20  # include/moe_w4a16.h
 MOE_STEP_GRAPH_MAX_LAYERS = 4096  # include/moe_w4a16.h
@@ -137,7 +140,23 @@ def lib():
         L.moe_adapter_workspace_bytes.restype = sz
         L.moe_adapter_forward.argtypes = [A, P, i64, i32, P, P, P, P, i64, P, i64, P, P, sz, P]
         L.moe_adapter_backward.argtypes = [A, P, i64, P, i64, P, i32, P, P, P, P, i64, P, i64, P, P, P, sz, P]
-        for n in ("moe_sort", "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+        L.moe_w4_packed_bytes.argtypes = [P]  # const moe_w4_dims_t*: its bytes
+        L.moe_w4_packed_bytes.restype = sz
+        L.moe_w4_pack.argtypes = [P, P, P, P, P, P]
+        L.moe_w4_unpack.argtypes = [P, P, P, P, P, P]
+        L.moe_w4_few_rows.argtypes = [P, i32]
+        L.moe_w4_few_rows.restype = i32
+        L.moe_w4_workspace_bytes.argtypes = [P, i32]
+        L.moe_w4_workspace_bytes.restype = sz
+        L.moe_w4_forward.argtypes = [P, P, P, i64, i32, P, P, i64, P, i64, P, sz, P]
+        L.moe_w4_backward.argtypes = [P, P, P, i64, i32, P, P, i64, P, i64, P, sz, P]
+        f32 = ctypes.c_float
+        L.moe_distill_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_distill_workspace_bytes.restype = sz
+        L.moe_distill_forward.argtypes = [P, i32, i64, i32, i32, P, P, i32, f32, P, P, P, sz, P]
+        L.moe_distill_backward.argtypes = [P, i32, i64, i32, i32, P, P, i32, f32, P, P, P, i64, P]
+        for n in ("moe_w4_pack", "moe_w4_unpack", "moe_w4_forward", "moe_w4_backward", "moe_distill_forward",
+                  "moe_distill_backward", "moe_sort", "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
                   "moe_route_backward", "moe_adapter_forward", "moe_adapter_backward"):
             getattr(L, n).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -472,3 +491,5 @@ class Tier:
 from .dispatch import (MOE_T_BF16, MOE_T_F16, MOE_T_F32, moe_combine, moe_combine_backward, moe_dispatch,  # noqa: E402
                        moe_dispatch_backward, moe_route_backward, moe_sort, moe_sort_rows)
 from .adapter import moe_adapter_backward, moe_adapter_forward  # noqa: E402
+from .w4 import W4Weights, moe_w4_backward, moe_w4_few_rows, moe_w4_forward, moe_w4_pack, moe_w4_unpack  # noqa: E402
+from .distill import moe_distill_backward, moe_distill_forward  # noqa: E402

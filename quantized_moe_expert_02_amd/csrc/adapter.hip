@@ -12,39 +12,11 @@
 // back transposed (ds_read_b64_tr_b16).
 #include <algorithm>
 
-#include "rows.h"
+#include "mat.h"
 
 namespace moe {
 
 namespace {
-
-template <int V>
-struct Const {
-  static constexpr int value = V;
-};
-
-// Matrix instructions of the two row types.
-template <int DT>
-struct Mat;
-template <>
-struct Mat<MOE_T_F16> {
-  typedef _Float16 elem;
-  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-  }
-};
-template <>
-struct Mat<MOE_T_BF16> {
-  typedef __bf16 elem;
-  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-};
-
-template <int DT>
-using v8_t = typename Mat<DT>::v8;
 
 // ---------------------------------------------------------------------------
 // fp32 factors on 16-bit matrix instructions.  u and v are sums and are not
@@ -1448,11 +1420,6 @@ __global__ __launch_bounds__(256) void k_grad_sum(AdapterArgs d, RowSet rs, cons
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-inline bool bad_ld(int64_t ld, int width) { return ld < width || ld % 8; }
-inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-constexpr int64_t kMaxElems = (int64_t)1 << 35;  // of x or dy
-
 int check_adapters(const moe_adapters_t* d, int32_t T) {
   if (!d || T < 0 || d->n < 1 || d->K <= 0 || d->N <= 0 || d->R <= 0) return MOE_E_INVAL;
   if (d->dtype != MOE_T_F16 && d->dtype != MOE_T_BF16) return MOE_E_INVAL;

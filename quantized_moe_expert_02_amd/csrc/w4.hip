@@ -1,0 +1,919 @@
+// Products of rows with frozen 4-bit weights that have group scales
+// (include/moe_w4.h): forward for few and for many rows, and the gradient of the
+// rows.
+//
+// Packed matrix: blocks of 16 rows x 128 columns, 1 KiB each, [row block][column
+// block].  Lane l = 16 g + r of a wavefront owns 16 bytes: dword j holds row r,
+// columns 32 j + 8 g .. + 7, one nibble each (column p in nibble p), offset
+// binary (u = q + 8).  So one 128-bit load per lane reads a whole block, and dword j
+// of all lanes is one operand of a 16x16x32 matrix instruction whose contraction
+// runs along the columns.  Rows and columns past the matrix hold q = 0 with scale 0.
+// Scales (and zero points) follow, [row block][column block][16 rows][SG], with SG =
+// 4, 2 or 1 groups per 128 columns (wider groups are repeated in every block).
+//
+// Masking a dword with 0x000F000F leaves the codes of columns p and p + 4 in the
+// two halves: operands hold eight columns in the order 0 4 1 5 2 6 3 7, and the
+// rows' operands are put in that order too.
+#include <algorithm>
+
+#include "mat.h"
+#include "moe_w4.h"
+
+namespace moe {
+
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kBlockRows = 16, kBlockCols = 128, kBlockBytes = 1024;
+
+struct W4Args {
+  const uint8_t* w;   // packed matrices
+  size_t stride;      // bytes from matrix to matrix
+  size_t soff, zoff;  // scales, zero points
+  int n, N, K, NB, KB;  // NB x KB blocks
+  const void* x;      // rows of the product (x, or dy in the gradient)
+  int64_t ldx;
+  int T;
+  const int32_t* offsets;
+  const void* add;
+  int64_t ldadd;
+  void* y;
+  int64_t ldy;
+  float* part;  // [split][T][width], or NULL
+  int split;
+};
+
+// A tile of up to BM rows of one matrix; e < 0: rows outside the groups; rows == 0: none.
+struct RowTile {
+  int e, r0, rows;
+};
+
+// Tiles are counted group by group, then come those of the rows outside.  Called by
+// whole wavefronts; every lane gets the same tile.
+template <int BM>
+__device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int n, int T, int tile) {
+  if (!offsets) return RowTile{0, tile * BM, min(BM, T - tile * BM)};
+  const int lane = threadIdx.x & 63;
+  const int per = (n + 63) / 64, e0 = min(lane * per, n), e1 = min(e0 + per, n);
+  const auto at = [&](int i) { return min(max(offsets[i], 0), T); };
+  int count = 0, lo = at(e0);
+  const int first = lo;
+  for (int e = e0; e < e1; ++e) {
+    const int hi = max(lo, at(e + 1));
+    count += (hi - lo + BM - 1) / BM;
+    lo = hi;
+  }
+  const int incl = wave_inclusive_scan(count);
+  const uint64_t owner = __ballot(incl - count <= tile && tile < incl);
+  RowTile r{-1, 0, 0};
+  if (owner) {
+    int left = tile - (incl - count);
+    lo = first;
+    for (int e = e0; e < e1; ++e) {
+      const int hi = max(lo, at(e + 1)), c = (hi - lo + BM - 1) / BM;
+      if (left >= 0 && left < c) r = RowTile{e, lo + left * BM, min(BM, hi - lo - left * BM)};
+      left -= c;
+      lo = hi;
+    }
+    const int l = __ffsll((unsigned long long)owner) - 1;
+    r.e = __builtin_amdgcn_readlane(r.e, l);
+    r.r0 = __builtin_amdgcn_readlane(r.r0, l);
+    r.rows = __builtin_amdgcn_readlane(r.rows, l);
+    return r;
+  }
+  const int head = at(0), end = max(head, at(n));
+  int t = tile - __builtin_amdgcn_readlane(incl, 63);
+  const int heads = (head + BM - 1) / BM;
+  if (t < heads) return RowTile{-1, t * BM, min(BM, head - t * BM)};
+  t -= heads;
+  if ((int64_t)end + (int64_t)t * BM >= T) return r;
+  return RowTile{-1, end + t * BM, min(BM, T - end - t * BM)};
+}
+
+// Upper bound on the tiles above.
+inline int64_t max_tiles(int n, int T, int BM, bool grouped) {
+  return grouped ? (int64_t)T / BM + std::min(n, T) + 2 : ceil_div(T, BM);
+}
+
+// ---------------------------------------------------------------------------
+// Codes into operands.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ half2_t as_half2(uint32_t v) { return __builtin_bit_cast(half2_t, v); }
+__device__ __forceinline__ uint32_t bits_of(half2_t v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ half2_t both(_Float16 v) { return half2_t{v, v}; }
+
+// binary16: 0x6400 | u is 1024 + u, and with the field at bit 4, 1024 + 16 u; one
+// packed subtraction or multiply-add leaves q - z exactly.  c = -(1032 + z).
+__device__ __forceinline__ void codes_f16(uint32_t d, half2_t c, half2_t (&v)[4]) {
+  const half2_t c16 = c + both((_Float16)960.0f);  // -(72 + z)
+  const half2_t sixteenth = both((_Float16)0.0625f);
+  const uint32_t e = d >> 8;
+  v[0] = as_half2((d & 0x000F000Fu) | 0x64006400u) + c;
+  v[1] = as_half2((d & 0x00F000F0u) | 0x64006400u) * sixteenth + c16;
+  v[2] = as_half2((e & 0x000F000Fu) | 0x64006400u) + c;
+  v[3] = as_half2((e & 0x00F000F0u) | 0x64006400u) * sixteenth + c16;
+}
+
+// Scales and zero points as the packed matrix holds them, and what the operands
+// need of them.
+template <int DT>
+__device__ __forceinline__ float scale_value(uint16_t s) {
+  if constexpr (DT == MOE_T_F16) return (float)__builtin_bit_cast(_Float16, s);
+  else return __builtin_bit_cast(float, (uint32_t)s << 16);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: one workgroup per R row blocks and 16 rows, its W wavefronts split the
+// columns and add their sums through LDS.  The rows are the first operand (index l
+// % 16: the row; rows past the tile are zeros) and a block the second (index l %
+// 16: its row), so that a lane's four sums belong to one weight row and are
+// multiplied by its scale.  binary16 factors are the codes q - z themselves;
+// bfloat16 holds 128 + u exactly, and (136 + z) times the sum of the rows' elements
+// is taken off each group's sum.
+// ---------------------------------------------------------------------------
+template <int SG>
+struct ScaleVec;
+template <>
+struct ScaleVec<1> {
+  typedef uint16_t s;
+  typedef int8_t z;
+};
+template <>
+struct ScaleVec<2> {
+  typedef uint32_t s;
+  typedef uint16_t z;
+};
+template <>
+struct ScaleVec<4> {
+  typedef uint64_t s;
+  typedef uint32_t z;
+};
+
+// The product of one output element in fp32, term by term as the formula has it.
+template <int DT, int SG, bool ZP>
+__device__ __attribute__((noinline)) float slow_dot(const uint8_t* w, size_t soff, size_t zoff, int K, int KB, int n,
+                                                    const void* xrow) {
+  typedef typename Mat<DT>::elem elem;
+  const elem* x = (const elem*)xrow;
+  const int nb = n / kBlockRows, r = n % kBlockRows;
+  float acc = 0.f;
+  for (int k = 0; k < K; ++k) {
+    const int kb = k / kBlockCols, c = k % kBlockCols;
+    const size_t block = (size_t)nb * KB + kb;
+    const uint8_t byte = w[block * kBlockBytes + ((c / 8 % 4) * 16 + r) * 16 + c / 32 * 4 + c % 8 / 2];
+    const int q = (int)(c & 1 ? byte >> 4 : byte & 15) - 8;
+    const size_t at = (block * 16 + r) * SG + c / (kBlockCols / SG);
+    const int z = ZP ? (int)((const int8_t*)(w + zoff))[at] : 0;
+    acc = fmaf((float)(q - z) * scale_value<DT>(((const uint16_t*)(w + soff))[at]), (float)x[k], acc);
+  }
+  return acc;
+}
+
+// Eight elements of a row in the operands' order.
+__device__ __forceinline__ u32x4 operand_order(u32x4 v) {
+  return u32x4{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+               __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+}
+
+template <int DT, int SG, bool ZP, int R, int W, int D>
+__global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a, int groups) {
+  typedef typename Mat<DT>::elem elem;
+  constexpr int GS = 4 / SG;  // matrix instructions per group
+  typedef typename ScaleVec<SG>::s svec;
+  typedef typename ScaleVec<SG>::z zvec;
+  __shared__ f32x4 red[W][R][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int tile = blockIdx.x / groups, nb0 = blockIdx.x % groups * R;
+  const RowTile t = find_tile<16>(a.offsets, a.n, a.T, tile);
+  if (t.rows <= 0) return;
+  const int li = lane & 15, g = lane >> 4;
+  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
+  const bool live = li < t.rows;
+  const elem* xrow = (const elem*)a.x + (int64_t)(t.r0 + (live ? li : 0)) * a.ldx + 8 * g;
+  u32x4 wv[D][R], xv[D][4];
+  svec sv[D][R];
+  zvec zv[D][R];
+  const auto load = [&](int d, int kb) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
+      wv[d][r] = __builtin_nontemporal_load((const u32x4*)(w + block * kBlockBytes) + lane);
+      sv[d][r] = ((const svec*)(w + a.soff))[block * 16 + li];
+      if (ZP) zv[d][r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = kb * kBlockCols + 32 * j;
+      xv[d][j] = live && k < a.K ? *(const u32x4*)(xrow + k) : u32x4{};
+    }
+  };
+  f32x4 acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = f32x4{};
+  const auto multiply = [&](int d) {
+    v8_t<DT> ones;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ones[i] = (elem)1.0f;
+#pragma unroll
+    for (int s = 0; s < SG; ++s) {
+      f32x4 sum[R], xsum{};
+#pragma unroll
+      for (int r = 0; r < R; ++r) sum[r] = f32x4{};
+#pragma unroll
+      for (int j = s * GS; j < (s + 1) * GS; ++j) {
+        const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, operand_order(xv[d][j]));
+        if (DT == MOE_T_BF16) xsum = Mat<DT>::mma(xf, ones, xsum);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t c = wv[d][r][j];
+          u32x4 b;
+          if constexpr (DT == MOE_T_F16) {
+            const int z = ZP ? (int)(int8_t)((uint32_t)zv[d][r] >> (8 * s)) : 0;
+            half2_t v[4];
+            codes_f16(c, both((_Float16)(float)(-1032 - z)), v);
+            b = u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])};
+          } else {
+            b = u32x4{(c & 0x000F000Fu) | 0x43004300u, (c >> 4 & 0x000F000Fu) | 0x43004300u,
+                      (c >> 8 & 0x000F000Fu) | 0x43004300u, (c >> 12 & 0x000F000Fu) | 0x43004300u};
+          }
+          sum[r] = Mat<DT>::mma(xf, __builtin_bit_cast(v8_t<DT>, b), sum[r]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float f = scale_value<DT>((uint16_t)((uint64_t)sv[d][r] >> (16 * s)));
+        if constexpr (DT == MOE_T_BF16) {
+          const float off = (float)(136 + (ZP ? (int)(int8_t)((uint32_t)zv[d][r] >> (8 * s)) : 0));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[r][i] = fmaf(-off, xsum[i], sum[r][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(f, sum[r][i], acc[r][i]);
+      }
+    }
+  };
+  if (t.e >= 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (wave + d * W < a.KB) load(d, wave + d * W);
+    for (int kb = wave; kb < a.KB; kb += D * W) {
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (kb + d * W < a.KB) {
+          multiply(d);
+          if (kb + (d + D) * W < a.KB) load(d, kb + (d + D) * W);
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) red[wave][r][lane] = acc[r];
+  __syncthreads();
+  for (int i = threadIdx.x; i < R * 64; i += 64 * W) {
+    const int r = i >> 6, n = (nb0 + r) * kBlockRows + (i & 15), m0 = (i >> 4 & 3) * 4;
+    if (n >= a.N || m0 >= t.rows) continue;
+    f32x4 v = red[0][r][i & 63];
+#pragma unroll
+    for (int u = 1; u < W; ++u) v += red[u][r][i & 63];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (m0 + q >= t.rows) break;
+      const int64_t row = t.r0 + m0 + q;
+      float o = v[q];
+      // the terms 128 + u and 136 + z beside an infinity, or past fp32's range, need
+      // not cancel to the formula's value
+      if (DT == MOE_T_BF16 && !(fabsf(o) < INFINITY) && t.e >= 0)
+        o = slow_dot<DT, SG, ZP>(w, a.soff, a.zoff, a.K, a.KB, n, (const elem*)a.x + row * a.ldx);
+      if (a.add) o += (float)((const elem*)a.add)[row * a.ldadd + n];
+      ((elem*)a.y)[row * a.ldy + n] = (elem)o;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: tiles of BM = 16 MT rows.  Rows pass through two LDS buffers of 64
+// columns each (16-byte pieces, swizzled so that an operand's 16 rows cover all
+// banks).
+// ---------------------------------------------------------------------------
+constexpr int kTileThreads = 256;
+constexpr int kStageCols = 64;
+
+// Piece (row, c) of a buffer: 8 pieces of 16 bytes per row; rows 2i and 2i + 1 fill one
+// line of 64 banks.
+__device__ __forceinline__ int piece_at(int row, int c) { return row * 8 + (c ^ (row >> 1 & 7)); }
+
+// A workgroup's rows of one step, from memory to registers to LDS.
+template <int DT, int BM, bool ORDER>
+struct Stage {
+  static constexpr int P = BM * 8 / kTileThreads;  // pieces per thread
+  static_assert(P >= 1, "every thread stages a piece");
+  u32x4 v[P];
+  __device__ __forceinline__ void load(const W4Args& a, const RowTile& t, int c0, int width) {
+    typedef typename Mat<DT>::elem elem;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = threadIdx.x + p * kTileThreads, row = i >> 3, c = c0 + (i & 7) * 8;
+      v[p] = row < t.rows && c < width ? *(const u32x4*)((const elem*)a.x + (int64_t)(t.r0 + row) * a.ldx + c) : u32x4{};
+    }
+  }
+  __device__ __forceinline__ void store(u32x4* lds) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int i = threadIdx.x + p * kTileThreads;
+      lds[piece_at(i >> 3, i & 7)] = ORDER ? operand_order(v[p]) : v[p];
+    }
+  }
+};
+
+// Weights rounded to the rows' type as operands.  binary16: the exact code times the
+// scale, a packed product.  bfloat16: formed in fp32 (exactly: at most 8 + 9 bits) and
+// rounded.  One scale for all eight.
+template <int DT, bool ZP>
+struct GroupScale;
+template <bool ZP>
+struct GroupScale<MOE_T_F16, ZP> {
+  half2_t s, c;
+  __device__ __forceinline__ void set(uint16_t sv, int z) {
+    s = both(__builtin_bit_cast(_Float16, sv));
+    c = both((_Float16)(float)(-1032 - z));
+  }
+  __device__ __forceinline__ v8_t<MOE_T_F16> weights(uint32_t d) const {
+    half2_t v[4];
+    codes_f16(d, ZP ? c : both((_Float16)-1032.0f), v);
+    return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v[0] * s), bits_of(v[1] * s), bits_of(v[2] * s), bits_of(v[3] * s)});
+  }
+};
+__device__ __forceinline__ float byte_of(uint32_t v, int i) { return (float)(v >> (8 * i) & 0xFFu); }
+
+template <bool ZP>
+struct GroupScale<MOE_T_BF16, ZP> {
+  float s, c;
+  __device__ __forceinline__ void set(uint16_t sv, int z) {
+    s = scale_value<MOE_T_BF16>(sv);
+    c = (float)(-8 - z) * s;
+  }
+  __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
+    const uint32_t lo = d & 0x0F0F0F0Fu, hi = d >> 4 & 0x0F0F0F0Fu;
+    v8_t<MOE_T_BF16> v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[4 * i] = (__bf16)fmaf(byte_of(lo, i), s, c);
+      v[4 * i + 1] = (__bf16)fmaf(byte_of(lo, i + 2), s, c);
+      v[4 * i + 2] = (__bf16)fmaf(byte_of(hi, i), s, c);
+      v[4 * i + 3] = (__bf16)fmaf(byte_of(hi, i + 2), s, c);
+    }
+    return v;
+  }
+};
+
+// Four consecutive sums of a row, from column c: to the split's partial sums, or with add, rounded.
+template <int DT>
+__device__ __forceinline__ void put4(const W4Args& a, int width, int split, int64_t row, int c, f32x4 v) {
+  typedef typename Mat<DT>::elem elem;
+  struct alignas(8) E4 {
+    elem e[4];
+  };
+  if (a.part) {
+    *(f32x4*)(a.part + ((int64_t)split * a.T + row) * width + c) = v;
+    return;
+  }
+  if (a.add) {
+    const E4 o = *(const E4*)((const elem*)a.add + row * a.ldadd + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += (float)o.e[i];
+  }
+  E4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.e[i] = (elem)v[i];
+  *(E4*)((elem*)a.y + row * a.ldy + c) = o;
+}
+
+// Forward: each of four wavefronts takes R row blocks of the matrix, straight from
+// memory into operands, and all rows of the tile.
+template <int DT, int SG, bool ZP, int MT, int R>
+__global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int groups) {
+  constexpr int BM = 16 * MT;
+  typedef typename ScaleVec<SG>::s svec;
+  typedef typename ScaleVec<SG>::z zvec;
+  __shared__ u32x4 sx[2][BM * 8];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x % a.split, b = blockIdx.x / a.split;
+  const RowTile t = find_tile<BM>(a.offsets, a.n, a.T, b / groups);
+  if (t.rows <= 0) return;
+  const int nb0 = (b % groups * 4 + wave) * R;
+  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
+  f32x4 acc[MT][R];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[m][r] = f32x4{};
+  const int kb0 = (int)((int64_t)a.KB * split / a.split), kb1 = (int)((int64_t)a.KB * (split + 1) / a.split);
+  if (t.e >= 0 && kb0 < kb1) {
+    u32x4 wv[2][R];
+    svec sv[2][R];
+    zvec zv[2][R];
+    const auto load = [&](int d, int kb) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
+        wv[d][r] = ((const u32x4*)(w + block * kBlockBytes))[lane];
+        sv[d][r] = ((const svec*)(w + a.soff))[block * 16 + li];
+        if (ZP) zv[d][r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
+      }
+    };
+    Stage<DT, BM, true> st;
+    st.load(a, t, kb0 * kBlockCols, a.K);
+    load(0, kb0);
+    st.store(sx[0]);
+    __syncthreads();
+    const auto block = [&](int d, int kb) {
+      const int next = min(kb + 1, kb1 - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        st.load(a, t, h ? next * kBlockCols : kb * kBlockCols + kStageCols, a.K);
+        if (h == 0) load(d ^ 1, next);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int j = 2 * h + q;
+          v8_t<DT> wf[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            constexpr int GS = 4 / SG;
+            GroupScale<DT, ZP> s;
+            s.set((uint16_t)((uint64_t)sv[d][r] >> (16 * (j / GS))), ZP ? (int)(int8_t)((uint32_t)zv[d][r] >> (8 * (j / GS))) : 0);
+            wf[r] = s.weights(wv[d][r][j]);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[h][piece_at(16 * m + li, 4 * q + g)]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[m][r] = Mat<DT>::mma(wf[r], xf, acc[m][r]);
+          }
+        }
+        st.store(sx[h ^ 1]);
+        __syncthreads();
+      }
+    };
+    for (int kb = kb0; kb < kb1; kb += 2) {
+      block(0, kb);
+      if (kb + 1 < kb1) block(1, kb + 1);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = 16 * m + li, n = (nb0 + r) * kBlockRows + 4 * g;
+      if (row < t.rows && n < a.N) put4<DT>(a, a.N, split, t.r0 + row, n, acc[m][r]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the rows: the contraction runs across the matrix' rows.  A step takes
+// 64 of them: the packed blocks pass through LDS as they are, and
+// ds_read_b64_tr_b4 hands lane j of 16 the nibble j of 16 rows' eight bytes, so that
+// a lane holds 16 rows of one column.  The rows' addresses are given in the order
+// that puts neighbouring rows into the operands' halves.  A wavefront takes 64
+// columns (eight bytes of each lane's sixteen) and all rows of the tile.
+// ---------------------------------------------------------------------------
+constexpr int kStepRows = 64;
+constexpr int kGradCols = 256;
+
+// As GroupScale, with a scale for each of the eight.
+template <int DT, bool ZP>
+struct RowScales;
+template <bool ZP>
+struct RowScales<MOE_T_F16, ZP> {
+  half2_t s[4], c[4];
+  // sv: eight scales; cv: eight values -(1032 + z)
+  __device__ __forceinline__ void set(u32x4 sv, u32x4 cv) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] = as_half2(sv[i]);
+      c[i] = ZP ? as_half2(cv[i]) : both((_Float16)-1032.0f);
+    }
+  }
+  __device__ __forceinline__ v8_t<MOE_T_F16> weights(uint32_t d) const {
+    const half2_t k = both((_Float16)960.0f), sixteenth = both((_Float16)0.0625f);
+    const uint32_t e = d >> 8;
+    const half2_t v0 = as_half2((d & 0x000F000Fu) | 0x64006400u) + c[0];
+    const half2_t v1 = as_half2((d & 0x00F000F0u) | 0x64006400u) * sixteenth + (c[1] + k);
+    const half2_t v2 = as_half2((e & 0x000F000Fu) | 0x64006400u) + c[2];
+    const half2_t v3 = as_half2((e & 0x00F000F0u) | 0x64006400u) * sixteenth + (c[3] + k);
+    return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v0 * s[0]), bits_of(v1 * s[1]), bits_of(v2 * s[2]), bits_of(v3 * s[3])});
+  }
+};
+template <bool ZP>
+struct RowScales<MOE_T_BF16, ZP> {
+  float s[8], c[8];
+  // cv: eight values -(8 + z)
+  __device__ __forceinline__ void set(u32x4 sv, u32x4 cv) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i] = scale_value<MOE_T_BF16>((uint16_t)(sv[i / 2] >> (16 * (i & 1))));
+      c[i] = (ZP ? scale_value<MOE_T_BF16>((uint16_t)(cv[i / 2] >> (16 * (i & 1)))) : -8.0f) * s[i];
+    }
+  }
+  __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
+    const uint32_t lo = d & 0x0F0F0F0Fu, hi = d >> 4 & 0x0F0F0F0Fu;
+    v8_t<MOE_T_BF16> v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // halves 4i .. 4i + 3: nibbles 2i, 2i + 4, 2i + 1, 2i + 5
+      v[4 * i] = (__bf16)fmaf(byte_of(lo, i), s[4 * i], c[4 * i]);
+      v[4 * i + 1] = (__bf16)fmaf(byte_of(lo, i + 2), s[4 * i + 1], c[4 * i + 1]);
+      v[4 * i + 2] = (__bf16)fmaf(byte_of(hi, i), s[4 * i + 2], c[4 * i + 2]);
+      v[4 * i + 3] = (__bf16)fmaf(byte_of(hi, i + 2), s[4 * i + 3], c[4 * i + 3]);
+    }
+    return v;
+  }
+};
+
+template <int DT, int SG, bool ZP, int MT>
+__global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int groups) {
+  constexpr int BM = 16 * MT;
+  constexpr int CB = kGradCols / kBlockCols, SB = kStepRows / kBlockRows;  // blocks of a step: SB x CB
+  constexpr int NS = SB * CB * 16 * SG, SP = (NS + kTileThreads - 1) / kTileThreads;
+  typedef int v2i __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) v2i lds_v2i;
+  __shared__ u32x4 sx[2][BM * 8];
+  __shared__ u32x4 sw[2][SB * CB * 64];
+  __shared__ __attribute__((aligned(16))) uint16_t ss[2][CB * SG][kStepRows], sz[ZP ? 2 : 1][CB * SG][kStepRows];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x % a.split, b = blockIdx.x / a.split;
+  const RowTile t = find_tile<BM>(a.offsets, a.n, a.T, b / groups);
+  if (t.rows <= 0) return;
+  const int kb0 = b % groups * CB;
+  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
+  f32x4 acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{};
+  const int steps = (a.NB + SB - 1) / SB;
+  const int s0 = (int)((int64_t)steps * split / a.split), s1 = (int)((int64_t)steps * (split + 1) / a.split);
+  const int kbi = wave >> 1, jj = wave & 1;
+  // group of this lane's columns among the step's
+  const int cg = kbi * SG + (SG == 4 ? 2 * jj + (li >> 3) : SG == 2 ? jj : 0);
+  const int rho = (li & 8) + ((li & 7) < 4 ? 2 * (li & 7) : 2 * (li & 7) - 7);  // the row whose eight bytes this lane points at
+  if (t.e >= 0 && s0 < s1) {
+    Stage<DT, BM, false> st;
+    u32x4 wv[2];
+    uint16_t sv[SP], zv[SP];
+    const auto load = [&](int s) {
+      st.load(a, t, s * kStepRows, a.N);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int i = threadIdx.x + p * kTileThreads, rb = s * SB + (i >> 7), kb = kb0 + (i >> 6 & 1);
+        wv[p] = rb < a.NB && kb < a.KB ? ((const u32x4*)(w + ((size_t)rb * a.KB + kb) * kBlockBytes))[i & 63] : u32x4{};
+      }
+#pragma unroll
+      for (int p = 0; p < SP; ++p) {
+        const int i = threadIdx.x + p * kTileThreads;
+        const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
+        sv[p] = zv[p] = 0;
+        if (i < NS && rb < a.NB && kb < a.KB) {
+          const size_t at = ((size_t)rb * a.KB + kb) * 16 * SG + i % (16 * SG);
+          sv[p] = ((const uint16_t*)(w + a.soff))[at];
+          if (ZP) {
+            const int z = ((const int8_t*)(w + a.zoff))[at];
+            zv[p] = DT == MOE_T_F16 ? __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - z))
+                                    : __builtin_bit_cast(uint16_t, (__bf16)(float)(-8 - z));
+          }
+        }
+      }
+    };
+    const auto store = [&](int u) {
+      st.store(sx[u]);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) sw[u][threadIdx.x + p * kTileThreads] = wv[p];
+#pragma unroll
+      for (int p = 0; p < SP; ++p) {
+        const int i = threadIdx.x + p * kTileThreads;
+        if (i < NS) {
+          const int row = i / (CB * 16 * SG) * 16 + i / SG % 16, col = i / (16 * SG) % CB * SG + i % SG;
+          ss[u][col][row] = sv[p];
+          if (ZP) sz[u][col][row] = zv[p];
+        }
+      }
+    };
+    load(s0);
+    store(0);
+    __syncthreads();
+    for (int s = s0; s < s1; ++s) {
+      const int u = (s - s0) & 1;
+      if (s + 1 < s1) load(s + 1);
+      v2i code[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        code[f] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+            (lds_v2i*)((char*)&sw[u][(g * CB + kbi) * 64 + f * 16 + rho] + 8 * jj));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {  // rows 16 g + 8 q .. + 7 of the step
+        RowScales<DT, ZP> rs;
+        rs.set(*(const u32x4*)&ss[u][cg][16 * g + 8 * q], *(const u32x4*)&sz[ZP ? u : 0][cg][16 * g + 8 * q]);
+        v8_t<DT> wf[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) wf[f] = rs.weights((uint32_t)code[f][q]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[u][piece_at(16 * m + li, 2 * g + q)]);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) acc[m][f] = Mat<DT>::mma(wf[f], xf, acc[m][f]);
+        }
+      }
+      if (s + 1 < s1) store(u ^ 1);
+      __syncthreads();
+    }
+  }
+  // lane's sums 4 g .. + 3 of fragment f: nibbles 4 g .. + 3 of the eight bytes
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int row = 16 * m + li;
+      const int c = (kb0 + kbi) * kBlockCols + 32 * (2 * jj + (g >> 1)) + 8 * f + 4 * (g & 1);
+      if (row < t.rows && c < a.K) put4<DT>(a, a.K, split, t.r0 + row, c, acc[m][f]);
+    }
+}
+
+// The splits' partial sums added in their order.
+template <int DT>
+__global__ __launch_bounds__(256) void k_w4_sum(W4Args a, int width) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = width / 4, row = i / per;
+  if (row >= a.T) return;
+  const int c = (int)(i % per) * 4;
+  f32x4 v{};
+  for (int s = 0; s < a.split; ++s) v += *(const f32x4*)(a.part + ((int64_t)s * a.T + row) * width + c);
+  W4Args o = a;
+  o.part = nullptr;
+  put4<DT>(o, width, 0, row, c, v);
+}
+
+// ---------------------------------------------------------------------------
+// Packing.
+// ---------------------------------------------------------------------------
+struct PackArgs {
+  uint8_t* packed;
+  size_t stride, soff, zoff;
+  int N, K, NB, KB, group, SG, dtype;
+  uint8_t* q;
+  uint16_t* scales;
+  int8_t* zeros;
+};
+
+// One workgroup per block and matrix.
+template <bool PACK>
+__global__ __launch_bounds__(64) void k_w4_pack(PackArgs a) {
+  const int lane = threadIdx.x, li = lane & 15, g = lane >> 4;
+  const size_t block = blockIdx.x;
+  const int nb = (int)(block / a.KB), kb = (int)(block % a.KB), e = blockIdx.y, row = nb * kBlockRows + li;
+  uint8_t* w = a.packed + (size_t)e * a.stride;
+  const bool in = row < a.N;
+  const size_t r = (size_t)e * a.N + row;
+  u32x4* mine = (u32x4*)(w + block * kBlockBytes) + lane;
+  u32x4 d{0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
+  if (!PACK) d = *mine;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = kb * kBlockCols + 32 * j + 8 * g;
+    if (!in || c >= a.K) continue;
+    // (K is a multiple of 32: a dword of canonical codes is aligned)
+    uint32_t* at = (uint32_t*)(a.q + (r * a.K + c) / 2);
+    if (PACK) d[j] = *at ^ 0x88888888u;
+    else *at = d[j] ^ 0x88888888u;
+  }
+  if (PACK) *mine = d;
+  const int width = kBlockCols / a.SG, groups = a.K / a.group;
+  for (int i = lane; i < 16 * a.SG; i += 64) {
+    const int rr = nb * kBlockRows + i / a.SG, c = kb * kBlockCols + i % a.SG * width;
+    const bool have = rr < a.N && c < a.K;
+    uint16_t* s = (uint16_t*)(w + a.soff) + block * 16 * a.SG + i;
+    int8_t* z = (int8_t*)(w + a.zoff) + block * 16 * a.SG + i;
+    const size_t from = ((size_t)e * a.N + rr) * groups + c / a.group;
+    if (PACK) {
+      *s = have ? a.scales[from] : 0;
+      if (a.zeros) *z = have ? a.zeros[from] : 0;
+    } else if (have && c % a.group == 0) {
+      a.scales[from] = *s;
+      if (a.zeros) a.zeros[from] = *z;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxLd = 1 << 22;
+constexpr int kFewRows = 16;
+
+struct W4Layout {
+  int NB, KB, SG;
+  size_t soff, zoff, stride;
+};
+
+W4Layout w4_layout(const moe_w4_dims_t& d) {
+  W4Layout l;
+  l.NB = ceil_div(d.N, kBlockRows);
+  l.KB = ceil_div(d.K, kBlockCols);
+  l.SG = d.group == 32 ? 4 : d.group == 64 ? 2 : 1;
+  const size_t blocks = (size_t)l.NB * l.KB;
+  l.soff = blocks * kBlockBytes;
+  l.zoff = l.soff + round256(blocks * 16 * l.SG * 2);
+  l.stride = l.zoff + (d.zeros ? round256(blocks * 16 * l.SG) : 0);
+  return l;
+}
+
+int check_w4(const moe_w4_dims_t* d) {
+  if (!d || d->n < 1 || d->N <= 0 || d->K <= 0 || d->group <= 0 || (d->zeros != 0 && d->zeros != 1)) return MOE_E_INVAL;
+  if (d->dtype != MOE_T_F16 && d->dtype != MOE_T_BF16) return MOE_E_INVAL;
+  if (d->K % d->group) return MOE_E_INVAL;
+  if (d->K % 32 || d->K > kMaxWidth || d->N % 8 || d->N > (1 << 20) || d->n > kMaxExperts ||
+      (int64_t)d->n * d->N > (1 << 24))
+    return MOE_E_UNSUPPORTED;
+  if (d->group != 32 && d->group != 64 && d->group % 128 && d->group != d->K) return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_w4_rows(const moe_w4_dims_t* d, int32_t T) {
+  const int st = check_w4(d);
+  if (st != MOE_OK) return st;
+  if (T < 0) return MOE_E_INVAL;
+  return T > kMaxRows || (int64_t)T * std::max(d->N, d->K) > kMaxElems ? MOE_E_UNSUPPORTED : MOE_OK;
+}
+
+bool few_rows(const moe_w4_dims_t& d, int T) { return T <= (int64_t)kFewRows * d.n; }
+
+// Tile height and splits of a call with many rows.
+struct TilePlan {
+  int MT, R, groups, split;
+};
+
+constexpr int kTargetGroups = 512;
+
+TilePlan plan_tiles(const moe_w4_dims_t& d, int T, bool grad) {
+  TilePlan p;
+  const int avg = ceil_div(T, d.n);
+  p.MT = avg <= 32 ? 2 : avg <= 64 ? 4 : 8;
+  p.R = 4;
+  p.groups = grad ? ceil_div(d.K, kGradCols) : ceil_div(d.N, 64 * p.R);
+  const int64_t blocks = (int64_t)ceil_div(T, 16 * p.MT) * p.groups;
+  const int steps = grad ? ceil_div(d.N, kStepRows) : ceil_div(d.K, kBlockCols);
+  p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kTargetGroups / blocks, steps / 4));
+  return p;
+}
+
+size_t part_bytes(const moe_w4_dims_t& d, int T, const TilePlan& p, bool grad) {
+  return p.split > 1 ? (size_t)p.split * T * (grad ? d.K : d.N) * 4 : 0;
+}
+
+template <typename F>
+void by_format(const moe_w4_dims_t& d, int SG, F f) {
+  const auto zeros = [&](auto dt, auto sg) {
+    if (d.zeros) f(dt, sg, Const<1>{});
+    else f(dt, sg, Const<0>{});
+  };
+  const auto groups = [&](auto dt) {
+    if (SG == 4) zeros(dt, Const<4>{});
+    else if (SG == 2) zeros(dt, Const<2>{});
+    else zeros(dt, Const<1>{});
+  };
+  if (d.dtype == MOE_T_F16) groups(Const<MOE_T_F16>{});
+  else groups(Const<MOE_T_BF16>{});
+}
+
+int check_call(const moe_w4_dims_t* d, const void* packed, const void* x, int64_t ldx, int into, int32_t T,
+               const int32_t* offsets, const void* add, int64_t ldadd, const void* y, int64_t ldy, int out) {
+  if (bad(packed, 256)) return MOE_E_INVAL;
+  if (offsets ? !aligned_to(offsets, 4) : d->n != 1) return MOE_E_INVAL;
+  if (T == 0) return MOE_OK;
+  if (bad(x, 16) || bad_ld(ldx, into) || bad(y, 16) || bad_ld(ldy, out)) return MOE_E_INVAL;
+  if (add && (!aligned_to(add, 16) || bad_ld(ldadd, out))) return MOE_E_INVAL;
+  return ldx > kMaxLd || ldy > kMaxLd || (add && ldadd > kMaxLd) ? MOE_E_UNSUPPORTED : MOE_OK;
+}
+
+template <int DT>
+void launch_sum(const W4Args& a, int width, hipStream_t s) {
+  k_w4_sum<DT><<<ceil_div((int64_t)a.T * (width / 4), 256), 256, 0, s>>>(a, width);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_w4_packed_bytes(const moe_w4_dims_t* d) {
+  return check_w4(d) == MOE_OK ? (size_t)d->n * w4_layout(*d).stride : 0;
+}
+
+static int pack_call(const moe_w4_dims_t* d, const void* q, const void* scales, const void* zeros, const void* packed,
+                     bool pack, void* stream) {
+  const int st = check_w4(d);
+  if (st != MOE_OK) return st;
+  if (bad(q, 16) || bad(scales, 2) || bad(packed, 256) || (d->zeros != 0) != (zeros != nullptr)) return MOE_E_INVAL;
+  const W4Layout l = w4_layout(*d);
+  const PackArgs a{(uint8_t*)packed, l.stride, l.soff, l.zoff, d->N, d->K, l.NB, l.KB, d->group, l.SG, d->dtype,
+                   (uint8_t*)q, (uint16_t*)scales, (int8_t*)zeros};
+  const dim3 grid((unsigned)(l.NB * l.KB), (unsigned)d->n);
+  if (pack) k_w4_pack<true><<<grid, 64, 0, (hipStream_t)stream>>>(a);
+  else k_w4_pack<false><<<grid, 64, 0, (hipStream_t)stream>>>(a);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+}
+
+int moe_w4_pack(const moe_w4_dims_t* d, const void* q, const void* scales, const void* zeros, void* packed,
+                void* stream) {
+  return pack_call(d, q, scales, zeros, packed, true, stream);
+}
+
+int moe_w4_unpack(const moe_w4_dims_t* d, const void* packed, void* q, void* scales, void* zeros, void* stream) {
+  return pack_call(d, q, scales, zeros, packed, false, stream);
+}
+
+int32_t moe_w4_few_rows(const moe_w4_dims_t* d, int32_t T) {
+  return check_w4_rows(d, T) == MOE_OK && few_rows(*d, T) ? 1 : 0;
+}
+
+size_t moe_w4_workspace_bytes(const moe_w4_dims_t* d, int32_t T) {
+  if (check_w4_rows(d, T) != MOE_OK || T == 0) return 0;
+  const size_t f = few_rows(*d, T) ? 0 : part_bytes(*d, T, plan_tiles(*d, T, false), false);
+  return std::max(f, part_bytes(*d, T, plan_tiles(*d, T, true), true));
+}
+
+int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, int64_t ldx, int32_t T,
+                   const int32_t* offsets, const void* add, int64_t ldadd, void* y, int64_t ldy, void* ws,
+                   size_t ws_bytes, void* stream) {
+  int st = check_w4_rows(d, T);
+  if (st == MOE_OK) st = check_call(d, packed, x, ldx, d->K, T, offsets, add, ldadd, y, ldy, d->N);
+  if (st != MOE_OK || T == 0) return st;
+  const W4Layout l = w4_layout(*d);
+  const hipStream_t s = (hipStream_t)stream;
+  W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, x, ldx, T, offsets, add,
+           ldadd, y, ldy, nullptr, 1};
+  if (few_rows(*d, T)) {
+    by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
+      constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
+      constexpr bool ZP = decltype(zp)::value;
+      const int64_t tiles = max_tiles(d->n, T, 16, offsets != nullptr);
+      const auto launch = [&](auto kernel, int R, int W) {
+        const int groups = ceil_div(l.NB, R);
+        kernel<<<(unsigned)(tiles * groups), 64 * W, 0, s>>>(a, groups);
+      };
+      if (l.NB <= 1024) launch(k_w4_few<DT, SG, ZP, 1, 8, 3>, 1, 8);
+      else launch(k_w4_few<DT, SG, ZP, 4, 4, 2>, 4, 4);
+    });
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+  }
+  const TilePlan p = plan_tiles(*d, T, false);
+  const size_t need = part_bytes(*d, T, p, false);
+  if (need) {
+    if (bad(ws, 16)) return MOE_E_INVAL;
+    if (ws_bytes < need) return MOE_E_WORKSPACE;
+    a.part = (float*)ws;
+    a.split = p.split;
+  }
+  by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
+    constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
+    constexpr bool ZP = decltype(zp)::value;
+    const unsigned blocks = (unsigned)(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr) * p.groups * p.split);
+    if (p.MT == 2) k_w4_rows<DT, SG, ZP, 2, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    else if (p.MT == 4) k_w4_rows<DT, SG, ZP, 4, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    else k_w4_rows<DT, SG, ZP, 8, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    if (need) launch_sum<DT>(a, d->N, s);
+  });
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+}
+
+int moe_w4_backward(const moe_w4_dims_t* d, const void* packed, const void* dy, int64_t lddy, int32_t T,
+                    const int32_t* offsets, const void* add, int64_t ldadd, void* dx, int64_t lddx, void* ws,
+                    size_t ws_bytes, void* stream) {
+  int st = check_w4_rows(d, T);
+  if (st == MOE_OK) st = check_call(d, packed, dy, lddy, d->N, T, offsets, add, ldadd, dx, lddx, d->K);
+  if (st != MOE_OK || T == 0) return st;
+  const W4Layout l = w4_layout(*d);
+  const hipStream_t s = (hipStream_t)stream;
+  const TilePlan p = plan_tiles(*d, T, true);
+  const size_t need = part_bytes(*d, T, p, true);
+  if (need && bad(ws, 16)) return MOE_E_INVAL;
+  if (ws_bytes < need) return MOE_E_WORKSPACE;
+  const W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, dy, lddy, T, offsets,
+                 add, ldadd, dx, lddx, need ? (float*)ws : nullptr, p.split};
+  by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
+    constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
+    constexpr bool ZP = decltype(zp)::value;
+    const unsigned blocks = (unsigned)(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr) * p.groups * p.split);
+    if (p.MT == 2) k_w4_grad<DT, SG, ZP, 2><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    else if (p.MT == 4) k_w4_grad<DT, SG, ZP, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    else k_w4_grad<DT, SG, ZP, 8><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    if (need) launch_sum<DT>(a, d->K, s);
+  });
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+}
+
+}  // extern "C"
