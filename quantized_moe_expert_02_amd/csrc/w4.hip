@@ -106,16 +106,32 @@ __device__ __forceinline__ half2_t as_half2(uint32_t v) { return __builtin_bit_c
 __device__ __forceinline__ uint32_t bits_of(half2_t v) { return __builtin_bit_cast(uint32_t, v); }
 __device__ __forceinline__ half2_t both(_Float16 v) { return half2_t{v, v}; }
 
-// binary16: 0x6400 | u is 1024 + u, and with the field at bit 4, 1024 + 16 u; one
-// packed subtraction or multiply-add leaves q - z exactly.  c = -(1032 + z).
+// The codes of a dword as four pairs of binary16 numbers: 1024 + u, or, where the
+// field sits at bit 4, 1024 + 16 u.
+__device__ __forceinline__ void code_pairs(uint32_t d, half2_t (&v)[4]) {
+  const uint32_t e = d >> 8;
+  // (a & b) | c
+  v[0] = as_half2(__builtin_amdgcn_bitop3_b32(d, 0x000F000Fu, 0x64006400u, 0xEA));
+  v[1] = as_half2(__builtin_amdgcn_bitop3_b32(d, 0x00F000F0u, 0x64006400u, 0xEA));
+  v[2] = as_half2(__builtin_amdgcn_bitop3_b32(e, 0x000F000Fu, 0x64006400u, 0xEA));
+  v[3] = as_half2(__builtin_amdgcn_bitop3_b32(e, 0x00F000F0u, 0x64006400u, 0xEA));
+}
+
+// binary16: one packed subtraction or multiply-add leaves q - z exactly.  c = -(1032 + z).
 __device__ __forceinline__ void codes_f16(uint32_t d, half2_t c, half2_t (&v)[4]) {
   const half2_t c16 = c + both((_Float16)960.0f);  // -(72 + z)
   const half2_t sixteenth = both((_Float16)0.0625f);
-  const uint32_t e = d >> 8;
-  v[0] = as_half2((d & 0x000F000Fu) | 0x64006400u) + c;
-  v[1] = as_half2((d & 0x00F000F0u) | 0x64006400u) * sixteenth + c16;
-  v[2] = as_half2((e & 0x000F000Fu) | 0x64006400u) + c;
-  v[3] = as_half2((e & 0x00F000F0u) | 0x64006400u) * sixteenth + c16;
+  code_pairs(d, v);
+  v[0] += c;
+  v[1] = v[1] * sixteenth + c16;
+  v[2] += c;
+  v[3] = v[3] * sixteenth + c16;
+}
+
+// Two values rounded to bfloat16, in one instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf2_t));
 }
 
 // Scales and zero points as the packed matrix holds them, and what the operands
@@ -305,32 +321,47 @@ constexpr int kStageCols = 64;
 // line of 64 banks.
 __device__ __forceinline__ int piece_at(int row, int c) { return row * 8 + (c ^ (row >> 1 & 7)); }
 
-// A workgroup's rows of one step, from memory to registers to LDS.
-template <int DT, int BM, bool ORDER>
+// A workgroup's rows of one step of 64 columns, from memory to registers to LDS, 32
+// rows to a piece per thread.  Rows past the tile repeat its last (their sums are not
+// stored); of the last step's columns those past the width are zeros.
+template <int DT, int MT, bool ORDER>
 struct Stage {
-  static constexpr int P = BM * 8 / kTileThreads;  // pieces per thread
-  static_assert(P >= 1, "every thread stages a piece");
+  static constexpr int P = (MT + 1) / 2;
+  const char* base;
+  uint32_t at[P];
+  int width;
   u32x4 v[P];
-  __device__ __forceinline__ void load(const W4Args& a, const RowTile& t, int c0, int width) {
-    typedef typename Mat<DT>::elem elem;
+  __device__ __forceinline__ void init(const W4Args& a, const RowTile& t, int w) {
+    base = (const char*)a.x + (int64_t)t.r0 * a.ldx * 2;
+    width = w;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int i = threadIdx.x + p * kTileThreads, row = i >> 3, c = c0 + (i & 7) * 8;
-      v[p] = row < t.rows && c < width ? *(const u32x4*)((const elem*)a.x + (int64_t)(t.r0 + row) * a.ldx + c) : u32x4{};
+      const int row = min((int)(threadIdx.x >> 3) + 32 * p, t.rows - 1);
+      at[p] = (uint32_t)row * (uint32_t)(a.ldx * 2) + (threadIdx.x & 7) * 16;
     }
   }
-  __device__ __forceinline__ void store(u32x4* lds) const {
+  __device__ __forceinline__ bool tail(int c0) const { return c0 + kStageCols > width; }
+  __device__ __forceinline__ void load(int c0) {
+    const char* b = base + (size_t)c0 * 2;
+    const int left = width - c0;  // at least 8
+    const uint32_t back = tail(c0) ? max(0, (int)(threadIdx.x & 7) * 16 - (left / 8 * 16 - 16)) : 0;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int i = threadIdx.x + p * kTileThreads;
-      lds[piece_at(i >> 3, i & 7)] = ORDER ? operand_order(v[p]) : v[p];
+    for (int p = 0; p < P; ++p) v[p] = *(const u32x4*)(b + (at[p] - back));
+  }
+  __device__ __forceinline__ void store(u32x4* lds, int c0) {
+    if (tail(c0) && c0 + (int)(threadIdx.x & 7) * 8 >= width) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) v[p] = u32x4{};
     }
+#pragma unroll
+    for (int p = 0; p < P; ++p) lds[piece_at((threadIdx.x >> 3) + 32 * p, threadIdx.x & 7)] = ORDER ? operand_order(v[p]) : v[p];
   }
 };
 
 // Weights rounded to the rows' type as operands.  binary16: the exact code times the
-// scale, a packed product.  bfloat16: formed in fp32 (exactly: at most 8 + 9 bits) and
-// rounded.  One scale for all eight.
+// scale, a packed product.  bfloat16: (1024 + u) s - (1032 + z) s in one fp32
+// multiply-add, whose result is exact (at most 8 + 9 bits), then rounded.  One scale
+// for all eight.
 template <int DT, bool ZP>
 struct GroupScale;
 template <bool ZP>
@@ -346,28 +377,34 @@ struct GroupScale<MOE_T_F16, ZP> {
     return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v[0] * s), bits_of(v[1] * s), bits_of(v[2] * s), bits_of(v[3] * s)});
   }
 };
-__device__ __forceinline__ float byte_of(uint32_t v, int i) { return (float)(v >> (8 * i) & 0xFFu); }
-
 template <bool ZP>
 struct GroupScale<MOE_T_BF16, ZP> {
-  float s, c;
+  float s, s16, c, c16;
   __device__ __forceinline__ void set(uint16_t sv, int z) {
     s = scale_value<MOE_T_BF16>(sv);
-    c = (float)(-8 - z) * s;
+    s16 = s * 0.0625f;
+    c = (float)(-1032 - z) * s;
+    c16 = (float)(-72 - z) * s;
   }
   __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
-    const uint32_t lo = d & 0x0F0F0F0Fu, hi = d >> 4 & 0x0F0F0F0Fu;
-    v8_t<MOE_T_BF16> v;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      v[4 * i] = (__bf16)fmaf(byte_of(lo, i), s, c);
-      v[4 * i + 1] = (__bf16)fmaf(byte_of(lo, i + 2), s, c);
-      v[4 * i + 2] = (__bf16)fmaf(byte_of(hi, i), s, c);
-      v[4 * i + 3] = (__bf16)fmaf(byte_of(hi, i + 2), s, c);
-    }
-    return v;
+    half2_t v[4];
+    code_pairs(d, v);
+    return __builtin_bit_cast(v8_t<MOE_T_BF16>, u32x4{pack_bf16(fmaf((float)v[0][0], s, c), fmaf((float)v[0][1], s, c)),
+                                                      pack_bf16(fmaf((float)v[1][0], s16, c16), fmaf((float)v[1][1], s16, c16)),
+                                                      pack_bf16(fmaf((float)v[2][0], s, c), fmaf((float)v[2][1], s, c)),
+                                                      pack_bf16(fmaf((float)v[3][0], s16, c16), fmaf((float)v[3][1], s16, c16))});
   }
 };
+
+// f(Const<M>) with the smallest M of 1, 2, 4, .., MT groups of 16 that hold `rows`.
+template <int MT, typename F>
+__device__ __forceinline__ void by_height(int rows, F f) {
+  if constexpr (MT > 1) {
+    constexpr int HALF = MT > 4 ? 4 : MT / 2;
+    if (rows <= 16 * HALF) return by_height<HALF>(rows, f);
+  }
+  f(Const<MT>{});
+}
 
 // Four consecutive sums of a row, from column c: to the split's partial sums, or with add, rounded.
 template <int DT>
@@ -406,70 +443,78 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
   if (t.rows <= 0) return;
   const int nb0 = (b % groups * 4 + wave) * R;
   const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
-  f32x4 acc[MT][R];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < R; ++r) acc[m][r] = f32x4{};
   const int kb0 = (int)((int64_t)a.KB * split / a.split), kb1 = (int)((int64_t)a.KB * (split + 1) / a.split);
-  if (t.e >= 0 && kb0 < kb1) {
-    u32x4 wv[2][R];
-    svec sv[2][R];
-    zvec zv[2][R];
-    const auto load = [&](int d, int kb) {
+  by_height<MT>(t.rows, [&](auto mt) {
+    constexpr int M = decltype(mt)::value;  // groups of 16 rows that hold rows
+    f32x4 acc[M][R];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[m][r] = f32x4{};
+    if (t.e >= 0 && kb0 < kb1) {
+      const int c1 = min(kb1 * kBlockCols, a.K);  // columns of this split
+      u32x4 wv[R], wn[R];
+      svec sv[R], sn[R];
+      zvec zv[R], zn[R];
+      const auto load = [&](int kb) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
+          wn[r] = ((const u32x4*)(w + block * kBlockBytes))[lane];
+          sn[r] = ((const svec*)(w + a.soff))[block * 16 + li];
+          if (ZP) zn[r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
+        }
+      };
+      Stage<DT, M, true> st;
+      st.init(a, t, a.K);
+      st.load(kb0 * kBlockCols);
+      load(kb0);
+      st.store(sx[0], kb0 * kBlockCols);
+      __syncthreads();
+      for (int kb = kb0; kb < kb1; ++kb) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          wv[r] = wn[r];
+          sv[r] = sn[r];
+          zv[r] = zn[r];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = kb * kBlockCols + h * kStageCols, next = c + kStageCols;
+          if (c >= c1) break;
+          if (next < c1) st.load(next);
+          if (h == 0 && kb + 1 < kb1) load(kb + 1);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            constexpr int GS = 4 / SG;
+            const int j = 2 * h + q;
+            v8_t<DT> wf[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              GroupScale<DT, ZP> s;
+              s.set((uint16_t)((uint64_t)sv[r] >> (16 * (j / GS))), ZP ? (int)(int8_t)((uint32_t)zv[r] >> (8 * (j / GS))) : 0);
+              wf[r] = s.weights(wv[r][j]);
+            }
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+              const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[h][piece_at(16 * m + li, 4 * q + g)]);
+#pragma unroll
+              for (int r = 0; r < R; ++r) acc[m][r] = Mat<DT>::mma(wf[r], xf, acc[m][r]);
+            }
+          }
+          if (next < c1) st.store(sx[h ^ 1], next);
+          __syncthreads();
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
-        wv[d][r] = ((const u32x4*)(w + block * kBlockBytes))[lane];
-        sv[d][r] = ((const svec*)(w + a.soff))[block * 16 + li];
-        if (ZP) zv[d][r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
+        const int row = 16 * m + li, n = (nb0 + r) * kBlockRows + 4 * g;
+        if (row < t.rows && n < a.N) put4<DT>(a, a.N, split, t.r0 + row, n, acc[m][r]);
       }
-    };
-    Stage<DT, BM, true> st;
-    st.load(a, t, kb0 * kBlockCols, a.K);
-    load(0, kb0);
-    st.store(sx[0]);
-    __syncthreads();
-    const auto block = [&](int d, int kb) {
-      const int next = min(kb + 1, kb1 - 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        st.load(a, t, h ? next * kBlockCols : kb * kBlockCols + kStageCols, a.K);
-        if (h == 0) load(d ^ 1, next);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int j = 2 * h + q;
-          v8_t<DT> wf[R];
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            constexpr int GS = 4 / SG;
-            GroupScale<DT, ZP> s;
-            s.set((uint16_t)((uint64_t)sv[d][r] >> (16 * (j / GS))), ZP ? (int)(int8_t)((uint32_t)zv[d][r] >> (8 * (j / GS))) : 0);
-            wf[r] = s.weights(wv[d][r][j]);
-          }
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[h][piece_at(16 * m + li, 4 * q + g)]);
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[m][r] = Mat<DT>::mma(wf[r], xf, acc[m][r]);
-          }
-        }
-        st.store(sx[h ^ 1]);
-        __syncthreads();
-      }
-    };
-    for (int kb = kb0; kb < kb1; kb += 2) {
-      block(0, kb);
-      if (kb + 1 < kb1) block(1, kb + 1);
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int row = 16 * m + li, n = (nb0 + r) * kBlockRows + 4 * g;
-      if (row < t.rows && n < a.N) put4<DT>(a, a.N, split, t.r0 + row, n, acc[m][r]);
-    }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -499,36 +544,36 @@ struct RowScales<MOE_T_F16, ZP> {
   }
   __device__ __forceinline__ v8_t<MOE_T_F16> weights(uint32_t d) const {
     const half2_t k = both((_Float16)960.0f), sixteenth = both((_Float16)0.0625f);
-    const uint32_t e = d >> 8;
-    const half2_t v0 = as_half2((d & 0x000F000Fu) | 0x64006400u) + c[0];
-    const half2_t v1 = as_half2((d & 0x00F000F0u) | 0x64006400u) * sixteenth + (c[1] + k);
-    const half2_t v2 = as_half2((e & 0x000F000Fu) | 0x64006400u) + c[2];
-    const half2_t v3 = as_half2((e & 0x00F000F0u) | 0x64006400u) * sixteenth + (c[3] + k);
-    return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v0 * s[0]), bits_of(v1 * s[1]), bits_of(v2 * s[2]), bits_of(v3 * s[3])});
+    half2_t v[4];
+    code_pairs(d, v);
+    v[0] = (v[0] + c[0]) * s[0];
+    v[1] = (v[1] * sixteenth + (c[1] + k)) * s[1];
+    v[2] = (v[2] + c[2]) * s[2];
+    v[3] = (v[3] * sixteenth + (c[3] + k)) * s[3];
+    return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])});
   }
 };
 template <bool ZP>
 struct RowScales<MOE_T_BF16, ZP> {
-  float s[8], c[8];
+  float s[8], c[8];  // of pairs 1 and 3: for 1024 + 16 u
   // cv: eight values -(8 + z)
   __device__ __forceinline__ void set(u32x4 sv, u32x4 cv) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      s[i] = scale_value<MOE_T_BF16>((uint16_t)(sv[i / 2] >> (16 * (i & 1))));
-      c[i] = (ZP ? scale_value<MOE_T_BF16>((uint16_t)(cv[i / 2] >> (16 * (i & 1)))) : -8.0f) * s[i];
+      const bool high = i / 2 & 1;
+      const float f = scale_value<MOE_T_BF16>((uint16_t)(sv[i / 2] >> (16 * (i & 1))));
+      c[i] = ((ZP ? scale_value<MOE_T_BF16>((uint16_t)(cv[i / 2] >> (16 * (i & 1)))) : -8.0f) - (high ? 64.0f : 1024.0f)) * f;
+      s[i] = high ? f * 0.0625f : f;
     }
   }
   __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
-    const uint32_t lo = d & 0x0F0F0F0Fu, hi = d >> 4 & 0x0F0F0F0Fu;
-    v8_t<MOE_T_BF16> v;
+    half2_t v[4];
+    code_pairs(d, v);
+    u32x4 r;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // halves 4i .. 4i + 3: nibbles 2i, 2i + 4, 2i + 1, 2i + 5
-      v[4 * i] = (__bf16)fmaf(byte_of(lo, i), s[4 * i], c[4 * i]);
-      v[4 * i + 1] = (__bf16)fmaf(byte_of(lo, i + 2), s[4 * i + 1], c[4 * i + 1]);
-      v[4 * i + 2] = (__bf16)fmaf(byte_of(hi, i), s[4 * i + 2], c[4 * i + 2]);
-      v[4 * i + 3] = (__bf16)fmaf(byte_of(hi, i + 2), s[4 * i + 3], c[4 * i + 3]);
-    }
-    return v;
+    for (int i = 0; i < 4; ++i)
+      r[i] = pack_bf16(fmaf((float)v[i][0], s[2 * i], c[2 * i]), fmaf((float)v[i][1], s[2 * i + 1], c[2 * i + 1]));
+    return __builtin_bit_cast(v8_t<MOE_T_BF16>, r);
   }
 };
 
@@ -549,96 +594,98 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
   if (t.rows <= 0) return;
   const int kb0 = b % groups * CB;
   const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
-  f32x4 acc[MT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{};
   const int steps = (a.NB + SB - 1) / SB;
   const int s0 = (int)((int64_t)steps * split / a.split), s1 = (int)((int64_t)steps * (split + 1) / a.split);
   const int kbi = wave >> 1, jj = wave & 1;
   // group of this lane's columns among the step's
   const int cg = kbi * SG + (SG == 4 ? 2 * jj + (li >> 3) : SG == 2 ? jj : 0);
   const int rho = (li & 8) + ((li & 7) < 4 ? 2 * (li & 7) : 2 * (li & 7) - 7);  // the row whose eight bytes this lane points at
-  if (t.e >= 0 && s0 < s1) {
-    Stage<DT, BM, false> st;
-    u32x4 wv[2];
-    uint16_t sv[SP], zv[SP];
-    const auto load = [&](int s) {
-      st.load(a, t, s * kStepRows, a.N);
+  by_height<MT>(t.rows, [&](auto mt) {
+    constexpr int M = decltype(mt)::value;
+    f32x4 acc[M][4];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int i = threadIdx.x + p * kTileThreads, rb = s * SB + (i >> 7), kb = kb0 + (i >> 6 & 1);
-        wv[p] = rb < a.NB && kb < a.KB ? ((const u32x4*)(w + ((size_t)rb * a.KB + kb) * kBlockBytes))[i & 63] : u32x4{};
-      }
+    for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int p = 0; p < SP; ++p) {
-        const int i = threadIdx.x + p * kTileThreads;
-        const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
-        sv[p] = zv[p] = 0;
-        if (i < NS && rb < a.NB && kb < a.KB) {
-          const size_t at = ((size_t)rb * a.KB + kb) * 16 * SG + i % (16 * SG);
-          sv[p] = ((const uint16_t*)(w + a.soff))[at];
-          if (ZP) {
-            const int z = ((const int8_t*)(w + a.zoff))[at];
-            zv[p] = DT == MOE_T_F16 ? __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - z))
-                                    : __builtin_bit_cast(uint16_t, (__bf16)(float)(-8 - z));
-          }
+      for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{};
+    if (t.e >= 0 && s0 < s1) {
+      Stage<DT, M, false> st;
+      st.init(a, t, a.N);
+      u32x4 wv[2];
+      uint16_t sv[SP];
+      int8_t zv[SP];
+      // this thread's pieces of a step: blocks past the matrix repeat its last with scale 0
+      const int wi = threadIdx.x & 63, wk = min(kb0 + (int)(threadIdx.x >> 6 & 1), a.KB - 1);
+      const auto load = [&](int s) {
+        st.load(s * kStepRows);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int rb = min(s * SB + (int)(threadIdx.x >> 7) + 2 * p, a.NB - 1);
+          wv[p] = ((const u32x4*)(w + ((size_t)rb * a.KB + wk) * kBlockBytes))[wi];
         }
-      }
-    };
-    const auto store = [&](int u) {
-      st.store(sx[u]);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) sw[u][threadIdx.x + p * kTileThreads] = wv[p];
+        for (int p = 0; p < SP; ++p) {
+          const int i = min((int)threadIdx.x + p * kTileThreads, NS - 1);
+          const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
+          const size_t at = ((size_t)min(rb, a.NB - 1) * a.KB + min(kb, a.KB - 1)) * 16 * SG + i % (16 * SG);
+          sv[p] = ((const uint16_t*)(w + a.soff))[at];
+          if (ZP) zv[p] = ((const int8_t*)(w + a.zoff))[at];
+          if (rb >= a.NB || kb >= a.KB) sv[p] = 0;
+        }
+      };
+      const auto store = [&](int u, int s) {
+        st.store(sx[u], s * kStepRows);
 #pragma unroll
-      for (int p = 0; p < SP; ++p) {
-        const int i = threadIdx.x + p * kTileThreads;
-        if (i < NS) {
+        for (int p = 0; p < 2; ++p) sw[u][threadIdx.x + p * kTileThreads] = wv[p];
+#pragma unroll
+        for (int p = 0; p < SP; ++p) {
+          const int i = threadIdx.x + p * kTileThreads;
+          if (NS % kTileThreads && i >= NS) break;
           const int row = i / (CB * 16 * SG) * 16 + i / SG % 16, col = i / (16 * SG) % CB * SG + i % SG;
           ss[u][col][row] = sv[p];
-          if (ZP) sz[u][col][row] = zv[p];
+          if (ZP)
+            sz[u][col][row] = DT == MOE_T_F16 ? __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - zv[p]))
+                                              : __builtin_bit_cast(uint16_t, (__bf16)(float)(-8 - zv[p]));
         }
-      }
-    };
-    load(s0);
-    store(0);
-    __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-      const int u = (s - s0) & 1;
-      if (s + 1 < s1) load(s + 1);
-      v2i code[4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        code[f] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-            (lds_v2i*)((char*)&sw[u][(g * CB + kbi) * 64 + f * 16 + rho] + 8 * jj));
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {  // rows 16 g + 8 q .. + 7 of the step
-        RowScales<DT, ZP> rs;
-        rs.set(*(const u32x4*)&ss[u][cg][16 * g + 8 * q], *(const u32x4*)&sz[ZP ? u : 0][cg][16 * g + 8 * q]);
-        v8_t<DT> wf[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) wf[f] = rs.weights((uint32_t)code[f][q]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[u][piece_at(16 * m + li, 2 * g + q)]);
-#pragma unroll
-          for (int f = 0; f < 4; ++f) acc[m][f] = Mat<DT>::mma(wf[f], xf, acc[m][f]);
-        }
-      }
-      if (s + 1 < s1) store(u ^ 1);
+      };
+      load(s0);
+      store(0, s0);
       __syncthreads();
-    }
-  }
-  // lane's sums 4 g .. + 3 of fragment f: nibbles 4 g .. + 3 of the eight bytes
+      for (int s = s0; s < s1; ++s) {
+        const int u = (s - s0) & 1;
+        if (s + 1 < s1) load(s + 1);
+        v2i code[4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+        for (int f = 0; f < 4; ++f)
+          code[f] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+              (lds_v2i*)((char*)&sw[u][(g * CB + kbi) * 64 + f * 16 + rho] + 8 * jj));
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const int row = 16 * m + li;
-      const int c = (kb0 + kbi) * kBlockCols + 32 * (2 * jj + (g >> 1)) + 8 * f + 4 * (g & 1);
-      if (row < t.rows && c < a.K) put4<DT>(a, a.K, split, t.r0 + row, c, acc[m][f]);
+        for (int q = 0; q < 2; ++q) {  // rows 16 g + 8 q .. + 7 of the step
+          RowScales<DT, ZP> rs;
+          rs.set(*(const u32x4*)&ss[u][cg][16 * g + 8 * q], *(const u32x4*)&sz[ZP ? u : 0][cg][16 * g + 8 * q]);
+          v8_t<DT> wf[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) wf[f] = rs.weights((uint32_t)code[f][q]);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[u][piece_at(16 * m + li, 2 * g + q)]);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) acc[m][f] = Mat<DT>::mma(wf[f], xf, acc[m][f]);
+          }
+        }
+        if (s + 1 < s1) store(u ^ 1, s + 1);
+        __syncthreads();
+      }
     }
+    // lane's sums 4 g .. + 3 of fragment f: nibbles 4 g .. + 3 of the eight bytes
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int row = 16 * m + li;
+        const int c = (kb0 + kbi) * kBlockCols + 32 * (2 * jj + (g >> 1)) + 8 * f + 4 * (g & 1);
+        if (row < t.rows && c < a.K) put4<DT>(a, a.K, split, t.r0 + row, c, acc[m][f]);
+      }
+  });
 }
 
 // The splits' partial sums added in their order.
