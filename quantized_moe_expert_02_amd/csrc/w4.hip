@@ -52,47 +52,68 @@ struct RowTile {
   int e, r0, rows;
 };
 
+// A barrier for LDS alone: __syncthreads also waits for the loads from memory that are
+// still under way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Tiles are counted group by group, then come those of the rows outside.  Called by
-// whole wavefronts; every lane gets the same tile.
+// whole wavefronts; every lane gets the same.
 template <int BM>
-__device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int n, int T, int tile) {
-  if (!offsets) return RowTile{0, tile * BM, min(BM, T - tile * BM)};
-  const int lane = threadIdx.x & 63;
-  const int per = (n + 63) / 64, e0 = min(lane * per, n), e1 = min(e0 + per, n);
-  const auto at = [&](int i) { return min(max(offsets[i], 0), T); };
-  int count = 0, lo = at(e0);
-  const int first = lo;
-  for (int e = e0; e < e1; ++e) {
-    const int hi = max(lo, at(e + 1));
-    count += (hi - lo + BM - 1) / BM;
-    lo = hi;
-  }
-  const int incl = wave_inclusive_scan(count);
-  const uint64_t owner = __ballot(incl - count <= tile && tile < incl);
-  RowTile r{-1, 0, 0};
-  if (owner) {
-    int left = tile - (incl - count);
-    lo = first;
-    for (int e = e0; e < e1; ++e) {
-      const int hi = max(lo, at(e + 1)), c = (hi - lo + BM - 1) / BM;
-      if (left >= 0 && left < c) r = RowTile{e, lo + left * BM, min(BM, hi - lo - left * BM)};
-      left -= c;
+struct Tiles {
+  const int32_t* offsets;
+  int n, T;
+  int e0, e1, below, count;  // this lane's experts, the tiles before theirs and theirs
+  int grouped, head, end;    // tiles of all groups; the rows outside are [0, head) and [end, T)
+
+  __device__ __forceinline__ int at(int i) const { return min(max(offsets[i], 0), T); }
+  __device__ __forceinline__ Tiles(const int32_t* o, int n_, int T_) : offsets(o), n(n_), T(T_) {
+    if (!offsets) return;
+    const int per = (n + 63) / 64;
+    e0 = min((int)(threadIdx.x & 63) * per, n);
+    e1 = min(e0 + per, n);
+    count = 0;
+    for (int e = e0, lo = at(e0); e < e1; ++e) {
+      const int hi = max(lo, at(e + 1));
+      count += (hi - lo + BM - 1) / BM;
       lo = hi;
     }
-    const int l = __ffsll((unsigned long long)owner) - 1;
-    r.e = __builtin_amdgcn_readlane(r.e, l);
-    r.r0 = __builtin_amdgcn_readlane(r.r0, l);
-    r.rows = __builtin_amdgcn_readlane(r.rows, l);
+    const int incl = wave_inclusive_scan(count);
+    below = incl - count;
+    grouped = __builtin_amdgcn_readlane(incl, 63);
+    head = __builtin_amdgcn_readfirstlane(at(0));
+    end = __builtin_amdgcn_readfirstlane(max(head, at(n)));
+  }
+  __device__ __forceinline__ int total() const {
+    return offsets ? grouped + (head + BM - 1) / BM + (T - end + BM - 1) / BM : (T + BM - 1) / BM;
+  }
+  __device__ __forceinline__ RowTile find(int tile) const {
+    if (!offsets) return RowTile{0, tile * BM, min(BM, T - tile * BM)};
+    RowTile r{-1, 0, 0};
+    if (tile < grouped) {
+      const uint64_t owner = __ballot(below <= tile && tile < below + count);
+      int left = tile - below;
+      for (int e = e0, lo = at(e0); e < e1; ++e) {
+        const int hi = max(lo, at(e + 1)), c = (hi - lo + BM - 1) / BM;
+        if (left >= 0 && left < c) r = RowTile{e, lo + left * BM, min(BM, hi - lo - left * BM)};
+        left -= c;
+        lo = hi;
+      }
+      const int l = __ffsll((unsigned long long)owner) - 1;
+      return RowTile{__builtin_amdgcn_readlane(r.e, l), __builtin_amdgcn_readlane(r.r0, l),
+                     __builtin_amdgcn_readlane(r.rows, l)};
+    }
+    int t = tile - grouped;
+    const int heads = (head + BM - 1) / BM;
+    if (t < heads) return RowTile{-1, t * BM, min(BM, head - t * BM)};
+    t -= heads;
+    if (t < (T - end + BM - 1) / BM) r = RowTile{-1, end + t * BM, min(BM, T - end - t * BM)};
     return r;
   }
-  const int head = at(0), end = max(head, at(n));
-  int t = tile - __builtin_amdgcn_readlane(incl, 63);
-  const int heads = (head + BM - 1) / BM;
-  if (t < heads) return RowTile{-1, t * BM, min(BM, head - t * BM)};
-  t -= heads;
-  if ((int64_t)end + (int64_t)t * BM >= T) return r;
-  return RowTile{-1, end + t * BM, min(BM, T - end - t * BM)};
-}
+};
 
 // Upper bound on the tiles above.
 inline int64_t max_tiles(int n, int T, int BM, bool grouped) {
@@ -106,15 +127,19 @@ __device__ __forceinline__ half2_t as_half2(uint32_t v) { return __builtin_bit_c
 __device__ __forceinline__ uint32_t bits_of(half2_t v) { return __builtin_bit_cast(uint32_t, v); }
 __device__ __forceinline__ half2_t both(_Float16 v) { return half2_t{v, v}; }
 
+// (d & mask) | bits, one instruction.
+__device__ __forceinline__ uint32_t masked(uint32_t d, uint32_t mask, uint32_t bits) {
+  return (uint32_t)__builtin_amdgcn_bitop3_b32(d, mask, bits, 0xEA);
+}
+
 // The codes of a dword as four pairs of binary16 numbers: 1024 + u, or, where the
 // field sits at bit 4, 1024 + 16 u.
 __device__ __forceinline__ void code_pairs(uint32_t d, half2_t (&v)[4]) {
   const uint32_t e = d >> 8;
-  // (a & b) | c
-  v[0] = as_half2(__builtin_amdgcn_bitop3_b32(d, 0x000F000Fu, 0x64006400u, 0xEA));
-  v[1] = as_half2(__builtin_amdgcn_bitop3_b32(d, 0x00F000F0u, 0x64006400u, 0xEA));
-  v[2] = as_half2(__builtin_amdgcn_bitop3_b32(e, 0x000F000Fu, 0x64006400u, 0xEA));
-  v[3] = as_half2(__builtin_amdgcn_bitop3_b32(e, 0x00F000F0u, 0x64006400u, 0xEA));
+  v[0] = as_half2(masked(d, 0x000F000Fu, 0x64006400u));
+  v[1] = as_half2(masked(d, 0x00F000F0u, 0x64006400u));
+  v[2] = as_half2(masked(e, 0x000F000Fu, 0x64006400u));
+  v[3] = as_half2(masked(e, 0x00F000F0u, 0x64006400u));
 }
 
 // binary16: one packed subtraction or multiply-add leaves q - z exactly.  c = -(1032 + z).
@@ -143,8 +168,10 @@ __device__ __forceinline__ float scale_value(uint16_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: one workgroup per R row blocks and 16 rows, its W wavefronts split the
-// columns and add their sums through LDS.  The rows are the first operand (index l
+// Few rows: an item is 16 rows and one row block of a matrix; the W wavefronts of a
+// workgroup split its columns, KPW column blocks each, and add their sums through LDS.
+// A workgroup takes a run of items and keeps its rows in registers from item to item
+// while the next item's blocks are under way.  The rows are the first operand (index l
 // % 16: the row; rows past the tile are zeros) and a block the second (index l %
 // 16: its row), so that a lane's four sums belong to one weight row and are
 // multiplied by its scale.  binary16 factors are the codes q - z themselves;
@@ -171,12 +198,13 @@ struct ScaleVec<4> {
 
 // The product of one output element in fp32, term by term as the formula has it.
 template <int DT, int SG, bool ZP>
-__device__ __attribute__((noinline)) float slow_dot(const uint8_t* w, size_t soff, size_t zoff, int K, int KB, int n,
+__device__ __forceinline__ float slow_dot(const uint8_t* w, size_t soff, size_t zoff, int K, int KB, int n,
                                                     const void* xrow) {
   typedef typename Mat<DT>::elem elem;
   const elem* x = (const elem*)xrow;
   const int nb = n / kBlockRows, r = n % kBlockRows;
   float acc = 0.f;
+#pragma unroll 1
   for (int k = 0; k < K; ++k) {
     const int kb = k / kBlockCols, c = k % kBlockCols;
     const size_t block = (size_t)nb * KB + kb;
@@ -195,116 +223,158 @@ __device__ __forceinline__ u32x4 operand_order(u32x4 v) {
                __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
 }
 
-template <int DT, int SG, bool ZP, int R, int W, int D>
-__global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a, int groups) {
+template <int DT, int SG, bool ZP, int W, int KPW>
+__global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
   typedef typename Mat<DT>::elem elem;
   constexpr int GS = 4 / SG;  // matrix instructions per group
   typedef typename ScaleVec<SG>::s svec;
   typedef typename ScaleVec<SG>::z zvec;
-  __shared__ f32x4 red[W][R][64];
+  __shared__ f32x4 red[2][W][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int tile = blockIdx.x / groups, nb0 = blockIdx.x % groups * R;
-  const RowTile t = find_tile<16>(a.offsets, a.n, a.T, tile);
-  if (t.rows <= 0) return;
   const int li = lane & 15, g = lane >> 4;
-  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
-  const bool live = li < t.rows;
-  const elem* xrow = (const elem*)a.x + (int64_t)(t.r0 + (live ? li : 0)) * a.ldx + 8 * g;
-  u32x4 wv[D][R], xv[D][4];
-  svec sv[D][R];
-  zvec zv[D][R];
-  const auto load = [&](int d, int kb) {
+  const Tiles<16> tiles(a.offsets, a.n, a.T);
+  const int64_t items = (int64_t)tiles.total() * a.NB;
+  const int i0 = (int)(items * blockIdx.x / gridDim.x), i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  if (i0 >= i1) return;
+  const int passes = (a.KB + W * KPW - 1) / (W * KPW);  // over the columns (one up to 128 W KPW of them)
+  u32x4 xv[KPW][4], wv[KPW], wn[KPW];
+  svec sv[KPW], sn[KPW];
+  zvec zv[KPW], zn[KPW];
+  int tile = i0 / a.NB, nb = i0 % a.NB;
+  RowTile t = tiles.find(tile), tn = t;
+  const auto block_of = [&](int pass, int u) { return (pass * W + wave) * KPW + u; };
+  const auto load_w = [&](const RowTile& rt, int b, int pass) {
+    if (rt.e < 0) return;
+    const uint8_t* w = a.w + (size_t)rt.e * a.stride;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
-      wv[d][r] = __builtin_nontemporal_load((const u32x4*)(w + block * kBlockBytes) + lane);
-      sv[d][r] = ((const svec*)(w + a.soff))[block * 16 + li];
-      if (ZP) zv[d][r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = kb * kBlockCols + 32 * j;
-      xv[d][j] = live && k < a.K ? *(const u32x4*)(xrow + k) : u32x4{};
+    for (int u = 0; u < KPW; ++u) {
+      const int kb = block_of(pass, u);
+      if (kb >= a.KB) break;
+      const size_t block = (size_t)b * a.KB + kb;
+      wn[u] = __builtin_nontemporal_load((const u32x4*)(w + block * kBlockBytes) + lane);
+      sn[u] = ((const svec*)(w + a.soff))[block * 16 + li];
+      if (ZP) zn[u] = ((const zvec*)(w + a.zoff))[block * 16 + li];
     }
   };
-  f32x4 acc[R];
+  const auto load_x = [&](const RowTile& rt, int pass) {
+    if (rt.e < 0) return;
+    const elem* row = (const elem*)a.x + (int64_t)(rt.r0 + min(li, rt.rows - 1)) * a.ldx + 8 * g;
 #pragma unroll
-  for (int r = 0; r < R; ++r) acc[r] = f32x4{};
-  const auto multiply = [&](int d) {
+    for (int u = 0; u < KPW; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = block_of(pass, u) * kBlockCols + 32 * j;
+        xv[u][j] = u32x4{};
+        if (k < a.K && li < rt.rows) xv[u][j] = *(const u32x4*)(row + k);
+      }
+#pragma unroll
+    for (int u = 0; u < KPW; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xv[u][j] = operand_order(xv[u][j]);
+  };
+  f32x4 acc;
+  const auto multiply = [&](int u) {
     v8_t<DT> ones;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ones[i] = (elem)1.0f;
 #pragma unroll
     for (int s = 0; s < SG; ++s) {
-      f32x4 sum[R], xsum{};
-#pragma unroll
-      for (int r = 0; r < R; ++r) sum[r] = f32x4{};
+      f32x4 sum{}, xsum{};
+      const int z = ZP ? (int)(int8_t)((uint32_t)zv[u] >> (8 * s)) : 0;
 #pragma unroll
       for (int j = s * GS; j < (s + 1) * GS; ++j) {
-        const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, operand_order(xv[d][j]));
+        const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, xv[u][j]);
         if (DT == MOE_T_BF16) xsum = Mat<DT>::mma(xf, ones, xsum);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint32_t c = wv[d][r][j];
-          u32x4 b;
-          if constexpr (DT == MOE_T_F16) {
-            const int z = ZP ? (int)(int8_t)((uint32_t)zv[d][r] >> (8 * s)) : 0;
-            half2_t v[4];
-            codes_f16(c, both((_Float16)(float)(-1032 - z)), v);
-            b = u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])};
-          } else {
-            b = u32x4{(c & 0x000F000Fu) | 0x43004300u, (c >> 4 & 0x000F000Fu) | 0x43004300u,
-                      (c >> 8 & 0x000F000Fu) | 0x43004300u, (c >> 12 & 0x000F000Fu) | 0x43004300u};
-          }
-          sum[r] = Mat<DT>::mma(xf, __builtin_bit_cast(v8_t<DT>, b), sum[r]);
+        const uint32_t c = wv[u][j];
+        u32x4 b;
+        if constexpr (DT == MOE_T_F16) {
+          half2_t v[4];
+          codes_f16(c, both((_Float16)(float)(-1032 - z)), v);
+          b = u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])};
+        } else {
+          b = u32x4{masked(c, 0x000F000Fu, 0x43004300u),
+                    masked(c >> 4, 0x000F000Fu, 0x43004300u),
+                    masked(c >> 8, 0x000F000Fu, 0x43004300u),
+                    masked(c >> 12, 0x000F000Fu, 0x43004300u)};
         }
+        sum = Mat<DT>::mma(xf, __builtin_bit_cast(v8_t<DT>, b), sum);
+      }
+      const float f = scale_value<DT>((uint16_t)((uint64_t)sv[u] >> (16 * s)));
+      if constexpr (DT == MOE_T_BF16) {
+        const float off = (float)(-136 - z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = fmaf(off, xsum[i], sum[i]);
       }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float f = scale_value<DT>((uint16_t)((uint64_t)sv[d][r] >> (16 * s)));
-        if constexpr (DT == MOE_T_BF16) {
-          const float off = (float)(136 + (ZP ? (int)(int8_t)((uint32_t)zv[d][r] >> (8 * s)) : 0));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[r][i] = fmaf(-off, xsum[i], sum[r][i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(f, sum[r][i], acc[r][i]);
-      }
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, sum[i], acc[i]);
     }
   };
-  if (t.e >= 0) {
+  load_w(t, nb, 0);
+  load_x(t, 0);
+  for (int i = i0; i < i1; ++i) {
+    const int nb_now = nb;
+    acc = f32x4{};
+    for (int pass = 0; pass < passes; ++pass) {
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (wave + d * W < a.KB) load(d, wave + d * W);
-    for (int kb = wave; kb < a.KB; kb += D * W) {
-#pragma unroll
-      for (int d = 0; d < D; ++d)
-        if (kb + d * W < a.KB) {
-          multiply(d);
-          if (kb + (d + D) * W < a.KB) load(d, kb + (d + D) * W);
+      for (int u = 0; u < KPW; ++u) {
+        wv[u] = wn[u];
+        sv[u] = sn[u];
+        zv[u] = zn[u];
+      }
+      if (pass + 1 < passes) {
+        load_w(t, nb_now, pass + 1);
+      } else if (i + 1 < i1) {
+        if (++nb == a.NB) {
+          nb = 0;
+          tn = tiles.find(++tile);
         }
+        load_w(tn, nb, 0);
+      }
+      if (t.e >= 0) {
+#pragma unroll
+        for (int u = 0; u < KPW; ++u)
+          if (block_of(pass, u) < a.KB) multiply(u);
+      }
+      if (passes > 1) load_x(pass + 1 < passes ? t : tn, (pass + 1) % passes);
     }
-  }
+    const int p = i & 1;
+    red[p][wave][lane] = acc;
+    lds_barrier();
+    const int n = nb_now * kBlockRows + li;
+    if (wave == i % W && n < a.N && 4 * g < t.rows) {
+      f32x4 v = red[p][0][lane];
+#pragma unroll 3
+      for (int u = 1; u < W; ++u) v += red[p][u][lane];
+      const int live = min(4, t.rows - 4 * g);
+      const int64_t row = t.r0 + 4 * g;
+      if (DT == MOE_T_BF16 && t.e >= 0) {
+        // the terms 128 + u and 136 + z beside an infinity, or past fp32's range, need
+        // not cancel to the formula's value
+        bool finite = true;
 #pragma unroll
-  for (int r = 0; r < R; ++r) red[wave][r][lane] = acc[r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < R * 64; i += 64 * W) {
-    const int r = i >> 6, n = (nb0 + r) * kBlockRows + (i & 15), m0 = (i >> 4 & 3) * 4;
-    if (n >= a.N || m0 >= t.rows) continue;
-    f32x4 v = red[0][r][i & 63];
+        for (int q = 0; q < 4; ++q) finite &= fabsf(v[q]) < INFINITY;
+        if (!finite) {
+#pragma unroll 1
+          for (int q = 0; q < live; ++q) {
+            const float o = slow_dot<DT, SG, ZP>(a.w + (size_t)t.e * a.stride, a.soff, a.zoff, a.K, a.KB, n,
+                                                 (const elem*)a.x + (row + q) * a.ldx);
 #pragma unroll
-    for (int u = 1; u < W; ++u) v += red[u][r][i & 63];
+            for (int k = 0; k < 4; ++k)
+              if (k == q && !(fabsf(v[k]) < INFINITY)) v[k] = o;
+          }
+        }
+      }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (m0 + q >= t.rows) break;
-      const int64_t row = t.r0 + m0 + q;
-      float o = v[q];
-      // the terms 128 + u and 136 + z beside an infinity, or past fp32's range, need
-      // not cancel to the formula's value
-      if (DT == MOE_T_BF16 && !(fabsf(o) < INFINITY) && t.e >= 0)
-        o = slow_dot<DT, SG, ZP>(w, a.soff, a.zoff, a.K, a.KB, n, (const elem*)a.x + row * a.ldx);
-      if (a.add) o += (float)((const elem*)a.add)[row * a.ldadd + n];
-      ((elem*)a.y)[row * a.ldy + n] = (elem)o;
+      for (int q = 0; q < 4; ++q) {
+        if (q >= live) break;
+        float o = v[q];
+        if (a.add) o += (float)((const elem*)a.add)[(row + q) * a.ldadd + n];
+        ((elem*)a.y)[(row + q) * a.ldy + n] = (elem)o;
+      }
+    }
+    if (nb == 0 && i + 1 < i1) {
+      t = tn;
+      if (passes == 1) load_x(t, 0);
     }
   }
 }
@@ -439,7 +509,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, g = lane >> 4;
   const int split = blockIdx.x % a.split, b = blockIdx.x / a.split;
-  const RowTile t = find_tile<BM>(a.offsets, a.n, a.T, b / groups);
+  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(b / groups);
   if (t.rows <= 0) return;
   const int nb0 = (b % groups * 4 + wave) * R;
   const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
@@ -470,7 +540,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
       st.load(kb0 * kBlockCols);
       load(kb0);
       st.store(sx[0], kb0 * kBlockCols);
-      __syncthreads();
+      lds_barrier();
       for (int kb = kb0; kb < kb1; ++kb) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -503,7 +573,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
             }
           }
           if (next < c1) st.store(sx[h ^ 1], next);
-          __syncthreads();
+          lds_barrier();
         }
       }
     }
@@ -590,7 +660,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, g = lane >> 4;
   const int split = blockIdx.x % a.split, b = blockIdx.x / a.split;
-  const RowTile t = find_tile<BM>(a.offsets, a.n, a.T, b / groups);
+  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(b / groups);
   if (t.rows <= 0) return;
   const int kb0 = b % groups * CB;
   const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
@@ -649,7 +719,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
       };
       load(s0);
       store(0, s0);
-      __syncthreads();
+      lds_barrier();
       for (int s = s0; s < s1; ++s) {
         const int u = (s - s0) & 1;
         if (s + 1 < s1) load(s + 1);
@@ -673,7 +743,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
           }
         }
         if (s + 1 < s1) store(u ^ 1, s + 1);
-        __syncthreads();
+        lds_barrier();
       }
     }
     // lane's sums 4 g .. + 3 of fragment f: nibbles 4 g .. + 3 of the eight bytes
@@ -757,6 +827,7 @@ __global__ __launch_bounds__(64) void k_w4_pack(PackArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxLd = 1 << 22;
 constexpr int kFewRows = 16;
+constexpr int kCUs = 256;
 
 struct W4Layout {
   int NB, KB, SG;
@@ -904,16 +975,17 @@ int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, in
   W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, x, ldx, T, offsets, add,
            ldadd, y, ldy, nullptr, 1};
   if (few_rows(*d, T)) {
+    const int64_t items = max_tiles(d->n, T, 16, offsets != nullptr) * l.NB;
     by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
       constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
       constexpr bool ZP = decltype(zp)::value;
-      const int64_t tiles = max_tiles(d->n, T, 16, offsets != nullptr);
-      const auto launch = [&](auto kernel, int R, int W) {
-        const int groups = ceil_div(l.NB, R);
-        kernel<<<(unsigned)(tiles * groups), 64 * W, 0, s>>>(a, groups);
+      const auto launch = [&](auto kernel, int W, int per_cu) {
+        kernel<<<(unsigned)std::min<int64_t>(items, kCUs * per_cu), 64 * W, 0, s>>>(a);
       };
-      if (l.NB <= 1024) launch(k_w4_few<DT, SG, ZP, 1, 8, 3>, 1, 8);
-      else launch(k_w4_few<DT, SG, ZP, 4, 4, 2>, 4, 4);
+      if (l.KB <= 4) launch(k_w4_few<DT, SG, ZP, 4, 1>, 4, 6);
+      else if (l.KB <= 8) launch(k_w4_few<DT, SG, ZP, 4, 2>, 4, 5);
+      else if (l.KB <= 16) launch(k_w4_few<DT, SG, ZP, 8, 2>, 8, 2);
+      else launch(k_w4_few<DT, SG, ZP, 16, 3>, 16, 1);
     });
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
   }
