@@ -380,53 +380,60 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: tiles of BM = 16 MT rows.  Rows pass through two LDS buffers of 64
-// columns each (16-byte pieces, swizzled so that an operand's 16 rows cover all
-// banks).
+// Many rows: tiles of BM = 16 MT rows, which pass through two LDS buffers.
 // ---------------------------------------------------------------------------
 constexpr int kTileThreads = 256;
-constexpr int kStageCols = 64;
 
-// Piece (row, c) of a buffer: 8 pieces of 16 bytes per row; rows 2i and 2i + 1 fill one
-// line of 64 banks.
-__device__ __forceinline__ int piece_at(int row, int c) { return row * 8 + (c ^ (row >> 1 & 7)); }
+// A workgroup's rows of one step of CS columns (64 or 128), from memory to registers
+// to LDS, 16-byte pieces.  Pieces are swizzled so that an operand's 16 rows cover all
+// banks (a line of 64 banks holds 16 pieces: one row of 128 columns or two of 64).  Rows
+// past the tile repeat its last (their sums are not stored); of the last step's
+// columns those past the width are zeros.
+template <int CS>
+__device__ __forceinline__ int piece_at(int row, int c) {
+  return CS == 128 ? row * 16 + (c ^ (row & 15)) : row * 8 + (c ^ (row >> 1 & 7));
+}
 
-// A workgroup's rows of one step of 64 columns, from memory to registers to LDS, 32
-// rows to a piece per thread.  Rows past the tile repeat its last (their sums are not
-// stored); of the last step's columns those past the width are zeros.
-template <int DT, int MT, bool ORDER>
+template <int DT, int MT, int CS, bool ORDER>
 struct Stage {
-  static constexpr int P = (MT + 1) / 2;
+  static constexpr int PR = CS / 8, RP = kTileThreads / PR;  // pieces per row, rows per pass
+  static constexpr int P = (16 * MT + RP - 1) / RP;
+  struct Pieces {
+    u32x4 v[P];
+  };
   const char* base;
   uint32_t at[P];
-  int width;
-  u32x4 v[P];
-  __device__ __forceinline__ void init(const W4Args& a, const RowTile& t, int w) {
+  int width, c;
+  __device__ __forceinline__ Stage(const W4Args& a, const RowTile& t, int w) {
     base = (const char*)a.x + (int64_t)t.r0 * a.ldx * 2;
     width = w;
+    c = threadIdx.x % PR;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int row = min((int)(threadIdx.x >> 3) + 32 * p, t.rows - 1);
-      at[p] = (uint32_t)row * (uint32_t)(a.ldx * 2) + (threadIdx.x & 7) * 16;
+      const int row = min((int)threadIdx.x / PR + RP * p, t.rows - 1);
+      at[p] = (uint32_t)row * (uint32_t)(a.ldx * 2) + c * 16;
     }
   }
-  __device__ __forceinline__ bool tail(int c0) const { return c0 + kStageCols > width; }
-  __device__ __forceinline__ void load(int c0) {
+  __device__ __forceinline__ void load(Pieces& v, int c0) const {
     const char* b = base + (size_t)c0 * 2;
-    const int left = width - c0;  // at least 8
-    const uint32_t back = tail(c0) ? max(0, (int)(threadIdx.x & 7) * 16 - (left / 8 * 16 - 16)) : 0;
+    const uint32_t back = max(0, c - (min(width - c0, CS) / 8 - 1)) * 16;  // to the last piece of the row
 #pragma unroll
-    for (int p = 0; p < P; ++p) v[p] = *(const u32x4*)(b + (at[p] - back));
+    for (int p = 0; p < P; ++p) v.v[p] = *(const u32x4*)(b + (at[p] - back));
   }
-  __device__ __forceinline__ void store(u32x4* lds, int c0) {
-    if (tail(c0) && c0 + (int)(threadIdx.x & 7) * 8 >= width) {
+  __device__ __forceinline__ void store(const Pieces& v, u32x4* lds, int c0) const {
+    const bool in = c0 + c * 8 < width;
 #pragma unroll
-      for (int p = 0; p < P; ++p) v[p] = u32x4{};
+    for (int p = 0; p < P; ++p) {
+      u32x4 o = ORDER ? operand_order(v.v[p]) : v.v[p];
+      if (c0 + CS > width) o = in ? o : u32x4{};
+      lds[piece_at<CS>(threadIdx.x / PR + RP * p, c)] = o;
     }
-#pragma unroll
-    for (int p = 0; p < P; ++p) lds[piece_at((threadIdx.x >> 3) + 32 * p, threadIdx.x & 7)] = ORDER ? operand_order(v[p]) : v[p];
   }
 };
+
+// Steps that are loaded ahead: tiles of few rows have little to do between loads, and
+// registers to spare.
+constexpr int steps_ahead(int M) { return M <= 2 ? 3 : M <= 4 ? 2 : 1; }
 
 // Weights rounded to the rows' type as operands.  binary16: the exact code times the
 // scale, a packed product.  bfloat16: (1024 + u) s - (1032 + z) s in one fp32
@@ -505,7 +512,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
   constexpr int BM = 16 * MT;
   typedef typename ScaleVec<SG>::s svec;
   typedef typename ScaleVec<SG>::z zvec;
-  __shared__ u32x4 sx[2][BM * 8];
+  __shared__ u32x4 sx[2][BM * 16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, g = lane >> 4;
   const int split = blockIdx.x % a.split, b = blockIdx.x / a.split;
@@ -522,42 +529,52 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[m][r] = f32x4{};
     if (t.e >= 0 && kb0 < kb1) {
-      const int c1 = min(kb1 * kBlockCols, a.K);  // columns of this split
-      u32x4 wv[R], wn[R];
-      svec sv[R], sn[R];
-      zvec zv[R], zn[R];
-      const auto load = [&](int kb) {
+      typedef Stage<DT, M, kBlockCols, true> St;
+      constexpr int D = steps_ahead(M);
+      const St st(a, t, a.K);
+      struct Step {
+        typename St::Pieces x;
+        u32x4 w[R];
+        svec s[R];
+        zvec z[R];
+      } step[D];
+      // (steps past the last read it again and go unused: without branches around loads
+      // the waits for them are exact)
+      const auto load = [&](Step& u, int kb) {
+        kb = min(kb, kb1 - 1);
+        st.load(u.x, kb * kBlockCols);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
-          wn[r] = ((const u32x4*)(w + block * kBlockBytes))[lane];
-          sn[r] = ((const svec*)(w + a.soff))[block * 16 + li];
-          if (ZP) zn[r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
+          u.w[r] = ((const u32x4*)(w + block * kBlockBytes))[lane];
+          u.s[r] = ((const svec*)(w + a.soff))[block * 16 + li];
+          if (ZP) u.z[r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
         }
       };
-      Stage<DT, M, true> st;
-      st.init(a, t, a.K);
-      st.load(kb0 * kBlockCols);
-      load(kb0);
-      st.store(sx[0], kb0 * kBlockCols);
+#pragma unroll
+      for (int d = 0; d < D; ++d) load(step[d], kb0 + d);
+      st.store(step[0].x, sx[0], kb0 * kBlockCols);
       lds_barrier();
-      for (int kb = kb0; kb < kb1; ++kb) {
+      int buf = 0;
+      for (int k0 = kb0; k0 < kb1; k0 += D) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          wv[r] = wn[r];
-          sv[r] = sn[r];
-          zv[r] = zn[r];
-        }
+        for (int d = 0; d < D; ++d) {
+          const int kb = k0 + d;
+          if (kb >= kb1) break;
+          u32x4 wv[R];
+          svec sv[R];
+          zvec zv[R];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = kb * kBlockCols + h * kStageCols, next = c + kStageCols;
-          if (c >= c1) break;
-          if (next < c1) st.load(next);
-          if (h == 0 && kb + 1 < kb1) load(kb + 1);
+          for (int r = 0; r < R; ++r) {
+            wv[r] = step[d].w[r];
+            sv[r] = step[d].s[r];
+            zv[r] = step[d].z[r];
+          }
+          load(step[d], kb + D);
+          const u32x4* x = sx[buf];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int j = 0; j < 4; ++j) {
             constexpr int GS = 4 / SG;
-            const int j = 2 * h + q;
             v8_t<DT> wf[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -567,12 +584,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
             }
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-              const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[h][piece_at(16 * m + li, 4 * q + g)]);
+              const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, x[piece_at<kBlockCols>(16 * m + li, 4 * j + g)]);
 #pragma unroll
               for (int r = 0; r < R; ++r) acc[m][r] = Mat<DT>::mma(wf[r], xf, acc[m][r]);
             }
           }
-          if (next < c1) st.store(sx[h ^ 1], next);
+          buf ^= 1;
+          st.store(step[(d + 1) % D].x, sx[buf], min(kb + 1, kb1 - 1) * kBlockCols);
           lds_barrier();
         }
       }
@@ -678,72 +696,85 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
 #pragma unroll
       for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{};
     if (t.e >= 0 && s0 < s1) {
-      Stage<DT, M, false> st;
-      st.init(a, t, a.N);
-      u32x4 wv[2];
-      uint16_t sv[SP];
-      int8_t zv[SP];
+      typedef Stage<DT, M, kStepRows, false> St;
+      constexpr int D = steps_ahead(M);
+      const St st(a, t, a.N);
+      struct Step {
+        typename St::Pieces x;
+        u32x4 w[2];
+        uint16_t s[SP];
+        int8_t z[SP];
+      } step[D];
       // this thread's pieces of a step: blocks past the matrix repeat its last with scale 0
       const int wi = threadIdx.x & 63, wk = min(kb0 + (int)(threadIdx.x >> 6 & 1), a.KB - 1);
-      const auto load = [&](int s) {
-        st.load(s * kStepRows);
+      const auto load = [&](Step& u, int s) {
+        s = min(s, s1 - 1);
+        st.load(u.x, s * kStepRows);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const int rb = min(s * SB + (int)(threadIdx.x >> 7) + 2 * p, a.NB - 1);
-          wv[p] = ((const u32x4*)(w + ((size_t)rb * a.KB + wk) * kBlockBytes))[wi];
+          u.w[p] = ((const u32x4*)(w + ((size_t)rb * a.KB + wk) * kBlockBytes))[wi];
         }
 #pragma unroll
         for (int p = 0; p < SP; ++p) {
           const int i = min((int)threadIdx.x + p * kTileThreads, NS - 1);
           const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
           const size_t at = ((size_t)min(rb, a.NB - 1) * a.KB + min(kb, a.KB - 1)) * 16 * SG + i % (16 * SG);
-          sv[p] = ((const uint16_t*)(w + a.soff))[at];
-          if (ZP) zv[p] = ((const int8_t*)(w + a.zoff))[at];
-          if (rb >= a.NB || kb >= a.KB) sv[p] = 0;
+          u.s[p] = ((const uint16_t*)(w + a.soff))[at];
+          if (ZP) u.z[p] = ((const int8_t*)(w + a.zoff))[at];
         }
       };
-      const auto store = [&](int u, int s) {
-        st.store(sx[u], s * kStepRows);
+      const auto store = [&](const Step& u, int buf, int s) {
+        s = min(s, s1 - 1);
+        st.store(u.x, sx[buf], s * kStepRows);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) sw[u][threadIdx.x + p * kTileThreads] = wv[p];
+        for (int p = 0; p < 2; ++p) sw[buf][threadIdx.x + p * kTileThreads] = u.w[p];
 #pragma unroll
         for (int p = 0; p < SP; ++p) {
           const int i = threadIdx.x + p * kTileThreads;
           if (NS % kTileThreads && i >= NS) break;
+          const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
           const int row = i / (CB * 16 * SG) * 16 + i / SG % 16, col = i / (16 * SG) % CB * SG + i % SG;
-          ss[u][col][row] = sv[p];
+          ss[buf][col][row] = rb < a.NB && kb < a.KB ? u.s[p] : 0;
           if (ZP)
-            sz[u][col][row] = DT == MOE_T_F16 ? __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - zv[p]))
-                                              : __builtin_bit_cast(uint16_t, (__bf16)(float)(-8 - zv[p]));
+            sz[buf][col][row] = DT == MOE_T_F16 ? __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - u.z[p]))
+                                                : __builtin_bit_cast(uint16_t, (__bf16)(float)(-8 - u.z[p]));
         }
       };
-      load(s0);
-      store(0, s0);
+#pragma unroll
+      for (int d = 0; d < D; ++d) load(step[d], s0 + d);
+      store(step[0], 0, s0);
       lds_barrier();
-      for (int s = s0; s < s1; ++s) {
-        const int u = (s - s0) & 1;
-        if (s + 1 < s1) load(s + 1);
-        v2i code[4];
+      int buf = 0;
+      for (int k0 = s0; k0 < s1; k0 += D) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          code[f] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-              (lds_v2i*)((char*)&sw[u][(g * CB + kbi) * 64 + f * 16 + rho] + 8 * jj));
+        for (int d = 0; d < D; ++d) {
+          const int s = k0 + d;
+          if (s >= s1) break;
+          load(step[d], s + D);
+          v2i code[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // rows 16 g + 8 q .. + 7 of the step
-          RowScales<DT, ZP> rs;
-          rs.set(*(const u32x4*)&ss[u][cg][16 * g + 8 * q], *(const u32x4*)&sz[ZP ? u : 0][cg][16 * g + 8 * q]);
-          v8_t<DT> wf[4];
+          for (int f = 0; f < 4; ++f)
+            code[f] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                (lds_v2i*)((char*)&sw[buf][(g * CB + kbi) * 64 + f * 16 + rho] + 8 * jj));
 #pragma unroll
-          for (int f = 0; f < 4; ++f) wf[f] = rs.weights((uint32_t)code[f][q]);
+          for (int q = 0; q < 2; ++q) {  // rows 16 g + 8 q .. + 7 of the step
+            RowScales<DT, ZP> rs;
+            rs.set(*(const u32x4*)&ss[buf][cg][16 * g + 8 * q], *(const u32x4*)&sz[ZP ? buf : 0][cg][16 * g + 8 * q]);
+            v8_t<DT> wf[4];
 #pragma unroll
-          for (int m = 0; m < M; ++m) {
-            const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[u][piece_at(16 * m + li, 2 * g + q)]);
+            for (int f = 0; f < 4; ++f) wf[f] = rs.weights((uint32_t)code[f][q]);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) acc[m][f] = Mat<DT>::mma(wf[f], xf, acc[m][f]);
+            for (int m = 0; m < M; ++m) {
+              const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[buf][piece_at<kStepRows>(16 * m + li, 2 * g + q)]);
+#pragma unroll
+              for (int f = 0; f < 4; ++f) acc[m][f] = Mat<DT>::mma(wf[f], xf, acc[m][f]);
+            }
           }
+          buf ^= 1;
+          store(step[(d + 1) % D], buf, s + 1);
+          lds_barrier();
         }
-        if (s + 1 < s1) store(u ^ 1, s + 1);
-        lds_barrier();
       }
     }
     // lane's sums 4 g .. + 3 of fragment f: nibbles 4 g .. + 3 of the eight bytes
