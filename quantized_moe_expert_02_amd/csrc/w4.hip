@@ -60,14 +60,17 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Tiles are counted group by group, then come those of the rows outside.  Called by
+// Tiles in their order: the full ones of all groups, their rests, then those of the rows
+// outside (workgroups start in that order, the ones with most to do first).  Called by
 // whole wavefronts; every lane gets the same.
 template <int BM>
 struct Tiles {
   const int32_t* offsets;
   int n, T;
-  int e0, e1, below, count;  // this lane's experts, the tiles before theirs and theirs
-  int grouped, head, end;    // tiles of all groups; the rows outside are [0, head) and [end, T)
+  int e0, e1;              // this lane's experts
+  int full, rest;          // their tiles,
+  int full_at, rest_at;    // and the number of their first ones
+  int head, end, grouped;  // the rows outside are [0, head) and [end, T); tiles of all groups
 
   __device__ __forceinline__ int at(int i) const { return min(max(offsets[i], 0), T); }
   __device__ __forceinline__ Tiles(const int32_t* o, int n_, int T_) : offsets(o), n(n_), T(T_) {
@@ -75,15 +78,17 @@ struct Tiles {
     const int per = (n + 63) / 64;
     e0 = min((int)(threadIdx.x & 63) * per, n);
     e1 = min(e0 + per, n);
-    count = 0;
+    full = rest = 0;
     for (int e = e0, lo = at(e0); e < e1; ++e) {
       const int hi = max(lo, at(e + 1));
-      count += (hi - lo + BM - 1) / BM;
+      full += (hi - lo) / BM;
+      rest += (hi - lo) % BM != 0;
       lo = hi;
     }
-    const int incl = wave_inclusive_scan(count);
-    below = incl - count;
-    grouped = __builtin_amdgcn_readlane(incl, 63);
+    const int f = wave_inclusive_scan(full), r = wave_inclusive_scan(rest);
+    full_at = f - full;
+    rest_at = __builtin_amdgcn_readlane(f, 63) + r - rest;
+    grouped = __builtin_amdgcn_readlane(f, 63) + __builtin_amdgcn_readlane(r, 63);
     head = __builtin_amdgcn_readfirstlane(at(0));
     end = __builtin_amdgcn_readfirstlane(max(head, at(n)));
   }
@@ -94,15 +99,16 @@ struct Tiles {
     if (!offsets) return RowTile{0, tile * BM, min(BM, T - tile * BM)};
     RowTile r{-1, 0, 0};
     if (tile < grouped) {
-      const uint64_t owner = __ballot(below <= tile && tile < below + count);
-      int left = tile - below;
+      const int nth_full = tile - full_at, nth_rest = tile - rest_at;
+      const bool in_full = nth_full >= 0 && nth_full < full, mine = in_full || (nth_rest >= 0 && nth_rest < rest);
+      const int l = __ffsll((unsigned long long)__ballot(mine)) - 1;
+      int left = in_full ? nth_full : nth_rest;
       for (int e = e0, lo = at(e0); e < e1; ++e) {
-        const int hi = max(lo, at(e + 1)), c = (hi - lo + BM - 1) / BM;
-        if (left >= 0 && left < c) r = RowTile{e, lo + left * BM, min(BM, hi - lo - left * BM)};
+        const int hi = max(lo, at(e + 1)), f = (hi - lo) / BM, k = (hi - lo) % BM, c = in_full ? f : (k != 0);
+        if (left >= 0 && left < c) r = in_full ? RowTile{e, lo + left * BM, BM} : RowTile{e, hi - k, k};
         left -= c;
         lo = hi;
       }
-      const int l = __ffsll((unsigned long long)owner) - 1;
       return RowTile{__builtin_amdgcn_readlane(r.e, l), __builtin_amdgcn_readlane(r.r0, l),
                      __builtin_amdgcn_readlane(r.rows, l)};
     }
@@ -118,6 +124,22 @@ struct Tiles {
 // Upper bound on the tiles above.
 inline int64_t max_tiles(int n, int T, int BM, bool grouped) {
   return grouped ? (int64_t)T / BM + std::min(n, T) + 2 : ceil_div(T, BM);
+}
+
+// Tile and run of columns of workgroup b, of `groups` runs per tile.  Workgroups go to the
+// 8 dies in turn.  Tiles of groups: all runs of a tile on one die, whose L2 then holds
+// its rows (16,384 rows of 64 experts, 6144 x 2048: 500 -> 475 us; of 256, 2048 x
+// 1024: 151 -> 144).  One matrix: neither order was faster.
+struct Place {
+  int tile, run;
+};
+__device__ __forceinline__ Place place_of(int b, int groups, bool grouped) {
+  if (!grouped) return Place{b / groups, b % groups};
+  const int loc = b / 8;
+  return Place{loc / groups * 8 + b % 8, loc % groups};
+}
+inline int64_t places(int64_t tiles, int groups, bool grouped) {
+  return (grouped ? (tiles + 7) / 8 * 8 : tiles) * groups;
 }
 
 // ---------------------------------------------------------------------------
@@ -515,10 +537,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
   __shared__ u32x4 sx[2][BM * 16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.split, b = blockIdx.x / a.split;
-  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(b / groups);
+  const int split = blockIdx.x % a.split;
+  const Place at = place_of(blockIdx.x / a.split, groups, a.offsets);
+  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(at.tile);
   if (t.rows <= 0) return;
-  const int nb0 = (b % groups * 4 + wave) * R;
+  const int nb0 = (at.run * 4 + wave) * R;
   const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
   const int kb0 = (int)((int64_t)a.KB * split / a.split), kb1 = (int)((int64_t)a.KB * (split + 1) / a.split);
   by_height<MT>(t.rows, [&](auto mt) {
@@ -677,10 +700,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
   __shared__ __attribute__((aligned(16))) uint16_t ss[2][CB * SG][kStepRows], sz[ZP ? 2 : 1][CB * SG][kStepRows];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.split, b = blockIdx.x / a.split;
-  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(b / groups);
+  const int split = blockIdx.x % a.split;
+  const Place at = place_of(blockIdx.x / a.split, groups, a.offsets);
+  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(at.tile);
   if (t.rows <= 0) return;
-  const int kb0 = b % groups * CB;
+  const int kb0 = at.run * CB;
   const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
   const int steps = (a.NB + SB - 1) / SB;
   const int s0 = (int)((int64_t)steps * split / a.split), s1 = (int)((int64_t)steps * (split + 1) / a.split);
@@ -897,22 +921,45 @@ int check_w4_rows(const moe_w4_dims_t* d, int32_t T) {
 
 bool few_rows(const moe_w4_dims_t& d, int T) { return T <= (int64_t)kFewRows * d.n; }
 
-// Tile height and splits of a call with many rows.
+// Tiles of a call with many rows: MT groups of 16 rows by 64 R weight rows (forward) or
+// 256 columns (gradient), and parts that a tile's sums are split into.
 struct TilePlan {
   int MT, R, groups, split;
 };
 
-constexpr int kTargetGroups = 512;
+// Measured in us; 6144 x 6144 unless said.  One matrix: the largest tiles that still give
+// nearly two workgroups per CU (8,192 rows of 8192 x 8192: forward 128 x 256 1,033, 64 x
+// 256 1,223, gradient 128 rows 1,112, 96 1,161, 64 1,290; 2,048 rows: forward 128 x 256 185
+// (384 workgroups), 128 x 192 163 (512), gradient 128 rows 203, 96 183), else 64 rows
+// (2,048 rows of 2048 x 6144: 128 x 256 115, 64 x 256 69).  Experts: 128 (gradient 96) rows
+// only where they have that many on average (256 experts, 2048 x 1024, of 128 rows 180,
+// in tiles of 64 238; 16,384 rows by Zipf's law 167 and 153; their gradient 88 and 89).
+// The sums are split while all workgroups are resident at once (64 rows: 4 parts 19.7, 8
+// 13.8, 12 17.1, with 24 tiles).
+constexpr int kTwoPerCU = 460, kOnePerCU = 256, kStepsPerPart = 3;
 
 TilePlan plan_tiles(const moe_w4_dims_t& d, int T, bool grad) {
   TilePlan p;
   const int avg = ceil_div(T, d.n);
-  p.MT = avg <= 32 ? 2 : avg <= 64 ? 4 : 8;
+  const auto blocks = [&](int MT, int R) {
+    return (int64_t)ceil_div(T, 16 * MT) * (grad ? ceil_div(d.K, kGradCols) : ceil_div(d.N, 64 * R));
+  };
   p.R = 4;
+  if (avg <= 32) {
+    p.MT = 2;
+  } else if (d.n > 1) {
+    p.MT = avg <= 96 ? 4 : grad ? 6 : 8;
+  } else if (blocks(8, 4) >= kTwoPerCU) {
+    p.MT = 8;
+  } else if (grad) {
+    p.MT = blocks(6, 4) >= kTwoPerCU ? 6 : 4;
+  } else {
+    p.R = blocks(8, 3) >= kTwoPerCU ? 3 : 4;
+    p.MT = p.R == 3 ? 8 : 4;
+  }
   p.groups = grad ? ceil_div(d.K, kGradCols) : ceil_div(d.N, 64 * p.R);
-  const int64_t blocks = (int64_t)ceil_div(T, 16 * p.MT) * p.groups;
   const int steps = grad ? ceil_div(d.N, kStepRows) : ceil_div(d.K, kBlockCols);
-  p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kTargetGroups / blocks, steps / 4));
+  p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kOnePerCU / blocks(p.MT, p.R), steps / kStepsPerPart));
   return p;
 }
 
@@ -1031,9 +1078,11 @@ int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, in
   by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
     constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
     constexpr bool ZP = decltype(zp)::value;
-    const unsigned blocks = (unsigned)(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr) * p.groups * p.split);
+    const unsigned blocks =
+        (unsigned)(places(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr), p.groups, offsets != nullptr) * p.split);
     if (p.MT == 2) k_w4_rows<DT, SG, ZP, 2, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
     else if (p.MT == 4) k_w4_rows<DT, SG, ZP, 4, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    else if (p.R == 3) k_w4_rows<DT, SG, ZP, 8, 3><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
     else k_w4_rows<DT, SG, ZP, 8, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
     if (need) launch_sum<DT>(a, d->N, s);
   });
@@ -1057,9 +1106,11 @@ int moe_w4_backward(const moe_w4_dims_t* d, const void* packed, const void* dy, 
   by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
     constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
     constexpr bool ZP = decltype(zp)::value;
-    const unsigned blocks = (unsigned)(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr) * p.groups * p.split);
+    const unsigned blocks =
+        (unsigned)(places(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr), p.groups, offsets != nullptr) * p.split);
     if (p.MT == 2) k_w4_grad<DT, SG, ZP, 2><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
     else if (p.MT == 4) k_w4_grad<DT, SG, ZP, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
+    else if (p.MT == 6) k_w4_grad<DT, SG, ZP, 6><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
     else k_w4_grad<DT, SG, ZP, 8><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
     if (need) launch_sum<DT>(a, d->K, s);
   });
