@@ -13,8 +13,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMaxEntries = 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
@@ -77,17 +75,50 @@ __device__ __forceinline__ void add_run(Run& r, const float (&z)[N], float c) {
   for (int i = 0; i < N; ++i) r.s += __builtin_amdgcn_exp2f((z[i] - f) * c);
 }
 
-// The columns [c0, c1) of a row as unaligned ends and 16-byte vectors between:
-// one(i) for single columns, many(i) for kVec columns from i.
-template <int DT, typename One, typename Many>
-__device__ __forceinline__ void over_row(const typename RowType<DT>::elem* row, int c0, int c1, One one, Many many) {
-  constexpr int VEC = kVec<DT>;
-  const int shift = (int)((uintptr_t)(row + c0) % 16 / sizeof(typename RowType<DT>::elem));
-  const int head = min(c1, c0 + (shift ? VEC - shift : 0)), vectors = (c1 - head) / VEC, tail = head + vectors * VEC;
-  if ((int)threadIdx.x < head - c0) one(c0 + threadIdx.x);
-  for (int v = threadIdx.x; v < vectors; v += kThreads) many(head + v * VEC);
-  if ((int)threadIdx.x < c1 - tail) one(tail + threadIdx.x);
-}
+// The columns [c0, c1) of a row as unaligned ends and 16-byte vectors between, kBatch of
+// them on their way per thread (results may be written over the row: without batches
+// every load would wait for the store before it).  The first batch is requested where the
+// object is made, ahead of what else a workgroup has to read.
+constexpr int kBatch = 4;
+template <int DT, bool STREAM, int TH>
+struct RowScan {
+  typedef typename RowType<DT>::elem elem;
+  static constexpr int VEC = kVec<DT>;
+  const u32x4* p;
+  int c0, c1, head, vectors, tail;
+  u32x4 x[kBatch];
+  __device__ __forceinline__ RowScan(const elem* row, int c0_, int c1_) : c0(c0_), c1(c1_) {
+    const int shift = (int)((uintptr_t)(row + c0) % 16 / sizeof(elem));
+    head = min(c1, c0 + (shift ? VEC - shift : 0));
+    vectors = (c1 - head) / VEC;
+    tail = head + vectors * VEC;
+    p = (const u32x4*)(row + head);
+    if (vectors) load((int)threadIdx.x);
+  }
+  __device__ __forceinline__ void load(int v) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const u32x4* q = p + min(v + u * TH, vectors - 1);
+      x[u] = STREAM ? __builtin_nontemporal_load(q) : *q;
+    }
+  }
+  // one(i) for single columns, many(i, v) for the VEC columns from i
+  template <typename One, typename Many>
+  __device__ __forceinline__ void run(One one, Many many) {
+    for (int v = threadIdx.x; v < vectors; v += kBatch * TH) {
+      if (v >= kBatch * TH) load(v);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (v + u * TH < vectors) many(head + (v + u * TH) * VEC, x[u]);
+    }
+    ends(one);
+  }
+  template <typename One>
+  __device__ __forceinline__ void ends(One one) const {
+    if ((int)threadIdx.x < head - c0) one(c0 + threadIdx.x);
+    if ((int)threadIdx.x < c1 - tail) one(tail + threadIdx.x);
+  }
+};
 
 // The teacher's probabilities of row t, by one wavefront: top and norm with p = 2^((a
 // - top) c) / norm.  False if the row keeps no entry.
@@ -143,40 +174,42 @@ __device__ __forceinline__ void drop_row(const DistillArgs& a, int t) {
   if (threadIdx.x == 0) a.loss[t] = a.stats[2 * (int64_t)t] = a.stats[2 * (int64_t)t + 1] = 0.0f;
 }
 
-// One workgroup per row, or (PART) per chunk of one.
-template <int DT, bool PART>
-__global__ __launch_bounds__(kThreads) void k_distill(DistillArgs a) {
+// A workgroup of TH threads per row, or (PART) per chunk of one.
+template <int DT, bool PART, bool STREAM, int TH>
+__global__ __launch_bounds__(TH) void k_distill(DistillArgs a) {
   typedef typename RowType<DT>::elem elem;
-  constexpr int VEC = kVec<DT>;
-  __shared__ Run runs[kWaves];
+  constexpr int VEC = kVec<DT>, W = TH / 64;
+  __shared__ Run runs[W];
   const int t = PART ? blockIdx.x / a.chunks : blockIdx.x, ch = PART ? blockIdx.x % a.chunks : 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const elem* z = (const elem*)a.z + (int64_t)t * a.ldz;
+  const int c0 = PART ? ch * a.chunk : 0, c1 = PART ? min(a.V, c0 + a.chunk) : a.V;
+  RowScan<DT, STREAM, TH> scan(z, c0, c1);
   const Teacher te = teacher_of(a, t);
   if (!te.any) {
     if (!PART) drop_row(a, t);
     return;
   }
-  const elem* z = (const elem*)a.z + (int64_t)t * a.ldz;
-  const int c0 = PART ? ch * a.chunk : 0, c1 = PART ? min(a.V, c0 + a.chunk) : a.V;
   Run r{-INFINITY, 0.0f};
-  over_row<DT>(
-      z, c0, c1,
+  scan.run(
       [&](int i) {
         const float v[1] = {(float)z[i]};
         add_run(r, v, a.c);
       },
-      [&](int i) {
+      [&](int, u32x4 x) {
         float v[VEC];
-        unpack_vec<DT>(*(const u32x4*)(z + i), v);
+        unpack_vec<DT>(x, v);
         add_run(r, v, a.c);
       });
   r = wave_join(r, a.c);
-  if (lane == 0) runs[wave] = r;
-  __syncthreads();
-  if (wave) return;
-  r = runs[0];
+  if (W > 1) {
+    if (lane == 0) runs[wave] = r;
+    __syncthreads();
+    if (wave) return;
+    r = runs[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) r = join(r, runs[i], a.c);
+    for (int i = 1; i < W; ++i) r = join(r, runs[i], a.c);
+  }
   if (PART) {
     if (lane == 0) a.part[(int64_t)t * a.chunks + ch] = make_float2(r.m, r.s);
   } else {
@@ -201,18 +234,40 @@ __global__ __launch_bounds__(64) void k_distill_join(DistillArgs a) {
 // The gradient of a chunk of a row.  The teacher's entries in the chunk are written
 // after the others, each id once with the sum of its probabilities; their logits are
 // read before anything is written, so that dz may be z.
-template <int DT>
-__global__ __launch_bounds__(kThreads) void k_distill_grad(DistillArgs a) {
+struct Entry {
+  int id;   // -1: not in the chunk
+  float p, z, sum;  // sum: of p over the entries of the same id; < 0 but for the first of them
+};
+
+template <int DT, bool STREAM, int TH>
+__global__ __launch_bounds__(TH) void k_distill_grad(DistillArgs a) {
   typedef typename RowType<DT>::elem elem;
   constexpr int VEC = kVec<DT>;
-  __shared__ int s_id[kMaxEntries];
-  __shared__ float s_p[kMaxEntries];
+  extern __shared__ Entry entry[];
   const int t = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks;
   const elem* z = (const elem*)a.z + (int64_t)t * a.ldz;
   elem* dz = (elem*)a.dz + (int64_t)t * a.lddz;
   const int c0 = ch * a.chunk, c1 = min(a.V, c0 + a.chunk);
-  const Teacher te = teacher_of(a, t);
+  RowScan<DT, STREAM, TH> scan(z, c0, c1);
   const float m = a.stats[2 * (int64_t)t], l2 = a.stats[2 * (int64_t)t + 1] * kLog2e, w = a.dloss[t] * a.rtau;
+  const Teacher te = teacher_of(a, t);
+  const bool same = (uintptr_t)z % 16 == (uintptr_t)dz % 16;
+  const auto put = [&](int i, const float (&v)[VEC]) {
+    if (same) {
+      const u32x4 o = pack_vec<DT>(v);
+      if (STREAM) __builtin_nontemporal_store(o, (u32x4*)(dz + i));
+      else *(u32x4*)(dz + i) = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) dz[i + e] = (elem)v[e];
+    }
+  };
+  if (!te.any) {
+    const float zero[VEC] = {};
+    for (int v = threadIdx.x; v < scan.vectors; v += TH) put(scan.head + v * VEC, zero);
+    scan.ends([&](int i) { dz[i] = (elem)0.0f; });
+    return;
+  }
   const auto q = [&](float v) { return __builtin_amdgcn_exp2f(fmaf(v - m, a.c, -l2)); };
   // A product that is rounded to fp32 before it is to the rows' type, in every form of
   // the loop (the compiler may fuse the two), so that alignment does not show.
@@ -221,73 +276,68 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(DistillArgs a) {
     asm("" : "+v"(p));
     return p;
   };
-  constexpr int PER = kMaxEntries / kThreads;
-  float own[PER], sum[PER];
-  bool first[PER];
-  if (te.any) {
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int j = threadIdx.x + u * kThreads;
-      if (j < a.k) {
-        const int id = a.ids[(int64_t)t * a.k + j];
-        const bool here = id >= c0 && id < c1;
-        s_id[j] = here ? id : -1;
-        s_p[j] = here ? __builtin_amdgcn_exp2f((a.teacher[(int64_t)t * a.k + j] - te.top) * a.c) / te.norm : 0.0f;
-        own[u] = here ? (float)z[id] : 0.0f;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int j = threadIdx.x + u * kThreads;
-      first[u] = j < a.k && s_id[j] >= 0;
-      sum[u] = 0.0f;
-      if (first[u])
-        for (int i = 0; i < a.k; ++i)
-          if (s_id[i] == s_id[j]) {
-            first[u] &= i >= j;
-            sum[u] += s_p[i];
-          }
-    }
+  for (int j = threadIdx.x; j < a.k; j += TH) {
+    const int id = a.ids[(int64_t)t * a.k + j];
+    const bool here = id >= c0 && id < c1;
+    Entry e{-1, 0.0f, 0.0f, -1.0f};
+    if (here) e = Entry{id, __builtin_amdgcn_exp2f((a.teacher[(int64_t)t * a.k + j] - te.top) * a.c) / te.norm, (float)z[id], -1.0f};
+    entry[j] = e;
   }
-  const bool same = (uintptr_t)z % 16 == (uintptr_t)dz % 16;
-  over_row<DT>(
-      z, c0, c1, [&](int i) { dz[i] = (elem)(te.any ? weighted(q((float)z[i])) : 0.0f); },
-      [&](int i) {
-        float v[VEC];
-        if (te.any) {
-          unpack_vec<DT>(*(const u32x4*)(z + i), v);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v[e] = weighted(q(v[e]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v[e] = 0.0f;
-        }
-        if (same) {
-          *(u32x4*)(dz + i) = pack_vec<DT>(v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) dz[i + e] = (elem)v[e];
-        }
-      });
-  if (!te.any) return;
   __syncthreads();
+  for (int j = threadIdx.x; j < a.k; j += TH) {
+    const int id = entry[j].id;
+    if (id < 0) continue;
+    bool first = true;
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < a.k; ++i) {
+      const bool eq = entry[i].id == id;
+      first &= !eq || i >= j;
+      sum += eq ? entry[i].p : 0.0f;
+    }
+    if (first) entry[j].sum = sum;
+  }
+  scan.run([&](int i) { dz[i] = (elem)weighted(q((float)z[i])); },
+           [&](int i, u32x4 x) {
+             float v[VEC];
+             unpack_vec<DT>(x, v);
 #pragma unroll
-  for (int u = 0; u < PER; ++u)
-    if (first[u]) dz[s_id[threadIdx.x + u * kThreads]] = (elem)weighted(q(own[u]) - sum[u]);
+             for (int e = 0; e < VEC; ++e) v[e] = weighted(q(v[e]));
+             put(i, v);
+           });
+  __syncthreads();
+  for (int j = threadIdx.x; j < a.k; j += TH) {
+    const Entry e = entry[j];
+    if (e.id >= 0 && !(e.sum < 0.0f)) dz[e.id] = (elem)weighted(q(e.z) - e.sum);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int kTargetBlocks = 1024;
-constexpr int kMinChunk = 8192;
+// Rows of up to 16 KB take a wavefront each (4,096 rows of 8,000 bfloat16 logits: 64
+// threads 17.5 us, 512 25.6; gradient 41.5 and 48.2; of 16,000: 31.8 and 33.8, gradient 74
+// and 65).
+constexpr int64_t kShortRow = 16 << 10;
+// Longer ones 512 threads, and where that makes too few workgroups, chunks of 16 to 64 KB,
+// about 512 in all (loss of 64 rows of 128,000 bfloat16 logits: whole rows 14.1 us, 64 KB 9.9,
+// 32 KB 10.4; 301 rows of 100,003 binary16: 22.1 and 20.9 (so whole from 256 rows); 4
+// rows of 128,000 fp32: 16.7, 16 KB 6.4).  The gradient, which joins nothing, always takes
+// chunks (2,048 rows of 128,000 bfloat16: whole rows 203, 64 KB 190).
+constexpr int kWholeRows = 256;
 
-// Columns per workgroup: whole rows where there are many.
-int chunk_of(int T, int V) {
-  const int chunks = std::min(ceil_div(kTargetBlocks, T), ceil_div(V, kMinChunk));
-  return T >= kTargetBlocks / 2 ? V : (ceil_div(V, std::max(chunks, 1)) + 7) / 8 * 8;
+int chunk_of(int T, int V, int dtype, bool grad) {
+  const int64_t b = (int64_t)elem_bytes(dtype), bytes = std::min<int64_t>(std::max<int64_t>((int64_t)T * V * b / 512, 16 << 10), 64 << 10);
+  if (V * b <= kShortRow || (!grad && T >= kWholeRows)) return V;
+  const int chunks = ceil_div(V * b, bytes);
+  return std::min(V, ceil_div(ceil_div(V, chunks), 8) * 8);
 }
+
+// Logits too large for the last-level cache to keep are read and written past the caches
+// (2,048 rows of 128,000 bfloat16: 94.4 us plainly, 85.7 streamed, gradient 208 and 190;
+// 512 rows 29.3 and 25.9, gradient 57.7 and 51.6).
+constexpr int64_t kStream = (int64_t)112 << 20;
+bool streamed(int T, int V, int dtype) { return (int64_t)T * V * (int64_t)elem_bytes(dtype) >= kStream; }
 
 int check_shape(int32_t T, int32_t V, int32_t dtype) {
   if (T < 0 || V < 1 || dtype < MOE_T_F16 || dtype > MOE_T_F32) return MOE_E_INVAL;
@@ -299,7 +349,7 @@ int check_distill(const void* z, int32_t dtype, int64_t ldz, int32_t T, int32_t 
   const int st = check_shape(T, V, dtype);
   if (st != MOE_OK) return st;
   if (k < 1 || !(tau > 0.0f && tau < INFINITY) || ldz < V) return MOE_E_INVAL;
-  if (k > kMaxEntries || ldz > (int64_t)1 << 40 || (int64_t)T * ldz > (int64_t)1 << 40) return MOE_E_UNSUPPORTED;
+  if (k > kMaxEntries || ldz > (int64_t)1 << 36 || (int64_t)T * ldz > (int64_t)1 << 36) return MOE_E_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   return bad(z, (unsigned)elem_bytes(dtype)) || bad(ids, 4) || bad(teacher, 4) ? MOE_E_INVAL : MOE_OK;
 }
@@ -321,7 +371,7 @@ extern "C" {
 
 size_t moe_distill_workspace_bytes(int32_t T, int32_t V, int32_t dtype) {
   if (check_shape(T, V, dtype) != MOE_OK || T == 0) return 0;
-  const int chunks = ceil_div(V, chunk_of(T, V));
+  const int chunks = ceil_div(V, chunk_of(T, V, dtype, false));
   return chunks > 1 ? (size_t)T * chunks * sizeof(float2) : 0;
 }
 
@@ -331,7 +381,7 @@ int moe_distill_forward(const void* z, int32_t dtype, int64_t ldz, int32_t T, in
   const int st = check_distill(z, dtype, ldz, T, V, ids, teacher, k, tau);
   if (st != MOE_OK || T == 0) return st;
   if (bad(loss, 4) || bad(stats, 4)) return MOE_E_INVAL;
-  const int chunk = chunk_of(T, V), chunks = ceil_div(V, chunk);
+  const int chunk = chunk_of(T, V, dtype, false), chunks = ceil_div(V, chunk);
   if (chunks > 1 && bad(ws, 16)) return MOE_E_INVAL;
   if (ws_bytes < moe_distill_workspace_bytes(T, V, dtype)) return MOE_E_WORKSPACE;
   const hipStream_t s = (hipStream_t)stream;
@@ -340,9 +390,11 @@ int moe_distill_forward(const void* z, int32_t dtype, int64_t ldz, int32_t T, in
   by_type(dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     if (chunks == 1) {
-      k_distill<DT, false><<<T, kThreads, 0, s>>>(a);
+      if (V * (int64_t)elem_bytes(dtype) <= kShortRow) k_distill<DT, false, false, 64><<<T, 64, 0, s>>>(a);
+      else if (streamed(T, V, dtype)) k_distill<DT, false, true, 512><<<T, 512, 0, s>>>(a);
+      else k_distill<DT, false, false, 512><<<T, 512, 0, s>>>(a);
     } else {
-      k_distill<DT, true><<<T * chunks, kThreads, 0, s>>>(a);
+      k_distill<DT, true, false, 512><<<T * chunks, 512, 0, s>>>(a);
       k_distill_join<DT><<<T, 64, 0, s>>>(a);
     }
   });
@@ -355,14 +407,20 @@ int moe_distill_backward(const void* z, int32_t dtype, int64_t ldz, int32_t T, i
   const int st = check_distill(z, dtype, ldz, T, V, ids, teacher, k, tau);
   if (st != MOE_OK) return st;
   if (lddz < V || (dz == z && lddz != ldz)) return MOE_E_INVAL;
-  if (lddz > (int64_t)1 << 40 || (int64_t)T * lddz > (int64_t)1 << 40) return MOE_E_UNSUPPORTED;
+  if (lddz > (int64_t)1 << 36 || (int64_t)T * lddz > (int64_t)1 << 36) return MOE_E_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (bad(stats, 4) || bad(dloss, 4) || bad(dz, (unsigned)elem_bytes(dtype))) return MOE_E_INVAL;
-  const int chunk = chunk_of(T, V), chunks = ceil_div(V, chunk);
+  const int chunk = chunk_of(T, V, dtype, true), chunks = ceil_div(V, chunk);
   const hipStream_t s = (hipStream_t)stream;
   const DistillArgs a{z, ldz, T, V, k, ids, teacher, kLog2e / tau, 1.0f / tau, chunk, chunks, nullptr,
                       (float*)stats, nullptr, dloss, dz, lddz};
-  by_type(dtype, [&](auto dt) { k_distill_grad<decltype(dt)::value><<<T * chunks, kThreads, 0, s>>>(a); });
+  by_type(dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const size_t lds = k * sizeof(Entry);
+    if (V * (int64_t)elem_bytes(dtype) <= kShortRow) k_distill_grad<DT, false, 64><<<T * chunks, 64, lds, s>>>(a);
+    else if (streamed(T, V, dtype)) k_distill_grad<DT, true, 512><<<T * chunks, 512, lds, s>>>(a);
+    else k_distill_grad<DT, false, 512><<<T * chunks, 512, lds, s>>>(a);
+  });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 

@@ -1,817 +1,10 @@
-// Products of rows with frozen 4-bit weights that have group scales
-// (include/moe_w4.h): forward for few and for many rows, and the gradient of the
-// rows.
-//
-// Packed matrix: blocks of 16 rows x 128 columns, 1 KiB each, [row block][column
-// block].  Lane l = 16 g + r of a wavefront owns 16 bytes: dword j holds row r,
-// columns 32 j + 8 g .. + 7, one nibble each (column p in nibble p), offset
-// binary (u = q + 8).  So one 128-bit load per lane reads a whole block, and dword j
-// of all lanes is one operand of a 16x16x32 matrix instruction whose contraction
-// runs along the columns.  Rows and columns past the matrix hold q = 0 with scale 0.
-// Scales (and zero points) follow, [row block][column block][16 rows][SG], with SG =
-// 4, 2 or 1 groups per 128 columns (wider groups are repeated in every block).
-//
-// Masking a dword with 0x000F000F leaves the codes of columns p and p + 4 in the
-// two halves: operands hold eight columns in the order 0 4 1 5 2 6 3 7, and the
-// rows' operands are put in that order too.
-#include <algorithm>
-
-#include "mat.h"
-#include "moe_w4.h"
+// Entry points of include/moe_w4.h, packing, and the sum of split products; the
+// products themselves are in w4_few.hip, w4_rows.hip and w4_grad.hip.
+#include "w4.h"
 
 namespace moe {
 
 namespace {
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
-
-constexpr int kBlockRows = 16, kBlockCols = 128, kBlockBytes = 1024;
-
-struct W4Args {
-  const uint8_t* w;   // packed matrices
-  size_t stride;      // bytes from matrix to matrix
-  size_t soff, zoff;  // scales, zero points
-  int n, N, K, NB, KB;  // NB x KB blocks
-  const void* x;      // rows of the product (x, or dy in the gradient)
-  int64_t ldx;
-  int T;
-  const int32_t* offsets;
-  const void* add;
-  int64_t ldadd;
-  void* y;
-  int64_t ldy;
-  float* part;  // [split][T][width], or NULL
-  int split;
-};
-
-// A tile of up to BM rows of one matrix; e < 0: rows outside the groups; rows == 0: none.
-struct RowTile {
-  int e, r0, rows;
-};
-
-// A barrier for LDS alone: __syncthreads also waits for the loads from memory that are
-// still under way.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// Tiles in their order: the full ones of all groups, their rests, then those of the rows
-// outside (workgroups start in that order, the ones with most to do first).  Called by
-// whole wavefronts; every lane gets the same.
-template <int BM>
-struct Tiles {
-  const int32_t* offsets;
-  int n, T;
-  int e0, e1;              // this lane's experts
-  int full, rest;          // their tiles,
-  int full_at, rest_at;    // and the number of their first ones
-  int head, end, grouped;  // the rows outside are [0, head) and [end, T); tiles of all groups
-
-  __device__ __forceinline__ int at(int i) const { return min(max(offsets[i], 0), T); }
-  __device__ __forceinline__ Tiles(const int32_t* o, int n_, int T_) : offsets(o), n(n_), T(T_) {
-    if (!offsets) return;
-    const int per = (n + 63) / 64;
-    e0 = min((int)(threadIdx.x & 63) * per, n);
-    e1 = min(e0 + per, n);
-    full = rest = 0;
-    for (int e = e0, lo = at(e0); e < e1; ++e) {
-      const int hi = max(lo, at(e + 1));
-      full += (hi - lo) / BM;
-      rest += (hi - lo) % BM != 0;
-      lo = hi;
-    }
-    const int f = wave_inclusive_scan(full), r = wave_inclusive_scan(rest);
-    full_at = f - full;
-    rest_at = __builtin_amdgcn_readlane(f, 63) + r - rest;
-    grouped = __builtin_amdgcn_readlane(f, 63) + __builtin_amdgcn_readlane(r, 63);
-    head = __builtin_amdgcn_readfirstlane(at(0));
-    end = __builtin_amdgcn_readfirstlane(max(head, at(n)));
-  }
-  __device__ __forceinline__ int total() const {
-    return offsets ? grouped + (head + BM - 1) / BM + (T - end + BM - 1) / BM : (T + BM - 1) / BM;
-  }
-  __device__ __forceinline__ RowTile find(int tile) const {
-    if (!offsets) return RowTile{0, tile * BM, min(BM, T - tile * BM)};
-    RowTile r{-1, 0, 0};
-    if (tile < grouped) {
-      const int nth_full = tile - full_at, nth_rest = tile - rest_at;
-      const bool in_full = nth_full >= 0 && nth_full < full, mine = in_full || (nth_rest >= 0 && nth_rest < rest);
-      const int l = __ffsll((unsigned long long)__ballot(mine)) - 1;
-      int left = in_full ? nth_full : nth_rest;
-      for (int e = e0, lo = at(e0); e < e1; ++e) {
-        const int hi = max(lo, at(e + 1)), f = (hi - lo) / BM, k = (hi - lo) % BM, c = in_full ? f : (k != 0);
-        if (left >= 0 && left < c) r = in_full ? RowTile{e, lo + left * BM, BM} : RowTile{e, hi - k, k};
-        left -= c;
-        lo = hi;
-      }
-      return RowTile{__builtin_amdgcn_readlane(r.e, l), __builtin_amdgcn_readlane(r.r0, l),
-                     __builtin_amdgcn_readlane(r.rows, l)};
-    }
-    int t = tile - grouped;
-    const int heads = (head + BM - 1) / BM;
-    if (t < heads) return RowTile{-1, t * BM, min(BM, head - t * BM)};
-    t -= heads;
-    if (t < (T - end + BM - 1) / BM) r = RowTile{-1, end + t * BM, min(BM, T - end - t * BM)};
-    return r;
-  }
-};
-
-// Upper bound on the tiles above.
-inline int64_t max_tiles(int n, int T, int BM, bool grouped) {
-  return grouped ? (int64_t)T / BM + std::min(n, T) + 2 : ceil_div(T, BM);
-}
-
-// Tile and run of columns of workgroup b, of `groups` runs per tile.  Workgroups go to the
-// 8 dies in turn.  Tiles of groups: all runs of a tile on one die, whose L2 then holds
-// its rows (16,384 rows of 64 experts, 6144 x 2048: 500 -> 475 us; of 256, 2048 x
-// 1024: 151 -> 144).  One matrix: neither order was faster.
-struct Place {
-  int tile, run;
-};
-__device__ __forceinline__ Place place_of(int b, int groups, bool grouped) {
-  if (!grouped) return Place{b / groups, b % groups};
-  const int loc = b / 8;
-  return Place{loc / groups * 8 + b % 8, loc % groups};
-}
-inline int64_t places(int64_t tiles, int groups, bool grouped) {
-  return (grouped ? (tiles + 7) / 8 * 8 : tiles) * groups;
-}
-
-// ---------------------------------------------------------------------------
-// Codes into operands.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ half2_t as_half2(uint32_t v) { return __builtin_bit_cast(half2_t, v); }
-__device__ __forceinline__ uint32_t bits_of(half2_t v) { return __builtin_bit_cast(uint32_t, v); }
-__device__ __forceinline__ half2_t both(_Float16 v) { return half2_t{v, v}; }
-
-// (d & mask) | bits, one instruction.
-__device__ __forceinline__ uint32_t masked(uint32_t d, uint32_t mask, uint32_t bits) {
-  return (uint32_t)__builtin_amdgcn_bitop3_b32(d, mask, bits, 0xEA);
-}
-
-// The codes of a dword as four pairs of binary16 numbers: 1024 + u, or, where the
-// field sits at bit 4, 1024 + 16 u.
-__device__ __forceinline__ void code_pairs(uint32_t d, half2_t (&v)[4]) {
-  const uint32_t e = d >> 8;
-  v[0] = as_half2(masked(d, 0x000F000Fu, 0x64006400u));
-  v[1] = as_half2(masked(d, 0x00F000F0u, 0x64006400u));
-  v[2] = as_half2(masked(e, 0x000F000Fu, 0x64006400u));
-  v[3] = as_half2(masked(e, 0x00F000F0u, 0x64006400u));
-}
-
-// binary16: one packed subtraction or multiply-add leaves q - z exactly.  c = -(1032 + z).
-__device__ __forceinline__ void codes_f16(uint32_t d, half2_t c, half2_t (&v)[4]) {
-  const half2_t c16 = c + both((_Float16)960.0f);  // -(72 + z)
-  const half2_t sixteenth = both((_Float16)0.0625f);
-  code_pairs(d, v);
-  v[0] += c;
-  v[1] = v[1] * sixteenth + c16;
-  v[2] += c;
-  v[3] = v[3] * sixteenth + c16;
-}
-
-// Two values rounded to bfloat16, in one instruction.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf2_t));
-}
-
-// Scales and zero points as the packed matrix holds them, and what the operands
-// need of them.
-template <int DT>
-__device__ __forceinline__ float scale_value(uint16_t s) {
-  if constexpr (DT == MOE_T_F16) return (float)__builtin_bit_cast(_Float16, s);
-  else return __builtin_bit_cast(float, (uint32_t)s << 16);
-}
-
-// ---------------------------------------------------------------------------
-// Few rows: an item is 16 rows and one row block of a matrix; the W wavefronts of a
-// workgroup split its columns, KPW column blocks each, and add their sums through LDS.
-// A workgroup takes a run of items and keeps its rows in registers from item to item
-// while the next item's blocks are under way.  The rows are the first operand (index l
-// % 16: the row; rows past the tile are zeros) and a block the second (index l %
-// 16: its row), so that a lane's four sums belong to one weight row and are
-// multiplied by its scale.  binary16 factors are the codes q - z themselves;
-// bfloat16 holds 128 + u exactly, and (136 + z) times the sum of the rows' elements
-// is taken off each group's sum.
-// ---------------------------------------------------------------------------
-template <int SG>
-struct ScaleVec;
-template <>
-struct ScaleVec<1> {
-  typedef uint16_t s;
-  typedef int8_t z;
-};
-template <>
-struct ScaleVec<2> {
-  typedef uint32_t s;
-  typedef uint16_t z;
-};
-template <>
-struct ScaleVec<4> {
-  typedef uint64_t s;
-  typedef uint32_t z;
-};
-
-// The product of one output element in fp32, term by term as the formula has it.
-template <int DT, int SG, bool ZP>
-__device__ __forceinline__ float slow_dot(const uint8_t* w, size_t soff, size_t zoff, int K, int KB, int n,
-                                                    const void* xrow) {
-  typedef typename Mat<DT>::elem elem;
-  const elem* x = (const elem*)xrow;
-  const int nb = n / kBlockRows, r = n % kBlockRows;
-  float acc = 0.f;
-#pragma unroll 1
-  for (int k = 0; k < K; ++k) {
-    const int kb = k / kBlockCols, c = k % kBlockCols;
-    const size_t block = (size_t)nb * KB + kb;
-    const uint8_t byte = w[block * kBlockBytes + ((c / 8 % 4) * 16 + r) * 16 + c / 32 * 4 + c % 8 / 2];
-    const int q = (int)(c & 1 ? byte >> 4 : byte & 15) - 8;
-    const size_t at = (block * 16 + r) * SG + c / (kBlockCols / SG);
-    const int z = ZP ? (int)((const int8_t*)(w + zoff))[at] : 0;
-    acc = fmaf((float)(q - z) * scale_value<DT>(((const uint16_t*)(w + soff))[at]), (float)x[k], acc);
-  }
-  return acc;
-}
-
-// Eight elements of a row in the operands' order.
-__device__ __forceinline__ u32x4 operand_order(u32x4 v) {
-  return u32x4{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-               __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
-}
-
-template <int DT, int SG, bool ZP, int W, int KPW>
-__global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
-  typedef typename Mat<DT>::elem elem;
-  constexpr int GS = 4 / SG;  // matrix instructions per group
-  typedef typename ScaleVec<SG>::s svec;
-  typedef typename ScaleVec<SG>::z zvec;
-  __shared__ f32x4 red[2][W][64];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int li = lane & 15, g = lane >> 4;
-  const Tiles<16> tiles(a.offsets, a.n, a.T);
-  const int64_t items = (int64_t)tiles.total() * a.NB;
-  const int i0 = (int)(items * blockIdx.x / gridDim.x), i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
-  if (i0 >= i1) return;
-  const int passes = (a.KB + W * KPW - 1) / (W * KPW);  // over the columns (one up to 128 W KPW of them)
-  u32x4 xv[KPW][4], wv[KPW], wn[KPW];
-  svec sv[KPW], sn[KPW];
-  zvec zv[KPW], zn[KPW];
-  int tile = i0 / a.NB, nb = i0 % a.NB;
-  RowTile t = tiles.find(tile), tn = t;
-  const auto block_of = [&](int pass, int u) { return (pass * W + wave) * KPW + u; };
-  const auto load_w = [&](const RowTile& rt, int b, int pass) {
-    if (rt.e < 0) return;
-    const uint8_t* w = a.w + (size_t)rt.e * a.stride;
-#pragma unroll
-    for (int u = 0; u < KPW; ++u) {
-      const int kb = block_of(pass, u);
-      if (kb >= a.KB) break;
-      const size_t block = (size_t)b * a.KB + kb;
-      wn[u] = __builtin_nontemporal_load((const u32x4*)(w + block * kBlockBytes) + lane);
-      sn[u] = ((const svec*)(w + a.soff))[block * 16 + li];
-      if (ZP) zn[u] = ((const zvec*)(w + a.zoff))[block * 16 + li];
-    }
-  };
-  const auto load_x = [&](const RowTile& rt, int pass) {
-    if (rt.e < 0) return;
-    const elem* row = (const elem*)a.x + (int64_t)(rt.r0 + min(li, rt.rows - 1)) * a.ldx + 8 * g;
-#pragma unroll
-    for (int u = 0; u < KPW; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = block_of(pass, u) * kBlockCols + 32 * j;
-        xv[u][j] = u32x4{};
-        if (k < a.K && li < rt.rows) xv[u][j] = *(const u32x4*)(row + k);
-      }
-#pragma unroll
-    for (int u = 0; u < KPW; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xv[u][j] = operand_order(xv[u][j]);
-  };
-  f32x4 acc;
-  const auto multiply = [&](int u) {
-    v8_t<DT> ones;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ones[i] = (elem)1.0f;
-#pragma unroll
-    for (int s = 0; s < SG; ++s) {
-      f32x4 sum{}, xsum{};
-      const int z = ZP ? (int)(int8_t)((uint32_t)zv[u] >> (8 * s)) : 0;
-#pragma unroll
-      for (int j = s * GS; j < (s + 1) * GS; ++j) {
-        const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, xv[u][j]);
-        if (DT == MOE_T_BF16) xsum = Mat<DT>::mma(xf, ones, xsum);
-        const uint32_t c = wv[u][j];
-        u32x4 b;
-        if constexpr (DT == MOE_T_F16) {
-          half2_t v[4];
-          codes_f16(c, both((_Float16)(float)(-1032 - z)), v);
-          b = u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])};
-        } else {
-          b = u32x4{masked(c, 0x000F000Fu, 0x43004300u),
-                    masked(c >> 4, 0x000F000Fu, 0x43004300u),
-                    masked(c >> 8, 0x000F000Fu, 0x43004300u),
-                    masked(c >> 12, 0x000F000Fu, 0x43004300u)};
-        }
-        sum = Mat<DT>::mma(xf, __builtin_bit_cast(v8_t<DT>, b), sum);
-      }
-      const float f = scale_value<DT>((uint16_t)((uint64_t)sv[u] >> (16 * s)));
-      if constexpr (DT == MOE_T_BF16) {
-        const float off = (float)(-136 - z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = fmaf(off, xsum[i], sum[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, sum[i], acc[i]);
-    }
-  };
-  load_w(t, nb, 0);
-  load_x(t, 0);
-  for (int i = i0; i < i1; ++i) {
-    const int nb_now = nb;
-    acc = f32x4{};
-    for (int pass = 0; pass < passes; ++pass) {
-#pragma unroll
-      for (int u = 0; u < KPW; ++u) {
-        wv[u] = wn[u];
-        sv[u] = sn[u];
-        zv[u] = zn[u];
-      }
-      if (pass + 1 < passes) {
-        load_w(t, nb_now, pass + 1);
-      } else if (i + 1 < i1) {
-        if (++nb == a.NB) {
-          nb = 0;
-          tn = tiles.find(++tile);
-        }
-        load_w(tn, nb, 0);
-      }
-      if (t.e >= 0) {
-#pragma unroll
-        for (int u = 0; u < KPW; ++u)
-          if (block_of(pass, u) < a.KB) multiply(u);
-      }
-      if (passes > 1) load_x(pass + 1 < passes ? t : tn, (pass + 1) % passes);
-    }
-    const int p = i & 1;
-    red[p][wave][lane] = acc;
-    lds_barrier();
-    const int n = nb_now * kBlockRows + li;
-    if (wave == i % W && n < a.N && 4 * g < t.rows) {
-      f32x4 v = red[p][0][lane];
-#pragma unroll 3
-      for (int u = 1; u < W; ++u) v += red[p][u][lane];
-      const int live = min(4, t.rows - 4 * g);
-      const int64_t row = t.r0 + 4 * g;
-      if (DT == MOE_T_BF16 && t.e >= 0) {
-        // the terms 128 + u and 136 + z beside an infinity, or past fp32's range, need
-        // not cancel to the formula's value
-        bool finite = true;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) finite &= fabsf(v[q]) < INFINITY;
-        if (!finite) {
-#pragma unroll 1
-          for (int q = 0; q < live; ++q) {
-            const float o = slow_dot<DT, SG, ZP>(a.w + (size_t)t.e * a.stride, a.soff, a.zoff, a.K, a.KB, n,
-                                                 (const elem*)a.x + (row + q) * a.ldx);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k == q && !(fabsf(v[k]) < INFINITY)) v[k] = o;
-          }
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q >= live) break;
-        float o = v[q];
-        if (a.add) o += (float)((const elem*)a.add)[(row + q) * a.ldadd + n];
-        ((elem*)a.y)[(row + q) * a.ldy + n] = (elem)o;
-      }
-    }
-    if (nb == 0 && i + 1 < i1) {
-      t = tn;
-      if (passes == 1) load_x(t, 0);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Many rows: tiles of BM = 16 MT rows, which pass through two LDS buffers.
-// ---------------------------------------------------------------------------
-constexpr int kTileThreads = 256;
-
-// A workgroup's rows of one step of CS columns (64 or 128), from memory to registers
-// to LDS, 16-byte pieces.  Pieces are swizzled so that an operand's 16 rows cover all
-// banks (a line of 64 banks holds 16 pieces: one row of 128 columns or two of 64).  Rows
-// past the tile repeat its last (their sums are not stored); of the last step's
-// columns those past the width are zeros.
-template <int CS>
-__device__ __forceinline__ int piece_at(int row, int c) {
-  return CS == 128 ? row * 16 + (c ^ (row & 15)) : row * 8 + (c ^ (row >> 1 & 7));
-}
-
-template <int DT, int MT, int CS, bool ORDER>
-struct Stage {
-  static constexpr int PR = CS / 8, RP = kTileThreads / PR;  // pieces per row, rows per pass
-  static constexpr int P = (16 * MT + RP - 1) / RP;
-  struct Pieces {
-    u32x4 v[P];
-  };
-  const char* base;
-  uint32_t at[P];
-  int width, c;
-  __device__ __forceinline__ Stage(const W4Args& a, const RowTile& t, int w) {
-    base = (const char*)a.x + (int64_t)t.r0 * a.ldx * 2;
-    width = w;
-    c = threadIdx.x % PR;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int row = min((int)threadIdx.x / PR + RP * p, t.rows - 1);
-      at[p] = (uint32_t)row * (uint32_t)(a.ldx * 2) + c * 16;
-    }
-  }
-  __device__ __forceinline__ void load(Pieces& v, int c0) const {
-    const char* b = base + (size_t)c0 * 2;
-    const uint32_t back = max(0, c - (min(width - c0, CS) / 8 - 1)) * 16;  // to the last piece of the row
-#pragma unroll
-    for (int p = 0; p < P; ++p) v.v[p] = *(const u32x4*)(b + (at[p] - back));
-  }
-  __device__ __forceinline__ void store(const Pieces& v, u32x4* lds, int c0) const {
-    const bool in = c0 + c * 8 < width;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      u32x4 o = ORDER ? operand_order(v.v[p]) : v.v[p];
-      if (c0 + CS > width) o = in ? o : u32x4{};
-      lds[piece_at<CS>(threadIdx.x / PR + RP * p, c)] = o;
-    }
-  }
-};
-
-// Steps that are loaded ahead: tiles of few rows have little to do between loads, and
-// registers to spare.
-constexpr int steps_ahead(int M) { return M <= 2 ? 3 : M <= 4 ? 2 : 1; }
-
-// Weights rounded to the rows' type as operands.  binary16: the exact code times the
-// scale, a packed product.  bfloat16: (1024 + u) s - (1032 + z) s in one fp32
-// multiply-add, whose result is exact (at most 8 + 9 bits), then rounded.  One scale
-// for all eight.
-template <int DT, bool ZP>
-struct GroupScale;
-template <bool ZP>
-struct GroupScale<MOE_T_F16, ZP> {
-  half2_t s, c;
-  __device__ __forceinline__ void set(uint16_t sv, int z) {
-    s = both(__builtin_bit_cast(_Float16, sv));
-    c = both((_Float16)(float)(-1032 - z));
-  }
-  __device__ __forceinline__ v8_t<MOE_T_F16> weights(uint32_t d) const {
-    half2_t v[4];
-    codes_f16(d, ZP ? c : both((_Float16)-1032.0f), v);
-    return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v[0] * s), bits_of(v[1] * s), bits_of(v[2] * s), bits_of(v[3] * s)});
-  }
-};
-template <bool ZP>
-struct GroupScale<MOE_T_BF16, ZP> {
-  float s, s16, c, c16;
-  __device__ __forceinline__ void set(uint16_t sv, int z) {
-    s = scale_value<MOE_T_BF16>(sv);
-    s16 = s * 0.0625f;
-    c = (float)(-1032 - z) * s;
-    c16 = (float)(-72 - z) * s;
-  }
-  __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
-    half2_t v[4];
-    code_pairs(d, v);
-    return __builtin_bit_cast(v8_t<MOE_T_BF16>, u32x4{pack_bf16(fmaf((float)v[0][0], s, c), fmaf((float)v[0][1], s, c)),
-                                                      pack_bf16(fmaf((float)v[1][0], s16, c16), fmaf((float)v[1][1], s16, c16)),
-                                                      pack_bf16(fmaf((float)v[2][0], s, c), fmaf((float)v[2][1], s, c)),
-                                                      pack_bf16(fmaf((float)v[3][0], s16, c16), fmaf((float)v[3][1], s16, c16))});
-  }
-};
-
-// f(Const<M>) with the smallest M of 1, 2, 4, .., MT groups of 16 that hold `rows`.
-template <int MT, typename F>
-__device__ __forceinline__ void by_height(int rows, F f) {
-  if constexpr (MT > 1) {
-    constexpr int HALF = MT > 4 ? 4 : MT / 2;
-    if (rows <= 16 * HALF) return by_height<HALF>(rows, f);
-  }
-  f(Const<MT>{});
-}
-
-// Four consecutive sums of a row, from column c: to the split's partial sums, or with add, rounded.
-template <int DT>
-__device__ __forceinline__ void put4(const W4Args& a, int width, int split, int64_t row, int c, f32x4 v) {
-  typedef typename Mat<DT>::elem elem;
-  struct alignas(8) E4 {
-    elem e[4];
-  };
-  if (a.part) {
-    *(f32x4*)(a.part + ((int64_t)split * a.T + row) * width + c) = v;
-    return;
-  }
-  if (a.add) {
-    const E4 o = *(const E4*)((const elem*)a.add + row * a.ldadd + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += (float)o.e[i];
-  }
-  E4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o.e[i] = (elem)v[i];
-  *(E4*)((elem*)a.y + row * a.ldy + c) = o;
-}
-
-// Forward: each of four wavefronts takes R row blocks of the matrix, straight from
-// memory into operands, and all rows of the tile.
-template <int DT, int SG, bool ZP, int MT, int R>
-__global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int groups) {
-  constexpr int BM = 16 * MT;
-  typedef typename ScaleVec<SG>::s svec;
-  typedef typename ScaleVec<SG>::z zvec;
-  __shared__ u32x4 sx[2][BM * 16];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int li = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.split;
-  const Place at = place_of(blockIdx.x / a.split, groups, a.offsets);
-  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(at.tile);
-  if (t.rows <= 0) return;
-  const int nb0 = (at.run * 4 + wave) * R;
-  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
-  const int kb0 = (int)((int64_t)a.KB * split / a.split), kb1 = (int)((int64_t)a.KB * (split + 1) / a.split);
-  by_height<MT>(t.rows, [&](auto mt) {
-    constexpr int M = decltype(mt)::value;  // groups of 16 rows that hold rows
-    f32x4 acc[M][R];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int r = 0; r < R; ++r) acc[m][r] = f32x4{};
-    if (t.e >= 0 && kb0 < kb1) {
-      typedef Stage<DT, M, kBlockCols, true> St;
-      constexpr int D = steps_ahead(M);
-      const St st(a, t, a.K);
-      struct Step {
-        typename St::Pieces x;
-        u32x4 w[R];
-        svec s[R];
-        zvec z[R];
-      } step[D];
-      // (steps past the last read it again and go unused: without branches around loads
-      // the waits for them are exact)
-      const auto load = [&](Step& u, int kb) {
-        kb = min(kb, kb1 - 1);
-        st.load(u.x, kb * kBlockCols);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
-          u.w[r] = ((const u32x4*)(w + block * kBlockBytes))[lane];
-          u.s[r] = ((const svec*)(w + a.soff))[block * 16 + li];
-          if (ZP) u.z[r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
-        }
-      };
-#pragma unroll
-      for (int d = 0; d < D; ++d) load(step[d], kb0 + d);
-      st.store(step[0].x, sx[0], kb0 * kBlockCols);
-      lds_barrier();
-      int buf = 0;
-      for (int k0 = kb0; k0 < kb1; k0 += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          const int kb = k0 + d;
-          if (kb >= kb1) break;
-          u32x4 wv[R];
-          svec sv[R];
-          zvec zv[R];
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            wv[r] = step[d].w[r];
-            sv[r] = step[d].s[r];
-            zv[r] = step[d].z[r];
-          }
-          load(step[d], kb + D);
-          const u32x4* x = sx[buf];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            constexpr int GS = 4 / SG;
-            v8_t<DT> wf[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              GroupScale<DT, ZP> s;
-              s.set((uint16_t)((uint64_t)sv[r] >> (16 * (j / GS))), ZP ? (int)(int8_t)((uint32_t)zv[r] >> (8 * (j / GS))) : 0);
-              wf[r] = s.weights(wv[r][j]);
-            }
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-              const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, x[piece_at<kBlockCols>(16 * m + li, 4 * j + g)]);
-#pragma unroll
-              for (int r = 0; r < R; ++r) acc[m][r] = Mat<DT>::mma(wf[r], xf, acc[m][r]);
-            }
-          }
-          buf ^= 1;
-          st.store(step[(d + 1) % D].x, sx[buf], min(kb + 1, kb1 - 1) * kBlockCols);
-          lds_barrier();
-        }
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int row = 16 * m + li, n = (nb0 + r) * kBlockRows + 4 * g;
-        if (row < t.rows && n < a.N) put4<DT>(a, a.N, split, t.r0 + row, n, acc[m][r]);
-      }
-  });
-}
-
-// ---------------------------------------------------------------------------
-// Gradient of the rows: the contraction runs across the matrix' rows.  A step takes
-// 64 of them: the packed blocks pass through LDS as they are, and
-// ds_read_b64_tr_b4 hands lane j of 16 the nibble j of 16 rows' eight bytes, so that
-// a lane holds 16 rows of one column.  The rows' addresses are given in the order
-// that puts neighbouring rows into the operands' halves.  A wavefront takes 64
-// columns (eight bytes of each lane's sixteen) and all rows of the tile.
-// ---------------------------------------------------------------------------
-constexpr int kStepRows = 64;
-constexpr int kGradCols = 256;
-
-// As GroupScale, with a scale for each of the eight.
-template <int DT, bool ZP>
-struct RowScales;
-template <bool ZP>
-struct RowScales<MOE_T_F16, ZP> {
-  half2_t s[4], c[4];
-  // sv: eight scales; cv: eight values -(1032 + z)
-  __device__ __forceinline__ void set(u32x4 sv, u32x4 cv) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i] = as_half2(sv[i]);
-      c[i] = ZP ? as_half2(cv[i]) : both((_Float16)-1032.0f);
-    }
-  }
-  __device__ __forceinline__ v8_t<MOE_T_F16> weights(uint32_t d) const {
-    const half2_t k = both((_Float16)960.0f), sixteenth = both((_Float16)0.0625f);
-    half2_t v[4];
-    code_pairs(d, v);
-    v[0] = (v[0] + c[0]) * s[0];
-    v[1] = (v[1] * sixteenth + (c[1] + k)) * s[1];
-    v[2] = (v[2] + c[2]) * s[2];
-    v[3] = (v[3] * sixteenth + (c[3] + k)) * s[3];
-    return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])});
-  }
-};
-template <bool ZP>
-struct RowScales<MOE_T_BF16, ZP> {
-  float s[8], c[8];  // of pairs 1 and 3: for 1024 + 16 u
-  // cv: eight values -(8 + z)
-  __device__ __forceinline__ void set(u32x4 sv, u32x4 cv) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool high = i / 2 & 1;
-      const float f = scale_value<MOE_T_BF16>((uint16_t)(sv[i / 2] >> (16 * (i & 1))));
-      c[i] = ((ZP ? scale_value<MOE_T_BF16>((uint16_t)(cv[i / 2] >> (16 * (i & 1)))) : -8.0f) - (high ? 64.0f : 1024.0f)) * f;
-      s[i] = high ? f * 0.0625f : f;
-    }
-  }
-  __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
-    half2_t v[4];
-    code_pairs(d, v);
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = pack_bf16(fmaf((float)v[i][0], s[2 * i], c[2 * i]), fmaf((float)v[i][1], s[2 * i + 1], c[2 * i + 1]));
-    return __builtin_bit_cast(v8_t<MOE_T_BF16>, r);
-  }
-};
-
-template <int DT, int SG, bool ZP, int MT>
-__global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int groups) {
-  constexpr int BM = 16 * MT;
-  constexpr int CB = kGradCols / kBlockCols, SB = kStepRows / kBlockRows;  // blocks of a step: SB x CB
-  constexpr int NS = SB * CB * 16 * SG, SP = (NS + kTileThreads - 1) / kTileThreads;
-  typedef int v2i __attribute__((ext_vector_type(2)));
-  typedef __attribute__((address_space(3))) v2i lds_v2i;
-  __shared__ u32x4 sx[2][BM * 8];
-  __shared__ u32x4 sw[2][SB * CB * 64];
-  __shared__ __attribute__((aligned(16))) uint16_t ss[2][CB * SG][kStepRows], sz[ZP ? 2 : 1][CB * SG][kStepRows];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int li = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.split;
-  const Place at = place_of(blockIdx.x / a.split, groups, a.offsets);
-  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(at.tile);
-  if (t.rows <= 0) return;
-  const int kb0 = at.run * CB;
-  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
-  const int steps = (a.NB + SB - 1) / SB;
-  const int s0 = (int)((int64_t)steps * split / a.split), s1 = (int)((int64_t)steps * (split + 1) / a.split);
-  const int kbi = wave >> 1, jj = wave & 1;
-  // group of this lane's columns among the step's
-  const int cg = kbi * SG + (SG == 4 ? 2 * jj + (li >> 3) : SG == 2 ? jj : 0);
-  const int rho = (li & 8) + ((li & 7) < 4 ? 2 * (li & 7) : 2 * (li & 7) - 7);  // the row whose eight bytes this lane points at
-  by_height<MT>(t.rows, [&](auto mt) {
-    constexpr int M = decltype(mt)::value;
-    f32x4 acc[M][4];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{};
-    if (t.e >= 0 && s0 < s1) {
-      typedef Stage<DT, M, kStepRows, false> St;
-      constexpr int D = steps_ahead(M);
-      const St st(a, t, a.N);
-      struct Step {
-        typename St::Pieces x;
-        u32x4 w[2];
-        uint16_t s[SP];
-        int8_t z[SP];
-      } step[D];
-      // this thread's pieces of a step: blocks past the matrix repeat its last with scale 0
-      const int wi = threadIdx.x & 63, wk = min(kb0 + (int)(threadIdx.x >> 6 & 1), a.KB - 1);
-      const auto load = [&](Step& u, int s) {
-        s = min(s, s1 - 1);
-        st.load(u.x, s * kStepRows);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int rb = min(s * SB + (int)(threadIdx.x >> 7) + 2 * p, a.NB - 1);
-          u.w[p] = ((const u32x4*)(w + ((size_t)rb * a.KB + wk) * kBlockBytes))[wi];
-        }
-#pragma unroll
-        for (int p = 0; p < SP; ++p) {
-          const int i = min((int)threadIdx.x + p * kTileThreads, NS - 1);
-          const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
-          const size_t at = ((size_t)min(rb, a.NB - 1) * a.KB + min(kb, a.KB - 1)) * 16 * SG + i % (16 * SG);
-          u.s[p] = ((const uint16_t*)(w + a.soff))[at];
-          if (ZP) u.z[p] = ((const int8_t*)(w + a.zoff))[at];
-        }
-      };
-      const auto store = [&](const Step& u, int buf, int s) {
-        s = min(s, s1 - 1);
-        st.store(u.x, sx[buf], s * kStepRows);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) sw[buf][threadIdx.x + p * kTileThreads] = u.w[p];
-#pragma unroll
-        for (int p = 0; p < SP; ++p) {
-          const int i = threadIdx.x + p * kTileThreads;
-          if (NS % kTileThreads && i >= NS) break;
-          const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
-          const int row = i / (CB * 16 * SG) * 16 + i / SG % 16, col = i / (16 * SG) % CB * SG + i % SG;
-          ss[buf][col][row] = rb < a.NB && kb < a.KB ? u.s[p] : 0;
-          if (ZP)
-            sz[buf][col][row] = DT == MOE_T_F16 ? __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - u.z[p]))
-                                                : __builtin_bit_cast(uint16_t, (__bf16)(float)(-8 - u.z[p]));
-        }
-      };
-#pragma unroll
-      for (int d = 0; d < D; ++d) load(step[d], s0 + d);
-      store(step[0], 0, s0);
-      lds_barrier();
-      int buf = 0;
-      for (int k0 = s0; k0 < s1; k0 += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          const int s = k0 + d;
-          if (s >= s1) break;
-          load(step[d], s + D);
-          v2i code[4];
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-            code[f] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                (lds_v2i*)((char*)&sw[buf][(g * CB + kbi) * 64 + f * 16 + rho] + 8 * jj));
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {  // rows 16 g + 8 q .. + 7 of the step
-            RowScales<DT, ZP> rs;
-            rs.set(*(const u32x4*)&ss[buf][cg][16 * g + 8 * q], *(const u32x4*)&sz[ZP ? buf : 0][cg][16 * g + 8 * q]);
-            v8_t<DT> wf[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) wf[f] = rs.weights((uint32_t)code[f][q]);
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-              const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, sx[buf][piece_at<kStepRows>(16 * m + li, 2 * g + q)]);
-#pragma unroll
-              for (int f = 0; f < 4; ++f) acc[m][f] = Mat<DT>::mma(wf[f], xf, acc[m][f]);
-            }
-          }
-          buf ^= 1;
-          store(step[(d + 1) % D], buf, s + 1);
-          lds_barrier();
-        }
-      }
-    }
-    // lane's sums 4 g .. + 3 of fragment f: nibbles 4 g .. + 3 of the eight bytes
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int row = 16 * m + li;
-        const int c = (kb0 + kbi) * kBlockCols + 32 * (2 * jj + (g >> 1)) + 8 * f + 4 * (g & 1);
-        if (row < t.rows && c < a.K) put4<DT>(a, a.K, split, t.r0 + row, c, acc[m][f]);
-      }
-  });
-}
 
 // The splits' partial sums added in their order.
 template <int DT>
@@ -882,12 +75,6 @@ __global__ __launch_bounds__(64) void k_w4_pack(PackArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxLd = 1 << 22;
 constexpr int kFewRows = 16;
-constexpr int kCUs = 256;
-
-struct W4Layout {
-  int NB, KB, SG;
-  size_t soff, zoff, stride;
-};
 
 W4Layout w4_layout(const moe_w4_dims_t& d) {
   W4Layout l;
@@ -920,12 +107,6 @@ int check_w4_rows(const moe_w4_dims_t* d, int32_t T) {
 }
 
 bool few_rows(const moe_w4_dims_t& d, int T) { return T <= (int64_t)kFewRows * d.n; }
-
-// Tiles of a call with many rows: MT groups of 16 rows by 64 R weight rows (forward) or
-// 256 columns (gradient), and parts that a tile's sums are split into.
-struct TilePlan {
-  int MT, R, groups, split;
-};
 
 // Measured in us; 6144 x 6144 unless said.  One matrix: the largest tiles that still give
 // nearly two workgroups per CU (8,192 rows of 8192 x 8192: forward 128 x 256 1,033, 64 x
@@ -967,21 +148,6 @@ size_t part_bytes(const moe_w4_dims_t& d, int T, const TilePlan& p, bool grad) {
   return p.split > 1 ? (size_t)p.split * T * (grad ? d.K : d.N) * 4 : 0;
 }
 
-template <typename F>
-void by_format(const moe_w4_dims_t& d, int SG, F f) {
-  const auto zeros = [&](auto dt, auto sg) {
-    if (d.zeros) f(dt, sg, Const<1>{});
-    else f(dt, sg, Const<0>{});
-  };
-  const auto groups = [&](auto dt) {
-    if (SG == 4) zeros(dt, Const<4>{});
-    else if (SG == 2) zeros(dt, Const<2>{});
-    else zeros(dt, Const<1>{});
-  };
-  if (d.dtype == MOE_T_F16) groups(Const<MOE_T_F16>{});
-  else groups(Const<MOE_T_BF16>{});
-}
-
 int check_call(const moe_w4_dims_t* d, const void* packed, const void* x, int64_t ldx, int into, int32_t T,
                const int32_t* offsets, const void* add, int64_t ldadd, const void* y, int64_t ldy, int out) {
   if (bad(packed, 256)) return MOE_E_INVAL;
@@ -992,9 +158,10 @@ int check_call(const moe_w4_dims_t* d, const void* packed, const void* x, int64_
   return ldx > kMaxLd || ldy > kMaxLd || (add && ldadd > kMaxLd) ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
-template <int DT>
-void launch_sum(const W4Args& a, int width, hipStream_t s) {
-  k_w4_sum<DT><<<ceil_div((int64_t)a.T * (width / 4), 256), 256, 0, s>>>(a, width);
+void launch_sum(const W4Args& a, int dtype, int width, hipStream_t s) {
+  const int blocks = ceil_div((int64_t)a.T * (width / 4), 256);
+  if (dtype == MOE_T_F16) k_w4_sum<MOE_T_F16><<<blocks, 256, 0, s>>>(a, width);
+  else k_w4_sum<MOE_T_BF16><<<blocks, 256, 0, s>>>(a, width);
 }
 
 }  // namespace
@@ -1053,18 +220,7 @@ int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, in
   W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, x, ldx, T, offsets, add,
            ldadd, y, ldy, nullptr, 1};
   if (few_rows(*d, T)) {
-    const int64_t items = max_tiles(d->n, T, 16, offsets != nullptr) * l.NB;
-    by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
-      constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
-      constexpr bool ZP = decltype(zp)::value;
-      const auto launch = [&](auto kernel, int W, int per_cu) {
-        kernel<<<(unsigned)std::min<int64_t>(items, kCUs * per_cu), 64 * W, 0, s>>>(a);
-      };
-      if (l.KB <= 4) launch(k_w4_few<DT, SG, ZP, 4, 1>, 4, 6);
-      else if (l.KB <= 8) launch(k_w4_few<DT, SG, ZP, 4, 2>, 4, 5);
-      else if (l.KB <= 16) launch(k_w4_few<DT, SG, ZP, 8, 2>, 8, 2);
-      else launch(k_w4_few<DT, SG, ZP, 16, 3>, 16, 1);
-    });
+    launch_w4_few(a, *d, l, s);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
   }
   const TilePlan p = plan_tiles(*d, T, false);
@@ -1075,17 +231,8 @@ int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, in
     a.part = (float*)ws;
     a.split = p.split;
   }
-  by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
-    constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
-    constexpr bool ZP = decltype(zp)::value;
-    const unsigned blocks =
-        (unsigned)(places(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr), p.groups, offsets != nullptr) * p.split);
-    if (p.MT == 2) k_w4_rows<DT, SG, ZP, 2, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    else if (p.MT == 4) k_w4_rows<DT, SG, ZP, 4, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    else if (p.R == 3) k_w4_rows<DT, SG, ZP, 8, 3><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    else k_w4_rows<DT, SG, ZP, 8, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    if (need) launch_sum<DT>(a, d->N, s);
-  });
+  launch_w4_rows(a, *d, l, p, s);
+  if (need) launch_sum(a, d->dtype, d->N, s);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
@@ -1103,17 +250,8 @@ int moe_w4_backward(const moe_w4_dims_t* d, const void* packed, const void* dy, 
   if (ws_bytes < need) return MOE_E_WORKSPACE;
   const W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, dy, lddy, T, offsets,
                  add, ldadd, dx, lddx, need ? (float*)ws : nullptr, p.split};
-  by_format(*d, l.SG, [&](auto dt, auto sg, auto zp) {
-    constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
-    constexpr bool ZP = decltype(zp)::value;
-    const unsigned blocks =
-        (unsigned)(places(max_tiles(d->n, T, 16 * p.MT, offsets != nullptr), p.groups, offsets != nullptr) * p.split);
-    if (p.MT == 2) k_w4_grad<DT, SG, ZP, 2><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    else if (p.MT == 4) k_w4_grad<DT, SG, ZP, 4><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    else if (p.MT == 6) k_w4_grad<DT, SG, ZP, 6><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    else k_w4_grad<DT, SG, ZP, 8><<<blocks, kTileThreads, 0, s>>>(a, p.groups);
-    if (need) launch_sum<DT>(a, d->K, s);
-  });
+  launch_w4_grad(a, *d, l, p, s);
+  if (need) launch_sum(a, d->dtype, d->K, s);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 

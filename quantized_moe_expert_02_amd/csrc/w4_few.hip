@@ -1,0 +1,213 @@
+// Products of few rows with 4-bit weights (include/moe_w4.h, layout in w4.h).
+#include "w4.h"
+
+namespace moe {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Few rows: an item is 16 rows and one row block of a matrix; the W wavefronts of a
+// workgroup split its columns, KPW column blocks each, and add their sums through LDS.
+// A workgroup takes a run of items and keeps its rows in registers from item to item
+// while the next item's blocks are under way.  The rows are the first operand (index l
+// % 16: the row; rows past the tile are zeros) and a block the second (index l %
+// 16: its row), so that a lane's four sums belong to one weight row and are
+// multiplied by its scale.  binary16 factors are the codes q - z themselves;
+// bfloat16 holds 128 + u exactly, and (136 + z) times the sum of the rows' elements
+// is taken off each group's sum.
+// ---------------------------------------------------------------------------
+// The product of one output element in fp32, term by term as the formula has it.
+template <int DT, int SG, bool ZP>
+__device__ __forceinline__ float slow_dot(const uint8_t* w, size_t soff, size_t zoff, int K, int KB, int n,
+                                                    const void* xrow) {
+  typedef typename Mat<DT>::elem elem;
+  const elem* x = (const elem*)xrow;
+  const int nb = n / kBlockRows, r = n % kBlockRows;
+  float acc = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < K; ++k) {
+    const int kb = k / kBlockCols, c = k % kBlockCols;
+    const size_t block = (size_t)nb * KB + kb;
+    const uint8_t byte = w[block * kBlockBytes + ((c / 8 % 4) * 16 + r) * 16 + c / 32 * 4 + c % 8 / 2];
+    const int q = (int)(c & 1 ? byte >> 4 : byte & 15) - 8;
+    const size_t at = (block * 16 + r) * SG + c / (kBlockCols / SG);
+    const int z = ZP ? (int)((const int8_t*)(w + zoff))[at] : 0;
+    acc = fmaf((float)(q - z) * scale_value<DT>(((const uint16_t*)(w + soff))[at]), (float)x[k], acc);
+  }
+  return acc;
+}
+
+template <int DT, int SG, bool ZP, int W, int KPW>
+__global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
+  typedef typename Mat<DT>::elem elem;
+  constexpr int GS = 4 / SG;  // matrix instructions per group
+  typedef typename ScaleVec<SG>::s svec;
+  typedef typename ScaleVec<SG>::z zvec;
+  __shared__ f32x4 red[2][W][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, g = lane >> 4;
+  const Tiles<16> tiles(a.offsets, a.n, a.T);
+  const int64_t items = (int64_t)tiles.total() * a.NB;
+  const int i0 = (int)(items * blockIdx.x / gridDim.x), i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  if (i0 >= i1) return;
+  const int passes = (a.KB + W * KPW - 1) / (W * KPW);  // over the columns (one up to 128 W KPW of them)
+  u32x4 xv[KPW][4], wv[KPW], wn[KPW];
+  svec sv[KPW], sn[KPW];
+  zvec zv[KPW], zn[KPW];
+  int tile = i0 / a.NB, nb = i0 % a.NB;
+  RowTile t = tiles.find(tile), tn = t;
+  const auto block_of = [&](int pass, int u) { return (pass * W + wave) * KPW + u; };
+  const auto load_w = [&](const RowTile& rt, int b, int pass) {
+    if (rt.e < 0) return;
+    const uint8_t* w = a.w + (size_t)rt.e * a.stride;
+#pragma unroll
+    for (int u = 0; u < KPW; ++u) {
+      const int kb = block_of(pass, u);
+      if (kb >= a.KB) break;
+      const size_t block = (size_t)b * a.KB + kb;
+      wn[u] = __builtin_nontemporal_load((const u32x4*)(w + block * kBlockBytes) + lane);
+      sn[u] = ((const svec*)(w + a.soff))[block * 16 + li];
+      if (ZP) zn[u] = ((const zvec*)(w + a.zoff))[block * 16 + li];
+    }
+  };
+  const auto load_x = [&](const RowTile& rt, int pass) {
+    if (rt.e < 0) return;
+    const elem* row = (const elem*)a.x + (int64_t)(rt.r0 + min(li, rt.rows - 1)) * a.ldx + 8 * g;
+#pragma unroll
+    for (int u = 0; u < KPW; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = block_of(pass, u) * kBlockCols + 32 * j;
+        xv[u][j] = u32x4{};
+        if (k < a.K && li < rt.rows) xv[u][j] = *(const u32x4*)(row + k);
+      }
+#pragma unroll
+    for (int u = 0; u < KPW; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xv[u][j] = operand_order(xv[u][j]);
+  };
+  f32x4 acc;
+  const auto multiply = [&](int u) {
+    v8_t<DT> ones;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ones[i] = (elem)1.0f;
+#pragma unroll
+    for (int s = 0; s < SG; ++s) {
+      f32x4 sum{}, xsum{};
+      const int z = ZP ? (int)(int8_t)((uint32_t)zv[u] >> (8 * s)) : 0;
+#pragma unroll
+      for (int j = s * GS; j < (s + 1) * GS; ++j) {
+        const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, xv[u][j]);
+        if (DT == MOE_T_BF16) xsum = Mat<DT>::mma(xf, ones, xsum);
+        const uint32_t c = wv[u][j];
+        u32x4 b;
+        if constexpr (DT == MOE_T_F16) {
+          half2_t v[4];
+          codes_f16(c, both((_Float16)(float)(-1032 - z)), v);
+          b = u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])};
+        } else {
+          b = u32x4{masked(c, 0x000F000Fu, 0x43004300u),
+                    masked(c >> 4, 0x000F000Fu, 0x43004300u),
+                    masked(c >> 8, 0x000F000Fu, 0x43004300u),
+                    masked(c >> 12, 0x000F000Fu, 0x43004300u)};
+        }
+        sum = Mat<DT>::mma(xf, __builtin_bit_cast(v8_t<DT>, b), sum);
+      }
+      const float f = scale_value<DT>((uint16_t)((uint64_t)sv[u] >> (16 * s)));
+      if constexpr (DT == MOE_T_BF16) {
+        const float off = (float)(-136 - z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = fmaf(off, xsum[i], sum[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, sum[i], acc[i]);
+    }
+  };
+  load_w(t, nb, 0);
+  load_x(t, 0);
+  for (int i = i0; i < i1; ++i) {
+    const int nb_now = nb;
+    acc = f32x4{};
+    for (int pass = 0; pass < passes; ++pass) {
+#pragma unroll
+      for (int u = 0; u < KPW; ++u) {
+        wv[u] = wn[u];
+        sv[u] = sn[u];
+        zv[u] = zn[u];
+      }
+      if (pass + 1 < passes) {
+        load_w(t, nb_now, pass + 1);
+      } else if (i + 1 < i1) {
+        if (++nb == a.NB) {
+          nb = 0;
+          tn = tiles.find(++tile);
+        }
+        load_w(tn, nb, 0);
+      }
+      if (t.e >= 0) {
+#pragma unroll
+        for (int u = 0; u < KPW; ++u)
+          if (block_of(pass, u) < a.KB) multiply(u);
+      }
+      if (passes > 1) load_x(pass + 1 < passes ? t : tn, (pass + 1) % passes);
+    }
+    const int p = i & 1;
+    red[p][wave][lane] = acc;
+    lds_barrier();
+    const int n = nb_now * kBlockRows + li;
+    if (wave == i % W && n < a.N && 4 * g < t.rows) {
+      f32x4 v = red[p][0][lane];
+#pragma unroll 3
+      for (int u = 1; u < W; ++u) v += red[p][u][lane];
+      const int live = min(4, t.rows - 4 * g);
+      const int64_t row = t.r0 + 4 * g;
+      if (DT == MOE_T_BF16 && t.e >= 0) {
+        // the terms 128 + u and 136 + z beside an infinity, or past fp32's range, need
+        // not cancel to the formula's value
+        bool finite = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) finite &= fabsf(v[q]) < INFINITY;
+        if (!finite) {
+#pragma unroll 1
+          for (int q = 0; q < live; ++q) {
+            const float o = slow_dot<DT, SG, ZP>(a.w + (size_t)t.e * a.stride, a.soff, a.zoff, a.K, a.KB, n,
+                                                 (const elem*)a.x + (row + q) * a.ldx);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k == q && !(fabsf(v[k]) < INFINITY)) v[k] = o;
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q >= live) break;
+        float o = v[q];
+        if (a.add) o += (float)((const elem*)a.add)[(row + q) * a.ldadd + n];
+        ((elem*)a.y)[(row + q) * a.ldy + n] = (elem)o;
+      }
+    }
+    if (nb == 0 && i + 1 < i1) {
+      t = tn;
+      if (passes == 1) load_x(t, 0);
+    }
+  }
+}
+
+}  // namespace
+
+void launch_w4_few(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, hipStream_t s) {
+  const int64_t items = max_tiles(d.n, a.T, 16, a.offsets != nullptr) * l.NB;
+  by_format(d, l.SG, [&](auto dt, auto sg, auto zp) {
+    constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
+    constexpr bool ZP = decltype(zp)::value;
+    const auto launch = [&](auto kernel, int W, int per_cu) {
+      kernel<<<(unsigned)std::min<int64_t>(items, kCUs * per_cu), 64 * W, 0, s>>>(a);
+    };
+    if (l.KB <= 4) launch(k_w4_few<DT, SG, ZP, 4, 1>, 4, 6);
+    else if (l.KB <= 8) launch(k_w4_few<DT, SG, ZP, 4, 2>, 4, 5);
+    else if (l.KB <= 16) launch(k_w4_few<DT, SG, ZP, 8, 2>, 8, 2);
+    else launch(k_w4_few<DT, SG, ZP, 16, 3>, 16, 1);
+  });
+}
+
+}  // namespace moe

@@ -1,0 +1,126 @@
+// Products of many rows with 4-bit weights (include/moe_w4.h, layout in w4.h).
+#include "w4.h"
+
+namespace moe {
+
+namespace {
+
+// Forward: each of four wavefronts takes R row blocks of the matrix, straight from
+// memory into operands, and all rows of the tile.
+template <int DT, int SG, bool ZP, int MT, int R>
+__global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int groups) {
+  constexpr int BM = 16 * MT;
+  typedef typename ScaleVec<SG>::s svec;
+  typedef typename ScaleVec<SG>::z zvec;
+  __shared__ u32x4 sx[2][BM * 16];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x % a.split;
+  const Place at = place_of(blockIdx.x / a.split, groups, a.offsets);
+  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(at.tile);
+  if (t.rows <= 0) return;
+  const int nb0 = (at.run * 4 + wave) * R;
+  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
+  const int kb0 = (int)((int64_t)a.KB * split / a.split), kb1 = (int)((int64_t)a.KB * (split + 1) / a.split);
+  by_height<MT, R == 3>(t.rows, [&](auto mt) {
+    constexpr int M = decltype(mt)::value;  // groups of 16 rows that hold rows
+    f32x4 acc[M][R];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[m][r] = f32x4{};
+    if (t.e >= 0 && kb0 < kb1) {
+      typedef Stage<DT, M, kBlockCols, true> St;
+      constexpr int D = steps_ahead(M);
+      const St st(a, t, a.K);
+      struct Step {
+        typename St::Pieces x;
+        u32x4 w[R];
+        svec s[R];
+        zvec z[R];
+      } step[D];
+      // (steps past the last read it again and go unused: without branches around loads
+      // the waits for them are exact)
+      const auto load = [&](Step& u, int kb) {
+        kb = min(kb, kb1 - 1);
+        st.load(u.x, kb * kBlockCols);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
+          u.w[r] = ((const u32x4*)(w + block * kBlockBytes))[lane];
+          u.s[r] = ((const svec*)(w + a.soff))[block * 16 + li];
+          if (ZP) u.z[r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
+        }
+      };
+#pragma unroll
+      for (int d = 0; d < D; ++d) load(step[d], kb0 + d);
+      st.store(step[0].x, sx[0], kb0 * kBlockCols);
+      lds_barrier();
+      int buf = 0;
+      for (int k0 = kb0; k0 < kb1; k0 += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const int kb = k0 + d;
+          if (kb >= kb1) break;
+          u32x4 wv[R];
+          svec sv[R];
+          zvec zv[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            wv[r] = step[d].w[r];
+            sv[r] = step[d].s[r];
+            zv[r] = step[d].z[r];
+          }
+          load(step[d], kb + D);
+          const u32x4* x = sx[buf];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            constexpr int GS = 4 / SG;
+            v8_t<DT> wf[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              GroupScale<DT, ZP> s;
+              s.set((uint16_t)((uint64_t)sv[r] >> (16 * (j / GS))), ZP ? (int)(int8_t)((uint32_t)zv[r] >> (8 * (j / GS))) : 0);
+              wf[r] = s.weights(wv[r][j]);
+            }
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+              const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, x[piece_at<kBlockCols>(16 * m + li, 4 * j + g)]);
+#pragma unroll
+              for (int r = 0; r < R; ++r) acc[m][r] = Mat<DT>::mma(wf[r], xf, acc[m][r]);
+            }
+          }
+          buf ^= 1;
+          st.store(step[(d + 1) % D].x, sx[buf], min(kb + 1, kb1 - 1) * kBlockCols);
+          lds_barrier();
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int row = 16 * m + li, n = (nb0 + r) * kBlockRows + 4 * g;
+        if (row < t.rows && n < a.N) put4<DT>(a, a.N, split, t.r0 + row, n, acc[m][r]);
+      }
+  });
+}
+
+}  // namespace
+
+void launch_w4_rows(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, const TilePlan& p, hipStream_t s) {
+  by_format(d, l.SG, [&](auto dt, auto sg, auto zp) {
+    constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
+    constexpr bool ZP = decltype(zp)::value;
+    const auto launch = [&](auto kernel) {
+      const int64_t tiles = max_tiles(d.n, a.T, 16 * p.MT, a.offsets != nullptr);
+      kernel<<<(unsigned)(places(tiles, p.groups, a.offsets != nullptr) * p.split), kTileThreads, 0, s>>>(a, p.groups);
+    };
+    if (p.MT == 2) launch(k_w4_rows<DT, SG, ZP, 2, 4>);
+    else if (p.MT == 4) launch(k_w4_rows<DT, SG, ZP, 4, 4>);
+    else if (p.R == 3) launch(k_w4_rows<DT, SG, ZP, 8, 3>);
+    else launch(k_w4_rows<DT, SG, ZP, 8, 4>);
+  });
+}
+
+}  // namespace moe
