@@ -11,9 +11,8 @@
 // Scales (and zero points) follow, [row block][column block][16 rows][SG], with SG =
 // 4, 2 or 1 groups per 128 columns (wider groups are repeated in every block).
 //
-// Masking a dword with 0x000F000F leaves the codes of columns p and p + 4 in the
-// two halves: operands hold eight columns in the order 0 4 1 5 2 6 3 7, and the
-// rows' operands are put in that order too.
+// Masking a dword with 0x000F000F leaves the codes of two neighbouring columns in its
+// halves: what a 16-bit operand holds, but for the number format.
 #pragma once
 
 #include <algorithm>
@@ -207,12 +206,6 @@ struct ScaleVec<4> {
   typedef uint32_t z;
 };
 
-// Eight elements of a row in the operands' order.
-__device__ __forceinline__ u32x4 operand_order(u32x4 v) {
-  return u32x4{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-               __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
-}
-
 // ---------------------------------------------------------------------------
 // Many rows: tiles of BM = 16 MT rows, which pass through two LDS buffers.
 // ---------------------------------------------------------------------------
@@ -228,7 +221,7 @@ __device__ __forceinline__ int piece_at(int row, int c) {
   return CS == 128 ? row * 16 + (c ^ (row & 15)) : row * 8 + (c ^ (row >> 1 & 7));
 }
 
-template <int DT, int MT, int CS, bool ORDER>
+template <int DT, int MT, int CS>
 struct Stage {
   static constexpr int PR = CS / 8, RP = kTileThreads / PR;  // pieces per row, rows per pass
   static constexpr int P = (16 * MT + RP - 1) / RP;
@@ -248,19 +241,21 @@ struct Stage {
       at[p] = (uint32_t)row * (uint32_t)(a.ldx * 2) + c * 16;
     }
   }
+  // pieces P0 .. P1 - 1
+  template <int P0 = 0, int P1 = P>
   __device__ __forceinline__ void load(Pieces& v, int c0) const {
     const char* b = base + (size_t)c0 * 2;
     const uint32_t back = max(0, c - (min(width - c0, CS) / 8 - 1)) * 16;  // to the last piece of the row
 #pragma unroll
-    for (int p = 0; p < P; ++p) v.v[p] = *(const u32x4*)(b + (at[p] - back));
+    for (int p = P0; p < P1; ++p) v.v[p] = *(const u32x4*)(b + (at[p] - back));
   }
+  template <int P0 = 0, int P1 = P>
   __device__ __forceinline__ void store(const Pieces& v, u32x4* lds, int c0) const {
-    const bool in = c0 + c * 8 < width;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      u32x4 o = ORDER ? operand_order(v.v[p]) : v.v[p];
-      if (c0 + CS > width) o = in ? o : u32x4{};
-      lds[piece_at<CS>(threadIdx.x / PR + RP * p, c)] = o;
+    for (int p = P0; p < P1; ++p) lds[piece_at<CS>(threadIdx.x / PR + RP * p, c)] = v.v[p];
+    if (c0 + CS > width && c0 + c * 8 >= width) {
+#pragma unroll
+      for (int p = P0; p < P1; ++p) lds[piece_at<CS>(threadIdx.x / PR + RP * p, c)] = u32x4{};
     }
   }
 };

@@ -31,6 +31,20 @@ struct PackArgs {
   int8_t* zeros;
 };
 
+// Nibbles 0 .. 7 to 0 2 4 6 1 3 5 7 (even columns to the low half), and back.
+__device__ __forceinline__ uint32_t to_halves(uint32_t v) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o |= (v >> (4 * i) & 15) << (4 * (i / 2 + (i & 1) * 4));
+  return o;
+}
+__device__ __forceinline__ uint32_t from_halves(uint32_t v) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o |= (v >> (4 * (i / 2 + (i & 1) * 4)) & 15) << (4 * i);
+  return o;
+}
+
 // One workgroup per block and matrix.
 template <bool PACK>
 __global__ __launch_bounds__(64) void k_w4_pack(PackArgs a) {
@@ -49,8 +63,8 @@ __global__ __launch_bounds__(64) void k_w4_pack(PackArgs a) {
     if (!in || c >= a.K) continue;
     // (K is a multiple of 32: a dword of canonical codes is aligned)
     uint32_t* at = (uint32_t*)(a.q + (r * a.K + c) / 2);
-    if (PACK) d[j] = *at ^ 0x88888888u;
-    else *at = d[j] ^ 0x88888888u;
+    if (PACK) d[j] = to_halves(*at ^ 0x88888888u);
+    else *at = from_halves(d[j]) ^ 0x88888888u;
   }
   if (PACK) *mine = d;
   const int width = kBlockCols / a.SG, groups = a.K / a.group;
@@ -108,15 +122,15 @@ int check_w4_rows(const moe_w4_dims_t* d, int32_t T) {
 
 bool few_rows(const moe_w4_dims_t& d, int T) { return T <= (int64_t)kFewRows * d.n; }
 
-// Measured in us; 6144 x 6144 unless said.  One matrix: the largest tiles that still give
-// nearly two workgroups per CU (8,192 rows of 8192 x 8192: forward 128 x 256 1,033, 64 x
-// 256 1,223, gradient 128 rows 1,112, 96 1,161, 64 1,290; 2,048 rows: forward 128 x 256 185
-// (384 workgroups), 128 x 192 163 (512), gradient 128 rows 203, 96 183), else 64 rows
-// (2,048 rows of 2048 x 6144: 128 x 256 115, 64 x 256 69).  Experts: 128 (gradient 96) rows
-// only where they have that many on average (256 experts, 2048 x 1024, of 128 rows 180,
-// in tiles of 64 238; 16,384 rows by Zipf's law 167 and 153; their gradient 88 and 89).
-// The sums are split while all workgroups are resident at once (64 rows: 4 parts 19.7, 8
-// 13.8, 12 17.1, with 24 tiles).
+// Measured in us.  One matrix: tiles of 128 rows where they give nearly two workgroups
+// per CU, else 64 (6144 x 6144, 2,048 rows: forward 128 x 192 147, 64 x 256 186; 8,192 rows,
+// gradient 128 rows 550, 64 642; 2,048 rows of 2048 x 6144: forward 64 x 256 68, 128 x 192
+// 96, gradient 64 rows 62, 128 66), and 32 for up to 32 rows.  Experts: forward 96 x
+// 256 (256 experts, 2048 x 1024, 15,565 rows by Zipf's law: 135, 64 x 256 138, 128 x 192 206;
+// 64 experts, 6144 x 2048, 16,384 rows: 463, 532, 513); gradient 64 rows, or 128 where they
+// have nearly that many on average (the same: 87 and 107; 530 and 472).
+// The sums are split while all workgroups are resident at once (6144 x 6144, 64 rows: 4
+// parts 19.7, 8 13.8, 12 17.1, with 24 tiles).
 constexpr int kTwoPerCU = 460, kOnePerCU = 256, kStepsPerPart = 3;
 
 TilePlan plan_tiles(const moe_w4_dims_t& d, int T, bool grad) {
@@ -126,17 +140,15 @@ TilePlan plan_tiles(const moe_w4_dims_t& d, int T, bool grad) {
     return (int64_t)ceil_div(T, 16 * MT) * (grad ? ceil_div(d.K, kGradCols) : ceil_div(d.N, 64 * R));
   };
   p.R = 4;
-  if (avg <= 32) {
+  if (d.n > 1) {
+    p.MT = !grad ? 6 : avg <= 96 ? 4 : 8;
+  } else if (T <= 32) {
     p.MT = 2;
-  } else if (d.n > 1) {
-    p.MT = avg <= 96 ? 4 : grad ? 6 : 8;
-  } else if (blocks(8, 4) >= kTwoPerCU) {
+  } else if (blocks(8, 3) >= kTwoPerCU) {
     p.MT = 8;
-  } else if (grad) {
-    p.MT = blocks(6, 4) >= kTwoPerCU ? 6 : 4;
+    p.R = 3;
   } else {
-    p.R = blocks(8, 3) >= kTwoPerCU ? 3 : 4;
-    p.MT = p.R == 3 ? 8 : 4;
+    p.MT = 4;
   }
   p.groups = grad ? ceil_div(d.K, kGradCols) : ceil_div(d.N, 64 * p.R);
   const int steps = grad ? ceil_div(d.N, kStepRows) : ceil_div(d.K, kBlockCols);

@@ -28,8 +28,9 @@ __device__ __forceinline__ float slow_dot(const uint8_t* w, size_t soff, size_t 
   for (int k = 0; k < K; ++k) {
     const int kb = k / kBlockCols, c = k % kBlockCols;
     const size_t block = (size_t)nb * KB + kb;
-    const uint8_t byte = w[block * kBlockBytes + ((c / 8 % 4) * 16 + r) * 16 + c / 32 * 4 + c % 8 / 2];
-    const int q = (int)(c & 1 ? byte >> 4 : byte & 15) - 8;
+    const int nibble = c % 8 / 2 + (c & 1) * 4;
+    const uint8_t byte = w[block * kBlockBytes + ((c / 8 % 4) * 16 + r) * 16 + c / 32 * 4 + nibble / 2];
+    const int q = (int)(nibble & 1 ? byte >> 4 : byte & 15) - 8;
     const size_t at = (block * 16 + r) * SG + c / (kBlockCols / SG);
     const int z = ZP ? (int)((const int8_t*)(w + zoff))[at] : 0;
     acc = fmaf((float)(q - z) * scale_value<DT>(((const uint16_t*)(w + soff))[at]), (float)x[k], acc);
@@ -81,10 +82,12 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
         xv[u][j] = u32x4{};
         if (k < a.K && li < rt.rows) xv[u][j] = *(const u32x4*)(row + k);
       }
+    // (the rows are awaited here: in the loop, where it is not known whether they are still
+    // under way, the wait would be for the blocks requested after them too)
 #pragma unroll
     for (int u = 0; u < KPW; ++u)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xv[u][j] = operand_order(xv[u][j]);
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(xv[u][j]));
   };
   f32x4 acc;
   const auto multiply = [&](int u) {

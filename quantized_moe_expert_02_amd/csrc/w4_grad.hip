@@ -62,6 +62,8 @@ struct RowScales<MOE_T_BF16, ZP> {
   }
 };
 
+__device__ __forceinline__ uint32_t bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+
 template <int DT, int SG, bool ZP, int MT>
 __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int groups) {
   constexpr int BM = 16 * MT;
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
 #pragma unroll
       for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{};
     if (t.e >= 0 && s0 < s1) {
-      typedef Stage<DT, M, kStepRows, false> St;
+      typedef Stage<DT, M, kStepRows> St;
       constexpr int D = steps_ahead(M);
       const St st(a, t, a.N);
       struct Step {
@@ -150,6 +152,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
           const int s = k0 + d;
           if (s >= s1) break;
           load(step[d], s + D);
+          __builtin_amdgcn_sched_barrier(0);  // (or the loads sink to where their results are used)
           v2i code[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f)
@@ -175,14 +178,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
         }
       }
     }
-    // lane's sums 4 g .. + 3 of fragment f: nibbles 4 g .. + 3 of the eight bytes
+    // A lane's sums of fragment f belong to nibbles 4 g .. + 3 of the eight bytes: the even
+    // columns of eight where g is even, else the odd ones.  Two exchanges between
+    // neighbouring g give each four columns in a row.
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
+        const auto lo = __builtin_amdgcn_permlane16_swap(bits(acc[m][f][0]), bits(acc[m][f][2]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(bits(acc[m][f][1]), bits(acc[m][f][3]), false, false);
+        const f32x4 v = __builtin_bit_cast(f32x4, u32x4{lo[0], lo[1], hi[0], hi[1]});
         const int row = 16 * m + li;
         const int c = (kb0 + kbi) * kBlockCols + 32 * (2 * jj + (g >> 1)) + 8 * f + 4 * (g & 1);
-        if (row < t.rows && c < a.K) put4<DT>(a, a.K, split, t.r0 + row, c, acc[m][f]);
+        if (row < t.rows && c < a.K) put4<DT>(a, a.K, split, t.r0 + row, c, v);
       }
   });
 }
@@ -199,7 +207,6 @@ void launch_w4_grad(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, 
     };
     if (p.MT == 2) launch(k_w4_grad<DT, SG, ZP, 2>);
     else if (p.MT == 4) launch(k_w4_grad<DT, SG, ZP, 4>);
-    else if (p.MT == 6) launch(k_w4_grad<DT, SG, ZP, 6>);
     else launch(k_w4_grad<DT, SG, ZP, 8>);
   });
 }

@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[m][r] = f32x4{};
     if (t.e >= 0 && kb0 < kb1) {
-      typedef Stage<DT, M, kBlockCols, true> St;
+      typedef Stage<DT, M, kBlockCols> St;
       constexpr int D = steps_ahead(M);
       const St st(a, t, a.K);
       struct Step {
@@ -41,9 +41,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
       } step[D];
       // (steps past the last read it again and go unused: without branches around loads
       // the waits for them are exact)
-      const auto load = [&](Step& u, int kb) {
-        kb = min(kb, kb1 - 1);
-        st.load(u.x, kb * kBlockCols);
+      const auto load_w = [&](Step& u, int kb) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const size_t block = (size_t)min(nb0 + r, a.NB - 1) * a.KB + kb;
@@ -52,8 +50,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
           if (ZP) u.z[r] = ((const zvec*)(w + a.zoff))[block * 16 + li];
         }
       };
+      const auto last = [&](int kb) { return min(kb, kb1 - 1); };
+      // with a single step ahead its rows come in two parts, one after the other through
+      // the same registers
+      constexpr bool PARTS = D == 1;
+      constexpr int PH = PARTS ? St::P / 2 : St::P;
 #pragma unroll
-      for (int d = 0; d < D; ++d) load(step[d], kb0 + d);
+      for (int d = 0; d < D; ++d) {
+        st.load(step[d].x, last(kb0 + d) * kBlockCols);
+        load_w(step[d], last(kb0 + d));
+      }
       st.store(step[0].x, sx[0], kb0 * kBlockCols);
       lds_barrier();
       int buf = 0;
@@ -71,11 +77,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
             sv[r] = step[d].s[r];
             zv[r] = step[d].z[r];
           }
-          load(step[d], kb + D);
+          const int c_far = last(kb + D) * kBlockCols, c_next = last(kb + 1) * kBlockCols;
+          st.template load<0, PH>(step[d].x, c_far);
+          load_w(step[d], last(kb + D));
+          __builtin_amdgcn_sched_barrier(0);  // (or the loads sink to where their results are used)
           const u32x4* x = sx[buf];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             constexpr int GS = 4 / SG;
+            if (PARTS && j == 2) {
+              st.template store<0, PH>(step[0].x, sx[buf ^ 1], c_next);
+              st.template load<PH, St::P>(step[0].x, c_far);
+              __builtin_amdgcn_sched_barrier(0);
+            }
             v8_t<DT> wf[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -90,8 +104,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
               for (int r = 0; r < R; ++r) acc[m][r] = Mat<DT>::mma(wf[r], xf, acc[m][r]);
             }
           }
+          if (PARTS) st.template store<PH, St::P>(step[0].x, sx[buf ^ 1], c_next);
+          else st.store(step[(d + 1) % D].x, sx[buf ^ 1], c_next);
           buf ^= 1;
-          st.store(step[(d + 1) % D].x, sx[buf], min(kb + 1, kb1 - 1) * kBlockCols);
           lds_barrier();
         }
       }
@@ -118,8 +133,8 @@ void launch_w4_rows(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, 
     };
     if (p.MT == 2) launch(k_w4_rows<DT, SG, ZP, 2, 4>);
     else if (p.MT == 4) launch(k_w4_rows<DT, SG, ZP, 4, 4>);
-    else if (p.R == 3) launch(k_w4_rows<DT, SG, ZP, 8, 3>);
-    else launch(k_w4_rows<DT, SG, ZP, 8, 4>);
+    else if (p.MT == 6) launch(k_w4_rows<DT, SG, ZP, 6, 4>);
+    else launch(k_w4_rows<DT, SG, ZP, 8, 3>);
   });
 }
 
