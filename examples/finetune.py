@@ -3,11 +3,12 @@ adapter per request.
 
 Trained: the router, and a low-rank adapter on every expert's down projection.
 A step runs the router (moe_route), lays the tokens out by expert
-(moe_dispatch), adds the adapters to the frozen experts' outputs
+(moe_dispatch), multiplies them by the frozen experts' 4-bit matrices
+(moe_w4_forward), adds the adapters to the experts' outputs
 (moe_adapter_forward), combines them (moe_combine), and goes back through the
-gradients of all four.  The frozen experts' own products are plain torch
-matmuls on dequantised weights, because the layer's 4-bit kernels have no
-backward pass; torch.autograd strings the pieces together.
+gradients of all five; torch.autograd strings the pieces together.  The layer is
+first tuned towards outputs of its own width, then, under a frozen 4-bit output
+head, towards a teacher's top logits (moe_distill_forward).
 
   python examples/finetune.py [--steps 30] [--tokens 512]
 """
@@ -78,6 +79,35 @@ class Combine(torch.autograd.Function):
         return do, dw, dy if ctx.needs_input_grad[2] else None, None, None
 
 
+class Product(torch.autograd.Function):
+    """Rows times the frozen 4-bit matrix of their group (one matrix: of all rows)."""
+
+    @staticmethod
+    def forward(ctx, x, w, offsets=None):
+        ctx.w, ctx.offsets = w, offsets
+        return moe.moe_w4_forward(x, w, offsets=offsets)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return moe.moe_w4_backward(dy.contiguous(), ctx.w, offsets=ctx.offsets), None, None
+
+
+class Distillation(torch.autograd.Function):
+    """Every row's divergence from a teacher's top logits."""
+
+    @staticmethod
+    def forward(ctx, logits, ids, teacher, temperature):
+        loss, stats = moe.moe_distill_forward(logits, ids, teacher, temperature)
+        ctx.save_for_backward(logits, ids, teacher, stats)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        logits, ids, teacher, stats = ctx.saved_tensors
+        return moe.moe_distill_backward(logits, ids, teacher, stats, dloss.contiguous(), ctx.temperature), None, None, None
+
+
 def dequantise(dims, packed, dtype=torch.float16):
     """The three matrices of one packed int4 expert."""
     qg, sg, qu, su, qd, sd, _ = moe.moe_unpack(dims, packed)
@@ -90,8 +120,17 @@ def dequantise(dims, packed, dtype=torch.float16):
     return matrix(qg, sg), matrix(qu, su), matrix(qd, sd)
 
 
-def swiglu(x, w_gate, w_up):
-    return F.silu(x @ w_gate.t()) * (x @ w_up.t())
+def products(dims, packed):
+    """(gate and up, down) of packed int4 experts [n], as moe_w4_forward takes them: one scale per row."""
+    parts = [moe.moe_unpack(dims, p) for p in packed]
+    qg, sg, qu, su, qd, sd = (torch.stack([p[i] for p in parts]) for i in range(6))
+    gate_up = moe.moe_w4_pack(torch.cat((qg, qu), 1), torch.cat((sg, su), 1)[:, :, None].contiguous())
+    return gate_up, moe.moe_w4_pack(qd, sd[:, :, None].contiguous())
+
+
+def swiglu(x, gate_up, offsets=None):
+    gate, up = Product.apply(x, gate_up, offsets).chunk(2, dim=1)
+    return F.silu(gate) * up
 
 
 class Layer:
@@ -101,7 +140,8 @@ class Layer:
         self.dims, self.packed = dims, moe.PackedLayer.from_layer(synth.make_layer(dims, seed), device=device)
         if self.packed.router_b is None:
             self.packed.router_b = torch.zeros(dims.n_experts, device=device)
-        self.frozen = [dequantise(dims, p) for p in self.packed.packed]
+        self.experts = products(dims, self.packed.packed[:dims.n_experts])
+        self.shared = products(dims, self.packed.packed[dims.n_experts:]) if dims.has_shared else None
         g = torch.Generator().manual_seed(1)
         shape = (dims.n_experts, rank, dims.inter)
         self.a = (torch.randn(shape, generator=g) / dims.inter ** 0.5).to(device)
@@ -110,23 +150,25 @@ class Layer:
         for p in self.trained():
             p.requires_grad_()
 
+    @property
+    def frozen(self):
+        """The frozen matrices, expert by expert (the shared one last), dequantised."""
+        return [dequantise(self.dims, p) for p in self.packed.packed]
+
     def trained(self):
         return [self.packed.router_w, self.packed.router_b, self.a, self.b]
 
     def forward(self, x):
         """y [T][hidden] of x [T][hidden], with gradients."""
         xs, topk_w, offsets, pairs, pos, idx = RouteDispatch.apply(x, self.packed.router_w, self.packed.router_b, self.packed)
-        ends = offsets.tolist()
-        act = [swiglu(xs[r0:r1], *self.frozen[e][:2]) for e, (r0, r1) in enumerate(zip(ends, ends[1:]))]
-        base = [h @ self.frozen[e][2].t() for e, h in enumerate(act)]
-        left = xs.shape[0] - ends[-1]  # rows past the groups: slots that top-p dropped
-        act, base = (torch.cat(v + [v[0].new_zeros((left, v[0].shape[1]))]) for v in (act, base))
+        act = swiglu(xs, self.experts[0], offsets)
+        base = Product.apply(act, self.experts[1], offsets)  # (rows past the groups, of slots that top-p dropped: zeros)
         ids = torch.where(pairs < 0, -1, idx.reshape(-1)[pairs.clamp(min=0).long()])
         rows = torch.arange(xs.shape[0], dtype=torch.int32, device=x.device)  # they are in the adapters' order already
         o = Adapters.apply(act, self.a, self.b, base, ids, self.scale, offsets, rows)
         shared = None
         if self.dims.has_shared:
-            shared = swiglu(x, *self.frozen[-1][:2]) @ self.frozen[-1][2].t()
+            shared = Product.apply(swiglu(x, self.shared[0]), self.shared[1])
         return Combine.apply(o, topk_w, shared, pairs, pos)
 
 
@@ -139,6 +181,21 @@ def train(layer, x, target, steps, lr=(1e-4, 5e-4)):
         optimiser.zero_grad()
         loss = (layer.forward(x).float() - target).square().sum() / target.square().sum()
         (loss * 1024).backward()  # (scaled, which Adam does not see, to keep the 16-bit gradients in range)
+        optimiser.step()
+        losses.append(loss.detach())
+    return torch.stack(losses).tolist()
+
+
+def distil(layer, head, x, ids, teacher, steps, temperature=2.0, lr=(1e-4, 5e-4)):
+    """Adam on the mean divergence of the logits head(layer(x)) (x added as the residual)
+    from a teacher's top logits `teacher` at `ids`: the losses before each step."""
+    groups = [dict(params=p, lr=r) for p, r in zip((layer.trained()[:2], layer.trained()[2:]), lr)]
+    losses, optimiser = [], torch.optim.Adam(groups)
+    for _ in range(steps):
+        optimiser.zero_grad()
+        logits = Product.apply(x + layer.forward(x), head)
+        loss = Distillation.apply(logits, ids, teacher, temperature).mean()
+        (loss * 1024).backward()
         optimiser.step()
         losses.append(loss.detach())
     return torch.stack(losses).tolist()
@@ -166,6 +223,16 @@ def main():
         target = y + 0.3 * y @ turn / dims.hidden ** 0.5
     losses = train(layer, x, target, args.steps)
     print(f"loss {losses[0]:.3e} -> {losses[-1]:.3e} in {args.steps} steps of {args.tokens} tokens")
+
+    vocab, k = 1024, 16  # a 4-bit head with a scale for every 64 columns, and a teacher whose layer is turned as above
+    g = torch.Generator().manual_seed(4)
+    q = torch.randint(0, 256, (vocab, dims.hidden // 2), generator=g, dtype=torch.uint8).to("cuda")
+    scales = (torch.rand((vocab, dims.hidden // 64), generator=g) * 0.04 + 0.02).half().to("cuda")
+    head = moe.moe_w4_pack(q, scales)
+    with torch.no_grad():
+        teacher, ids = torch.topk(moe.moe_w4_forward((x + target).half(), head).float(), k, dim=1)
+    losses = distil(Layer(dims), head, x, ids.int(), teacher, args.steps)
+    print(f"distilled {losses[0]:.3e} -> {losses[-1]:.3e} in {args.steps} steps, {k} of {vocab} logits")
 
     torch.manual_seed(3)
     n, rank = 4, 8  # four requests' adapters of ranks up to 8
