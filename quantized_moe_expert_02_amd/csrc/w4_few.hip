@@ -57,7 +57,7 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
   zvec zv[KPW], zn[KPW];
   int tile = i0 / a.NB, nb = i0 % a.NB;
   RowTile t = tiles.find(tile), tn = t;
-  const auto block_of = [&](int pass, int u) { return (pass * W + wave) * KPW + u; };
+  const auto block_of = [&](int pass, int u) { return (pass * KPW + u) * W + wave; };
   const auto load_w = [&](const RowTile& rt, int b, int pass) {
     if (rt.e < 0) return;
     const uint8_t* w = a.w + (size_t)rt.e * a.stride;
@@ -206,9 +206,16 @@ void launch_w4_few(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, h
     const auto launch = [&](auto kernel, int W, int per_cu) {
       kernel<<<(unsigned)std::min<int64_t>(items, kCUs * per_cu), 64 * W, 0, s>>>(a);
     };
-    if (l.KB <= 4) launch(k_w4_few<DT, SG, ZP, 4, 1>, 4, 6);
+    // Wavefronts and column blocks of each so that W KPW fits the columns, and workgroups as
+    // registers allow (us; 128,000 rows, K 2048, T 1, binary16, groups of 128: 4 x 4 28.2, 8 x 2
+    // 32.9; T 8, bfloat16, groups of 32 with zero points, which need more registers: 53.9 and
+    // 41.6; 24,576 rows, K 2560: 8 x 3 11.7, 16 x 3 14.3; K 5120: 16 x 3 17.7, 8 x 6 19.4;
+    // 60,000 rows, K 512: 2 x 2 7.8, 4 x 1 9.8).
+    if (l.KB <= 4) launch(k_w4_few<DT, SG, ZP, 2, 2>, 2, 8);
     else if (l.KB <= 8) launch(k_w4_few<DT, SG, ZP, 4, 2>, 4, 5);
+    else if (l.KB <= 16 && SG == 1) launch(k_w4_few<DT, SG, ZP, 4, 4>, 4, 3);
     else if (l.KB <= 16) launch(k_w4_few<DT, SG, ZP, 8, 2>, 8, 2);
+    else if (l.KB <= 24) launch(k_w4_few<DT, SG, ZP, 8, 3>, 8, 2);
     else launch(k_w4_few<DT, SG, ZP, 16, 3>, 16, 1);
   });
 }
