@@ -37,7 +37,7 @@ size_t moe_distill_workspace_bytes(int32_t T, int32_t V, int32_t dtype);
 
 /* loss fp32 [T] and stats fp32 [T][2] = (m, l) of logits z [T][V] (dtype; row
  * stride ldz >= V, in elements); ids int32 [T][k] and teacher fp32 [T][k].
- * Supported: 1 <= k <= 1024, 1 <= V <= 2^24, T up to 2^20, tau > 0 and finite, rows
+ * Supported: 1 <= k <= 1024, 1 <= V <= 2^24, T up to 2^20, 2^-64 <= tau <= 2^64, rows
  * and strides up to 2^36 elements of z in all. */
 int moe_distill_forward(const void* z, int32_t dtype, int64_t ldz, int32_t T, int32_t V, const int32_t* ids,
                         const float* teacher, int32_t k, float tau, float* loss, float* stats, void* ws,

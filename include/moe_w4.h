@@ -15,10 +15,10 @@
  * int8.  Sums are fp32 and rounded once.  In forward calls of few rows
  * (moe_w4_few_rows) the codes are exact factors and a group's sum is multiplied by
  * its scale in fp32; otherwise the product (q - z) s is rounded to the rows' type
- * before it is multiplied (binary16: to no finer than 2^-24).  Infinities and NaNs
- * in rows propagate as the formulas say; rows of other experts and rows outside
- * the groups are never read.  A row's values do not depend on the rows beside it
- * where calls have the same T and n.
+ * before it is multiplied (binary16: to no finer than 2^-24).  Scales are finite.
+ * Infinities and NaNs in rows propagate as the formulas say; rows of other experts and
+ * rows outside the groups are never read.  A row's values do not depend on the rows
+ * beside it where calls have the same T and n.
  */
 #ifndef MOE_W4_H
 #define MOE_W4_H
@@ -56,12 +56,12 @@ int moe_w4_unpack(const moe_w4_dims_t* d, const void* packed, void* q, void* sca
 /* 1 if a forward call on T rows takes the path for few rows (see above). */
 int32_t moe_w4_few_rows(const moe_w4_dims_t* d, int32_t T);
 
-/* Bytes of scratch memory that a forward or a backward call on T rows needs
- * (0 for an unsupported shape, and where a call needs none: ws may be NULL then). */
-size_t moe_w4_workspace_bytes(const moe_w4_dims_t* d, int32_t T);
+/* Bytes of scratch memory that a forward (backward == 0) or backward call on T rows
+ * needs (0 for an unsupported shape, and where a call needs none: ws may be NULL then). */
+size_t moe_w4_workspace_bytes(const moe_w4_dims_t* d, int32_t T, int32_t backward);
 
 /* y [T][N] (row stride ldy) = add + W_e x; x [T][K] (row stride ldx); add [T][N]
- * (row stride ldadd) or NULL (it may be y itself).  offsets int32 [n + 1],
+ * (row stride ldadd) or NULL (it may be y itself; x may not).  offsets int32 [n + 1],
  * ascending, as moe_sort gives them (any align), or NULL if n == 1.  Row strides
  * are multiples of 8 up to 2^22; T up to 2^20, and at most 2^35 elements of x
  * or y.  (Offsets are clamped to 0 .. T; where they descend, y is unspecified.) */

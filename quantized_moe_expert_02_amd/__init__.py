@@ -146,7 +146,7 @@ def lib():
         L.moe_w4_unpack.argtypes = [P, P, P, P, P, P]
         L.moe_w4_few_rows.argtypes = [P, i32]
         L.moe_w4_few_rows.restype = i32
-        L.moe_w4_workspace_bytes.argtypes = [P, i32]
+        L.moe_w4_workspace_bytes.argtypes = [P, i32, i32]
         L.moe_w4_workspace_bytes.restype = sz
         L.moe_w4_forward.argtypes = [P, P, P, i64, i32, P, P, i64, P, i64, P, sz, P]
         L.moe_w4_backward.argtypes = [P, P, P, i64, i32, P, P, i64, P, i64, P, sz, P]

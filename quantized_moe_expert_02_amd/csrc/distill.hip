@@ -349,6 +349,7 @@ int check_distill(const void* z, int32_t dtype, int64_t ldz, int32_t T, int32_t 
   const int st = check_shape(T, V, dtype);
   if (st != MOE_OK) return st;
   if (k < 1 || !(tau > 0.0f && tau < INFINITY) || ldz < V) return MOE_E_INVAL;
+  if (tau < 0x1p-64f || tau > 0x1p64f) return MOE_E_UNSUPPORTED;
   if (k > kMaxEntries || ldz > (int64_t)1 << 36 || (int64_t)T * ldz > (int64_t)1 << 36) return MOE_E_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   return bad(z, (unsigned)elem_bytes(dtype)) || bad(ids, 4) || bad(teacher, 4) ? MOE_E_INVAL : MOE_OK;

@@ -215,10 +215,9 @@ int32_t moe_w4_few_rows(const moe_w4_dims_t* d, int32_t T) {
   return check_w4_rows(d, T) == MOE_OK && few_rows(*d, T) ? 1 : 0;
 }
 
-size_t moe_w4_workspace_bytes(const moe_w4_dims_t* d, int32_t T) {
-  if (check_w4_rows(d, T) != MOE_OK || T == 0) return 0;
-  const size_t f = few_rows(*d, T) ? 0 : part_bytes(*d, T, plan_tiles(*d, T, false), false);
-  return std::max(f, part_bytes(*d, T, plan_tiles(*d, T, true), true));
+size_t moe_w4_workspace_bytes(const moe_w4_dims_t* d, int32_t T, int32_t backward) {
+  if (check_w4_rows(d, T) != MOE_OK || T == 0 || (!backward && few_rows(*d, T))) return 0;
+  return part_bytes(*d, T, plan_tiles(*d, T, backward != 0), backward != 0);
 }
 
 int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, int64_t ldx, int32_t T,

@@ -67,7 +67,7 @@ def moe_w4_few_rows(w: W4Weights, T: int) -> bool:
     return bool(lib().moe_w4_few_rows(w.dims, T))
 
 
-def _product(fn, name, x, w, into, width, offsets, add, out, stream):
+def _product(fn, backward, name, x, w, into, width, offsets, add, out, stream):
     _rows_dtype(name, x)
     n, dev, T = w.shape[0], x.device, x.shape[0]
     ldx = _check_rows(name, x, w.dtype, (T, into), dev)
@@ -83,7 +83,7 @@ def _product(fn, name, x, w, into, width, offsets, add, out, stream):
         out = x.new_empty((T, width))
         made.append(out)
     ldy = _check_rows("out", out, w.dtype, (T, width), dev)
-    need = lib().moe_w4_workspace_bytes(w.dims, T)
+    need = lib().moe_w4_workspace_bytes(w.dims, T, backward)
     ws = None
     if need:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -98,10 +98,10 @@ def moe_w4_forward(x: torch.Tensor, w: W4Weights, offsets: Optional[torch.Tensor
     """y[t] = add[t] + W_e @ x[t], x [T][K]; rows offsets[e] .. offsets[e + 1] - 1
     (int32 [n + 1], as moe_dispatch gives them) use matrix e, rows outside every
     group get add[t] or zeros; `add` may be `out`."""
-    return _product(lib().moe_w4_forward, "x", x, w, w.shape[2], w.shape[1], offsets, add, out, stream)
+    return _product(lib().moe_w4_forward, 0, "x", x, w, w.shape[2], w.shape[1], offsets, add, out, stream)
 
 
 def moe_w4_backward(dy: torch.Tensor, w: W4Weights, offsets: Optional[torch.Tensor] = None,
                     add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dx[t] = add[t] + W_e.T @ dy[t], dy [T][N]: the gradient of moe_w4_forward's rows."""
-    return _product(lib().moe_w4_backward, "dy", dy, w, w.shape[1], w.shape[2], offsets, add, out, stream)
+    return _product(lib().moe_w4_backward, 1, "dy", dy, w, w.shape[1], w.shape[2], offsets, add, out, stream)

@@ -124,6 +124,15 @@ def test_gradient(N, K, group, zeros, T, dtype):
     run_case(c, True, T % 2 == 0, f"grad T={T} N={N} K={K} group={group} zeros={zeros} {dtype}")
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("N,K,group,zeros,backward", [(10000, 160, 32, True, False), (9800, 256, 128, False, False),
+                                                      (72, 16384, 64, True, True), (136, 15000 // 32 * 32, 0, False, True)])
+def test_large_tiles(N, K, group, zeros, backward, dtype):
+    """Enough workgroups for tiles of 128 rows, the last of them ragged."""
+    c = make(1100, K, N, 1, group, dtype, zeros, N, backward=backward)
+    run_case(c, backward, False, f"large N={N} K={K} backward={backward} {dtype}")
+
+
 # rows before, between and after the groups, empty groups, one group, uneven groups
 OFFSETS = [(5, [0, 3, 3, 9, 10, 40], 47), (4, [2, 2, 2, 2, 2], 5), (3, [0, 0, 60, 61], 61), (1, [7, 40], 64),
            (1, [0, 100], 100), (7, [0, 130, 131, 131, 200, 201, 330, 700], 700), (130, list(range(0, 262, 2)), 261), (2, [0, 0, 0], 40)]

@@ -46,10 +46,11 @@ def test_w4_sizes(L):
         groups = blocks * (4 if group == 32 else 2 if group == 64 else 1)
         assert size <= n * (rows * blocks * 64 + rows * groups * 3 + 512)
     for d, _ in BAD_DIMS:
-        assert L.moe_w4_packed_bytes(d) == 0 and L.moe_w4_workspace_bytes(d, 4) == 0 and L.moe_w4_few_rows(d, 4) == 0
-    assert L.moe_w4_workspace_bytes(dims(), 0) == 0 and L.moe_w4_workspace_bytes(dims(), -1) == 0
+        assert L.moe_w4_packed_bytes(d) == 0 and L.moe_w4_workspace_bytes(d, 4, 1) == 0 and L.moe_w4_few_rows(d, 4) == 0
+    for back in (0, 1):
+        assert L.moe_w4_workspace_bytes(dims(), 0, back) == 0 and L.moe_w4_workspace_bytes(dims(), -1, back) == 0
     assert L.moe_w4_few_rows(dims(), 1) == 1 and L.moe_w4_few_rows(dims(), 2000) == 0
-    assert L.moe_w4_workspace_bytes(dims(N=64, K=6144, group=128), 64) > 0  # few tiles: the columns are split
+    assert L.moe_w4_workspace_bytes(dims(N=64, K=6144, group=128), 64, 0) > 0  # few tiles: the columns are split
 
 
 def test_w4_pack_refuses(L):
@@ -76,7 +77,7 @@ def test_w4_products_refuse(L):
         # a call that splits its sums needs a workspace
         d = dims(N=1024, K=8192, group=128)
         into, out = (8192, 1024) if into == 256 else (1024, 8192)
-        assert L.moe_w4_workspace_bytes(d, 64) > 0
+        assert L.moe_w4_workspace_bytes(d, 64, int(fn is L.moe_w4_backward)) > 0
         split = dict(good, d=d, ldx=into, ldy=out, T=64, offsets=None)
         _expect(fn, split, [("ws", None, INVAL), ("ws", P + 8, INVAL), ("ws_bytes", 1024, WORKSPACE)])
     # rows times width
@@ -90,7 +91,7 @@ def test_distill_refuses(L):
     common = [("z", None, INVAL), ("z", P + 1, INVAL), ("dtype", 3, INVAL), ("dtype", -1, INVAL), ("ldz", 999, INVAL), ("T", -1, INVAL),
               ("T", (1 << 20) + 1, UNSUPPORTED), ("V", 0, INVAL), ("ids", None, INVAL), ("ids", P + 2, INVAL), ("teacher", None, INVAL),
               ("k", 0, INVAL), ("k", 1025, UNSUPPORTED), ("tau", 0.0, INVAL), ("tau", -1.0, INVAL), ("tau", float("nan"), INVAL),
-              ("tau", float("inf"), INVAL), ("ldz", 1 << 41, UNSUPPORTED), ("ldz", 1 << 39, UNSUPPORTED), ("stats", None, INVAL),
+              ("tau", float("inf"), INVAL), ("tau", 2.0 ** -65, UNSUPPORTED), ("tau", 2.0 ** 65, UNSUPPORTED), ("ldz", 1 << 41, UNSUPPORTED), ("ldz", 1 << 39, UNSUPPORTED), ("stats", None, INVAL),
               ("stats", P + 2, INVAL), ("T", 0, OK)]
     _expect(L.moe_distill_forward, f, common + [("loss", None, INVAL), ("loss", P + 1, INVAL)])
     _expect(L.moe_distill_forward, dict(f, V=(1 << 24) + 1, ldz=1 << 25), [("k", 4, UNSUPPORTED)])
