@@ -72,18 +72,33 @@ struct Tiles {
   int head, end, grouped;  // the rows outside are [0, head) and [end, T); tiles of all groups
 
   __device__ __forceinline__ int at(int i) const { return min(max(offsets[i], 0), T); }
+  // f(expert, first row, end) for this lane's experts, four offsets on their way at a time
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    int lo = 0;
+    for (int e = e0; e < e1; e += 4) {
+      int b[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) b[i] = at(min(e + i, e1));
+      if (e == e0) lo = b[0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int hi = max(lo, b[i + 1]);
+        if (e + i < e1) f(e + i, lo, hi);
+        lo = hi;
+      }
+    }
+  }
   __device__ __forceinline__ Tiles(const int32_t* o, int n_, int T_) : offsets(o), n(n_), T(T_) {
     if (!offsets) return;
     const int per = (n + 63) / 64;
     e0 = min((int)(threadIdx.x & 63) * per, n);
     e1 = min(e0 + per, n);
     full = rest = 0;
-    for (int e = e0, lo = at(e0); e < e1; ++e) {
-      const int hi = max(lo, at(e + 1));
+    each([&](int, int lo, int hi) {
       full += (hi - lo) / BM;
       rest += (hi - lo) % BM != 0;
-      lo = hi;
-    }
+    });
     const int f = wave_inclusive_scan(full), r = wave_inclusive_scan(rest);
     full_at = f - full;
     rest_at = __builtin_amdgcn_readlane(f, 63) + r - rest;
@@ -102,12 +117,11 @@ struct Tiles {
       const bool in_full = nth_full >= 0 && nth_full < full, mine = in_full || (nth_rest >= 0 && nth_rest < rest);
       const int l = __ffsll((unsigned long long)__ballot(mine)) - 1;
       int left = in_full ? nth_full : nth_rest;
-      for (int e = e0, lo = at(e0); e < e1; ++e) {
-        const int hi = max(lo, at(e + 1)), f = (hi - lo) / BM, k = (hi - lo) % BM, c = in_full ? f : (k != 0);
+      each([&](int e, int lo, int hi) {
+        const int f = (hi - lo) / BM, k = (hi - lo) % BM, c = in_full ? f : (k != 0);
         if (left >= 0 && left < c) r = in_full ? RowTile{e, lo + left * BM, BM} : RowTile{e, hi - k, k};
         left -= c;
-        lo = hi;
-      }
+      });
       return RowTile{__builtin_amdgcn_readlane(r.e, l), __builtin_amdgcn_readlane(r.r0, l),
                      __builtin_amdgcn_readlane(r.rows, l)};
     }
