@@ -38,18 +38,23 @@ struct RowScales<MOE_T_F16, ZP> {
     return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])});
   }
 };
+// bfloat16: the factor s and the addend c of (1024 + u) s + c, or (1024 + 16 u) s + c for
+// pairs 1 and 3, are made once for all wavefronts, where the scales are staged.
 template <bool ZP>
 struct RowScales<MOE_T_BF16, ZP> {
-  float s[8], c[8];  // of pairs 1 and 3: for 1024 + 16 u
-  // cv: eight values -(8 + z)
-  __device__ __forceinline__ void set(u32x4 sv, u32x4 cv) {
+  float2 f[8];
+  __device__ __forceinline__ void set(const float2* p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool high = i / 2 & 1;
-      const float f = scale_value<MOE_T_BF16>((uint16_t)(sv[i / 2] >> (16 * (i & 1))));
-      c[i] = ((ZP ? scale_value<MOE_T_BF16>((uint16_t)(cv[i / 2] >> (16 * (i & 1)))) : -8.0f) - (high ? 64.0f : 1024.0f)) * f;
-      s[i] = high ? f * 0.0625f : f;
+    for (int i = 0; i < 8; i += 2) {
+      const f32x4 v = *(const f32x4*)(p + i);
+      f[i] = make_float2(v[0], v[1]);
+      f[i + 1] = make_float2(v[2], v[3]);
     }
+  }
+  // for row `row` of a step
+  static __device__ __forceinline__ float2 of(uint16_t scale, int z, int row) {
+    const float v = scale_value<MOE_T_BF16>(scale);
+    return row & 2 ? make_float2(v * 0.0625f, (float)(-72 - z) * v) : make_float2(v, (float)(-1032 - z) * v);
   }
   __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
     half2_t v[4];
@@ -57,7 +62,8 @@ struct RowScales<MOE_T_BF16, ZP> {
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      r[i] = pack_bf16(fmaf((float)v[i][0], s[2 * i], c[2 * i]), fmaf((float)v[i][1], s[2 * i + 1], c[2 * i + 1]));
+      r[i] = pack_bf16(fmaf((float)v[i][0], f[2 * i].x, f[2 * i].y),
+                       fmaf((float)v[i][1], f[2 * i + 1].x, f[2 * i + 1].y));
     return __builtin_bit_cast(v8_t<MOE_T_BF16>, r);
   }
 };
@@ -73,7 +79,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
   typedef __attribute__((address_space(3))) v2i lds_v2i;
   __shared__ u32x4 sx[2][BM * 8];
   __shared__ u32x4 sw[2][SB * CB * 64];
-  __shared__ __attribute__((aligned(16))) uint16_t ss[2][CB * SG][kStepRows], sz[ZP ? 2 : 1][CB * SG][kStepRows];
+  // scales by group and row: as they are with the zero points' -(1032 + z), or as RowScales has them
+  constexpr bool F16 = DT == MOE_T_F16;
+  __shared__ __attribute__((aligned(16))) uint16_t ss[F16 ? 2 : 1][CB * SG][F16 ? kStepRows : 8],
+      sz[F16 && ZP ? 2 : 1][CB * SG][F16 ? kStepRows : 8];
+  __shared__ __attribute__((aligned(16))) float2 sf[F16 ? 1 : 2][CB * SG][F16 ? 2 : kStepRows];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, g = lane >> 4;
   const int split = blockIdx.x % a.split;
@@ -135,10 +145,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
           if (NS % kTileThreads && i >= NS) break;
           const int rb = s * SB + i / (CB * 16 * SG), kb = kb0 + i / (16 * SG) % CB;
           const int row = i / (CB * 16 * SG) * 16 + i / SG % 16, col = i / (16 * SG) % CB * SG + i % SG;
-          ss[buf][col][row] = rb < a.NB && kb < a.KB ? u.s[p] : 0;
-          if (ZP)
-            sz[buf][col][row] = DT == MOE_T_F16 ? __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - u.z[p]))
-                                                : __builtin_bit_cast(uint16_t, (__bf16)(float)(-8 - u.z[p]));
+          const uint16_t sc = rb < a.NB && kb < a.KB ? u.s[p] : 0;
+          const int z = ZP ? u.z[p] : 0;
+          if constexpr (F16) {
+            ss[buf][col][row] = sc;
+            if (ZP) sz[buf][col][row] = __builtin_bit_cast(uint16_t, (_Float16)(float)(-1032 - z));
+          } else {
+            sf[buf][col][row] = RowScales<DT, ZP>::of(sc, z, row);
+          }
         }
       };
 #pragma unroll
@@ -161,7 +175,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
 #pragma unroll
           for (int q = 0; q < 2; ++q) {  // rows 16 g + 8 q .. + 7 of the step
             RowScales<DT, ZP> rs;
-            rs.set(*(const u32x4*)&ss[buf][cg][16 * g + 8 * q], *(const u32x4*)&sz[ZP ? buf : 0][cg][16 * g + 8 * q]);
+            const int r0 = 16 * g + 8 * q;
+            if constexpr (F16) rs.set(*(const u32x4*)&ss[buf][cg][r0], *(const u32x4*)&sz[ZP ? buf : 0][cg][r0]);
+            else rs.set(&sf[buf][cg][r0]);
             v8_t<DT> wf[4];
 #pragma unroll
             for (int f = 0; f < 4; ++f) wf[f] = rs.weights((uint32_t)code[f][q]);
