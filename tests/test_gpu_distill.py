@@ -219,6 +219,13 @@ def test_captured_and_on_another_stream():
     assert torch.equal(loss, outs[0]) and torch.equal(stats, outs[1])
 
 
+def test_no_rows():
+    z, ids, te = torch.empty((0, 50), device=DEV), torch.empty((0, 4), dtype=torch.int32, device=DEV), torch.empty((0, 4), device=DEV)
+    loss, stats = moe.moe_distill_forward(z, ids, te)
+    assert loss.shape == (0,) and stats.shape == (0, 2)
+    assert moe.moe_distill_backward(z, ids, te, stats, loss).shape == (0, 50)
+
+
 def test_refuses():
     c = dev(make(3, 50, 4, F16, 8))
     stats = torch.zeros((3, 2), device=DEV)

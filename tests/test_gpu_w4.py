@@ -135,7 +135,8 @@ def test_large_tiles(N, K, group, zeros, backward, dtype):
 
 # rows before, between and after the groups, empty groups, one group, uneven groups
 OFFSETS = [(5, [0, 3, 3, 9, 10, 40], 47), (4, [2, 2, 2, 2, 2], 5), (3, [0, 0, 60, 61], 61), (1, [7, 40], 64),
-           (1, [0, 100], 100), (7, [0, 130, 131, 131, 200, 201, 330, 700], 700), (130, list(range(0, 262, 2)), 261), (2, [0, 0, 0], 40)]
+           (1, [0, 100], 100), (7, [0, 130, 131, 131, 200, 201, 330, 700], 700), (130, list(range(0, 262, 2)), 261), (2, [0, 0, 0], 40),
+           (6, [2, 3, 3, 9, 9, 12, 13], 16), (3, [0, 0, 16, 16], 16), (1, [3, 9], 12), (90, [0] * 30 + [1] * 20 + [5] * 40 + [40], 44)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
