@@ -294,7 +294,8 @@ struct GroupScale<MOE_T_F16, ZP> {
   __device__ __forceinline__ v8_t<MOE_T_F16> weights(uint32_t d) const {
     half2_t v[4];
     codes_f16(d, ZP ? c : both((_Float16)-1032.0f), v);
-    return __builtin_bit_cast(v8_t<MOE_T_F16>, u32x4{bits_of(v[0] * s), bits_of(v[1] * s), bits_of(v[2] * s), bits_of(v[3] * s)});
+    return __builtin_bit_cast(v8_t<MOE_T_F16>,
+                              u32x4{bits_of(v[0] * s), bits_of(v[1] * s), bits_of(v[2] * s), bits_of(v[3] * s)});
   }
 };
 template <bool ZP>
@@ -309,10 +310,13 @@ struct GroupScale<MOE_T_BF16, ZP> {
   __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
     half2_t v[4];
     code_pairs(d, v);
-    return __builtin_bit_cast(v8_t<MOE_T_BF16>, u32x4{pack_bf16(fmaf((float)v[0][0], s, c), fmaf((float)v[0][1], s, c)),
-                                                      pack_bf16(fmaf((float)v[1][0], s16, c16), fmaf((float)v[1][1], s16, c16)),
-                                                      pack_bf16(fmaf((float)v[2][0], s, c), fmaf((float)v[2][1], s, c)),
-                                                      pack_bf16(fmaf((float)v[3][0], s16, c16), fmaf((float)v[3][1], s16, c16))});
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = i & 1 ? s16 : s, o = i & 1 ? c16 : c;
+      r[i] = pack_bf16(fmaf((float)v[i][0], f, o), fmaf((float)v[i][1], f, o));
+    }
+    return __builtin_bit_cast(v8_t<MOE_T_BF16>, r);
   }
 };
 

@@ -6,7 +6,12 @@ namespace moe {
 namespace {
 
 // Forward: each of four wavefronts takes R row blocks of the matrix, straight from
-// memory into operands, and all rows of the tile.
+// memory into operands, and all rows of the tile, which pass through LDS.  So a block is
+// decoded once per tile and by one wavefront.  Bound by decoding and matrix instructions, which
+// hardly overlap: a 16x16x32 instruction takes 16 cycles, with 2, 3, 4 and 6 vector
+// instructions beside it 18.8, 21.8, 25.0 and 31.0; the more rows a tile has the less
+// decoding weighs.  2,048 rows of 6144 x 6144 bfloat16 147 us (1.05 PFLOP/s); 16,384 rows
+// of 256 experts of 1024 x 2048, laid out by Zipf's law, 135 us.
 template <int DT, int SG, bool ZP, int MT, int R>
 __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int groups) {
   constexpr int BM = 16 * MT;
@@ -94,7 +99,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int group
 #pragma unroll
             for (int r = 0; r < R; ++r) {
               GroupScale<DT, ZP> s;
-              s.set((uint16_t)((uint64_t)sv[r] >> (16 * (j / GS))), ZP ? (int)(int8_t)((uint32_t)zv[r] >> (8 * (j / GS))) : 0);
+              s.set((uint16_t)((uint64_t)sv[r] >> (16 * (j / GS))),
+                    ZP ? (int)(int8_t)((uint32_t)zv[r] >> (8 * (j / GS))) : 0);
               wf[r] = s.weights(wv[r][j]);
             }
 #pragma unroll
