@@ -379,9 +379,10 @@ inline void by_format(const moe_w4_dims_t& d, int SG, F f) {
   else groups(Const<MOE_T_BF16>{});
 }
 
-// Launches of forward calls of few and of many rows, and of the gradient.
+// Launches of forward calls of few and of many rows, and of the gradient of few (tiles of 16 M) and of many.
 void launch_w4_few(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, hipStream_t s);
 void launch_w4_rows(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, const TilePlan& p, hipStream_t s);
+void launch_w4_grad_few(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, int M, hipStream_t s);
 void launch_w4_grad(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, const TilePlan& p, hipStream_t s);
 
 }  // namespace moe

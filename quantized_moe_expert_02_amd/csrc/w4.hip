@@ -161,6 +161,22 @@ TilePlan plan_tiles(const moe_w4_dims_t& d, int T, bool grad) {
   return p;
 }
 
+// The gradient of one matrix by the kernel for few rows, in tiles of 16 or 32 rows: where that
+// makes at most a workgroup per CU, and the steps are few enough for eight wavefronts
+// (us, 16 or 32 rows a tile, and split over workgroups: 6144 x 6144, 16 rows 14.9, 16.9 and
+// 14.8, 64 rows 26.5, 19.4 and 23.5, 128 rows 38.0, 36.5 and 29.3; 2048 x 2048, 64 rows 7.5,
+// 9.1 and 14.7, 256 rows 11.6, 9.4 and 19.9; 128,000 x 2048, 8 rows 282, 316 and 59).
+// 0: the other kernel.
+constexpr int kFewSteps = 96;
+
+int few_grad_rows(const moe_w4_dims_t& d, int T) {
+  if (d.n > 1 || ceil_div(d.N, kStepRows) > kFewSteps) return 0;
+  const int groups = ceil_div(d.K, 64);
+  for (int M = 1; M <= 2; ++M)
+    if ((int64_t)ceil_div(T, 16 * M) * groups <= kCUs) return M;
+  return 0;
+}
+
 size_t part_bytes(const moe_w4_dims_t& d, int T, const TilePlan& p, bool grad) {
   return p.split > 1 ? (size_t)p.split * T * (grad ? d.K : d.N) * 4 : 0;
 }
@@ -221,7 +237,7 @@ int32_t moe_w4_few_rows(const moe_w4_dims_t* d, int32_t T) {
 }
 
 size_t moe_w4_workspace_bytes(const moe_w4_dims_t* d, int32_t T, int32_t backward) {
-  if (check_w4_rows(d, T) != MOE_OK || T == 0 || (!backward && few_rows(*d, T))) return 0;
+  if (check_w4_rows(d, T) != MOE_OK || T == 0 || (backward ? few_grad_rows(*d, T) != 0 : few_rows(*d, T))) return 0;
   return part_bytes(*d, T, plan_tiles(*d, T, backward != 0), backward != 0);
 }
 
@@ -260,12 +276,20 @@ int moe_w4_backward(const moe_w4_dims_t* d, const void* packed, const void* dy, 
   if (st != MOE_OK || T == 0) return st;
   const W4Layout l = w4_layout(*d);
   const hipStream_t s = (hipStream_t)stream;
+  W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, dy, lddy, T, offsets, add,
+           ldadd, dx, lddx, nullptr, 1};
+  if (const int M = few_grad_rows(*d, T)) {
+    launch_w4_grad_few(a, *d, l, M, s);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
+  }
   const TilePlan p = plan_tiles(*d, T, true);
   const size_t need = part_bytes(*d, T, p, true);
-  if (need && bad(ws, 16)) return MOE_E_INVAL;
-  if (ws_bytes < need) return MOE_E_WORKSPACE;
-  const W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, dy, lddy, T, offsets,
-                 add, ldadd, dx, lddx, need ? (float*)ws : nullptr, p.split};
+  if (need) {
+    if (bad(ws, 16)) return MOE_E_INVAL;
+    if (ws_bytes < need) return MOE_E_WORKSPACE;
+    a.part = (float*)ws;
+  }
+  a.split = p.split;
   launch_w4_grad(a, *d, l, p, s);
   if (need) launch_sum(a, d->dtype, d->K, s);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;

@@ -221,7 +221,164 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_w4_grad(W4Args a, int group
   });
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: a workgroup takes 64 columns (eight bytes of each lane's sixteen of a block); its W
+// wavefronts take the steps of 64 matrix rows in turn and add their sums through LDS, so
+// that no partial sums go through memory and one launch does.  A wavefront has its own
+// LDS and no barriers until the end; rows and scales come from memory straight into operands.
+// Bound by its chain of loads, codes' turn and sum: 45 rows of 1000 x 2080 binary16, groups
+// of 32 with zero points, 5.8 us (split over workgroups and summed 11.3).
+// ---------------------------------------------------------------------------
+// The scales and zero points of eight rows, as memory holds them, for a lane's group `in` of SG.
+template <int DT, int SG, bool ZP>
+struct EightRows {
+  u32x4 s[SG];
+  uint32_t z[ZP ? 2 * SG : 1];
+  __device__ __forceinline__ void load(const uint8_t* scales, const uint8_t* zeros, size_t at) {
+#pragma unroll
+    for (int i = 0; i < SG; ++i) s[i] = ((const u32x4*)(scales + at * 2))[i];
+    if constexpr (ZP) {
+#pragma unroll
+      for (int i = 0; i < 2 * SG; ++i) z[i] = ((const uint32_t*)(zeros + at))[i];
+    }
+  }
+  // scales of rows 2 i and 2 i + 1
+  __device__ __forceinline__ uint32_t pair(int i, int in) const {
+    if constexpr (SG == 1) return s[0][i];
+    const auto word = [&](int r) -> uint32_t {
+      if constexpr (SG == 2) return s[r / 4][r % 4];
+      const uint32_t lo = s[r * SG / 8][r % 2 * 2], hi = s[r * SG / 8][r % 2 * 2 + 1];
+      return in & 2 ? hi : lo;
+    };
+    return __builtin_amdgcn_perm(word(2 * i + 1), word(2 * i), in & 1 ? 0x07060302u : 0x05040100u);
+  }
+  __device__ __forceinline__ int zero(int r, int in) const {
+    return ZP ? (int)(int8_t)(z[ZP ? r * SG / 4 : 0] >> (8 * (r * SG % 4 + in))) : 0;
+  }
+  __device__ __forceinline__ RowScales<DT, ZP> get(int in, bool none) const {
+    RowScales<DT, ZP> rs;
+    u32x4 sv{}, cv{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sv[i] = none ? 0u : pair(i, in);
+    if constexpr (DT == MOE_T_F16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        cv[i] = bits_of(half2_t{(_Float16)(float)(-1032 - zero(2 * i, in)), (_Float16)(float)(-1032 - zero(2 * i + 1, in))});
+      rs.set(sv, cv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rs.f[i] = RowScales<DT, ZP>::of((uint16_t)(sv[i / 2] >> (16 * (i & 1))), zero(i, in), i);
+    }
+    return rs;
+  }
+};
+
+template <int DT, int SG, bool ZP, int M, int W>
+__global__ __launch_bounds__(64 * W) void k_w4_grad_few(W4Args a, int groups) {
+  constexpr int BM = 16 * M, SB = kStepRows / kBlockRows;
+  typedef typename Mat<DT>::elem elem;
+  typedef int v2i __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) v2i lds_v2i;
+  __shared__ uint64_t sw[W][SB * 64];
+  __shared__ f32x4 red[W][4][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, g = lane >> 4;
+  const Place at = place_of(blockIdx.x, groups, a.offsets);
+  const RowTile t = Tiles<BM>(a.offsets, a.n, a.T).find(at.tile);
+  if (t.rows <= 0) return;
+  const int h = at.run, kb = h >> 1;  // half block
+  const int in = SG == 4 ? 2 * (h & 1) + (li >> 3) : SG == 2 ? h & 1 : 0;
+  const int rho = (li & 8) + ((li & 7) < 4 ? 2 * (li & 7) : 2 * (li & 7) - 7);  // as above
+  const uint8_t* w = a.w + (size_t)max(t.e, 0) * a.stride;
+  const int steps = t.e < 0 ? 0 : (a.NB + SB - 1) / SB;
+  f32x4 acc[M][4];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{};
+  struct Step {
+    uint64_t w[SB];
+    u32x4 x[M][2];
+    EightRows<DT, SG, ZP> s[2];
+  };
+  // (blocks past the matrix repeat its last, with scale 0 and rows of zeros)
+  const auto load = [&](Step& u, int s) {
+#pragma unroll
+    for (int p = 0; p < SB; ++p) {
+      const size_t block = (size_t)min(s * SB + p, a.NB - 1) * a.KB + kb;
+      u.w[p] = *(const uint64_t*)(w + block * kBlockBytes + lane * 16 + 8 * (h & 1));
+    }
+    const size_t scales = ((size_t)min(s * SB + g, a.NB - 1) * a.KB + kb) * 16 * SG;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      u.s[q].load(w + a.soff, w + a.zoff, scales + 8 * q * SG);
+      const int c = s * kStepRows + 16 * g + 8 * q;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int64_t row = t.r0 + min(16 * m + li, t.rows - 1);
+        u.x[m][q] = *(const u32x4*)((const elem*)a.x + row * a.ldx + min(c, a.N - 8));
+        if (c >= a.N) u.x[m][q] = u32x4{};
+      }
+    }
+  };
+  Step now, next;
+  if (wave < steps) load(now, wave);
+  for (int s = wave; s < steps; s += W) {
+    if (s + W < steps) load(next, s + W);
+#pragma unroll
+    for (int p = 0; p < SB; ++p) sw[wave][p * 64 + (lane ^ (p & 1) * 16)] = now.w[p];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    v2i code[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+      code[f] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+          (lds_v2i*)&sw[wave][g * 64 + ((f * 16 + rho) ^ (g & 1) * 16)]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    const bool none = s * SB + g >= a.NB;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const RowScales<DT, ZP> rs = now.s[q].get(in, none);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const v8_t<DT> wf = rs.weights((uint32_t)code[f][q]);
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[m][f] = Mat<DT>::mma(wf, __builtin_bit_cast(v8_t<DT>, now.x[m][q]), acc[m][f]);
+      }
+    }
+    now = next;
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) red[wave][f][lane] = acc[m][f];
+    __syncthreads();
+    if (wave < 4) {
+      f32x4 v = red[0][wave][lane];
+#pragma unroll
+      for (int u = 1; u < W; ++u) v += red[u][wave][lane];
+      const auto lo = __builtin_amdgcn_permlane16_swap(bits(v[0]), bits(v[2]), false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(bits(v[1]), bits(v[3]), false, false);
+      v = __builtin_bit_cast(f32x4, u32x4{lo[0], lo[1], hi[0], hi[1]});
+      const int row = 16 * m + li, c = h * 64 + 32 * (g >> 1) + 8 * wave + 4 * (g & 1);
+      if (row < t.rows && c < a.K) put4<DT>(a, a.K, 0, t.r0 + row, c, v);
+    }
+    if (m + 1 < M) __syncthreads();
+  }
+}
+
 }  // namespace
+
+void launch_w4_grad_few(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, int M, hipStream_t s) {
+  by_format(d, l.SG, [&](auto dt, auto sg, auto zp) {
+    constexpr int DT = decltype(dt)::value, SG = decltype(sg)::value;
+    constexpr bool ZP = decltype(zp)::value;
+    const int groups = ceil_div(d.K, 64);
+    const int64_t tiles = max_tiles(d.n, a.T, 16 * M, a.offsets != nullptr);
+    const unsigned grid = (unsigned)places(tiles, groups, a.offsets != nullptr);
+    if (M == 1) k_w4_grad_few<DT, SG, ZP, 1, 8><<<grid, 512, 0, s>>>(a, groups);
+    else k_w4_grad_few<DT, SG, ZP, 2, 8><<<grid, 512, 0, s>>>(a, groups);
+  });
+}
 
 void launch_w4_grad(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, const TilePlan& p, hipStream_t s) {
   by_format(d, l.SG, [&](auto dt, auto sg, auto zp) {

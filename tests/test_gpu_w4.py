@@ -125,6 +125,45 @@ def test_gradient(N, K, group, zeros, T, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T,N,K,group,zeros", [(2, 6144, 128, 128, False), (45, 6144, 96, 32, "wide"), (64, 1000, 2080, 32, True),
+                                               (100, 2056, 2048, 64, True), (16, 8, 16384, 128, True), (17, 72, 8160, 0, False),
+                                               (40, 6152, 256, 64, False), (512, 24, 1024, 512, True), (4096, 40, 32, 32, True)])
+def test_short_gradient(T, N, K, group, zeros, dtype):
+    """Around the borders between the gradient's kernels: most are a workgroup per CU or fewer of the one without workspace."""
+    c = make(T, K, N, 1, group, dtype, zeros, T + N, backward=True)
+    run_case(c, True, T % 2 == 1, f"short grad T={T} N={N} K={K} group={group} zeros={zeros} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_short_gradient_in_place(group, dtype):
+    """Rows outside one group unread, add the same as out, called on two streams at once and replayed: the same bits."""
+    c = make(50, 1152, 328, 1, group, dtype, True, 11, [5, 43], backward=True)
+    c["x"][:5] = c["x"][43:] = float("nan")
+    print("short grad in place", group, dtype, flush=True)
+    w, dy, add, off = pack(c), c["x"].to(DEV), c["add"].to(DEV), c["offsets"].to(DEV)
+    plain = moe.moe_w4_backward(dy, w, offsets=off, add=add)
+    ref, norm = product(torch.nan_to_num(c["x"]), weights(c["q"], c["scales"], c["zeros"]), c["offsets"], True)
+    m = weights(c["q"], c["scales"], c["zeros"])
+    c["x"] = torch.nan_to_num(c["x"])
+    check(plain, ref + c["add"].double(), tolerance(c, m, norm, False, True), dtype, "short grad")
+    assert torch.equal(plain[:5], add[:5]) and torch.equal(plain[43:], add[43:])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [moe.moe_w4_backward(dy, w, offsets=off, add=add, stream=s) for s in streams for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, plain) for o in outs)
+    out, graph = add.clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_w4_backward(dy, w, offsets=off, add=out, out=out)
+    for _ in range(3):
+        out.copy_(add)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, plain)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("N,K,group,zeros,backward", [(10000, 160, 32, True, False), (9800, 256, 128, False, False),
                                                       (72, 16384, 64, True, True), (136, 15000 // 32 * 32, 0, False, True)])
 def test_large_tiles(N, K, group, zeros, backward, dtype):

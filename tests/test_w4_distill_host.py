@@ -51,6 +51,9 @@ def test_w4_sizes(L):
         assert L.moe_w4_workspace_bytes(dims(), 0, back) == 0 and L.moe_w4_workspace_bytes(dims(), -1, back) == 0
     assert L.moe_w4_few_rows(dims(), 1) == 1 and L.moe_w4_few_rows(dims(), 2000) == 0
     assert L.moe_w4_workspace_bytes(dims(N=64, K=6144, group=128), 64, 0) > 0  # few tiles: the columns are split
+    # short gradients of one matrix need none: up to 6,144 rows of it, and a workgroup of 64 columns and 32 rows per CU
+    for N, K, T, need in ((6144, 6144, 64, 0), (6152, 6144, 64, 1), (6144, 6144, 96, 1), (1024, 8192, 64, 0), (1024, 8192, 65, 1)):
+        assert (L.moe_w4_workspace_bytes(dims(N=N, K=K, group=128), T, 1) > 0) == bool(need), (N, K, T)
 
 
 def test_w4_pack_refuses(L):
@@ -75,8 +78,8 @@ def test_w4_products_refuse(L):
             ("offsets", None, INVAL), ("offsets", P + 2, INVAL), ("add", P + 8, INVAL), ("add", P, INVAL), ("y", None, INVAL),
             ("y", P + 4, INVAL), ("ldy", out - 8, INVAL), ("ldy", out + 1, INVAL), ("T", 0, OK)])
         # a call that splits its sums needs a workspace
-        d = dims(N=1024, K=8192, group=128)
-        into, out = (8192, 1024) if into == 256 else (1024, 8192)
+        d = dims(N=8192, K=8192, group=128)
+        into = out = 8192
         assert L.moe_w4_workspace_bytes(d, 64, int(fn is L.moe_w4_backward)) > 0
         split = dict(good, d=d, ldx=into, ldy=out, T=64, offsets=None)
         _expect(fn, split, [("ws", None, INVAL), ("ws", P + 8, INVAL), ("ws_bytes", 1024, WORKSPACE)])
