@@ -113,7 +113,32 @@ def test_few_rows(N, K, group, zeros, T, dtype):
 @pytest.mark.parametrize("N,K,group,zeros", SHAPES[:8])
 def test_many_rows(N, K, group, zeros, T, dtype):
     c = make(T, K, N, 1, group, dtype, zeros, T + N)
-    assert not run_case(c, False, T % 2 == 0, f"rows T={T} N={N} K={K} group={group} zeros={zeros} {dtype}")
+    run_case(c, False, T % 2 == 0, f"rows T={T} N={N} K={K} group={group} zeros={zeros} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T", [513, 578, 1000])
+@pytest.mark.parametrize("N,K,group,zeros", SHAPES[:8])
+def test_more_rows(N, K, group, zeros, T, dtype):
+    """Past the kernel for few rows, with split sums where the matrix is small."""
+    c = make(T, K, N, 1, group, dtype, zeros, T + N)
+    assert not run_case(c, False, T % 2 == 0, f"more rows T={T} N={N} K={K} group={group} zeros={zeros} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T", [17, 33, 70])
+@pytest.mark.parametrize("N,K,group,zeros", [(10248, 4128, 32, True), (10312, 4160, 64, False), (20520, 2080, 0, True)])
+def test_rows_of_large_matrices(N, K, group, zeros, T, dtype):
+    """Few rows of a matrix too large for the kernel for few rows: tiles of 32 and 64 rows."""
+    c = make(T, K, N, 1, group, dtype, zeros, T + N)
+    assert not run_case(c, False, T % 2 == 0, f"large matrix T={T} N={N} K={K} group={group} zeros={zeros} {dtype}")
+
+
+def test_borders_of_few_rows():
+    """moe_w4_few_rows on both sides of its rule, with rows outside one group."""
+    for N, K, T, few in ((2048, 2048, 320, True), (2048, 2048, 321, False), (64, 256, 512, True), (64, 256, 513, False)):
+        c = make(T, K, N, 1, 128, BF16, True, T, [3, T - 5])
+        assert run_case(c, False, True, f"border N={N} K={K} T={T}") == few
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -200,7 +225,7 @@ def test_groups(n, offsets, T, backward, dtype):
 
 
 @pytest.mark.parametrize("backward", [False, True])
-@pytest.mark.parametrize("T", [5, 90])
+@pytest.mark.parametrize("T", [5, 90, 1200])
 def test_strides_and_in_place(T, backward):
     """Rows of wider buffers, add the same as out, and nothing written beside the rows."""
     c = make(T, 416, 104, 1, 32, F16, True, 3, backward=backward)
@@ -222,7 +247,7 @@ def test_strides_and_in_place(T, backward):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("T,backward", [(2, False), (40, False), (2, True)])
+@pytest.mark.parametrize("T,backward", [(2, False), (40, False), (2, True), (5000, False), (5000, True)])
 def test_infinities(T, backward, dtype):
     """Infinities and NaNs of a row stay in that row and are the formula's."""
     c = make(T, 256, 64, 1, 64, dtype, True, 9, backward=backward)
