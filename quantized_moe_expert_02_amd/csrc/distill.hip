@@ -327,14 +327,17 @@ constexpr int64_t kShortRow = 16 << 10;
 // Longer ones 512 threads, and where that makes too few workgroups, chunks of 16 to 64 KB,
 // about 512 in all (loss of 64 rows of 128,000 bfloat16 logits: whole rows 14.1 us, 64 KB 9.9,
 // 32 KB 10.4; 301 rows of 100,003 binary16: 22.1 and 20.9 (so whole from 256 rows); 4
-// rows of 128,000 fp32: 16.7, 16 KB 6.4).  The gradient, which joins nothing, always takes
+// rows of 128,000 fp32: 13.9, 16 KB 6.3).  Up to 64 Ki columns the loss takes whole rows too, which
+// is one launch instead of two and hardly longer on the GPU (whole and in chunks, us: 4 rows of
+// 32,000 bfloat16 logits 5.3 and 6.5, 128 rows 5.8 and 7.9; of 64,000 7.4 and 6.6, 9.0 and
+// 10.0; 4 rows of 64,000 fp32 8.5 and 6.2).  The gradient, which joins nothing, always takes
 // chunks (2,048 rows of 128,000 bfloat16: whole rows 203, 64 KB 190).
-constexpr int kWholeRows = 256;
+constexpr int kWholeRows = 256, kWholeColumns = 64 << 10;
 
 int chunk_of(int T, int V, int dtype, bool grad) {
   const int64_t b = (int64_t)elem_bytes(dtype), share = (int64_t)T * V * b / 512;
   const int64_t bytes = std::min<int64_t>(std::max<int64_t>(share, 16 << 10), 64 << 10);
-  if (V * b <= kShortRow || (!grad && T >= kWholeRows)) return V;
+  if (V * b <= kShortRow || (!grad && (T >= kWholeRows || V <= kWholeColumns))) return V;
   const int chunks = ceil_div(V * b, bytes);
   return std::min(V, ceil_div(ceil_div(V, chunks), 8) * 8);
 }

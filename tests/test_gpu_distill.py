@@ -85,12 +85,13 @@ def run_case(c, tau, what, **kw):
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("T,V,k,tau", [(1, 1, 1, 1.0), (3, 5, 5, 0.5), (2, 513, 1, 2.0), (5, 1000, 64, 1.0), (7, 8193, 33, 1.5),
-                                       (1, 100003, 20, 1.0), (4, 40001, 1024, 2.0), (600, 257, 16, 1.0), (30, 20000, 100, 0.7)])
+                                       (1, 100003, 20, 1.0), (4, 40001, 1024, 2.0), (600, 257, 16, 1.0), (30, 20000, 100, 0.7),
+                                       (2, 65536, 9, 1.0), (9, 65537, 1024, 0.6), (3, 131075, 50, 2.0)])
 def test_loss_and_gradient(T, V, k, tau, dtype):
     run_case(make(T, V, k, dtype, T + V, repeat=k > V), tau, f"T={T} V={V} k={k} tau={tau} {dtype}")
 
 
-@pytest.mark.parametrize("T,V", [(6, 300), (6, 30000), (520, 300)])
+@pytest.mark.parametrize("T,V", [(6, 300), (6, 30000), (520, 300), (6, 70001)])
 def test_entries(T, V):
     """Repeated ids, dropped entries, rows that keep none (their logits are not read)."""
     c = make(T, V, 40, F16, 1, repeat=True)
@@ -112,7 +113,7 @@ def test_entries(T, V):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
-@pytest.mark.parametrize("V", [700, 30000])
+@pytest.mark.parametrize("V", [700, 30000, 70001])
 def test_masks(V, dtype):
     """Masked logits: -infinity and the type's lowest value, whole stretches of them."""
     low = torch.finfo(dtype).min
@@ -129,7 +130,7 @@ def test_masks(V, dtype):
     assert bool((grad[0, V // 3:][d["z"][0, V // 3:] == -INF] == 0).all())
 
 
-@pytest.mark.parametrize("V", [700, 30000])
+@pytest.mark.parametrize("V", [700, 30000, 70001])
 def test_infinite_results(V):
     """A teacher's entry at a logit of -infinity: an infinite loss, a finite gradient.
     Rows without a finite logit, with NaN or +infinity: NaN, in that row only."""
@@ -150,7 +151,7 @@ def test_infinite_results(V):
 
 
 @pytest.mark.parametrize("dtype", [F16, F32])
-@pytest.mark.parametrize("T,V,pad,shift", [(4, 1001, 0, 1), (3, 30001, 7, 3), (515, 129, 2, 0)])
+@pytest.mark.parametrize("T,V,pad,shift", [(4, 1001, 0, 1), (3, 30001, 7, 3), (515, 129, 2, 0), (3, 70003, 5, 1)])
 def test_strides_and_in_place(T, V, pad, shift, dtype):
     c = make(T, V, 9, dtype, 4)
     print("strides", T, V, pad, shift, dtype, flush=True)
