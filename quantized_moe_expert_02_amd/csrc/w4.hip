@@ -123,18 +123,20 @@ int check_w4_rows(const moe_w4_dims_t* d, int32_t T) {
 // Up to 16 rows of one matrix, or half as many rows as experts (us, few and many rows' kernel:
 // 256 experts, 2048 x 1024, by Zipf's law, 64 rows 17.9 and 21.1, 128 23.3 and 23.4, 512 53 and
 // 48, 4,096 128 and 82; 128 experts, 6144 x 2048, evenly, 64 rows 87 and 97, 128 164 and 169).
-// More of one matrix, up to 512, where 16 rows at a time decode at most 40 Ki blocks (us, few and
-// many rows' kernel with its sum: 2048 x 2048, 64 rows 7.4 and 14.3, 256 14.0 and 18.9, 512 21.0
-// and 21.6; 6144 x 6144, 32 rows 15.1 and 16.4, 48 23.4 and 20.3; 6144 x 2048 with groups
-// of 32 and zero points, 96 rows 18.7 and 20.3, 256 33.3 and 27.8; 32,000 x 2048, 24
-// rows 21.9 and 18.8).
-constexpr int kFewRowsMost = 512;
+// More of one matrix, up to 512, where that kernel passes over the columns once and, 16 rows
+// at a time, decodes at most 40 Ki blocks (us, few and many rows' kernel with its sum: 2048 x
+// 2048, 64 rows 7.4 and 14.3, 256 14.0 and 18.9, 512 21.0 and 21.6; 6144 x 6144, 32 rows 15.1
+// and 16.4, 48 23.4 and 20.3; 6144 x 2048 with groups of 32 and zero points, 96 rows 18.7 and
+// 20.3, 256 33.3 and 27.8; 32,000 x 2048, 24 rows 21.9 and 18.8; in several passes, 512 rows of
+// 40 x 16384 26.8 and 20.0, 300 of 8 x 65536 73 and 33).
+constexpr int kFewRowsMost = 512, kOnePass = 48;
 constexpr int64_t kFewBlocks = 40 << 10;
 
 bool few_rows(const moe_w4_dims_t& d, int T) {
   if (T <= std::max(kFewRows, d.n / 2)) return true;
-  const int64_t blocks = (int64_t)ceil_div(d.N, kBlockRows) * ceil_div(d.K, kBlockCols);
-  return d.n == 1 && T <= kFewRowsMost && ceil_div(T, 16) * blocks <= kFewBlocks;
+  const int KB = ceil_div(d.K, kBlockCols);
+  return d.n == 1 && T <= kFewRowsMost && KB <= kOnePass &&
+         (int64_t)ceil_div(T, 16) * ceil_div(d.N, kBlockRows) * KB <= kFewBlocks;
 }
 
 // Measured in us.  One matrix: tiles of 128 rows where they give nearly two workgroups

@@ -134,9 +134,21 @@ def test_rows_of_large_matrices(N, K, group, zeros, T, dtype):
     assert not run_case(c, False, T % 2 == 0, f"large matrix T={T} N={N} K={K} group={group} zeros={zeros} {dtype}")
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T,N,K,group,zeros,offsets", [(100, 40, 16384, 128, False, None), (70, 24, 8160, 32, True, [18, 55]),
+                                                       (512, 8, 12800, 64, True, [0, 511]), (33, 72, 6240, 0, True, None),
+                                                       (16, 40, 16384, 128, False, [3, 13]), (14, 72, 12320, 32, True, [5, 14])])
+def test_wide_matrices(T, N, K, group, zeros, offsets, dtype):
+    """Several passes over the columns by the kernel for few rows, and split sums; rows outside one group."""
+    c = make(T, K, N, 1, group, dtype, zeros, T, offsets)
+    few = run_case(c, False, offsets is not None, f"wide T={T} N={N} K={K} {dtype}")
+    assert few == (T <= 16)
+
+
 def test_borders_of_few_rows():
     """moe_w4_few_rows on both sides of its rule, with rows outside one group."""
-    for N, K, T, few in ((2048, 2048, 320, True), (2048, 2048, 321, False), (64, 256, 512, True), (64, 256, 513, False)):
+    for N, K, T, few in ((2048, 2048, 320, True), (2048, 2048, 321, False), (64, 256, 512, True), (64, 256, 513, False),
+                         (72, 6144, 400, True), (72, 6272, 400, False)):
         c = make(T, K, N, 1, 128, BF16, True, T, [3, T - 5])
         assert run_case(c, False, True, f"border N={N} K={K} T={T}") == few
 
