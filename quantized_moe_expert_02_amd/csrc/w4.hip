@@ -150,13 +150,17 @@ bool few_rows(const moe_w4_dims_t& d, int T) {
 // parts 19.7, 8 13.8, 12 17.1, with 24 tiles).
 constexpr int kTwoPerCU = 460, kOnePerCU = 256, kStepsPerPart = 3;
 
+// Tiles of BM rows that a call is expected to have: of the experts that can have rows, half
+// are taken to have a tile that is not full.
+int64_t likely_tiles(const moe_w4_dims_t& d, int T, int BM) {
+  return d.n > 1 ? T / BM + (std::min(d.n, T) + 1) / 2 : ceil_div(T, BM);
+}
+
 TilePlan plan_tiles(const moe_w4_dims_t& d, int T, bool grad) {
   TilePlan p;
   const int avg = ceil_div(T, d.n);
-  // (of the experts that can have rows, half are taken to have a tile that is not full)
   const auto blocks = [&](int MT, int R) {
-    const int64_t tiles = d.n > 1 ? T / (16 * MT) + (std::min(d.n, T) + 1) / 2 : ceil_div(T, 16 * MT);
-    return tiles * (grad ? ceil_div(d.K, kGradCols) : ceil_div(d.N, 64 * R));
+    return likely_tiles(d, T, 16 * MT) * (grad ? ceil_div(d.K, kGradCols) : ceil_div(d.N, 64 * R));
   };
   p.R = 4;
   if (d.n > 1) {
@@ -175,19 +179,20 @@ TilePlan plan_tiles(const moe_w4_dims_t& d, int T, bool grad) {
   return p;
 }
 
-// The gradient of one matrix by the kernel for few rows, in tiles of 16 or 32 rows: where that
-// makes at most a workgroup per CU, and the steps are few enough for eight wavefronts
+// The gradient by the kernel for few rows, in tiles of 16 or 32 rows: where that makes at
+// most a workgroup per CU, and the steps are few enough for eight wavefronts
 // (us, 16 or 32 rows a tile, and split over workgroups: 6144 x 6144, 16 rows 14.9, 16.9 and
 // 14.8, 64 rows 26.5, 19.4 and 23.5, 128 rows 38.0, 36.5 and 29.3; 2048 x 2048, 64 rows 7.5,
-// 9.1 and 14.7, 256 rows 11.6, 9.4 and 19.9; 128,000 x 2048, 8 rows 282, 316 and 59).
+// 9.1 and 14.7, 256 rows 11.6, 9.4 and 19.9; 128,000 x 2048, 8 rows 282, 316 and 59; 8 experts
+// of 1024 x 1024, 64 rows 5.7, 6.3 and 10.3; 16 of 2048 x 512, 128 rows 7.0, 8.0 and 12.7).
 // 0: the other kernel.
 constexpr int kFewSteps = 96;
 
 int few_grad_rows(const moe_w4_dims_t& d, int T) {
-  if (d.n > 1 || ceil_div(d.N, kStepRows) > kFewSteps) return 0;
+  if (ceil_div(d.N, kStepRows) > kFewSteps) return 0;
   const int groups = ceil_div(d.K, 64);
   for (int M = 1; M <= 2; ++M)
-    if ((int64_t)ceil_div(T, 16 * M) * groups <= kCUs) return M;
+    if (likely_tiles(d, T, 16 * M) * groups <= kCUs) return M;
   return 0;
 }
 

@@ -220,7 +220,7 @@ OFFSETS = [(5, [0, 3, 3, 9, 10, 40], 47), (4, [2, 2, 2, 2, 2], 5), (3, [0, 0, 60
 @pytest.mark.parametrize("n,offsets,T", OFFSETS)
 def test_groups(n, offsets, T, backward, dtype):
     offsets = [min(v, T) for v in offsets]
-    for N, K, group, zeros, add in ((72, 160, 32, True, True), (200, 384, 128, False, False)):
+    for N, K, group, zeros, add in ((72, 160, 32, True, True), (200, 384, 128, False, False)) + ((40, 4128, 32, True, True),) * backward:
         c = make(T, K, N, n, group, dtype, zeros, n + T, offsets, backward)
         for e0, e1 in ((0, offsets[0]), (offsets[-1], T)):  # not read
             c["x"][e0:e1] = float("nan")

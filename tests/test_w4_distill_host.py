@@ -51,7 +51,9 @@ def test_w4_sizes(L):
         assert L.moe_w4_workspace_bytes(dims(), 0, back) == 0 and L.moe_w4_workspace_bytes(dims(), -1, back) == 0
     assert L.moe_w4_few_rows(dims(), 1) == 1 and L.moe_w4_few_rows(dims(), 2000) == 0
     assert L.moe_w4_workspace_bytes(dims(N=8192, K=6144, group=128), 64, 0) > 0  # few tiles: the columns are split
-    # short gradients of one matrix need none: up to 6,144 rows of it, and a workgroup of 64 columns and 32 rows per CU
+    # short gradients need none: up to 6,144 matrix rows, and a workgroup of 64 columns and 32 rows per CU
+    for n, N, K, T, need in ((8, 1024, 1024, 128, 0), (8, 1024, 2048, 256, 1), (64, 512, 256, 64, 0), (8, 6152, 1024, 16, 1)):
+        assert (L.moe_w4_workspace_bytes(dims(n, N, K, 128), T, 1) > 0) == bool(need), (n, N, K, T)
     for N, K, T, need in ((6144, 6144, 64, 0), (6152, 6144, 64, 1), (6144, 6144, 96, 1), (1024, 8192, 64, 0), (1024, 8192, 65, 1)):
         assert (L.moe_w4_workspace_bytes(dims(N=N, K=K, group=128), T, 1) > 0) == bool(need), (N, K, T)
 
