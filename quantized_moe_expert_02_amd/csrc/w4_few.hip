@@ -17,32 +17,10 @@ namespace {
 // is taken off each group's sum.
 // Bound by memory where there is much to read (64 rows of 256 experts of 2048 x 6144
 // binary16, 369 MB: 73 us, 5.1 TB/s), by the vector unit beside it with groups of 32 and zero
-// points (8 rows of 128,000 x 2048 bfloat16, 158 MB: 40.5 us, 3.9 TB/s), and by its start in
+// points (8 rows of 128,000 x 2048 bfloat16, 158 MB: 43.5 us, 3.6 TB/s), and by its start in
 // short calls (one row of 6144 x 6144: 9 us).  An item per workgroup instead of runs: 136
 // and 61 us for the first two.
 // ---------------------------------------------------------------------------
-// The product of one output element in fp32, term by term as the formula has it.
-template <int DT, int SG, bool ZP>
-__device__ __forceinline__ float slow_dot(const uint8_t* w, size_t soff, size_t zoff, int K, int KB, int n,
-                                                    const void* xrow) {
-  typedef typename Mat<DT>::elem elem;
-  const elem* x = (const elem*)xrow;
-  const int nb = n / kBlockRows, r = n % kBlockRows;
-  float acc = 0.f;
-#pragma unroll 1
-  for (int k = 0; k < K; ++k) {
-    const int kb = k / kBlockCols, c = k % kBlockCols;
-    const size_t block = (size_t)nb * KB + kb;
-    const int nibble = c % 8 / 2 + (c & 1) * 4;
-    const uint8_t byte = w[block * kBlockBytes + ((c / 8 % 4) * 16 + r) * 16 + c / 32 * 4 + nibble / 2];
-    const int q = (int)(nibble & 1 ? byte >> 4 : byte & 15) - 8;
-    const size_t at = (block * 16 + r) * SG + c / (kBlockCols / SG);
-    const int z = ZP ? (int)((const int8_t*)(w + zoff))[at] : 0;
-    acc = fmaf((float)(q - z) * scale_value<DT>(((const uint16_t*)(w + soff))[at]), (float)x[k], acc);
-  }
-  return acc;
-}
-
 template <int DT, int SG, bool ZP, int W, int KPW>
 __global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
   typedef typename Mat<DT>::elem elem;
@@ -96,37 +74,25 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
   };
   f32x4 acc;
   const auto multiply = [&](int u) {
-    v8_t<DT> ones;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ones[i] = (elem)1.0f;
 #pragma unroll
     for (int s = 0; s < SG; ++s) {
-      f32x4 sum{}, xsum{};
+      f32x4 sum{};
       const int z = ZP ? (int)(int8_t)((uint32_t)zv[u] >> (8 * s)) : 0;
+      GroupScale<MOE_T_BF16, ZP> small;
+      small.set(0x3800, z);  // 2^-15
 #pragma unroll
       for (int j = s * GS; j < (s + 1) * GS; ++j) {
-        const v8_t<DT> xf = __builtin_bit_cast(v8_t<DT>, xv[u][j]);
-        if (DT == MOE_T_BF16) xsum = Mat<DT>::mma(xf, ones, xsum);
-        const uint32_t c = wv[u][j];
-        u32x4 b;
+        v8_t<DT> b;
         if constexpr (DT == MOE_T_F16) {
           half2_t v[4];
-          codes_f16(c, both((_Float16)(float)(-1032 - z)), v);
-          b = u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])};
+          codes_f16(wv[u][j], both((_Float16)(float)(-1032 - z)), v);
+          b = __builtin_bit_cast(v8_t<DT>, u32x4{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])});
         } else {
-          b = u32x4{masked(c, 0x000F000Fu, 0x43004300u),
-                    masked(c >> 4, 0x000F000Fu, 0x43004300u),
-                    masked(c >> 8, 0x000F000Fu, 0x43004300u),
-                    masked(c >> 12, 0x000F000Fu, 0x43004300u)};
+          b = small.weights(wv[u][j]);
         }
-        sum = Mat<DT>::mma(xf, __builtin_bit_cast(v8_t<DT>, b), sum);
+        sum = Mat<DT>::mma(__builtin_bit_cast(v8_t<DT>, xv[u][j]), b, sum);
       }
       const float f = scale_value<DT>((uint16_t)((uint64_t)sv[u] >> (16 * s)));
-      if constexpr (DT == MOE_T_BF16) {
-        const float off = (float)(-136 - z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = fmaf(off, xsum[i], sum[i]);
-      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, sum[i], acc[i]);
     }
@@ -169,23 +135,7 @@ __global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
       for (int u = 1; u < W; ++u) v += red[p][u][lane];
       const int live = min(4, t.rows - 4 * g);
       const int64_t row = t.r0 + 4 * g;
-      if (DT == MOE_T_BF16 && t.e >= 0) {
-        // the terms 128 + u and 136 + z beside an infinity, or past fp32's range, need
-        // not cancel to the formula's value
-        bool finite = true;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) finite &= fabsf(v[q]) < INFINITY;
-        if (!finite) {
-#pragma unroll 1
-          for (int q = 0; q < live; ++q) {
-            const float o = slow_dot<DT, SG, ZP>(a.w + (size_t)t.e * a.stride, a.soff, a.zoff, a.K, a.KB, n,
-                                                 (const elem*)a.x + (row + q) * a.ldx);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k == q && !(fabsf(v[k]) < INFINITY)) v[k] = o;
-          }
-        }
-      }
+      if (DT == MOE_T_BF16) v *= 0x1p15f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (q >= live) break;
@@ -214,7 +164,7 @@ void launch_w4_few(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, h
     // Wavefronts and column blocks of each so that W KPW fits the columns, and workgroups as
     // registers allow (us; 128,000 rows, K 2048, T 1, binary16, groups of 128: 4 x 4 28.2, 8 x 2
     // 32.9; T 8, bfloat16, groups of 32 with zero points, which need more registers: 53.9 and
-    // 41.6; 24,576 rows, K 2560: 8 x 3 11.7, 16 x 3 14.3; K 5120: 16 x 3 17.7, 8 x 6 19.4;
+    // 41.6 with offset codes; 24,576 rows, K 2560: 8 x 3 11.7, 16 x 3 14.3; K 5120: 16 x 3 17.7, 8 x 6 19.4;
     // 60,000 rows, K 512: 2 x 2 7.8, 4 x 1 9.8).
     if (l.KB <= 4) launch(k_w4_few<DT, SG, ZP, 2, 2>, 2, 8);
     else if (l.KB <= 8) launch(k_w4_few<DT, SG, ZP, 4, 2>, 4, 5);
