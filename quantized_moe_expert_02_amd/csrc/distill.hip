@@ -34,15 +34,18 @@ struct DistillArgs {
   int64_t lddz;
 };
 
-// A running maximum m and the sum s of 2^((z - m) c).
+// A running maximum m (NaN from the first NaN on) and the sum s of 2^((z - m) c).
 struct Run {
   float m, s;
 };
 
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// NaN where either is (fmaxf passes NaNs over).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 __device__ __forceinline__ Run join(Run a, Run b, float c) {
-  const float m = fmaxf(a.m, b.m), f = finite_or_0(m);
+  const float m = larger(a.m, b.m), f = finite_or_0(m);
   return Run{m, a.s * __builtin_amdgcn_exp2f((a.m - f) * c) + b.s * __builtin_amdgcn_exp2f((b.m - f) * c)};
 }
 
@@ -63,10 +66,10 @@ __device__ __forceinline__ Run wave_join(Run r, float c) {
 
 template <int N>
 __device__ __forceinline__ void add_run(Run& r, const float (&z)[N], float c) {
-  float m = z[0];
+  float m = r.m;
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, z[i]);
-  if (m > r.m) {
+  for (int i = 0; i < N; ++i) m = larger(m, z[i]);
+  if (m != r.m) {
     r.s *= __builtin_amdgcn_exp2f((r.m - m) * c);
     r.m = m;
   }
