@@ -43,9 +43,10 @@ int moe_distill_forward(const void* z, int32_t dtype, int64_t ldz, int32_t T, in
                         const float* teacher, int32_t k, float tau, float* loss, float* stats, void* ws,
                         size_t ws_bytes, void* stream);
 
-/* dz [T][V] (row stride lddz >= V; dz may be z itself with lddz == ldz) for the
- * gradient dloss fp32 [T] of the loss; stats from the forward call.  Elements of
- * dz's rows past V are left as they were. */
+/* dz [T][V] (row stride lddz >= V) for the gradient dloss fp32 [T] of the loss; stats
+ * from the forward call.  dz may be z itself with lddz == ldz; otherwise its rows share
+ * no memory with z's (MOE_E_INVAL); rows of one stride may lie between each other, of two
+ * strides not.  Elements of dz's rows past V are left as they were. */
 int moe_distill_backward(const void* z, int32_t dtype, int64_t ldz, int32_t T, int32_t V, const int32_t* ids,
                          const float* teacher, int32_t k, float tau, const float* stats, const float* dloss,
                          void* dz, int64_t lddz, void* stream);

@@ -61,10 +61,12 @@ int32_t moe_w4_few_rows(const moe_w4_dims_t* d, int32_t T);
 size_t moe_w4_workspace_bytes(const moe_w4_dims_t* d, int32_t T, int32_t backward);
 
 /* y [T][N] (row stride ldy) = add + W_e x; x [T][K] (row stride ldx); add [T][N]
- * (row stride ldadd) or NULL (it may be y itself; x may not).  offsets int32 [n + 1],
- * ascending, as moe_sort gives them (any align), or NULL if n == 1.  Row strides
- * are multiples of 8 up to 2^22; T up to 2^20, and at most 2^35 elements of x
- * or y.  (Offsets are clamped to 0 .. T; where they descend, y is unspecified.) */
+ * (row stride ldadd) or NULL (it may be y itself).  Otherwise y's rows share no memory
+ * with x's or add's (MOE_E_INVAL); rows of one stride may lie between each other, of two
+ * strides not.  offsets int32 [n + 1], ascending, as moe_sort gives them (any align),
+ * or NULL if n == 1.  Row strides are multiples of 8 up to 2^22; T up to 2^20, and at
+ * most 2^35 elements of x or y.  (Offsets are clamped to 0 .. T; where they descend, y
+ * is unspecified.) */
 int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, int64_t ldx, int32_t T,
                    const int32_t* offsets, const void* add, int64_t ldadd, void* y, int64_t ldy, void* ws,
                    size_t ws_bytes, void* stream);

@@ -423,6 +423,8 @@ int moe_distill_backward(const void* z, int32_t dtype, int64_t ldz, int32_t T, i
   if (lddz > (int64_t)1 << 36 || (int64_t)T * lddz > (int64_t)1 << 36) return MOE_E_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (bad(stats, 4) || bad(dloss, 4) || bad(dz, (unsigned)elem_bytes(dtype))) return MOE_E_INVAL;
+  // (other workgroups may have written what one has yet to read)
+  if (dz != z && rows_overlap(z, ldz, V, dz, lddz, V, T, (int64_t)elem_bytes(dtype))) return MOE_E_INVAL;
   const int chunk = chunk_of(T, V, dtype, true), chunks = ceil_div(V, chunk);
   const hipStream_t s = (hipStream_t)stream;
   const DistillArgs a{z, ldz, T, V, k, ids, teacher, kLog2e / tau, 1.0f / tau, chunk, chunks, nullptr,

@@ -62,6 +62,20 @@ inline bool bad(const void* p, unsigned align) { return !p || !aligned_to(p, ali
 inline size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 inline size_t elem_bytes(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
 
+// Whether T rows of wp elements from p, ldp apart, share memory with T rows of wq from q, ldq
+// apart (ld >= w; elements of `bytes`).  Rows of one stride may lie between each other; of
+// rows of two strides the whole stretches are compared.
+inline bool rows_overlap(const void* p, int64_t ldp, int wp, const void* q, int64_t ldq, int wq, int64_t T,
+                         int64_t bytes) {
+  if (T <= 0) return false;
+  const int64_t at = (int64_t)((uintptr_t)q - (uintptr_t)p), a = wp * bytes, b = wq * bytes;
+  if (at >= (T - 1) * ldp * bytes + a || -at >= (T - 1) * ldq * bytes + b) return false;
+  if (ldp != ldq || T == 1) return true;
+  // row i + k of p starts r bytes before row i of q, row i + k + 1 ld - r bytes after it
+  const int64_t ld = ldp * bytes, r = (at % ld + ld) % ld, k = (at - r) / ld;
+  return (r < a && k < T && -k < T) || (ld - r < b && k + 1 < T && -k - 1 < T);
+}
+
 // Limits of one call, which keep every launch below 2^32 threads.
 constexpr int32_t kMaxRows = 1 << 20;   // T
 constexpr int32_t kMaxWidth = 1 << 16;  // H, K, N

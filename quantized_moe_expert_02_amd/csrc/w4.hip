@@ -210,6 +210,13 @@ int check_call(const moe_w4_dims_t* d, const void* packed, const void* x, int64_
   return ldx > kMaxLd || ldy > kMaxLd || (add && ldadd > kMaxLd) ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
+// Rows are read while others are written: y shares no memory with x, and with add only where it is add.
+bool outputs_overlap(const W4Args& a, int into, int out) {
+  const bool same = a.add == a.y && (a.ldadd == a.ldy || a.T == 1);
+  return rows_overlap(a.x, a.ldx, into, a.y, a.ldy, out, a.T, 2) ||
+         (a.add && !same && rows_overlap(a.add, a.ldadd, out, a.y, a.ldy, out, a.T, 2));
+}
+
 void launch_sum(const W4Args& a, int dtype, int width, hipStream_t s) {
   const int blocks = ceil_div((int64_t)a.T * (width / 4), 256);
   if (dtype == MOE_T_F16) k_w4_sum<MOE_T_F16><<<blocks, 256, 0, s>>>(a, width);
@@ -271,6 +278,7 @@ int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, in
   W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, x, ldx, T, offsets, add,
            ldadd, y, ldy, nullptr, 1};
   if (few_rows(*d, T)) {
+    if (outputs_overlap(a, d->K, d->N)) return MOE_E_INVAL;
     launch_w4_few(a, *d, l, s);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
   }
@@ -282,6 +290,7 @@ int moe_w4_forward(const moe_w4_dims_t* d, const void* packed, const void* x, in
     a.part = (float*)ws;
     a.split = p.split;
   }
+  if (outputs_overlap(a, d->K, d->N)) return MOE_E_INVAL;
   launch_w4_rows(a, *d, l, p, s);
   if (need) launch_sum(a, d->dtype, d->N, s);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
@@ -298,6 +307,7 @@ int moe_w4_backward(const moe_w4_dims_t* d, const void* packed, const void* dy, 
   W4Args a{(const uint8_t*)packed, l.stride, l.soff, l.zoff, d->n, d->N, d->K, l.NB, l.KB, dy, lddy, T, offsets, add,
            ldadd, dx, lddx, nullptr, 1};
   if (const int M = few_grad_rows(*d, T)) {
+    if (outputs_overlap(a, d->N, d->K)) return MOE_E_INVAL;
     launch_w4_grad_few(a, *d, l, M, s);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
   }
@@ -309,6 +319,7 @@ int moe_w4_backward(const moe_w4_dims_t* d, const void* packed, const void* dy, 
     a.part = (float*)ws;
   }
   a.split = p.split;
+  if (outputs_overlap(a, d->N, d->K)) return MOE_E_INVAL;
   launch_w4_grad(a, *d, l, p, s);
   if (need) launch_sum(a, d->dtype, d->K, s);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;

@@ -50,7 +50,7 @@ def moe_distill_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: torch
                          dloss: torch.Tensor, temperature: float = 1.0, out: Optional[torch.Tensor] = None,
                          stream=None) -> torch.Tensor:
     """dlogits [T][V] for dloss fp32 [T]; stats from the forward call; `out` may be
-    `logits`, whose values are then replaced."""
+    `logits`, whose values are then replaced, but must not share memory with it otherwise."""
     code, T, V, k, dev, ld = _teacher(logits, ids, teacher)
     _check("stats", stats, _F32, (T, 2), dev)
     _check("dloss", dloss, _F32, (T,), dev)

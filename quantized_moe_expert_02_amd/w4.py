@@ -97,11 +97,12 @@ def moe_w4_forward(x: torch.Tensor, w: W4Weights, offsets: Optional[torch.Tensor
                    add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = add[t] + W_e @ x[t], x [T][K]; rows offsets[e] .. offsets[e + 1] - 1
     (int32 [n + 1], as moe_dispatch gives them) use matrix e, rows outside every
-    group get add[t] or zeros; `add` may be `out`."""
+    group get add[t] or zeros; `add` may be `out`, which must not share memory with `x`."""
     return _product(lib().moe_w4_forward, 0, "x", x, w, w.shape[2], w.shape[1], offsets, add, out, stream)
 
 
 def moe_w4_backward(dy: torch.Tensor, w: W4Weights, offsets: Optional[torch.Tensor] = None,
                     add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """dx[t] = add[t] + W_e.T @ dy[t], dy [T][N]: the gradient of moe_w4_forward's rows."""
+    """dx[t] = add[t] + W_e.T @ dy[t], dy [T][N]: the gradient of moe_w4_forward's rows;
+    `add` and `out` as there."""
     return _product(lib().moe_w4_backward, 1, "dy", dy, w, w.shape[1], w.shape[2], offsets, add, out, stream)
