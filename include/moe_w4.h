@@ -13,9 +13,11 @@
  * Conventions are those of moe_dispatch.h.  Rows and scales are binary16 or
  * bfloat16 (one moe_dtype_t for all), codes int4 two's complement, zero points
  * int8.  Sums are fp32 and rounded once.  In forward calls of few rows
- * (moe_w4_few_rows) the codes are exact factors and a group's sum is multiplied by
- * its scale in fp32; otherwise the product (q - z) s is rounded to the rows' type
- * before it is multiplied (binary16: to no finer than 2^-24).  Scales are finite.
+ * (moe_w4_few_rows) the codes q - z are exact factors and a group's sum is multiplied
+ * by its scale in fp32.  Otherwise, and in all backward calls, the weight (q - z) s is
+ * rounded to the rows' type before it is multiplied, as a 16-bit model's weights are
+ * (binary16: to no finer than 2^-24, and infinite from 65520 on).  Scales are finite;
+ * where weights are rounded, bfloat16 scales are at most 2^117 in magnitude.
  * Infinities and NaNs in rows propagate as the formulas say; rows of other experts and
  * rows outside the groups are never read.  A row's values do not depend on the rows
  * beside it where calls have the same T and n.

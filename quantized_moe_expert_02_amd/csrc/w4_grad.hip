@@ -17,7 +17,7 @@ namespace {
 // 2048 x 6144 binary16 64 us (0.81 PFLOP/s), 16,384 rows of 256 experts of 2048 x 512
 // bfloat16, laid out by Zipf's law, 90 us.
 // ---------------------------------------------------------------------------
-// As GroupScale, with a scale for each of the eight.
+// As GroupScale (w4.h, also on why weights are rounded), with a scale for each of the eight.
 template <int DT, bool ZP>
 struct RowScales;
 template <bool ZP>
