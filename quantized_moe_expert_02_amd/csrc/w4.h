@@ -314,8 +314,9 @@ struct GroupScale<MOE_T_BF16, ZP> {
   __device__ __forceinline__ void set(uint16_t sv, int z) {
     s = scale_value<MOE_T_BF16>(sv);
     s16 = s * 0.0625f;
-    c = (float)(-1032 - z) * s;
-    c16 = (float)(-72 - z) * s;
+    const float minus_z = (float)-z;  // (each addend is exact: at most 11 + 8 bits)
+    c = fmaf(minus_z, s, -1032.0f * s);
+    c16 = fmaf(minus_z, s, -72.0f * s);
   }
   __device__ __forceinline__ v8_t<MOE_T_BF16> weights(uint32_t d) const {
     half2_t v[4];

@@ -128,7 +128,8 @@ int check_w4_rows(const moe_w4_dims_t* d, int32_t T) {
 // 2048, 64 rows 7.4 and 14.3, 256 14.0 and 18.9, 512 21.0 and 21.6; 6144 x 6144, 32 rows 15.1
 // and 16.4, 48 23.4 and 20.3; 6144 x 2048 with groups of 32 and zero points, 96 rows 18.7 and
 // 20.3, 256 33.3 and 27.8; 32,000 x 2048, 24 rows 21.9 and 18.8; in several passes, 512 rows of
-// 40 x 16384 26.8 and 20.0, 300 of 8 x 65536 73 and 33).
+// 40 x 16384 26.8 and 20.0, 300 of 8 x 65536 73 and 33; bfloat16, whose codes take more
+// instructions, 2048 x 2048, 64 rows 7.7 and 14.3, 256 15.2 and 18.7, 512 22.3 and 21.8).
 constexpr int kFewRowsMost = 512, kOnePass = 48;
 constexpr int64_t kFewBlocks = 40 << 10;
 

@@ -12,14 +12,17 @@ namespace {
 // while the next item's blocks are under way.  The rows are the first operand (index l
 // % 16: the row; rows past the tile are zeros) and a block the second (index l %
 // 16: its row), so that a lane's four sums belong to one weight row and are
-// multiplied by its scale.  binary16 factors are the codes q - z themselves;
-// bfloat16 holds 128 + u exactly, and (136 + z) times the sum of the rows' elements
-// is taken off each group's sum.
+// multiplied by its scale.  The factors are the codes q - z themselves, in bfloat16 2^-15 of
+// them (exact too: |q - z| <= 136), so that a group's sum, of up to 128 terms, stays in fp32's
+// range whatever the rows hold; the result is multiplied by 2^15.  (Offset codes, 128 + u,
+// with (136 + z) times the sum of the row taken off again, take 7 instead of 17 instructions
+// per dword, 40.2 us instead of 42.8 below, but lose what stands beside a large element.)
 // Bound by memory where there is much to read (64 rows of 256 experts of 2048 x 6144
-// binary16, 369 MB: 73 us, 5.1 TB/s), by the vector unit beside it with groups of 32 and zero
-// points (8 rows of 128,000 x 2048 bfloat16, 158 MB: 43.5 us, 3.6 TB/s), and by its start in
-// short calls (one row of 6144 x 6144: 9 us).  An item per workgroup instead of runs: 136
-// and 61 us for the first two.
+// binary16, 369 MB: 73 us, 5.1 TB/s).  With groups of 32 and zero points a block of four
+// dwords takes 105 vector and 4 matrix instructions beside it, 22 and 3 us of 8 rows of
+// 128,000 x 2048 bfloat16, which hide only in part behind its 158 MB: 42.8 us, 3.7 TB/s.  Short
+// calls (one row of 6144 x 6144: 9 us): the start, and 384 items on 256 workgroups.  An item
+// per workgroup instead of runs: 136 and 61 us for the first two.
 // ---------------------------------------------------------------------------
 template <int DT, int SG, bool ZP, int W, int KPW>
 __global__ __launch_bounds__(64 * W) void k_w4_few(W4Args a) {
@@ -163,8 +166,8 @@ void launch_w4_few(const W4Args& a, const moe_w4_dims_t& d, const W4Layout& l, h
     };
     // Wavefronts and column blocks of each so that W KPW fits the columns, and workgroups as
     // registers allow (us; 128,000 rows, K 2048, T 1, binary16, groups of 128: 4 x 4 28.2, 8 x 2
-    // 32.9; T 8, bfloat16, groups of 32 with zero points, which need more registers: 53.9 and
-    // 41.6 with offset codes; 24,576 rows, K 2560: 8 x 3 11.7, 16 x 3 14.3; K 5120: 16 x 3 17.7, 8 x 6 19.4;
+    // 32.9; T 8, bfloat16, groups of 32 with zero points, which need more registers: 47.6 and
+    // 42.8; 24,576 rows, K 2560: 8 x 3 11.7, 16 x 3 14.3; K 5120: 16 x 3 17.7, 8 x 6 19.4;
     // 60,000 rows, K 512: 2 x 2 7.8, 4 x 1 9.8).
     if (l.KB <= 4) launch(k_w4_few<DT, SG, ZP, 2, 2>, 2, 8);
     else if (l.KB <= 8) launch(k_w4_few<DT, SG, ZP, 4, 2>, 4, 5);
