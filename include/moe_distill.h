@@ -8,7 +8,8 @@
  *   p_j = exp(a_j / tau) / sum over kept i of exp(a_i / tau)
  *   m = max_v z_v,  l = log sum_v exp((z_v - m) / tau)
  *   log q_v = (z_v - m) / tau - l
- *   loss = sum over kept j of p_j (log p_j - log q_{id_j})    (0 where p_j = 0)
+ *   loss = sum over kept j of p_j (log p_j - log q_{id_j})    (0 where p_j = 0; one
+ *                                                             below 2^-126 counts as 0)
  *   gradient dz_v = dloss / tau * (q_v - sum over kept j with id_j = v of p_j)
  * An id may occur more than once.  A row that keeps no entry, or whose kept a_j are
  * all -infinity (a padding position), has loss, m, l and gradient 0, whatever its
