@@ -14,8 +14,10 @@ namespace {
 // columns (eight bytes of each lane's sixteen) and all rows of the tile.
 // Turned are codes, a quarter of what turning decoded weights would move.  Bound, as the
 // forward product, by decoding and matrix instructions, which take turns: 2,048 rows of
-// 2048 x 6144 binary16 64 us (0.81 PFLOP/s), 16,384 rows of 256 experts of 2048 x 512
-// bfloat16, laid out by Zipf's law, 90 us.
+// 2048 x 6144 binary16 64 us (0.81 PFLOP/s; vector instructions 56% and matrix instructions
+// 37% of a busy CU's cycles), 16,384 rows of 256 experts of 2048 x 512 bfloat16, laid out by
+// Zipf's law, 90 us (64% and 25%, and a third of the CUs' time without a workgroup: some 840
+// of unlike length on 512 places).
 // ---------------------------------------------------------------------------
 // As GroupScale (w4.h, also on why weights are rounded), with a scale for each of the eight.
 template <int DT, bool ZP>

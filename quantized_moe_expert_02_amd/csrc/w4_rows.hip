@@ -10,8 +10,11 @@ namespace {
 // decoded once per tile and by one wavefront.  Bound by decoding and matrix instructions, which
 // hardly overlap: a 16x16x32 instruction takes 16 cycles, with 2, 3, 4 and 6 vector
 // instructions beside it 18.8, 21.8, 25.0 and 31.0; the more rows a tile has the less
-// decoding weighs.  2,048 rows of 6144 x 6144 bfloat16 147 us (1.05 PFLOP/s); 16,384 rows
-// of 256 experts of 1024 x 2048, laid out by Zipf's law, 135 us.
+// decoding weighs.  2,048 rows of 6144 x 6144 bfloat16 147 us (1.05 PFLOP/s; vector
+// instructions 48% and matrix instructions 50% of a busy CU's cycles); 16,384 rows of 256
+// experts of 1024 x 2048, laid out by Zipf's law, 137 us (64% and 29%, and a fifth of the
+// CUs' time without a workgroup, most of it at the end); 512 and 4,096 rows of 256 experts of
+// 2048 x 1024 binary16 42 and 83 us (51% and 11%, 55% and 18%: waits for a tile's first steps).
 template <int DT, int SG, bool ZP, int MT, int R>
 __global__ __launch_bounds__(kTileThreads, 2) void k_w4_rows(W4Args a, int groups) {
   constexpr int BM = 16 * MT;
